@@ -380,6 +380,138 @@ ssd_status_t ssd_gated_rmsnorm(int64_t rows, int64_t dim, int64_t ngroups, ssd_d
                                const void *z, int64_t z_stride, const float *weight, float eps, void *out,
                                void *stream);
 
+/*
+ * The gated delta rule. No counterpart in the pages: the state update of a linear-attention
+ * layer that first takes back what the state holds under the new key. Per batch row b and head h
+ * (group of head h: h / (nheads / ngroups), as everywhere),
+ *     h'  = exp(g_t) h_{t-1}                       (decay; P x N state)
+ *     u_t = beta_t (x_t - h' B_t)                  (what is new in x_t under the key B_t)
+ *     h_t = h' + u_t B_t^T,    y_t = h_t C_t       (write, read with the query C_t)
+ * Layouts, types, streams and errors as in ssd_fwd:
+ *   x        [B, L, H, P]   dtype          values
+ *   g        [B, L, H]      dtype          log decay, used as given (g <= 0 expected; minus
+ *                                          infinity clears the state)
+ *   beta     [B, L, H]      dtype          write strength, used as given
+ *   Bm, Cm   [B, L, G, N]   dtype          keys and queries, used as given: the layer scales its
+ *                                          keys to unit length (ssd_add_rmsnorm with weight
+ *                                          N^-1/2); |B|^2 beta > 2 makes the recurrence grow
+ *   h0       [B, H, P, N]   fp32 or NULL   state before the first token (NULL = zeros)
+ *   y        [B, L, H, P]   dtype          output
+ *   h_final  [B, H, P, N]   fp32 or NULL   state after the last token
+ * Outputs may not overlap inputs. seqlen == 0 writes only h_final; batch == 0 does nothing.
+ */
+ssd_status_t ssd_delta_fwd_plan(const ssd_shape_t *shape, ssd_dtype_t dtype, ssd_plan_t *plan);
+ssd_status_t ssd_delta_fwd(const ssd_shape_t *shape, ssd_dtype_t dtype, const void *x, const void *g, const void *beta,
+                           const void *Bm, const void *Cm, const float *h0, void *y, float *h_final, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
+ * One generated token of the gated delta rule: state_out = the state after the token, y = its
+ * output. shape->seqlen must be 1.
+ *   state      [B, H, P, N]   fp32    state before the token
+ *   state_out  [B, H, P, N]   fp32    out; may be `state` itself (in place), no other overlap
+ *                                     (SSD_ERR_INVALID_ARG)
+ *   x          [B, H, P]      dtype
+ *   g, beta    [B, H]         dtype
+ *   Bm, Cm     [B, G, N]      dtype
+ *   y          [B, H, P]      dtype
+ * Requires dstate % 4 == 0.
+ */
+ssd_status_t ssd_delta_decode_step(const ssd_shape_t *shape, ssd_dtype_t dtype, const float *state, float *state_out,
+                                   const void *x, const void *g, const void *beta, const void *Bm, const void *Cm, void *y,
+                                   void *stream);
+
+/*
+ * Backward pass of ssd_delta_fwd: the gradient of sum(dy * y) + sum(dh_final * h_final) with
+ * respect to every input; the states are recomputed.
+ *   x, g, beta, Bm, Cm, h0     the forward's inputs
+ *   dy        [B, L, H, P]   dtype          cotangent of y
+ *   dh_final  [B, H, P, N]   fp32 or NULL   cotangent of h_final (NULL = 0)
+ *   dx        [B, L, H, P]   dtype          out
+ *   dg, dbeta [B, L, H]      dtype          out
+ *   dBm, dCm  [B, L, G, N]   dtype          out, summed over the heads of each group in a fixed order
+ *   dh0       [B, H, P, N]   fp32 or NULL   out (also when h0 is NULL: the gradient at h0 = 0)
+ *   workspace, workspace_bytes              >= ssd_delta_bwd_plan's workspace_bytes
+ * Outputs may not overlap inputs. seqlen == 0 writes dh0 = dh_final (or zeros).
+ */
+ssd_status_t ssd_delta_bwd_plan(const ssd_shape_t *shape, ssd_dtype_t dtype, ssd_plan_t *plan);
+ssd_status_t ssd_delta_bwd(const ssd_shape_t *shape, ssd_dtype_t dtype, const void *x, const void *g, const void *beta,
+                           const void *Bm, const void *Cm, const float *h0, const void *dy, const float *dh_final, void *dx,
+                           void *dg, void *dbeta, void *dBm, void *dCm, float *dh0, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
+ * The norm before a block, with the residual add and its scale: per row of `dim` channels,
+ *     r = residual + scale * x,    out = weight * r / sqrt(mean of r^2 + eps)
+ *   x         [rows, dim]   dtype               a branch's output
+ *   residual  [rows, dim]   res_dtype or NULL   the residual stream (NULL = 0)
+ *   scale     [dim]         fp32 or NULL        per-channel scale of the branch (NULL = 1)
+ *   weight    [dim]         fp32
+ *   res_out   [rows, dim]   res_dtype or NULL   out: r; may be `residual` itself (in place)
+ *   out       [rows, dim]   dtype               out; may be `x` itself
+ * No other overlap is allowed. res_dtype is dtype or SSD_F32. The norm is taken of r before its
+ * rounding to res_dtype. Requires dim <= 8192; 16-byte aligned pointers. Without residual and with
+ * weight = dim^-1/2 this scales rows to unit length.
+ */
+ssd_status_t ssd_add_rmsnorm(int64_t rows, int64_t dim, ssd_dtype_t dtype, ssd_dtype_t res_dtype, const void *x,
+                             const void *residual, const float *scale, const float *weight, float eps, void *res_out,
+                             void *out, void *stream);
+
+/*
+ * Its gradient, given the saved sum and the cotangents of both outputs.
+ *   res       [rows, dim]   res_dtype           the forward's r (res_out; x itself where the forward
+ *                                               had neither residual nor scale)
+ *   dout      [rows, dim]   dtype               cotangent of out
+ *   dres_in   [rows, dim]   res_dtype or NULL   cotangent of res_out (NULL = 0)
+ *   x         [rows, dim]   dtype or NULL       the forward's x, read for dscale alone
+ *   dres      [rows, dim]   res_dtype or NULL   out: gradient of the residual; may be dres_in itself
+ *   dx        [rows, dim]   dtype or NULL       out: scale * that gradient; may be dout itself
+ *   dw        [dim]         fp32 or NULL        out: gradient of weight, summed over the rows
+ *   dscale    [dim]         fp32 or NULL        out: gradient of scale (needs x)
+ *   workspace                                   ssd_norm_bwd_workspace_bytes(rows, dim) if dw or
+ *                                               dscale is wanted
+ * No other overlap is allowed. The sums over rows are in a fixed order. rows == 0 zeroes dw and
+ * dscale.
+ */
+ssd_status_t ssd_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, size_t *bytes);
+ssd_status_t ssd_add_rmsnorm_bwd(int64_t rows, int64_t dim, ssd_dtype_t dtype, ssd_dtype_t res_dtype, const void *res,
+                                 const float *weight, float eps, const void *dout, const void *dres_in, const void *x,
+                                 const float *scale, void *dres, void *dx, float *dw, float *dscale, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
+ * The norm after a layer, then the gate (ssd_gated_rmsnorm gates first): per row, in `ngroups`
+ * groups of dim / ngroups consecutive channels,
+ *     out = weight * y / sqrt(mean over the group of y^2 + eps) * silu(z)
+ *   y       [rows, dim]   dtype, 16-byte aligned
+ *   z       [rows, *]     dtype, row stride z_stride elements (>= dim), any element alignment
+ *   weight  [dim]         fp32
+ *   out     [rows, dim]   dtype, 16-byte aligned; may be y itself, no other overlap
+ * Requires dim / ngroups <= 8192.
+ */
+ssd_status_t ssd_norm_gate(int64_t rows, int64_t dim, int64_t ngroups, ssd_dtype_t dtype, const void *y, const void *z,
+                           int64_t z_stride, const float *weight, float eps, void *out, void *stream);
+
+/*
+ * The gradients of ssd_norm_gate and of ssd_gated_rmsnorm.
+ *   y, z, weight, eps         the forward's inputs
+ *   dout  [rows, dim]         cotangent of out
+ *   dy    [rows, dim]         out; may be y or dout itself
+ *   dz    [rows, *]           out, row stride dz_stride (>= dim): the columns of a wider row can be
+ *                             written in place; may be z itself at the same stride
+ *   dw    [dim] fp32 or NULL  out, summed over the rows in a fixed order
+ *   workspace                 ssd_norm_bwd_workspace_bytes(rows, dim) if dw is wanted
+ * No other overlap is allowed (of z and dz: SSD_ERR_INVALID_ARG). rows == 0 zeroes dw. Requires
+ * dim / ngroups <= 8192.
+ */
+ssd_status_t ssd_norm_gate_bwd(int64_t rows, int64_t dim, int64_t ngroups, ssd_dtype_t dtype, const void *y, const void *z,
+                               int64_t z_stride, const float *weight, float eps, const void *dout, void *dy, void *dz,
+                               int64_t dz_stride, float *dw, void *workspace, size_t workspace_bytes, void *stream);
+ssd_status_t ssd_gated_rmsnorm_bwd(int64_t rows, int64_t dim, int64_t ngroups, ssd_dtype_t dtype, const void *y,
+                                   const void *z, int64_t z_stride, const float *weight, float eps, const void *dout,
+                                   void *dy, void *dz, int64_t dz_stride, float *dw, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -308,3 +308,105 @@ def mamba2_mixer(u, in_proj_w, conv_w, conv_b, dt_bias, A, D, norm_w, out_proj_w
     o = gated_rmsnorm(y.reshape(*y.shape[:2], HP), z, norm_w, ngroups=norm_groups, eps=eps)
     return o @ out_proj_w.T, hf
 
+
+
+# ---- the gated delta rule and the norms around its block ----------------------------------
+
+def _delta_tokens(x, g, beta, Bm, Cm):
+    x, g, beta, Bm, Cm = map(_f64, (x, g, beta, Bm, Cm))
+    rep = x.shape[2] // Bm.shape[2]
+    return x, np.exp(g), beta, np.repeat(Bm, rep, axis=2), np.repeat(Cm, rep, axis=2)
+
+
+def delta_recurrent(x, g, beta, Bm, Cm, h0=None):
+    """h' = exp(g_t) h_{t-1}, h_t = h' + beta_t (x_t - h' B_t) B_t^T, y_t = h_t C_t, token by token.
+    x [B,L,H,P], g, beta [B,L,H], Bm, Cm [B,L,G,N]. Returns (y, h_final)."""
+    x, a, beta, k, q = _delta_tokens(x, g, beta, Bm, Cm)
+    Bsz, L, H, P = x.shape
+    S = np.zeros((Bsz, H, P, k.shape[3])) if h0 is None else _f64(h0).copy()
+    y = np.zeros_like(x)
+    for t in range(L):
+        S = a[:, t, :, None, None] * S
+        u = beta[:, t, :, None] * (x[:, t] - np.einsum("bhpn,bhn->bhp", S, k[:, t]))
+        S = S + u[..., None] * k[:, t, :, None, :]
+        y[:, t] = np.einsum("bhpn,bhn->bhp", S, q[:, t])
+    return y, S
+
+
+def delta_backward(x, g, beta, Bm, Cm, h0, dy, dh_final=None):
+    """The adjoint of delta_recurrent, token by token in reverse over kept states: a dict of dx, dg,
+    dbeta, dB, dC, dh0 for sum(dy y) + sum(dh_final h_final)."""
+    G = np.shape(Bm)[2]
+    x, a, beta, k, q = _delta_tokens(x, g, beta, Bm, Cm)
+    dy = _f64(dy)
+    Bsz, L, H, P = x.shape
+    N = k.shape[3]
+    S = np.zeros((Bsz, H, P, N)) if h0 is None else _f64(h0).copy()
+    kept = []
+    for t in range(L):
+        Sd = a[:, t, :, None, None] * S
+        err = x[:, t] - np.einsum("bhpn,bhn->bhp", Sd, k[:, t])
+        S = Sd + (beta[:, t, :, None] * err)[..., None] * k[:, t, :, None, :]
+        kept.append((Sd, err, S))
+    D = np.zeros((Bsz, H, P, N)) if dh_final is None else _f64(dh_final).copy()
+    dx, dg, dbeta, dk, dq = (np.zeros_like(v) for v in (x, a, beta, k, q))
+    for t in range(L - 1, -1, -1):
+        Sd, err, S = kept[t]
+        dq[:, t] = np.einsum("bhp,bhpn->bhn", dy[:, t], S)
+        D = D + dy[:, t, ..., None] * q[:, t, :, None, :]
+        du = np.einsum("bhpn,bhn->bhp", D, k[:, t])
+        dbeta[:, t] = np.sum(du * err, axis=-1)
+        dx[:, t] = beta[:, t, :, None] * du
+        dk[:, t] = (np.einsum("bhp,bhpn->bhn", beta[:, t, :, None] * err, D)
+                    - np.einsum("bhp,bhpn->bhn", dx[:, t], Sd))
+        D = D - dx[:, t, ..., None] * k[:, t, :, None, :]
+        dg[:, t] = np.sum(D * Sd, axis=(-1, -2))
+        D = a[:, t, :, None, None] * D
+    fold = lambda v: v.reshape(Bsz, L, G, H // G, N).sum(axis=3)  # noqa: E731
+    return {"dx": dx, "dg": dg, "dbeta": dbeta, "dB": fold(dk), "dC": fold(dq), "dh0": D}
+
+
+def add_rmsnorm(x, residual, weight, *, scale=None, eps):
+    """r = residual + scale x, out = weight r / sqrt(mean(r^2) + eps); returns (r, out)."""
+    r = _f64(x) * (1.0 if scale is None else _f64(scale)) + (0.0 if residual is None else _f64(residual))
+    return r, _f64(weight) * r / np.sqrt(np.mean(r * r, axis=-1, keepdims=True) + eps)
+
+
+def add_rmsnorm_backward(r, weight, dout, dres=None, *, x=None, scale=None, eps):
+    """Gradients of sum(dout out) + sum(dres r): a dict dres (of the residual), dx, dw, dscale."""
+    r, weight, dout = map(_f64, (r, weight, dout))
+    root = np.sqrt(np.mean(r * r, axis=-1, keepdims=True) + eps)
+    dr = weight * dout / root - r * np.mean(weight * dout * r, axis=-1, keepdims=True) / root ** 3
+    if dres is not None:
+        dr = dr + _f64(dres)
+    rows = tuple(range(r.ndim - 1))
+    out = {"dres": dr, "dx": dr if scale is None else _f64(scale) * dr, "dw": np.sum(dout * r / root, axis=rows)}
+    if scale is not None and x is not None:
+        out["dscale"] = np.sum(dr * _f64(x), axis=rows)
+    return out
+
+
+def norm_gate(y, z, weight, *, ngroups, eps):
+    """weight * y / sqrt(mean over the group of y^2 + eps) * silu(z)."""
+    y, z, weight = map(_f64, (y, z, weight))
+    yg = y.reshape(*y.shape[:-1], ngroups, -1)
+    n = yg / np.sqrt(np.mean(yg * yg, axis=-1, keepdims=True) + eps)
+    return n.reshape(y.shape) * weight * silu(z)
+
+
+def gate_norm_backward(y, z, weight, dout, *, ngroups, eps, gate_first):
+    """Gradients dy, dz, dw of norm_gate or (gate_first) gated_rmsnorm, by the chain rule through
+    n = a / sqrt(mean(a^2) + eps) with a the normalised quantity."""
+    y, z, weight, dout = map(_f64, (y, z, weight, dout))
+    shape = (*y.shape[:-1], ngroups, -1)
+    gate, sig = silu(z), 1.0 / (1.0 + np.exp(-z))
+    slope = sig + z * sig * (1.0 - sig)
+    a = (y * gate if gate_first else y).reshape(shape)
+    root = np.sqrt(np.mean(a * a, axis=-1, keepdims=True) + eps)
+    n = (a / root).reshape(y.shape)
+    dn = (weight * dout * (1.0 if gate_first else gate)).reshape(shape)
+    da = (dn / root - a * np.mean(dn * a, axis=-1, keepdims=True) / root ** 3).reshape(y.shape)
+    rows = tuple(range(y.ndim - 1))
+    if gate_first:
+        return {"dy": da * gate, "dz": da * y * slope, "dw": np.sum(dout * n, axis=rows)}
+    return {"dy": da, "dz": weight * dout * n * slope, "dw": np.sum(dout * n * gate, axis=rows)}

@@ -61,6 +61,20 @@ _SIGS = {
                           ctypes.c_int),
     "ssd_bwd": ([ctypes.POINTER(ShapeT), ctypes.c_int] + [_vp] * 7 + [_i64] + [_vp] * 9 + [_vp, _sz, _vp],
                 ctypes.c_int),
+    "ssd_delta_fwd_plan": ([ctypes.POINTER(ShapeT), ctypes.c_int, ctypes.POINTER(PlanT)], ctypes.c_int),
+    "ssd_delta_fwd": ([ctypes.POINTER(ShapeT), ctypes.c_int] + [_vp] * 9 + [_sz, _vp], ctypes.c_int),
+    "ssd_delta_decode_step": ([ctypes.POINTER(ShapeT), ctypes.c_int] + [_vp] * 9, ctypes.c_int),
+    "ssd_delta_bwd_plan": ([ctypes.POINTER(ShapeT), ctypes.c_int, ctypes.POINTER(PlanT)], ctypes.c_int),
+    "ssd_delta_bwd": ([ctypes.POINTER(ShapeT), ctypes.c_int] + [_vp] * 15 + [_sz, _vp], ctypes.c_int),
+    "ssd_norm_bwd_workspace_bytes": ([_i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
+    "ssd_add_rmsnorm": ([_i64, _i64, ctypes.c_int, ctypes.c_int] + [_vp] * 4 + [ctypes.c_float] + [_vp] * 3, ctypes.c_int),
+    "ssd_add_rmsnorm_bwd": ([_i64, _i64, ctypes.c_int, ctypes.c_int, _vp, _vp, ctypes.c_float] + [_vp] * 9 + [_sz, _vp],
+                            ctypes.c_int),
+    "ssd_norm_gate": ([_i64, _i64, _i64, ctypes.c_int, _vp, _vp, _i64, _vp, ctypes.c_float, _vp, _vp], ctypes.c_int),
+    "ssd_norm_gate_bwd": ([_i64, _i64, _i64, ctypes.c_int, _vp, _vp, _i64, _vp, ctypes.c_float, _vp, _vp, _vp, _i64, _vp,
+                           _vp, _sz, _vp], ctypes.c_int),
+    "ssd_gated_rmsnorm_bwd": ([_i64, _i64, _i64, ctypes.c_int, _vp, _vp, _i64, _vp, ctypes.c_float, _vp, _vp, _vp, _i64, _vp,
+                               _vp, _sz, _vp], ctypes.c_int),
 }
 
 CP_BLOCK = 128  # SSD_CP_BLOCK: tokens per decay block
@@ -386,3 +400,286 @@ def ssd_gated_rmsnorm(y, z, weight, *, ngroups, eps=1e-5, out=None, stream=None)
     _check(st, "ssd_gated_rmsnorm")
     return out
 
+
+
+# ---- the gated delta rule and the norms around its block ------------------------------
+
+
+def _need(name, t, shape, dtype, dev):
+    """t (None passes) has this shape and type, is contiguous and on `dev`."""
+    if t is None:
+        return
+    if t.device != dev or t.device.type != "cuda":
+        raise ValueError(f"{name}: libssd takes CUDA tensors on one device (got {t.device}, expected {dev})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: libssd takes contiguous tensors")
+
+
+class _On:
+    """The calls within run with `dev` current and allocate on `stream` (None: the device's current
+    stream), so that memory freed afterwards is not handed out again before the kernels are done."""
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream = dev, stream
+        self.ctx = None
+
+    def __enter__(self):
+        if self.stream is not None:
+            self.ctx = torch.cuda.stream(self.stream)
+        elif self.dev.index is not None and self.dev.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(self.dev)
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return ctypes.c_void_p((self.stream or torch.cuda.current_stream(self.dev)).cuda_stream)
+
+    def __exit__(self, *e):
+        if self.ctx is not None:
+            self.ctx.__exit__(*e)
+
+
+def _delta_shape(x, g, beta, B, C, batched):
+    """(ShapeT, dtype code) of the delta rule's inputs, checked against one another."""
+    lead = x.dim() - 2
+    if x.dim() != (4 if batched else 3) or B.dim() != x.dim():
+        raise ValueError("x and B: wrong number of dimensions")
+    dev, dt = x.device, x.dtype
+    code = _dtype_code(x)
+    H, P = x.shape[-2:]
+    G, N = B.shape[-2:]
+    _need("x", x, x.shape, dt, dev)
+    _need("g", g, x.shape[:lead + 1], dt, dev)
+    _need("beta", beta, x.shape[:lead + 1], dt, dev)
+    _need("B", B, (*x.shape[:lead], G, N), dt, dev)
+    _need("C", C, (*x.shape[:lead], G, N), dt, dev)
+    return ShapeT(x.shape[0], x.shape[1] if batched else 1, H, P, G, N), code
+
+
+def _delta_plan(fn, shape, code):
+    out = PlanT()
+    _check(getattr(lib(), fn)(ctypes.byref(shape), code, ctypes.byref(out)), fn)
+    return out
+
+
+def delta_fwd_plan(batch, seqlen, nheads, headdim, ngroups, dstate, dtype_code) -> dict:
+    """{'path': 'simt'|'mma'|'none', 'kernels': launches per call, 'workspace_bytes': int}."""
+    out = _delta_plan("ssd_delta_fwd_plan", ShapeT(batch, seqlen, nheads, headdim, ngroups, dstate), dtype_code)
+    return {"path": PATHS.get(out.path, str(out.path)), "kernels": out.kernels, "workspace_bytes": out.workspace_bytes}
+
+
+def delta_bwd_plan(batch, seqlen, nheads, headdim, ngroups, dstate, dtype_code) -> dict:
+    """As delta_fwd_plan, of ssd_delta_bwd."""
+    out = _delta_plan("ssd_delta_bwd_plan", ShapeT(batch, seqlen, nheads, headdim, ngroups, dstate), dtype_code)
+    return {"path": PATHS.get(out.path, str(out.path)), "kernels": out.kernels, "workspace_bytes": out.workspace_bytes}
+
+
+def _workspace(workspace, need, dev):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on the inputs' device")
+    return workspace
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def ssd_delta_fwd(x, g, beta, B, C, h0=None, *, y=None, h_final=None, return_final_state: bool = True, workspace=None,
+                  stream=None):
+    """y, h_final of the gated delta rule: x [B,L,H,P], g (log decay) and beta [B,L,H], B (keys) and
+    C (queries) [B,L,G,N], h0 [B,H,P,N] f32."""
+    shape, code = _delta_shape(x, g, beta, B, C, True)
+    dev = x.device
+    state = torch.Size((shape.batch, shape.nheads, shape.headdim, shape.dstate))
+    _need("h0", h0, state, torch.float32, dev)
+    _need("y", y, x.shape, x.dtype, dev)
+    _need("h_final", h_final, state, torch.float32, dev)
+    with _On(dev, stream) as st:
+        if y is None:
+            y = torch.empty_like(x)
+        if h_final is None and return_final_state:
+            h_final = torch.empty(state, dtype=torch.float32, device=dev)
+        ws = _workspace(workspace, _delta_plan("ssd_delta_fwd_plan", shape, code).workspace_bytes, dev)
+        _check(lib().ssd_delta_fwd(ctypes.byref(shape), code, _ptr(x), _ptr(g), _ptr(beta), _ptr(B), _ptr(C), _ptr(h0),
+                                   _ptr(y), _ptr(h_final), _ptr(ws), _bytes(ws), st), "ssd_delta_fwd")
+    return y, h_final
+
+
+def ssd_delta_decode_step(state, x, g, beta, B, C, *, state_out=None, y=None, stream=None):
+    """y [B,H,P] of one token of the gated delta rule; x [B,H,P], g and beta [B,H], B, C [B,G,N]. The
+    state [B,H,P,N] f32 is updated in place, or left alone and the new one written to state_out."""
+    shape, code = _delta_shape(x, g, beta, B, C, False)
+    dev = x.device
+    size = torch.Size((shape.batch, shape.nheads, shape.headdim, shape.dstate))
+    _need("state", state, size, torch.float32, dev)
+    _need("state_out", state_out, size, torch.float32, dev)
+    _need("y", y, x.shape, x.dtype, dev)
+    with _On(dev, stream) as st:
+        if y is None:
+            y = torch.empty_like(x)
+        _check(lib().ssd_delta_decode_step(ctypes.byref(shape), code, _ptr(state),
+                                           _ptr(state if state_out is None else state_out), _ptr(x), _ptr(g), _ptr(beta),
+                                           _ptr(B), _ptr(C), _ptr(y), st), "ssd_delta_decode_step")
+    return y
+
+
+def ssd_delta_bwd(x, g, beta, B, C, h0, dy, dh_final=None, *, want_dh0: bool = True, out=None, workspace=None, stream=None):
+    """Gradients of sum(dy * y) + sum(dh_final * h_final) through ssd_delta_fwd.
+
+    Returns a dict dx, dg, dbeta, dB, dC, dh0 (None unless want_dh0); `out` may supply any of those
+    tensors to write into."""
+    shape, code = _delta_shape(x, g, beta, B, C, True)
+    dev = x.device
+    state = torch.Size((shape.batch, shape.nheads, shape.headdim, shape.dstate))
+    _need("h0", h0, state, torch.float32, dev)
+    _need("dy", dy, x.shape, x.dtype, dev)
+    _need("dh_final", dh_final, state, torch.float32, dev)
+    o = dict(out or {})
+    with _On(dev, stream) as st:
+        for name, like in (("dx", x), ("dg", g), ("dbeta", beta), ("dB", B), ("dC", C)):
+            _need(name, o.get(name), like.shape, like.dtype, dev)
+            if o.get(name) is None:
+                o[name] = torch.empty_like(like)
+        _need("dh0", o.get("dh0"), state, torch.float32, dev)
+        if o.get("dh0") is None:
+            o["dh0"] = torch.empty(state, dtype=torch.float32, device=dev) if want_dh0 else None
+        ws = _workspace(workspace, _delta_plan("ssd_delta_bwd_plan", shape, code).workspace_bytes, dev)
+        _check(lib().ssd_delta_bwd(ctypes.byref(shape), code, _ptr(x), _ptr(g), _ptr(beta), _ptr(B), _ptr(C), _ptr(h0),
+                                   _ptr(dy), _ptr(dh_final), _ptr(o["dx"]), _ptr(o["dg"]), _ptr(o["dbeta"]), _ptr(o["dB"]),
+                                   _ptr(o["dC"]), _ptr(o["dh0"]), _ptr(ws), _bytes(ws), st), "ssd_delta_bwd")
+    return o
+
+
+def norm_bwd_workspace_bytes(rows, dim) -> int:
+    out = _sz(0)
+    _check(lib().ssd_norm_bwd_workspace_bytes(rows, dim, ctypes.byref(out)), "ssd_norm_bwd_workspace_bytes")
+    return out.value
+
+
+def ssd_add_rmsnorm(x, residual, weight, *, scale=None, eps=1e-5, res_out=None, out=None, want_res: bool = True, stream=None):
+    """res, out: r = residual + scale * x and weight * r / sqrt(mean(r^2) + eps) over the last axis.
+
+    residual (None = 0) is in x's type or fp32, weight and scale (None = 1) are fp32. res_out may be
+    residual itself. want_res=False (and no res_out given) returns None for r."""
+    dev, dim = x.device, x.shape[-1] if x.dim() else 0
+    rdt = next((t.dtype for t in (residual, res_out) if t is not None), x.dtype)
+    _need("x", x, x.shape, x.dtype, dev)
+    _need("residual", residual, x.shape, rdt, dev)
+    _need("weight", weight, (dim,), torch.float32, dev)
+    _need("scale", scale, (dim,), torch.float32, dev)
+    _need("res_out", res_out, x.shape, rdt, dev)
+    _need("out", out, x.shape, x.dtype, dev)
+    with _On(dev, stream) as st:
+        if res_out is None and want_res:
+            res_out = torch.empty(x.shape, dtype=rdt, device=dev)
+        if out is None:
+            out = torch.empty_like(x)
+        _check(lib().ssd_add_rmsnorm(x.numel() // dim if dim else 0, dim, _dtype_code(x), SSD_F32 if rdt == torch.float32 else
+                                     SSD_BF16, _ptr(x), _ptr(residual), _ptr(scale), _ptr(weight), float(eps), _ptr(res_out),
+                                     _ptr(out), st), "ssd_add_rmsnorm")
+    return res_out, out
+
+
+def ssd_add_rmsnorm_bwd(res, weight, dout, dres_in=None, *, x=None, scale=None, eps=1e-5, want_dw: bool = True, out=None,
+                        workspace=None, stream=None):
+    """Gradients of ssd_add_rmsnorm from its r (`res`), the cotangent dout of out and dres_in of r.
+
+    Returns a dict dres (the residual's), dx, dw (None unless want_dw), dscale (None unless scale and
+    the forward's x are given); `out` may supply any of those tensors to write into (dres may be
+    dres_in, dx may be dout)."""
+    dev, dim = dout.device, dout.shape[-1] if dout.dim() else 0
+    _need("dout", dout, dout.shape, dout.dtype, dev)
+    _need("res", res, dout.shape, res.dtype, dev)
+    _need("dres_in", dres_in, dout.shape, res.dtype, dev)
+    _need("x", x, dout.shape, dout.dtype, dev)
+    _need("weight", weight, (dim,), torch.float32, dev)
+    _need("scale", scale, (dim,), torch.float32, dev)
+    code, rcode = _dtype_code(dout), _dtype_code(res)
+    rows = dout.numel() // dim if dim else 0
+    o = dict(out or {})
+    with _On(dev, stream) as st:
+        for name, dt, shape, want in (("dres", res.dtype, dout.shape, True), ("dx", dout.dtype, dout.shape, True),
+                                      ("dw", torch.float32, (dim,), want_dw),
+                                      ("dscale", torch.float32, (dim,), scale is not None and x is not None)):
+            _need(name, o.get(name), shape, dt, dev)
+            if o.get(name) is None:
+                o[name] = torch.empty(shape, dtype=dt, device=dev) if want else None
+        sums = o["dw"] is not None or o["dscale"] is not None
+        ws = _workspace(workspace, norm_bwd_workspace_bytes(rows, dim) if sums else 0, dev)
+        _check(lib().ssd_add_rmsnorm_bwd(rows, dim, code, rcode, _ptr(res), _ptr(weight), float(eps), _ptr(dout),
+                                         _ptr(dres_in), _ptr(x), _ptr(scale), _ptr(o["dres"]), _ptr(o["dx"]), _ptr(o["dw"]),
+                                         _ptr(o["dscale"]), _ptr(ws), _bytes(ws), st), "ssd_add_rmsnorm_bwd")
+    return o
+
+
+def _rows_view(name, t, like, dev):
+    """The row stride of t [..., dim], a column slice of evenly spaced wider rows."""
+    if t.device != dev or t.dtype != like.dtype or t.shape != like.shape:
+        raise ValueError(f"{name}: expected {tuple(like.shape)} {like.dtype} on {dev}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: row views need unit column stride")
+    row = None
+    for i in range(t.dim() - 2, -1, -1):  # axes of one element have no stride to speak of
+        if t.shape[i] > 1:
+            if row is not None and t.stride(i) != span:
+                raise ValueError(f"{name}: row views need evenly spaced rows")
+            if row is None:
+                row = t.stride(i)
+            span = t.stride(i) * t.shape[i]
+    return t.shape[-1] if row is None else row
+
+
+def ssd_norm_gate(y, z, weight, *, ngroups, eps=1e-5, out=None, stream=None):
+    """out = weight * RMSNorm over `ngroups` groups of y * silu(z) (the norm first, then the gate);
+    y [..., dim] contiguous, z [..., dim] may be a column slice of wider rows."""
+    dev, dim = y.device, y.shape[-1] if y.dim() else 0
+    _need("y", y, y.shape, y.dtype, dev)
+    _need("weight", weight, (dim,), torch.float32, dev)
+    _need("out", out, y.shape, y.dtype, dev)
+    zs = _rows_view("z", z, y, dev)
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty_like(y)
+        _check(lib().ssd_norm_gate(y.numel() // dim if dim else 0, dim, ngroups, _dtype_code(y), _ptr(y), _ptr(z), zs,
+                                   _ptr(weight), float(eps), _ptr(out), st), "ssd_norm_gate")
+    return out
+
+
+def _gate_norm_bwd(fn, y, z, weight, dout, ngroups, eps, want_dw, out, workspace, stream):
+    dev, dim = y.device, y.shape[-1] if y.dim() else 0
+    _need("y", y, y.shape, y.dtype, dev)
+    _need("weight", weight, (dim,), torch.float32, dev)
+    _need("dout", dout, y.shape, y.dtype, dev)
+    zs = _rows_view("z", z, y, dev)
+    rows = y.numel() // dim if dim else 0
+    o = dict(out or {})
+    _need("dy", o.get("dy"), y.shape, y.dtype, dev)
+    _need("dw", o.get("dw"), (dim,), torch.float32, dev)
+    with _On(dev, stream) as st:
+        if o.get("dy") is None:
+            o["dy"] = torch.empty_like(y)
+        if o.get("dz") is None:
+            o["dz"] = torch.empty_like(y)
+        if o.get("dw") is None:
+            o["dw"] = torch.empty(dim, dtype=torch.float32, device=dev) if want_dw else None
+        dzs = _rows_view("dz", o["dz"], y, dev)
+        ws = _workspace(workspace, norm_bwd_workspace_bytes(rows, dim) if o["dw"] is not None else 0, dev)
+        _check(getattr(lib(), fn)(rows, dim, ngroups, _dtype_code(y), _ptr(y), _ptr(z), zs, _ptr(weight), float(eps),
+                                  _ptr(dout), _ptr(o["dy"]), _ptr(o["dz"]), dzs, _ptr(o["dw"]), _ptr(ws), _bytes(ws), st), fn)
+    return o
+
+
+def ssd_norm_gate_bwd(y, z, weight, dout, *, ngroups, eps=1e-5, want_dw: bool = True, out=None, workspace=None, stream=None):
+    """Gradients of ssd_norm_gate: a dict dy, dz, dw (None unless want_dw); `out` may supply any of
+    those tensors (dz may be a column slice of wider rows)."""
+    return _gate_norm_bwd("ssd_norm_gate_bwd", y, z, weight, dout, ngroups, eps, want_dw, out, workspace, stream)
+
+
+def ssd_gated_rmsnorm_bwd(y, z, weight, dout, *, ngroups, eps=1e-5, want_dw: bool = True, out=None, workspace=None,
+                          stream=None):
+    """Gradients of ssd_gated_rmsnorm, as ssd_norm_gate_bwd."""
+    return _gate_norm_bwd("ssd_gated_rmsnorm_bwd", y, z, weight, dout, ngroups, eps, want_dw, out, workspace, stream)

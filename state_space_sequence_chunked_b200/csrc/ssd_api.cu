@@ -2,7 +2,9 @@
 // Every check runs before any launch; on an error nothing is launched.
 #include <atomic>
 
+#include "ssd_delta.cuh"
 #include "ssd_internal.cuh"
+#include "ssd_norm.cuh"
 
 #define SSD_API extern "C" __attribute__((visibility("default")))
 
@@ -373,4 +375,273 @@ SSD_API ssd_status_t ssd_gated_rmsnorm(int64_t rows, int64_t dim, int64_t ngroup
         if (!aligned16(q)) return SSD_ERR_ALIGNMENT;
     return from_cuda(gated_rmsnorm_launch(rows, (int)dim, (int)ngroups, dtype, y, z, z_stride, weight, eps, out,
                                           static_cast<cudaStream_t>(stream)));
+}
+
+// ---- the gated delta rule -------------------------------------------------------------
+
+namespace {
+
+ssd_status_t make_delta(const ssd_shape_t *s, ssd_dtype_t dtype, ssd::DeltaProblem *p) {
+    ssd_status_t st = check_shape(s);
+    if (st != SSD_OK) return st;
+    if ((st = check_dtype(dtype)) != SSD_OK) return st;
+    *p = ssd::DeltaProblem{};
+    p->B = s->batch;
+    p->L = s->seqlen;
+    p->H = s->nheads;
+    p->P = s->headdim;
+    p->G = s->ngroups;
+    p->N = s->dstate;
+    p->dtype = dtype;
+    return SSD_OK;
+}
+
+ssd_plan_t delta_plan_of(const ssd::DeltaProblem &p, bool backward) {
+    ssd_plan_t out{};
+    if (p.B == 0 || p.L == 0) {
+        out.path = SSD_PATH_NONE;
+    } else {
+        out.path = SSD_PATH_SIMT;
+        out.kernels = backward ? 4 : 1;
+        out.workspace_bytes = backward ? delta_seq_bwd_workspace_bytes(p) : 0;
+    }
+    return out;
+}
+
+ssd_status_t state_or_zeros(float *dst, const float *src, const ssd::DeltaProblem &p, cudaStream_t s) {
+    const size_t bytes = (size_t)(p.B * p.H * p.P * p.N) * sizeof(float);
+    return from_cuda(src ? cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(dst, 0, bytes, s));
+}
+
+}  // namespace
+
+SSD_API ssd_status_t ssd_delta_fwd_plan(const ssd_shape_t *shape, ssd_dtype_t dtype, ssd_plan_t *plan) {
+    if (!plan) return SSD_ERR_INVALID_ARG;
+    DeltaProblem p;
+    const ssd_status_t st = make_delta(shape, dtype, &p);
+    if (st != SSD_OK) return st;
+    *plan = delta_plan_of(p, false);
+    return SSD_OK;
+}
+
+SSD_API ssd_status_t ssd_delta_bwd_plan(const ssd_shape_t *shape, ssd_dtype_t dtype, ssd_plan_t *plan) {
+    if (!plan) return SSD_ERR_INVALID_ARG;
+    DeltaProblem p;
+    const ssd_status_t st = make_delta(shape, dtype, &p);
+    if (st != SSD_OK) return st;
+    *plan = delta_plan_of(p, true);
+    return SSD_OK;
+}
+
+SSD_API ssd_status_t ssd_delta_fwd(const ssd_shape_t *shape, ssd_dtype_t dtype, const void *x, const void *g,
+                                   const void *beta, const void *Bm, const void *Cm, const float *h0, void *y,
+                                   float *h_final, void *workspace, size_t workspace_bytes, void *stream) {
+    DeltaProblem p;
+    ssd_status_t st = make_delta(shape, dtype, &p);
+    if (st != SSD_OK) return st;
+    if (p.B == 0) return SSD_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const void *ptrs[] = {x, g, beta, Bm, Cm, h0, y, h_final, workspace};
+    if (p.L > 0 && (!x || !g || !beta || !Bm || !Cm || !y)) return SSD_ERR_INVALID_ARG;
+    for (const void *q : ptrs)
+        if (q && !aligned16(q)) return SSD_ERR_ALIGNMENT;
+    if (p.L == 0) return h_final ? state_or_zeros(h_final, h0, p, s) : SSD_OK;
+    const ssd_plan_t plan = delta_plan_of(p, false);
+    if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes)) return SSD_ERR_WORKSPACE;
+    p.x = x;
+    p.g = g;
+    p.beta = beta;
+    p.Bm = Bm;
+    p.Cm = Cm;
+    p.h0 = h0;
+    p.y = y;
+    p.h_final = h_final;
+    return from_cuda(delta_seq_fwd(p, s));
+}
+
+SSD_API ssd_status_t ssd_delta_decode_step(const ssd_shape_t *shape, ssd_dtype_t dtype, const float *state,
+                                           float *state_out, const void *x, const void *g, const void *beta,
+                                           const void *Bm, const void *Cm, void *y, void *stream) {
+    DeltaProblem p;
+    ssd_status_t st = make_delta(shape, dtype, &p);
+    if (st != SSD_OK) return st;
+    if (p.L != 1) return SSD_ERR_INVALID_ARG;
+    if (p.N % 4 != 0) return SSD_ERR_UNSUPPORTED;
+    if (p.B == 0) return SSD_OK;
+    if (!state || !state_out || !x || !g || !beta || !Bm || !Cm || !y) return SSD_ERR_INVALID_ARG;
+    const void *ptrs[] = {state, state_out, x, g, beta, Bm, Cm, y};
+    for (const void *q : ptrs)
+        if (!aligned16(q)) return SSD_ERR_ALIGNMENT;
+    // state_out may be state itself (in place); any other overlap is not allowed.
+    const size_t state_bytes = (size_t)(p.B * p.H * p.P * p.N) * sizeof(float);
+    const char *a0 = reinterpret_cast<const char *>(state), *k0 = reinterpret_cast<const char *>(state_out);
+    if (a0 != k0 && a0 < k0 + state_bytes && k0 < a0 + state_bytes) return SSD_ERR_INVALID_ARG;
+    p.x = x;
+    p.g = g;
+    p.beta = beta;
+    p.Bm = Bm;
+    p.Cm = Cm;
+    p.y = y;
+    return from_cuda(delta_step(p, state, state_out, static_cast<cudaStream_t>(stream)));
+}
+
+SSD_API ssd_status_t ssd_delta_bwd(const ssd_shape_t *shape, ssd_dtype_t dtype, const void *x, const void *g,
+                                   const void *beta, const void *Bm, const void *Cm, const float *h0, const void *dy,
+                                   const float *dh_final, void *dx, void *dg, void *dbeta, void *dBm, void *dCm,
+                                   float *dh0, void *workspace, size_t workspace_bytes, void *stream) {
+    DeltaProblem p;
+    ssd_status_t st = make_delta(shape, dtype, &p);
+    if (st != SSD_OK) return st;
+    if (p.B == 0) return SSD_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p.L > 0 && (!x || !g || !beta || !Bm || !Cm || !dy || !dx || !dg || !dbeta || !dBm || !dCm)) return SSD_ERR_INVALID_ARG;
+    const void *ptrs[] = {x, g, beta, Bm, Cm, h0, dy, dh_final, dx, dg, dbeta, dBm, dCm, dh0, workspace};
+    for (const void *q : ptrs)
+        if (q && !aligned16(q)) return SSD_ERR_ALIGNMENT;
+    if (p.L == 0) return dh0 ? state_or_zeros(dh0, dh_final, p, s) : SSD_OK;
+    if (!workspace || workspace_bytes < delta_plan_of(p, true).workspace_bytes) return SSD_ERR_WORKSPACE;
+    p.x = x;
+    p.g = g;
+    p.beta = beta;
+    p.Bm = Bm;
+    p.Cm = Cm;
+    p.h0 = h0;
+    const DeltaGrads gr{dy, dh_final, dx, dg, dbeta, dBm, dCm, dh0};
+    return from_cuda(delta_seq_bwd(p, gr, workspace, s));
+}
+
+// ---- norms before and after a block -------------------------------------------------
+
+namespace {
+
+ssd_status_t check_norm(int64_t rows, int64_t dim, int64_t ngroups, ssd_dtype_t dtype, float eps) {
+    const ssd_status_t st = check_dtype(dtype);
+    if (st != SSD_OK) return st;
+    if (rows < 0 || dim < 1 || ngroups < 1 || dim % ngroups != 0 || !(eps >= 0.f)) return SSD_ERR_INVALID_ARG;
+    if (dim / ngroups > norm_max_group() || dim > 0x7fffffffLL / 4) return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+// the residual stream is kept in the storage type or in fp32
+ssd_status_t check_residual(ssd_dtype_t dtype, ssd_dtype_t res) {
+    const ssd_status_t st = check_dtype(res);
+    if (st != SSD_OK) return st;
+    return dtype == SSD_F32 && res != SSD_F32 ? SSD_ERR_UNSUPPORTED : SSD_OK;
+}
+
+template <size_t M>
+bool all_aligned16(const void *const (&ptrs)[M]) {
+    for (const void *q : ptrs)
+        if (q && !aligned16(q)) return false;
+    return true;
+}
+
+bool element_aligned(const void *p, ssd_dtype_t dtype) {
+    return (reinterpret_cast<uintptr_t>(p) & (dtype == SSD_F32 ? 3u : 1u)) == 0;
+}
+
+// Rows of z and dz that share memory have to be the same rows: the kernels write an element of dz
+// after reading that element of z. Element ranges [p, p + (rows - 1) stride + dim).
+bool gate_rows_clash(const void *z, int64_t zs, const void *dz, int64_t dzs, int64_t rows, int64_t dim, size_t es) {
+    const char *a = static_cast<const char *>(z), *b = static_cast<const char *>(dz);
+    const size_t na = ((size_t)(rows - 1) * (size_t)zs + (size_t)dim) * es, nb = ((size_t)(rows - 1) * (size_t)dzs + (size_t)dim) * es;
+    if (a + na <= b || b + nb <= a || (a == b && zs == dzs)) return false;
+    // two column ranges of the same wider rows
+    const size_t row = (size_t)zs * es, gap = a < b ? (size_t)(b - a) : (size_t)(a - b);
+    return !(zs == dzs && gap % row >= (size_t)dim * es && gap % row <= row - (size_t)dim * es);
+}
+
+}  // namespace
+
+SSD_API ssd_status_t ssd_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, size_t *bytes) {
+    if (!bytes || rows < 0 || dim < 1) return SSD_ERR_INVALID_ARG;
+    if (dim > 0x7fffffffLL / 4) return SSD_ERR_UNSUPPORTED;
+    *bytes = norm_bwd_workspace_bytes(rows, dim);
+    return SSD_OK;
+}
+
+SSD_API ssd_status_t ssd_add_rmsnorm(int64_t rows, int64_t dim, ssd_dtype_t dtype, ssd_dtype_t res_dtype, const void *x,
+                                     const void *residual, const float *scale, const float *weight, float eps,
+                                     void *res_out, void *out, void *stream) {
+    ssd_status_t st = check_norm(rows, dim, 1, dtype, eps);
+    if (st != SSD_OK) return st;
+    if ((st = check_residual(dtype, res_dtype)) != SSD_OK) return st;
+    if (rows == 0) return SSD_OK;
+    if (!x || !weight || !out) return SSD_ERR_INVALID_ARG;
+    const void *ptrs[] = {x, residual, scale, weight, res_out, out};
+    if (!all_aligned16(ptrs)) return SSD_ERR_ALIGNMENT;
+    const AddNormArgs a{rows, dim, dtype, res_dtype, x, residual, scale, weight, eps, res_out, out};
+    return from_cuda(add_rmsnorm_launch(a, static_cast<cudaStream_t>(stream)));
+}
+
+SSD_API ssd_status_t ssd_add_rmsnorm_bwd(int64_t rows, int64_t dim, ssd_dtype_t dtype, ssd_dtype_t res_dtype,
+                                         const void *res, const float *weight, float eps, const void *dout,
+                                         const void *dres_in, const void *x, const float *scale, void *dres, void *dx,
+                                         float *dw, float *dscale, void *workspace, size_t workspace_bytes, void *stream) {
+    ssd_status_t st = check_norm(rows, dim, 1, dtype, eps);
+    if (st != SSD_OK) return st;
+    if ((st = check_residual(dtype, res_dtype)) != SSD_OK) return st;
+    const void *ptrs[] = {res, weight, dout, dres_in, x, scale, dres, dx, dw, dscale, workspace};
+    if (!all_aligned16(ptrs)) return SSD_ERR_ALIGNMENT;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {
+        cudaError_t e = dw ? cudaMemsetAsync(dw, 0, (size_t)dim * sizeof(float), s) : cudaSuccess;
+        if (!e && dscale) e = cudaMemsetAsync(dscale, 0, (size_t)dim * sizeof(float), s);
+        return from_cuda(e);
+    }
+    if (!res || !weight || !dout || (dscale && !x)) return SSD_ERR_INVALID_ARG;
+    if ((dw || dscale) && (!workspace || workspace_bytes < norm_bwd_workspace_bytes(rows, dim))) return SSD_ERR_WORKSPACE;
+    const AddNormArgs a{rows, dim, dtype, res_dtype, x, res, scale, weight, eps, nullptr, nullptr};
+    const AddNormGrads g{dout, dres_in, dres, dx, dw, dscale};
+    return from_cuda(add_rmsnorm_bwd_launch(a, g, static_cast<float *>(workspace), s));
+}
+
+SSD_API ssd_status_t ssd_norm_gate(int64_t rows, int64_t dim, int64_t ngroups, ssd_dtype_t dtype, const void *y,
+                                   const void *z, int64_t z_stride, const float *weight, float eps, void *out,
+                                   void *stream) {
+    const ssd_status_t st = check_norm(rows, dim, ngroups, dtype, eps);
+    if (st != SSD_OK) return st;
+    if (z_stride < dim) return SSD_ERR_INVALID_ARG;
+    if (rows == 0) return SSD_OK;
+    if (!y || !z || !weight || !out) return SSD_ERR_INVALID_ARG;
+    const void *ptrs[] = {y, weight, out};
+    if (!all_aligned16(ptrs) || !element_aligned(z, dtype)) return SSD_ERR_ALIGNMENT;
+    const GateNormArgs a{rows, dim, ngroups, dtype, y, z, z_stride, weight, eps, out};
+    return from_cuda(norm_gate_launch(a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+ssd_status_t gate_norm_bwd(bool gate_first, int64_t rows, int64_t dim, int64_t ngroups, ssd_dtype_t dtype, const void *y,
+                           const void *z, int64_t z_stride, const float *weight, float eps, const void *dout, void *dy,
+                           void *dz, int64_t dz_stride, float *dw, void *workspace, size_t workspace_bytes, void *stream) {
+    const ssd_status_t st = check_norm(rows, dim, ngroups, dtype, eps);
+    if (st != SSD_OK) return st;
+    if (z_stride < dim || dz_stride < dim) return SSD_ERR_INVALID_ARG;
+    const void *ptrs[] = {y, weight, dout, dy, dw, workspace};
+    if (!all_aligned16(ptrs) || !element_aligned(z, dtype) || !element_aligned(dz, dtype)) return SSD_ERR_ALIGNMENT;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (rows == 0) return from_cuda(dw ? cudaMemsetAsync(dw, 0, (size_t)dim * sizeof(float), s) : cudaSuccess);
+    if (!y || !z || !weight || !dout || !dy || !dz) return SSD_ERR_INVALID_ARG;
+    if (gate_rows_clash(z, z_stride, dz, dz_stride, rows, dim, dtype == SSD_F32 ? 4 : 2)) return SSD_ERR_INVALID_ARG;
+    if (dw && (!workspace || workspace_bytes < norm_bwd_workspace_bytes(rows, dim))) return SSD_ERR_WORKSPACE;
+    const GateNormArgs a{rows, dim, ngroups, dtype, y, z, z_stride, weight, eps, nullptr};
+    const GateNormGrads g{dout, dy, dz, dz_stride, dw};
+    return from_cuda(gate_norm_bwd_launch(a, g, gate_first, static_cast<float *>(workspace), s));
+}
+}  // namespace
+
+SSD_API ssd_status_t ssd_norm_gate_bwd(int64_t rows, int64_t dim, int64_t ngroups, ssd_dtype_t dtype, const void *y,
+                                       const void *z, int64_t z_stride, const float *weight, float eps, const void *dout,
+                                       void *dy, void *dz, int64_t dz_stride, float *dw, void *workspace,
+                                       size_t workspace_bytes, void *stream) {
+    return gate_norm_bwd(false, rows, dim, ngroups, dtype, y, z, z_stride, weight, eps, dout, dy, dz, dz_stride, dw,
+                         workspace, workspace_bytes, stream);
+}
+
+SSD_API ssd_status_t ssd_gated_rmsnorm_bwd(int64_t rows, int64_t dim, int64_t ngroups, ssd_dtype_t dtype, const void *y,
+                                           const void *z, int64_t z_stride, const float *weight, float eps,
+                                           const void *dout, void *dy, void *dz, int64_t dz_stride, float *dw,
+                                           void *workspace, size_t workspace_bytes, void *stream) {
+    return gate_norm_bwd(true, rows, dim, ngroups, dtype, y, z, z_stride, weight, eps, dout, dy, dz, dz_stride, dw,
+                         workspace, workspace_bytes, stream);
 }

@@ -1,0 +1,42 @@
+// Internal declarations of the gated delta rule's kernels (not part of the ABI).
+#pragma once
+
+#include "ssd_internal.cuh"
+
+namespace ssd {
+
+// One problem, validated by the API layer.
+struct DeltaProblem {
+    int64_t B, L, H, P, G, N;
+    ssd_dtype_t dtype;
+    const void *x, *g, *beta, *Bm, *Cm;
+    const float *h0;
+    void *y;
+    float *h_final;
+};
+
+// Cotangents in and gradients out (dh_final and dh0 may be NULL).
+struct DeltaGrads {
+    const void *dy;
+    const float *dh_final;
+    void *dx, *dg, *dbeta, *dBm, *dCm;
+    float *dh0;
+};
+
+constexpr int kSeg = 32;  // tokens per segment of the general backward
+
+// A log decay as it enters a cumulated sum: exp of anything below is 0 in fp32 all the same, and a
+// decay of minus infinity (a reset of the state) must not turn differences of sums into NaN.
+__device__ __forceinline__ double clamp_log_decay(float g) { return g < -1e4f ? -1e4 : (double)g; }
+
+// ---- general path: fp32 arithmetic, token by token ----
+cudaError_t delta_seq_fwd(const DeltaProblem &p, cudaStream_t s);
+size_t delta_seq_bwd_workspace_bytes(const DeltaProblem &p);
+cudaError_t delta_seq_bwd(const DeltaProblem &p, const DeltaGrads &g, void *ws, cudaStream_t s);
+// dBm, dCm [B, L, G, N] from per-head fp32 parts [B, L, H, N], added in head order
+cudaError_t delta_group_sum_launch(const DeltaProblem &p, const float *dB_part, const float *dC_part, void *dBm, void *dCm,
+                                   cudaStream_t s);
+// one token (p.L, p.h0, p.h_final unused); state_out may be state_in
+cudaError_t delta_step(const DeltaProblem &p, const float *state_in, float *state_out, cudaStream_t s);
+
+}  // namespace ssd
