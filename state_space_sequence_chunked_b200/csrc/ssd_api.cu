@@ -400,6 +400,10 @@ ssd_plan_t delta_plan_of(const ssd::DeltaProblem &p, bool backward) {
     ssd_plan_t out{};
     if (p.B == 0 || p.L == 0) {
         out.path = SSD_PATH_NONE;
+    } else if (!backward && delta_mma_supported(p)) {
+        out.path = SSD_PATH_MMA;
+        out.kernels = 2;
+        out.workspace_bytes = delta_mma_fwd_workspace_bytes(p);
     } else {
         out.path = SSD_PATH_SIMT;
         out.kernels = backward ? 4 : 1;
@@ -456,7 +460,7 @@ SSD_API ssd_status_t ssd_delta_fwd(const ssd_shape_t *shape, ssd_dtype_t dtype, 
     p.h0 = h0;
     p.y = y;
     p.h_final = h_final;
-    return from_cuda(delta_seq_fwd(p, s));
+    return from_cuda(plan.path == SSD_PATH_MMA ? delta_mma_fwd(p, workspace, s) : delta_seq_fwd(p, s));
 }
 
 SSD_API ssd_status_t ssd_delta_decode_step(const ssd_shape_t *shape, ssd_dtype_t dtype, const float *state,

@@ -36,6 +36,12 @@ cudaError_t delta_seq_bwd(const DeltaProblem &p, const DeltaGrads &g, void *ws, 
 // dBm, dCm [B, L, G, N] from per-head fp32 parts [B, L, H, N], added in head order
 cudaError_t delta_group_sum_launch(const DeltaProblem &p, const float *dB_part, const float *dC_part, void *dBm, void *dCm,
                                    cudaStream_t s);
+// ---- chunked tensor-core path (bf16, dstate <= 128, dstate and headdim multiples of 8) ----
+constexpr int kDeltaChunk = 64;
+bool delta_mma_supported(const DeltaProblem &p);
+size_t delta_mma_fwd_workspace_bytes(const DeltaProblem &p);
+cudaError_t delta_mma_fwd(const DeltaProblem &p, void *ws, cudaStream_t s);
+
 // one token (p.L, p.h0, p.h_final unused); state_out may be state_in
 cudaError_t delta_step(const DeltaProblem &p, const float *state_in, float *state_out, cudaStream_t s);
 
