@@ -34,13 +34,19 @@ constexpr int kRowsCta = 64;     // state rows per CTA of the chain
 constexpr int kBlocks = 10;
 __host__ __device__ constexpr int block_at(int a, int b) { return a * (a + 1) / 2 + b; }
 
-// Per chunk and head, in the workspace: fragments of W (hi, lo) and of the masked Q K^T, one 16-byte
-// vector per lane and block, then the scalars exp(cum), exp(cum_end - cum), beta of the chunk's tokens.
-constexpr int kFragBytes = 512;                       // one vector per lane
-constexpr int kWBytes = kBlocks * 2 * kFragBytes;     // W hi, lo per block
+// Per chunk and head, in the workspace: fragments as right operands, one 16-byte vector per lane and
+// block, and the scalars exp(cum), exp(cum_end - cum), beta of the chunk's tokens, then cum as a sum of
+// two floats. The forward has W (hi, lo), the scalars and the masked Q K^T; the backward pass W, the
+// scalars, and both transposed (hi, lo).
+constexpr int kFragBytes = 512;  // one vector per lane
+constexpr int kWBytes = kBlocks * 2 * kFragBytes;
 constexpr int kPBytes = kBlocks * kFragBytes;
-constexpr int kScalBytes = 3 * kC * 4;
-constexpr int kPrepBytes = kWBytes + kPBytes + kScalBytes;
+constexpr int kScalBytes = 5 * kC * 4;
+template <bool BWD>
+struct Prep {
+    static constexpr int W = 0, scal = kWBytes, P = scal + kScalBytes, WT = scal + kScalBytes, PT = WT + kWBytes;
+    static constexpr int bytes = BWD ? PT + kWBytes : P + kPBytes;
+};
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -121,48 +127,77 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16 *__r
 }
 
 // ---------------------------------------------------------------------------------------------
-// k_delta_prep: grid (chunks, G * slices, B); a CTA forms K K^T and Q K^T of one chunk and group once and
-// walks the heads of its slice. Per head: M and the masked Q K^T (a warp per row of blocks), the
-// diagonal blocks of W by substitution in fp32 (a warp per block, a lane per column), then a block
-// column of W per warp:
+// k_delta_prep: grid (chunks, G * slices, B); a CTA forms K K^T and Q K^T of one chunk and group once (a warp
+// per 16 rows), then a warp takes a head at a time. Per head: the diagonal blocks of W by substitution
+// in fp32 (a lane per column), then the rows of blocks below, on tensor cores with every fp32 operand
+// in two bf16 parts:
 //     W_ab = -(I + W_aa diag(beta_a)) (M_ab (I + diag(beta_b) W_bb) + sum_{b<c<a} M_ac diag(beta_c) W_cb).
 constexpr int kLd = kC + 4;  // padded row of the fp32 tiles
-constexpr int kDl = 17;      // padded row of a diagonal block
+constexpr int kDl = 20;      // padded row of a diagonal block
 
+struct PrepWarp {
+    float diag[4][16 * kDl];
+    float2 cum[kC];  // cum as a sum of two floats
+    float beta[kC];
+};
 template <int NT>
 struct PrepSmem {
-    __nv_bfloat16 k[kC * NT], q[kC * NT];
-    float kk[kC * kLd], qk[kC * kLd], m[kC * kLd];
-    float diag[4][16 * kDl];
-    float ch[kC], cl[kC], beta[kC];  // cum as a sum of two floats
+    float kk[kC * kLd], qk[kC * kLd];
+    union {
+        struct {
+            __nv_bfloat16 k[kC * NT], q[kC * NT];
+        };
+        PrepWarp w[4];
+    };
 };
 
-__device__ __forceinline__ float decay_between(const float *ch, const float *cl, int i, int j) {
-    return __expf((ch[i] - ch[j]) + (cl[i] - cl[j]));
-}
+__device__ __forceinline__ float decay_between(float2 i, float2 j) { return __expf((i.x - j.x) + (i.y - j.y)); }
 
-// acc += a b for 16 x 16 fp32 blocks in accumulator layout, each split in two bf16 parts; row k of b
-// is scaled by sb (lane's rows g and g + 8).
-__device__ __forceinline__ void block_mma(float (&acc)[2][4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
-                                          const float (&b)[2][4], float s0, float s1) {
+// Right-operand fragments (hi, lo) of a 16 x 16 fp32 block in accumulator layout, rows g and g + 8 scaled.
+__device__ __forceinline__ void split_b(const float (&b)[2][4], float s0, float s1, uint32_t (&h)[4], uint32_t (&l)[4]) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-        uint32_t h0, l0, h1, l1;
-        split(s0 * b[n][0], s0 * b[n][1], h0, l0);
-        split(s1 * b[n][2], s1 * b[n][3], h1, l1);
-        h0 = trans8(h0), l0 = trans8(l0), h1 = trans8(h1), l1 = trans8(l1);
-        mma(acc[n], al, h0, h1);
-        mma(acc[n], ah, l0, l1);
-        mma(acc[n], ah, h0, h1);
+        split(s0 * b[n][0], s0 * b[n][1], h[2 * n], l[2 * n]);
+        split(s1 * b[n][2], s1 * b[n][3], h[2 * n + 1], l[2 * n + 1]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = trans8(h[e]), l[e] = trans8(l[e]);
+}
+__device__ __forceinline__ void block_mma(float (&acc)[2][4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
+                                          const uint32_t (&bh)[4], const uint32_t (&bl)[4]) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        mma(acc[n], al, bh[2 * n], bh[2 * n + 1]);
+        mma(acc[n], ah, bl[2 * n], bl[2 * n + 1]);
+        mma(acc[n], ah, bh[2 * n], bh[2 * n + 1]);
     }
 }
 
-template <int NT>
+// Fragments of block `at` of W, and for the backward pass of its transpose.
+template <bool BWD>
+__device__ __forceinline__ void put_w(char *out, int at, int lane, const float (&w)[2][4]) {
+    uint32_t hi[4], lo[4];  // rows 0-7: two halves of the columns, then rows 8-15
+    split(w[0][0], w[0][1], hi[0], lo[0]);
+    split(w[1][0], w[1][1], hi[1], lo[1]);
+    split(w[0][2], w[0][3], hi[2], lo[2]);
+    split(w[1][2], w[1][3], hi[3], lo[3]);
+    uint4 *o = reinterpret_cast<uint4 *>(out + Prep<BWD>::W) + at * 64 + lane;
+    o[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    o[32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if constexpr (BWD) {
+        o = reinterpret_cast<uint4 *>(out + Prep<BWD>::WT) + at * 64 + lane;
+        o[0] = make_uint4(trans8(hi[0]), trans8(hi[2]), trans8(hi[1]), trans8(hi[3]));
+        o[32] = make_uint4(trans8(lo[0]), trans8(lo[2]), trans8(lo[1]), trans8(lo[3]));
+    }
+}
+
+template <int NT, bool BWD>
 __global__ void __launch_bounds__(kThr)
     k_delta_prep(const __nv_bfloat16 *__restrict__ Bm, const __nv_bfloat16 *__restrict__ Cm, const __nv_bfloat16 *__restrict__ g,
                  const __nv_bfloat16 *__restrict__ beta, int64_t L, int H, int G, int N, int slices, char *__restrict__ ws) {
     extern __shared__ __align__(128) char raw[];
     PrepSmem<NT> &sm = *reinterpret_cast<PrepSmem<NT> *>(raw);
+    using Lay = Prep<BWD>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tg = lane & 3;
     const int64_t c = blockIdx.x, nc = gridDim.x, b = blockIdx.z, t0 = c * kC;
     const int grp = blockIdx.y / slices, slice = blockIdx.y % slices, per = H / G;
@@ -208,14 +243,15 @@ __global__ void __launch_bounds__(kThr)
             }
         }
     }
-    for (int h = h_begin; h < h_end; ++h) {
-        __syncthreads();
-        char *out = ws + ((b * H + h) * nc + c) * (int64_t)kPrepBytes;
-        float *scal = reinterpret_cast<float *>(out + kWBytes + kPBytes);
-        if (warp == 0) {  // cumulated log decay: 2 tokens per lane, fp64
+    __syncthreads();  // K and Q are done with: the warps' own memory lies over them
+    PrepWarp &wm = sm.w[warp];
+    for (int h = h_begin + warp; h < h_end; h += 4) {
+        char *out = ws + ((b * H + h) * nc + c) * (int64_t)Lay::bytes;
+        {  // cumulated log decay: 2 tokens per lane, fp64
             const int64_t at = (b * L + t0 + 2 * lane) * H + h;
             const bool in0 = t0 + 2 * lane < L, in1 = t0 + 2 * lane + 1 < L;
             const double g0 = in0 ? clamp_log_decay(to_f32(g[at])) : 0.0, g1 = in1 ? clamp_log_decay(to_f32(g[at + H])) : 0.0;
+            const float b0 = in0 ? to_f32(beta[at]) : 0.f, b1 = in1 ? to_f32(beta[at + H]) : 0.f;
             double sum = g0 + g1;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -223,114 +259,137 @@ __global__ void __launch_bounds__(kThr)
                 if (lane >= o) sum += up;
             }
             const double total = __shfl_sync(0xffffffffu, sum, 31), first = sum - g1;
-            const float b0 = in0 ? to_f32(beta[at]) : 0.f, b1 = in1 ? to_f32(beta[at + H]) : 0.f;
-            sm.ch[2 * lane] = (float)first, sm.cl[2 * lane] = (float)(first - (double)(float)first);
-            sm.ch[2 * lane + 1] = (float)sum, sm.cl[2 * lane + 1] = (float)(sum - (double)(float)sum);
-            sm.beta[2 * lane] = b0, sm.beta[2 * lane + 1] = b1;
-            reinterpret_cast<float2 *>(scal)[lane] = make_float2(expf((float)first), expf((float)sum));
-            reinterpret_cast<float2 *>(scal + kC)[lane] = make_float2(expf((float)(total - first)), expf((float)(total - sum)));
-            reinterpret_cast<float2 *>(scal + 2 * kC)[lane] = make_float2(b0, b1);
+            const float f0 = (float)first, f1 = (float)sum, l0 = (float)(first - (double)f0), l1 = (float)(sum - (double)f1);
+            wm.cum[2 * lane] = make_float2(f0, l0);
+            wm.cum[2 * lane + 1] = make_float2(f1, l1);
+            wm.beta[2 * lane] = b0, wm.beta[2 * lane + 1] = b1;
+            float2 *scal = reinterpret_cast<float2 *>(out + Lay::scal) + lane;
+            scal[0] = make_float2(expf(f0), expf(f1));
+            scal[kC / 2] = make_float2(expf((float)(total - first)), expf((float)(total - sum)));
+            scal[kC] = make_float2(b0, b1);
+            scal[3 * kC / 2] = make_float2(f0, f1);
+            scal[2 * kC] = make_float2(l0, l1);
         }
-        __syncthreads();
-        {  // row of blocks `warp`
-            uint4 *pout = reinterpret_cast<uint4 *>(out + kWBytes);
+        __syncwarp();
+        // block (a, cc): M in accumulator layout; the masked Q K^T goes out
+        const auto block = [&](int a, int cc, float (&m)[2][4]) {
+            float p[2][4];
+            const float2 ri[2] = {wm.cum[16 * a + gr], wm.cum[16 * a + gr + 8]};
 #pragma unroll
-            for (int bb = 0; bb < 4; ++bb) {
-                if (bb <= warp) {
-                    uint32_t pf[4];
+            for (int n = 0; n < 2; ++n) {
+                const int j = 16 * cc + 8 * n + 2 * tg;
+                const float4 cj = *reinterpret_cast<const float4 *>(&wm.cum[j]);
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const int j = 16 * bb + 8 * n + 2 * tg;
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const int i = 16 * warp + gr + 8 * r;
-                            const float2 kk = *reinterpret_cast<const float2 *>(&sm.kk[i * kLd + j]);
-                            const float2 qk = *reinterpret_cast<const float2 *>(&sm.qk[i * kLd + j]);
-                            const float e0 = j <= i ? decay_between(sm.ch, sm.cl, i, j) : 0.f;
-                            const float e1 = j + 1 <= i ? decay_between(sm.ch, sm.cl, i, j + 1) : 0.f;
-                            const float m0 = j < i ? kk.x * e0 : 0.f, m1 = j + 1 < i ? kk.y * e1 : 0.f;
-                            *reinterpret_cast<float2 *>(&sm.m[i * kLd + j]) = make_float2(m0, m1);
-                            pf[2 * r + n] = pack(j <= i ? qk.x * e0 : 0.f, j + 1 <= i ? qk.y * e1 : 0.f);
-                        }
-                    }
-                    pout[block_at(warp, bb) * 32 + lane] = make_uint4(pf[0], pf[1], pf[2], pf[3]);
+                for (int r = 0; r < 2; ++r) {
+                    const int i = 16 * a + gr + 8 * r;
+                    const float2 kk = *reinterpret_cast<const float2 *>(&sm.kk[i * kLd + j]);
+                    const float2 qk = *reinterpret_cast<const float2 *>(&sm.qk[i * kLd + j]);
+                    const float e0 = j <= i ? decay_between(ri[r], make_float2(cj.x, cj.y)) : 0.f;
+                    const float e1 = j + 1 <= i ? decay_between(ri[r], make_float2(cj.z, cj.w)) : 0.f;
+                    m[n][2 * r] = j < i ? kk.x * e0 : 0.f, m[n][2 * r + 1] = j + 1 < i ? kk.y * e1 : 0.f;
+                    p[n][2 * r] = j <= i ? qk.x * e0 : 0.f, p[n][2 * r + 1] = j + 1 <= i ? qk.y * e1 : 0.f;
                 }
+            }
+            if constexpr (BWD) {
+                uint32_t ph[4], pl[4];
+                split_b(p, 1.f, 1.f, ph, pl);
+                uint4 *o = reinterpret_cast<uint4 *>(out + Lay::PT) + block_at(a, cc) * 64 + lane;
+                o[0] = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+                o[32] = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+            } else {
+                reinterpret_cast<uint4 *>(out + Lay::P)[block_at(a, cc) * 32 + lane] =
+                    make_uint4(pack(p[0][0], p[0][1]), pack(p[1][0], p[1][1]), pack(p[0][2], p[0][3]), pack(p[1][2], p[1][3]));
+            }
+        };
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            float m[2][4];
+            block(a, a, m);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    *reinterpret_cast<float2 *>(&wm.diag[a][(gr + 8 * r) * kDl + 8 * n + 2 * tg]) =
+                        make_float2(m[n][2 * r], m[n][2 * r + 1]);
+        }
+        __syncwarp();
+        // a half warp per diagonal block, a lane per column: w_i = -m_ij - sum_{j<k<i} m_ik beta_k w_k
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int a = 2 * half + (lane >> 4), j = lane & 15;
+            float *m = wm.diag[a];
+            float w[16], bw[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float row[16];
+#pragma unroll
+                for (int k = 0; k < (i + 3) / 4; ++k) *reinterpret_cast<float4 *>(row + 4 * k) = *reinterpret_cast<const float4 *>(m + i * kDl + 4 * k);
+                float s0 = m[i * kDl + j], s1 = 0.f;
+#pragma unroll
+                for (int k = 0; k < i; ++k) (k & 1 ? s1 : s0) = fmaf(row[k], bw[k], k & 1 ? s1 : s0);
+                w[i] = i > j ? -(s0 + s1) : 0.f;
+                bw[i] = wm.beta[16 * a + i] * w[i];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m[i * kDl + j] = w[i];
+        }
+        __syncwarp();
+        uint32_t bh[6][4], bl[6][4];  // diag(beta) W_cb, c <= 2, as right operands
+        const auto diag = [&](int a, float (&d)[2][4]) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float2 v = *reinterpret_cast<const float2 *>(&wm.diag[a][(gr + 8 * r) * kDl + 8 * n + 2 * tg]);
+                    d[n][2 * r] = v.x, d[n][2 * r + 1] = v.y;
+                }
+        };
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            float m[3][2][4], d[2][4];
+            uint32_t mh[3][4], ml[3][4], dh[4], dl[4];
+            diag(a, d);
+            put_w<BWD>(out, block_at(a, a), lane, d);
+            const float s0 = wm.beta[16 * a + gr], s1 = wm.beta[16 * a + gr + 8];
+            if (a < 3) split_b(d, s0, s1, bh[block_at(a, a)], bl[block_at(a, a)]);
+            if (a == 0) continue;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float2 bj = *reinterpret_cast<const float2 *>(&wm.beta[16 * a + 8 * n + 2 * tg]);
+                d[n][0] *= bj.x, d[n][1] *= bj.y, d[n][2] *= bj.x, d[n][3] *= bj.y;
+            }
+            split_a(d[0], d[1], dh, dl);
+#pragma unroll
+            for (int cc = 0; cc < a; ++cc) {
+                block(a, cc, m[cc]);
+                split_a(m[cc][0], m[cc][1], mh[cc], ml[cc]);
+            }
+#pragma unroll
+            for (int bb = 0; bb < a; ++bb) {
+                float u[2][4], w[2][4];
+                uint32_t uh[4], ul[4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) u[n][e] = m[bb][n][e];
+#pragma unroll
+                for (int cc = bb; cc < a; ++cc) block_mma(u, mh[cc], ml[cc], bh[block_at(cc, bb)], bl[block_at(cc, bb)]);
+                split_b(u, 1.f, 1.f, uh, ul);
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[n][e] = u[n][e];
+                block_mma(w, dh, dl, uh, ul);
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[n][e] = -w[n][e];
+                put_w<BWD>(out, block_at(a, bb), lane, w);
+                if (a < 3) split_b(w, s0, s1, bh[block_at(a, bb)], bl[block_at(a, bb)]);
             }
         }
         __syncwarp();
-        if (lane < 16) {  // column `lane` of the diagonal block: w_i = -m_ij - sum_{j<m<i} m_im beta_m w_m
-            const float *m = sm.m + 16 * warp * kLd + 16 * warp, *bt = sm.beta + 16 * warp;
-            float w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float s = m[i * kLd + lane];
-#pragma unroll
-                for (int k = 0; k < i; ++k) s = fmaf(m[i * kLd + k], w[k], s);
-                s = i > lane ? -s : 0.f;
-                sm.diag[warp][i * kDl + lane] = s;
-                w[i] = bt[i] * s;
-            }
-        }
-        __syncthreads();
-        {  // block column `warp` of W
-            float wcol[4][2][4];
-            uint4 *wout = reinterpret_cast<uint4 *>(out);
-#pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                if (a < warp) continue;
-                if (a == warp) {
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            wcol[a][n][e] = sm.diag[a][(gr + 8 * (e >> 1)) * kDl + 8 * n + 2 * tg + (e & 1)];
-                } else {
-                    float u[2][4];
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            u[n][e] = sm.m[(16 * a + gr + 8 * (e >> 1)) * kLd + 16 * warp + 8 * n + 2 * tg + (e & 1)];
-#pragma unroll
-                    for (int cc = 0; cc < 3; ++cc) {
-                        if (cc < warp || cc >= a) continue;
-                        float m[2][4];
-                        uint32_t mh[4], ml[4];
-#pragma unroll
-                        for (int n = 0; n < 2; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                m[n][e] = sm.m[(16 * a + gr + 8 * (e >> 1)) * kLd + 16 * cc + 8 * n + 2 * tg + (e & 1)];
-                        split_a(m[0], m[1], mh, ml);
-                        block_mma(u, mh, ml, wcol[cc], sm.beta[16 * cc + gr], sm.beta[16 * cc + gr + 8]);
-                    }
-                    float d[2][4];
-                    uint32_t dh[4], dl[4];
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int j = 8 * n + 2 * tg + (e & 1);
-                            d[n][e] = sm.diag[a][(gr + 8 * (e >> 1)) * kDl + j] * sm.beta[16 * a + j];
-                            wcol[a][n][e] = u[n][e];
-                        }
-                    split_a(d[0], d[1], dh, dl);
-                    block_mma(wcol[a], dh, dl, u, 1.f, 1.f);
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) wcol[a][n][e] = -wcol[a][n][e];
-                }
-                uint32_t hi[4], lo[4];  // rows 0-7: two halves of the columns, then rows 8-15
-                split(wcol[a][0][0], wcol[a][0][1], hi[0], lo[0]);
-                split(wcol[a][1][0], wcol[a][1][1], hi[1], lo[1]);
-                split(wcol[a][0][2], wcol[a][0][3], hi[2], lo[2]);
-                split(wcol[a][1][2], wcol[a][1][3], hi[3], lo[3]);
-                const int at = block_at(a, warp) * 2;
-                wout[at * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                wout[(at + 1) * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
-        }
     }
 }
 
@@ -340,7 +399,7 @@ __global__ void __launch_bounds__(kThr)
 template <int NT>
 struct ChainStage {
     __nv_bfloat16 k[kC * NT], q[kC * NT], x[kC * kRowsCta];
-    char prep[kPrepBytes];
+    char prep[Prep<false>::bytes];
 };
 
 template <int NT>
@@ -354,6 +413,7 @@ __global__ void __launch_bounds__(kThr, 2)
     const int h = blockIdx.y, grp = h / (H / G), pc = blockIdx.x * kRowsCta, p0 = pc + 16 * warp;
     const int64_t b = blockIdx.z, nc = (L + kC - 1) / kC;
     const bool on = p0 < P;  // a warp with rows
+    constexpr int kPrepBytes = Prep<false>::bytes;
     const char *prep = ws + (b * H + h) * nc * (int64_t)kPrepBytes;
 
     const auto load = [&](int64_t c) {
@@ -390,8 +450,8 @@ __global__ void __launch_bounds__(kThr, 2)
         if (on) {
             const uint32_t ka = smem_addr(st.k), qa = smem_addr(st.q), xa = smem_addr(st.x);
             const uint4 *wf = reinterpret_cast<const uint4 *>(st.prep) + lane;
-            const uint4 *pf = reinterpret_cast<const uint4 *>(st.prep + kWBytes) + lane;
-            const float *eg = reinterpret_cast<const float *>(st.prep + kWBytes + kPBytes), *ek = eg + kC, *bt = eg + 2 * kC;
+            const uint4 *pf = reinterpret_cast<const uint4 *>(st.prep + Prep<false>::P) + lane;
+            const float *eg = reinterpret_cast<const float *>(st.prep + Prep<false>::scal), *ek = eg + kC, *bt = eg + 2 * kC;
             float R[8][4], Y[8][4];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -533,28 +593,29 @@ __global__ void __launch_bounds__(kThr, 2)
     }
 }
 
-template <int NT>
+template <int NT, bool BWD>
 cudaError_t prep_launch(const DeltaProblem &p, char *ws, cudaStream_t s) {
     using bf = __nv_bfloat16;
     const int64_t nc = (p.L + kC - 1) / kC, units = nc * p.G * p.B;
     const int per = (int)(p.H / p.G);
-    // heads of a group are walked by one CTA while that leaves work for every SM (4 CTAs fit on one)
-    int slices = units >= 148 * 4 ? 1 : (int)((148 * 4 + units - 1) / units);
-    if (slices > per) slices = per;
+    // a CTA walks all heads of a group while that leaves 3 CTAs (what fits) for every SM, and
+    // four heads at least, one per warp
+    int slices = units >= 148 * 3 ? 1 : (int)((148 * 3 + units - 1) / units);
+    if (slices > (per + 3) / 4) slices = (per + 3) / 4;
     cudaError_t e;
-    if ((e = cudaFuncSetAttribute(k_delta_prep<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(PrepSmem<NT>))))
-        return e;
+    constexpr int smem = sizeof(PrepSmem<NT>);
+    if ((e = cudaFuncSetAttribute(k_delta_prep<NT, BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
     dim3 grid((unsigned)nc, (unsigned)(p.G * slices), (unsigned)p.B);
-    k_delta_prep<NT><<<grid, kThr, sizeof(PrepSmem<NT>), s>>>(static_cast<const bf *>(p.Bm), static_cast<const bf *>(p.Cm),
-                                                              static_cast<const bf *>(p.g), static_cast<const bf *>(p.beta),
-                                                              p.L, (int)p.H, (int)p.G, (int)p.N, slices, ws);
+    k_delta_prep<NT, BWD><<<grid, kThr, smem, s>>>(static_cast<const bf *>(p.Bm), static_cast<const bf *>(p.Cm),
+                                                   static_cast<const bf *>(p.g), static_cast<const bf *>(p.beta), p.L,
+                                                   (int)p.H, (int)p.G, (int)p.N, slices, ws);
     return cudaGetLastError();
 }
 
 template <int NT>
 cudaError_t fwd_launch(const DeltaProblem &p, char *ws, cudaStream_t s) {
     using bf = __nv_bfloat16;
-    cudaError_t e = prep_launch<NT>(p, ws, s);
+    cudaError_t e = prep_launch<NT, false>(p, ws, s);
     if (e) return e;
     constexpr int smem = 2 * sizeof(ChainStage<NT>);
     if ((e = cudaFuncSetAttribute(k_delta_chain<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
@@ -572,7 +633,7 @@ bool delta_mma_supported(const DeltaProblem &p) {
 }
 
 size_t delta_mma_fwd_workspace_bytes(const DeltaProblem &p) {
-    return (size_t)(p.B * p.H) * (size_t)((p.L + kC - 1) / kC) * kPrepBytes;
+    return (size_t)(p.B * p.H) * (size_t)((p.L + kC - 1) / kC) * Prep<false>::bytes;
 }
 
 cudaError_t delta_mma_fwd(const DeltaProblem &p, void *ws, cudaStream_t s) {
