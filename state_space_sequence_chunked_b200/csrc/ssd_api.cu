@@ -400,10 +400,10 @@ ssd_plan_t delta_plan_of(const ssd::DeltaProblem &p, bool backward) {
     ssd_plan_t out{};
     if (p.B == 0 || p.L == 0) {
         out.path = SSD_PATH_NONE;
-    } else if (!backward && delta_mma_supported(p)) {
+    } else if (delta_mma_supported(p)) {
         out.path = SSD_PATH_MMA;
-        out.kernels = 2;
-        out.workspace_bytes = delta_mma_fwd_workspace_bytes(p);
+        out.kernels = backward ? delta_mma_bwd_kernels(p) : 2;
+        out.workspace_bytes = backward ? delta_mma_bwd_workspace_bytes(p) : delta_mma_fwd_workspace_bytes(p);
     } else {
         out.path = SSD_PATH_SIMT;
         out.kernels = backward ? 4 : 1;
@@ -503,7 +503,8 @@ SSD_API ssd_status_t ssd_delta_bwd(const ssd_shape_t *shape, ssd_dtype_t dtype, 
     for (const void *q : ptrs)
         if (q && !aligned16(q)) return SSD_ERR_ALIGNMENT;
     if (p.L == 0) return dh0 ? state_or_zeros(dh0, dh_final, p, s) : SSD_OK;
-    if (!workspace || workspace_bytes < delta_plan_of(p, true).workspace_bytes) return SSD_ERR_WORKSPACE;
+    const ssd_plan_t plan = delta_plan_of(p, true);
+    if (!workspace || workspace_bytes < plan.workspace_bytes) return SSD_ERR_WORKSPACE;
     p.x = x;
     p.g = g;
     p.beta = beta;
@@ -511,7 +512,7 @@ SSD_API ssd_status_t ssd_delta_bwd(const ssd_shape_t *shape, ssd_dtype_t dtype, 
     p.Cm = Cm;
     p.h0 = h0;
     const DeltaGrads gr{dy, dh_final, dx, dg, dbeta, dBm, dCm, dh0};
-    return from_cuda(delta_seq_bwd(p, gr, workspace, s));
+    return from_cuda(plan.path == SSD_PATH_MMA ? delta_mma_bwd(p, gr, workspace, s) : delta_seq_bwd(p, gr, workspace, s));
 }
 
 // ---- norms before and after a block -------------------------------------------------

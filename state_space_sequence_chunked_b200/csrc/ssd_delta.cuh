@@ -41,6 +41,9 @@ constexpr int kDeltaChunk = 64;
 bool delta_mma_supported(const DeltaProblem &p);
 size_t delta_mma_fwd_workspace_bytes(const DeltaProblem &p);
 cudaError_t delta_mma_fwd(const DeltaProblem &p, void *ws, cudaStream_t s);
+size_t delta_mma_bwd_workspace_bytes(const DeltaProblem &p);
+int delta_mma_bwd_kernels(const DeltaProblem &p);
+cudaError_t delta_mma_bwd(const DeltaProblem &p, const DeltaGrads &g, void *ws, cudaStream_t s);
 
 // one token (p.L, p.h0, p.h_final unused); state_out may be state_in
 cudaError_t delta_step(const DeltaProblem &p, const float *state_in, float *state_out, cudaStream_t s);

@@ -70,6 +70,10 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
                  : "r"(a)
                  : "memory");
 }
+__device__ __forceinline__ void stsm4(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+                 : "memory");
+}
 __device__ __forceinline__ void stsm4t(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(r0), "r"(r1), "r"(r2),
                  "r"(r3)
@@ -395,34 +399,144 @@ __global__ void __launch_bounds__(kThr)
 
 // ---------------------------------------------------------------------------------------------
 // k_delta_chain: grid (ceil(P / 64), H, B), a warp per 16 state rows, two stages of a chunk's operands
-// loaded ahead with cp.async.
-template <int NT>
+// loaded ahead with cp.async. kStore is the backward pass's recomputation: no Y, but the state entering
+// each chunk, err and u, each rounded to bf16 once (they are operands of products there).
+template <int NT, bool kStore>
 struct ChainStage {
-    __nv_bfloat16 k[kC * NT], q[kC * NT], x[kC * kRowsCta];
-    char prep[Prep<false>::bytes];
+    __nv_bfloat16 k[kC * NT];
+    __nv_bfloat16 q[kC * NT];  // kStore: the entering state on its way out
+    __nv_bfloat16 x[kC * kRowsCta];
+    static constexpr int prep_bytes = kStore ? Prep<true>::WT : Prep<false>::bytes;
+    char prep[prep_bytes];
 };
 
+// What the backward pass keeps per chunk: states [B, H, chunks, P, N], the others [B, L, H, P].
+struct ChainOut {
+    __nv_bfloat16 *y, *states, *err, *u;
+    float *h_final;
+};
+
+// Accumulators T^T (16 state rows x 64 tokens), rounded, over this warp's columns of a [token][row]
+// tile and from there to rows of `dst` ([B, L, H, P]).
+__device__ __forceinline__ void put_tokens(const float (&T)[8][4], char *tile, __nv_bfloat16 *__restrict__ dst, int64_t b,
+                                           int64_t L, int64_t t0, int H, int h, int P, int pc, int warp, int lane) {
+    const uint32_t ta = smem_addr(tile);
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj)
+        stsm4t(ta + at16<kRowsCta * 2>(16 * jj + (lane & 7) + ((lane >> 4) << 3), 2 * warp + ((lane >> 3) & 1)),
+               pack(T[2 * jj][0], T[2 * jj][1]), pack(T[2 * jj][2], T[2 * jj][3]), pack(T[2 * jj + 1][0], T[2 * jj + 1][1]),
+               pack(T[2 * jj + 1][2], T[2 * jj + 1][3]));
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = 16 * i + (lane >> 1), v = 2 * warp + (lane & 1);
+        if (t0 + t < L && pc + 8 * v < P)
+            *reinterpret_cast<uint4 *>(dst + ((b * L + t0 + t) * H + h) * (int64_t)P + pc + 8 * v) =
+                *reinterpret_cast<const uint4 *>(tile + at16<kRowsCta * 2>(t, v));
+    }
+    __syncwarp();
+}
+
+// A state (16 rows of N columns per warp), rounded, through `tile` to [P, N] rows at dst.
 template <int NT>
+__device__ __forceinline__ void put_state(const float (&S)[NT / 8][4], char *tile, __nv_bfloat16 *__restrict__ dst, int P, int N,
+                                          int pc, int warp, int lane) {
+    const uint32_t ta = smem_addr(tile);
+#pragma unroll
+    for (int s = 0; s < NT / 16; ++s)
+        stsm4(ta + at16<NT * 2>(16 * warp + (lane & 15), 2 * s + (lane >> 4)), pack(S[2 * s][0], S[2 * s][1]),
+              pack(S[2 * s][2], S[2 * s][3]), pack(S[2 * s + 1][0], S[2 * s + 1][1]), pack(S[2 * s + 1][2], S[2 * s + 1][3]));
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < NT / 16; ++i) {
+        const int r = 16 * warp + (i * 32 + lane) / (NT / 8), v = (i * 32 + lane) % (NT / 8);
+        if (pc + r < P && 8 * v < N)
+            *reinterpret_cast<uint4 *>(dst + (int64_t)(pc + r) * N + 8 * v) =
+                *reinterpret_cast<const uint4 *>(tile + at16<NT * 2>(r, v));
+    }
+    __syncwarp();
+}
+
+template <int NT>
+__device__ __forceinline__ void load_state(float (&S)[NT / 8][4], const float *__restrict__ src, int64_t row, int P, int N, int p,
+                                           int tg) {
+#pragma unroll
+    for (int j = 0; j < NT / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int n = 8 * j + 2 * tg + (e & 1), r = 8 * (e >> 1);
+            S[j][e] = src && n < N && p + r < P ? src[(row + r) * N + n] : 0.f;
+        }
+}
+template <int NT>
+__device__ __forceinline__ void store_state(const float (&S)[NT / 8][4], float *__restrict__ dst, int64_t row, int P, int N, int p,
+                                            int tg) {
+#pragma unroll
+    for (int j = 0; j < NT / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int n = 8 * j + 2 * tg + (e & 1), r = 8 * (e >> 1);
+            if (n < N && p + r < P) dst[(row + r) * N + n] = S[j][e];
+        }
+}
+
+// T *= per-token factors (tokens are the columns)
+__device__ __forceinline__ void scale_tokens(float (&T)[8][4], const float *f, int tg) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float2 e = *reinterpret_cast<const float2 *>(f + 8 * j + 2 * tg);
+        T[j][0] *= e.x, T[j][1] *= e.y, T[j][2] *= e.x, T[j][3] *= e.y;
+    }
+}
+// left operand (hi, lo) of tokens 16 k .. + 15 of T, scaled per token
+__device__ __forceinline__ void split_tokens(const float (&T)[8][4], int k, const float *f, float sign, int tg, uint32_t (&hi)[4],
+                                             uint32_t (&lo)[4]) {
+    float t[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const float2 e = *reinterpret_cast<const float2 *>(f + 16 * k + 8 * n + 2 * tg);
+        const float x = sign * e.x, y = sign * e.y;
+        t[n][0] = x * T[2 * k + n][0], t[n][1] = y * T[2 * k + n][1], t[n][2] = x * T[2 * k + n][2], t[n][3] = y * T[2 * k + n][3];
+    }
+    split_a(t[0], t[1], hi, lo);
+}
+// S += (the left operand of tokens 16 k .. + 15) times those rows of a [token][column] tile
+template <int NT>
+__device__ __forceinline__ void rank16(float (&S)[NT / 8][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], uint32_t tile, int k,
+                                       int lane) {
+#pragma unroll
+    for (int j = 0; j < NT / 16; ++j) {
+        uint32_t f[4];
+        ldsm4t(f, tile + at16<NT * 2>(16 * k + (lane & 15), 2 * j + (lane >> 4)));
+        mma(S[2 * j], lo, f[0], f[1]);
+        mma(S[2 * j + 1], lo, f[2], f[3]);
+        mma(S[2 * j], hi, f[0], f[1]);
+        mma(S[2 * j + 1], hi, f[2], f[3]);
+    }
+}
+
+template <int NT, bool kStore>
 __global__ void __launch_bounds__(kThr, 2)
     k_delta_chain(const __nv_bfloat16 *__restrict__ x, const __nv_bfloat16 *__restrict__ Bm, const __nv_bfloat16 *__restrict__ Cm,
                   const float *__restrict__ h0, const char *__restrict__ ws, int64_t L, int H, int P, int G, int N,
-                  __nv_bfloat16 *__restrict__ y, float *__restrict__ h_final) {
+                  const ChainOut out) {
     extern __shared__ __align__(128) char raw[];
-    ChainStage<NT> *stages = reinterpret_cast<ChainStage<NT> *>(raw);
+    using Stage = ChainStage<NT, kStore>;
+    using Lay = Prep<kStore>;
+    Stage *stages = reinterpret_cast<Stage *>(raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tg = lane & 3;
     const int h = blockIdx.y, grp = h / (H / G), pc = blockIdx.x * kRowsCta, p0 = pc + 16 * warp;
     const int64_t b = blockIdx.z, nc = (L + kC - 1) / kC;
     const bool on = p0 < P;  // a warp with rows
-    constexpr int kPrepBytes = Prep<false>::bytes;
-    const char *prep = ws + (b * H + h) * nc * (int64_t)kPrepBytes;
+    const char *prep = ws + (b * H + h) * nc * (int64_t)Lay::bytes;
 
     const auto load = [&](int64_t c) {
-        ChainStage<NT> &st = stages[c & 1];
+        Stage &st = stages[c & 1];
         load_tile<NT / 8>(smem_addr(st.k), Bm, b, L, c * kC, G, grp, N, 0);
-        load_tile<NT / 8>(smem_addr(st.q), Cm, b, L, c * kC, G, grp, N, 0);
+        if constexpr (!kStore) load_tile<NT / 8>(smem_addr(st.q), Cm, b, L, c * kC, G, grp, N, 0);
         load_tile<kRowsCta / 8>(smem_addr(st.x), x, b, L, c * kC, H, h, P, pc);
         const uint32_t dst = smem_addr(st.prep);
-        for (int i = tid; i < kPrepBytes / 16; i += kThr) cp16(dst + 16 * i, prep + c * kPrepBytes + 16 * i, true);
+        for (int i = tid; i < Stage::prep_bytes / 16; i += kThr) cp16(dst + 16 * i, prep + c * Lay::bytes + 16 * i, true);
         cp_commit();
     };
     load(0);
@@ -430,13 +544,7 @@ __global__ void __launch_bounds__(kThr, 2)
     // state rows p0 + gr and p0 + gr + 8, columns 8 j + 2 tg and + 1
     float S[NT / 8][4];
     const int64_t row = (b * H + h) * (int64_t)P + p0 + gr;
-#pragma unroll
-    for (int j = 0; j < NT / 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int n = 8 * j + 2 * tg + (e & 1), r = 8 * (e >> 1);
-            S[j][e] = h0 && n < N && p0 + gr + r < P ? h0[(row + r) * N + n] : 0.f;
-        }
+    load_state<NT>(S, h0, row, P, N, p0 + gr, tg);
 
     for (int64_t c = 0; c < nc; ++c) {
         if (c + 1 < nc) {
@@ -446,12 +554,13 @@ __global__ void __launch_bounds__(kThr, 2)
             cp_wait<0>();
         }
         __syncthreads();
-        ChainStage<NT> &st = stages[c & 1];
+        Stage &st = stages[c & 1];
         if (on) {
             const uint32_t ka = smem_addr(st.k), qa = smem_addr(st.q), xa = smem_addr(st.x);
-            const uint4 *wf = reinterpret_cast<const uint4 *>(st.prep) + lane;
-            const uint4 *pf = reinterpret_cast<const uint4 *>(st.prep + Prep<false>::P) + lane;
-            const float *eg = reinterpret_cast<const float *>(st.prep + Prep<false>::scal), *ek = eg + kC, *bt = eg + 2 * kC;
+            const uint4 *wf = reinterpret_cast<const uint4 *>(st.prep + Lay::W) + lane;
+            const float *eg = reinterpret_cast<const float *>(st.prep + Lay::scal), *ek = eg + kC, *bt = eg + 2 * kC;
+            if constexpr (kStore)
+                put_state<NT>(S, reinterpret_cast<char *>(st.q), out.states + ((b * H + h) * nc + c) * (int64_t)P * N, P, N, pc, warp, lane);
             float R[8][4], Y[8][4];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -464,14 +573,17 @@ __global__ void __launch_bounds__(kThr, 2)
                 split_a(S[2 * s], S[2 * s + 1], hi, lo);
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {
-                    uint32_t bk[4], bq[4];
+                    uint32_t bk[4];
                     const uint32_t off = at16<NT * 2>(16 * jj + (lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1));
                     ldsm4(bk, ka + off);
-                    ldsm4(bq, qa + off);
                     mma(R[2 * jj], lo, bk[0], bk[1]);
                     mma(R[2 * jj + 1], lo, bk[2], bk[3]);
-                    mma(Y[2 * jj], hi, bq[0], bq[1]);
-                    mma(Y[2 * jj + 1], hi, bq[2], bq[3]);
+                    if constexpr (!kStore) {
+                        uint32_t bq[4];
+                        ldsm4(bq, qa + off);
+                        mma(Y[2 * jj], hi, bq[0], bq[1]);
+                        mma(Y[2 * jj + 1], hi, bq[2], bq[3]);
+                    }
                     mma(R[2 * jj], hi, bk[0], bk[1]);
                     mma(R[2 * jj + 1], hi, bk[2], bk[3]);
                 }
@@ -489,23 +601,13 @@ __global__ void __launch_bounds__(kThr, 2)
                     R[j][1] = fmaf(-e.y, R[j][1], high(xf[2 * n]));
                     R[j][2] = fmaf(-e.x, R[j][2], low(xf[2 * n + 1]));
                     R[j][3] = fmaf(-e.y, R[j][3], high(xf[2 * n + 1]));
-                    Y[j][0] *= e.x, Y[j][1] *= e.y, Y[j][2] *= e.x, Y[j][3] *= e.y;
                 }
             }
-            // err = R + W (beta R): the blocks of a column of tokens at a time, from the last column on, so
-            // that R can take the sums in place (block row a needs the beta R of blocks b <= a only)
+            if constexpr (!kStore) scale_tokens(Y, eg, tg);
+            // err = R + W (beta R); beta R is taken of the whole chunk first, so R can take the sums in place
             uint32_t ah[4][4], al[4][4];
 #pragma unroll
-            for (int bb = 0; bb < 4; ++bb) {
-                float t[2][4];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float2 e = *reinterpret_cast<const float2 *>(bt + 16 * bb + 8 * n + 2 * tg);
-                    t[n][0] = e.x * R[2 * bb + n][0], t[n][1] = e.y * R[2 * bb + n][1];
-                    t[n][2] = e.x * R[2 * bb + n][2], t[n][3] = e.y * R[2 * bb + n][3];
-                }
-                split_a(t[0], t[1], ah[bb], al[bb]);
-            }
+            for (int bb = 0; bb < 4; ++bb) split_tokens(R, bb, bt, 1.f, tg, ah[bb], al[bb]);
 #pragma unroll
             for (int a = 0; a < 4; ++a)
 #pragma unroll
@@ -518,39 +620,27 @@ __global__ void __launch_bounds__(kThr, 2)
                     mma(R[2 * a], ah[bb], wh.x, wh.y);
                     mma(R[2 * a + 1], ah[bb], wh.z, wh.w);
                 }
-            // u = beta err; Y += tril(Q K^T o E) u
+            if constexpr (kStore)
+                put_tokens(R, reinterpret_cast<char *>(st.x), out.err, b, L, c * kC, H, h, P, pc, warp, lane);
+            scale_tokens(R, bt, tg);  // u = beta err
+            if constexpr (kStore) {
+                put_tokens(R, reinterpret_cast<char *>(st.x), out.u, b, L, c * kC, H, h, P, pc, warp, lane);
+            } else {  // Y += tril(Q K^T o E) u
+                const uint4 *pf = reinterpret_cast<const uint4 *>(st.prep + Prep<false>::P) + lane;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 e = *reinterpret_cast<const float2 *>(bt + 8 * j + 2 * tg);
-                R[j][0] *= e.x, R[j][1] *= e.y, R[j][2] *= e.x, R[j][3] *= e.y;
-            }
+                for (int bb = 0; bb < 4; ++bb) {
+                    uint32_t hi[4], lo[4];
+                    split_a(R[2 * bb], R[2 * bb + 1], hi, lo);
 #pragma unroll
-            for (int bb = 0; bb < 4; ++bb) {
-                uint32_t hi[4], lo[4];
-                split_a(R[2 * bb], R[2 * bb + 1], hi, lo);
-#pragma unroll
-                for (int a = bb; a < 4; ++a) {
-                    const uint4 f = pf[block_at(a, bb) * 32];
-                    mma(Y[2 * a], lo, f.x, f.y);
-                    mma(Y[2 * a + 1], lo, f.z, f.w);
-                    mma(Y[2 * a], hi, f.x, f.y);
-                    mma(Y[2 * a + 1], hi, f.z, f.w);
+                    for (int a = bb; a < 4; ++a) {
+                        const uint4 f = pf[block_at(a, bb) * 32];
+                        mma(Y[2 * a], lo, f.x, f.y);
+                        mma(Y[2 * a + 1], lo, f.z, f.w);
+                        mma(Y[2 * a], hi, f.x, f.y);
+                        mma(Y[2 * a + 1], hi, f.z, f.w);
+                    }
                 }
-            }
-            // Y over this warp's columns of the x tile, then to memory
-#pragma unroll
-            for (int jj = 0; jj < 4; ++jj)
-                stsm4t(xa + at16<kRowsCta * 2>(16 * jj + (lane & 7) + ((lane >> 4) << 3), 2 * warp + ((lane >> 3) & 1)),
-                       pack(Y[2 * jj][0], Y[2 * jj][1]), pack(Y[2 * jj][2], Y[2 * jj][3]), pack(Y[2 * jj + 1][0], Y[2 * jj + 1][1]),
-                       pack(Y[2 * jj + 1][2], Y[2 * jj + 1][3]));
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 16 * i + (lane >> 1), v = 2 * warp + (lane & 1);
-                const int64_t tt = c * kC + t;
-                if (tt < L && pc + 8 * v < P)
-                    *reinterpret_cast<uint4 *>(y + ((b * L + tt) * H + h) * (int64_t)P + pc + 8 * v) =
-                        *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(st.x) + at16<kRowsCta * 2>(t, v));
+                put_tokens(Y, reinterpret_cast<char *>(st.x), out.y, b, L, c * kC, H, h, P, pc, warp, lane);
             }
             // S <- exp(cum_end) S + (exp(cum_end - cum) u)^T K
             const float gamma = eg[kC - 1];
@@ -561,36 +651,504 @@ __global__ void __launch_bounds__(kThr, 2)
 #pragma unroll
             for (int bb = 0; bb < 4; ++bb) {
                 uint32_t hi[4], lo[4];
-                float t[2][4];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float2 e = *reinterpret_cast<const float2 *>(ek + 16 * bb + 8 * n + 2 * tg);
-                    t[n][0] = e.x * R[2 * bb + n][0], t[n][1] = e.y * R[2 * bb + n][1];
-                    t[n][2] = e.x * R[2 * bb + n][2], t[n][3] = e.y * R[2 * bb + n][3];
-                }
-                split_a(t[0], t[1], hi, lo);
-#pragma unroll
-                for (int j = 0; j < NT / 16; ++j) {
-                    uint32_t bk[4];
-                    ldsm4t(bk, ka + at16<NT * 2>(16 * bb + (lane & 15), 2 * j + (lane >> 4)));
-                    mma(S[2 * j], lo, bk[0], bk[1]);
-                    mma(S[2 * j + 1], lo, bk[2], bk[3]);
-                    mma(S[2 * j], hi, bk[0], bk[1]);
-                    mma(S[2 * j + 1], hi, bk[2], bk[3]);
-                }
+                split_tokens(R, bb, ek, 1.f, tg, hi, lo);
+                rank16<NT>(S, hi, lo, ka, bb, lane);
             }
         }
         __syncthreads();  // the stage is free
     }
-    if (h_final && on) {
+    if (out.h_final && on) store_state<NT>(S, out.h_final, row, P, N, p0 + gr, tg);
+}
+
+// ---------------------------------------------------------------------------------------------
+// k_delta_chain_bwd: the chain in reverse, laid out like the forward one. With D the cotangent of the
+// state leaving a chunk,
+//     F = tril(Q K^T o E)^T dY + (exp(cum_end - cum) K) D^T,   z = F + W^T (beta F),   r = beta z = dX,
+//     D <- exp(cum_end) D + (exp(cum) dY)^T Q - (exp(cum) r)^T K.
+// D of every chunk goes out in bf16 (an operand of k_delta_grads_mma), z too.
+template <int NT>
+struct ChainBwdStage {
+    __nv_bfloat16 k[kC * NT], q[kC * NT], dy[kC * kRowsCta];
+    char prep[Prep<true>::bytes - Prep<true>::scal];
+};
+template <int NT>
+struct ChainBwdSmem {
+    ChainBwdStage<NT> stage[2];
+    __nv_bfloat16 out[kRowsCta * NT];
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kThr, 1)
+    k_delta_chain_bwd(const __nv_bfloat16 *__restrict__ dy, const __nv_bfloat16 *__restrict__ Bm,
+                      const __nv_bfloat16 *__restrict__ Cm, const float *__restrict__ dh_final, const char *__restrict__ ws,
+                      int64_t L, int H, int P, int G, int N, __nv_bfloat16 *__restrict__ dx, __nv_bfloat16 *__restrict__ z,
+                      __nv_bfloat16 *__restrict__ cots, float *__restrict__ dh0) {
+    extern __shared__ __align__(128) char raw[];
+    using Lay = Prep<true>;
+    ChainBwdSmem<NT> &sm = *reinterpret_cast<ChainBwdSmem<NT> *>(raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tg = lane & 3;
+    const int h = blockIdx.y, grp = h / (H / G), pc = blockIdx.x * kRowsCta, p0 = pc + 16 * warp;
+    const int64_t b = blockIdx.z, nc = (L + kC - 1) / kC;
+    const bool on = p0 < P;
+    const char *prep = ws + (b * H + h) * nc * (int64_t)Lay::bytes + Lay::scal;
+
+    const auto load = [&](int64_t c) {
+        ChainBwdStage<NT> &st = sm.stage[c & 1];
+        load_tile<NT / 8>(smem_addr(st.k), Bm, b, L, c * kC, G, grp, N, 0);
+        load_tile<NT / 8>(smem_addr(st.q), Cm, b, L, c * kC, G, grp, N, 0);
+        load_tile<kRowsCta / 8>(smem_addr(st.dy), dy, b, L, c * kC, H, h, P, pc);
+        const uint32_t dst = smem_addr(st.prep);
+        for (int i = tid; i < (int)sizeof(st.prep) / 16; i += kThr) cp16(dst + 16 * i, prep + c * Lay::bytes + 16 * i, true);
+        cp_commit();
+    };
+    load(nc - 1);
+
+    float D[NT / 8][4];
+    const int64_t row = (b * H + h) * (int64_t)P + p0 + gr;
+    load_state<NT>(D, dh_final, row, P, N, p0 + gr, tg);
+
+    for (int64_t c = nc - 1; c >= 0; --c) {
+        if (c > 0) {
+            load(c - 1);
+            cp_wait<1>();
+        } else {
+            cp_wait<0>();
+        }
+        __syncthreads();
+        ChainBwdStage<NT> &st = sm.stage[c & 1];
+        if (on) {
+            const uint32_t ka = smem_addr(st.k), qa = smem_addr(st.q), ya = smem_addr(st.dy);
+            const float *eg = reinterpret_cast<const float *>(st.prep), *ek = eg + kC, *bt = eg + 2 * kC;
+            const uint4 *wf = reinterpret_cast<const uint4 *>(st.prep + Lay::WT - Lay::scal) + lane;
+            const uint4 *pf = reinterpret_cast<const uint4 *>(st.prep + Lay::PT - Lay::scal) + lane;
+            put_state<NT>(D, reinterpret_cast<char *>(sm.out), cots + ((b * H + h) * nc + c) * (int64_t)P * N, P, N, pc, warp, lane);
+            float F[8][4];
 #pragma unroll
-        for (int j = 0; j < NT / 8; ++j)
+            for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int n = 8 * j + 2 * tg + (e & 1), r = 8 * (e >> 1);
-                if (n < N && p0 + gr + r < P) h_final[(row + r) * N + n] = S[j][e];
+                for (int e = 0; e < 4; ++e) F[j][e] = 0.f;
+#pragma unroll
+            for (int s = 0; s < NT / 16; ++s) {  // D K^T
+                uint32_t hi[4], lo[4];
+                split_a(D[2 * s], D[2 * s + 1], hi, lo);
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) {
+                    uint32_t bk[4];
+                    ldsm4(bk, ka + at16<NT * 2>(16 * jj + (lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1)));
+                    mma(F[2 * jj], lo, bk[0], bk[1]);
+                    mma(F[2 * jj + 1], lo, bk[2], bk[3]);
+                    mma(F[2 * jj], hi, bk[0], bk[1]);
+                    mma(F[2 * jj + 1], hi, bk[2], bk[3]);
+                }
             }
+            scale_tokens(F, ek, tg);
+            uint32_t yf[4][4];  // dY^T as left operand, exact
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                ldsm4t(yf[k], ya + at16<kRowsCta * 2>(16 * k + (lane & 7) + ((lane >> 4) << 3), 2 * warp + ((lane >> 3) & 1)));
+#pragma unroll
+                for (int a = 0; a <= k; ++a) {  // tokens of block a gather from tokens of blocks k >= a
+                    const uint4 ph = pf[block_at(k, a) * 64], pl = pf[block_at(k, a) * 64 + 32];
+                    mma(F[2 * a], yf[k], pl.x, pl.y);
+                    mma(F[2 * a + 1], yf[k], pl.z, pl.w);
+                    mma(F[2 * a], yf[k], ph.x, ph.y);
+                    mma(F[2 * a + 1], yf[k], ph.z, ph.w);
+                }
+            }
+            uint32_t ah[4][4], al[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) split_tokens(F, k, bt, 1.f, tg, ah[k], al[k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int a = 0; a <= k; ++a) {
+                    const uint4 wh = wf[block_at(k, a) * 64], wl = wf[block_at(k, a) * 64 + 32];
+                    mma(F[2 * a], al[k], wh.x, wh.y);
+                    mma(F[2 * a + 1], al[k], wh.z, wh.w);
+                    mma(F[2 * a], ah[k], wl.x, wl.y);
+                    mma(F[2 * a + 1], ah[k], wl.z, wl.w);
+                    mma(F[2 * a], ah[k], wh.x, wh.y);
+                    mma(F[2 * a + 1], ah[k], wh.z, wh.w);
+                }
+            put_tokens(F, reinterpret_cast<char *>(st.dy), z, b, L, c * kC, H, h, P, pc, warp, lane);
+            scale_tokens(F, bt, tg);
+            put_tokens(F, reinterpret_cast<char *>(st.dy), dx, b, L, c * kC, H, h, P, pc, warp, lane);
+            const float gamma = eg[kC - 1];
+#pragma unroll
+            for (int j = 0; j < NT / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) D[j][e] *= gamma;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t hi[4], lo[4];
+                split_tokens(F, k, eg, -1.f, tg, hi, lo);
+                rank16<NT>(D, hi, lo, ka, k, lane);
+                float t[2][4];  // exp(cum) dY
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float2 e = *reinterpret_cast<const float2 *>(eg + 16 * k + 8 * n + 2 * tg);
+                    t[n][0] = e.x * low(yf[k][2 * n]), t[n][1] = e.y * high(yf[k][2 * n]);
+                    t[n][2] = e.x * low(yf[k][2 * n + 1]), t[n][3] = e.y * high(yf[k][2 * n + 1]);
+                }
+                split_a(t[0], t[1], hi, lo);
+                rank16<NT>(D, hi, lo, qa, k, lane);
+            }
+        }
+        __syncthreads();
     }
+    if (dh0 && on) store_state<NT>(D, dh0, row, P, N, p0 + gr, tg);
+}
+
+// ---------------------------------------------------------------------------------------------
+// k_delta_grads_mma: grid (chunks, G * slices, B), 8 warps; everything that sums over the state rows. With S
+// the state entering the chunk and D the cotangent leaving it, per head
+//     dP = tril((dY u^T) o E),   dM = -tril((r u^T) o E, -1),
+//     dQ = exp(cum) dY S + dP K,
+//     dK = dP^T Q + (dM + dM^T) K + exp(cum_end - cum) u D - exp(cum) r S,
+//     dbeta_i = z_i.err_i,   dg = the sum from i to the chunk's end of
+//         rows - columns of (dP o Q K^T + dM o K K^T) + exp(cum) dY_i.S q_i - exp(cum) r_i.S k_i - U_i,
+//         U_i = exp(cum_end - cum_i) u_i.D k_i, and at the last token + sum U + exp(cum_end) <D, S>.
+// No sum runs across chunks, and each pair of tokens enters once, in fp32. A CTA walks the heads of its
+// slice with dQ, dK in fp32 accumulators (no atomics), slabs of 64 state rows at a time; a warp holds 16
+// tokens by half of the columns (of dQ, dK, and of the pairs).
+constexpr int kGThr = 256;
+template <int NT>
+struct GradsSmem {
+    __nv_bfloat16 k[kC * NT], q[kC * NT];
+    struct Slab {
+        __nv_bfloat16 s[64 * NT], d[64 * NT], dy[kC * 64], u[kC * 64], r[kC * 64];
+    } slab[2];
+    __nv_bfloat16 dp[kC * kC], dm[kC * kC];  // dP; dM (strictly lower)
+    float2 cum[kC];
+    float eg[kC], ek[kC];
+    float rows[2][kC], cols[4][kC];  // sums by warp column half, by warp row block
+    float U[2][kC];
+    float dot[8], db[kC];
+};
+
+// As load_tile with kGThr threads, rows of [B, L, X, D].
+template <int NV>
+__device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16 *__restrict__ src, int64_t rows, int64_t stride, int cols) {
+    for (int i = threadIdx.x; i < 64 * NV; i += kGThr) {
+        const int t = i / NV, c = i % NV;
+        const bool in = t < rows && 8 * c < cols;
+        cp16(dst + at16<NV * 16>(t, c), in ? src + t * stride + 8 * c : src, in);
+    }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kGThr)
+    k_delta_grads_mma(const __nv_bfloat16 *__restrict__ dy, const __nv_bfloat16 *__restrict__ Bm,
+                      const __nv_bfloat16 *__restrict__ Cm, const char *__restrict__ ws, const __nv_bfloat16 *__restrict__ states,
+                      const __nv_bfloat16 *__restrict__ cots, const __nv_bfloat16 *__restrict__ err,
+                      const __nv_bfloat16 *__restrict__ u, const __nv_bfloat16 *__restrict__ z, const __nv_bfloat16 *__restrict__ dx,
+                      int64_t L, int H, int P, int G, int N, int slices, __nv_bfloat16 *__restrict__ dBm,
+                      __nv_bfloat16 *__restrict__ dCm, float *__restrict__ dB_part, float *__restrict__ dC_part,
+                      __nv_bfloat16 *__restrict__ dg, __nv_bfloat16 *__restrict__ dbeta) {
+    extern __shared__ __align__(128) char raw[];
+    using Lay = Prep<true>;
+    GradsSmem<NT> &sm = *reinterpret_cast<GradsSmem<NT> *>(raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tg = lane & 3;
+    const int rb = warp & 3, nh = warp >> 2;  // 16-token block of rows; half of the columns
+    constexpr int HT = NT / 16;               // 8-column tiles in half of the columns
+    const int64_t c = blockIdx.x, nc = gridDim.x, b = blockIdx.z, t0 = c * kC;
+    const int64_t nt = L - t0 < kC ? L - t0 : kC;
+    const int grp = blockIdx.y / slices, slice = blockIdx.y % slices, per = H / G;
+    const int h_begin = grp * per + per * slice / slices, h_end = grp * per + per * (slice + 1) / slices;
+    const int nslab = (P + 63) / 64, total = (h_end - h_begin) * nslab;
+    const uint32_t ka = smem_addr(sm.k), qa = smem_addr(sm.q), dpa = smem_addr(sm.dp), dma = smem_addr(sm.dm);
+
+    const auto load_slab = [&](int it) {
+        const int h = h_begin + it / nslab, p = it % nslab * 64;
+        auto &sl = sm.slab[it & 1];
+        const int64_t st = (((b * H + h) * nc + c) * (int64_t)P + p) * N, at = ((b * L + t0) * H + h) * (int64_t)P + p;
+        load_rows<NT / 8>(smem_addr(sl.s), states + st, P - p, N, N);
+        load_rows<NT / 8>(smem_addr(sl.d), cots + st, P - p, N, N);
+        load_rows<8>(smem_addr(sl.dy), dy + at, nt, (int64_t)H * P, P - p);
+        load_rows<8>(smem_addr(sl.u), u + at, nt, (int64_t)H * P, P - p);
+        load_rows<8>(smem_addr(sl.r), dx + at, nt, (int64_t)H * P, P - p);
+        cp_commit();
+    };
+    load_rows<NT / 8>(ka, Bm + ((b * L + t0) * G + grp) * (int64_t)N, nt, (int64_t)G * N, N);
+    load_rows<NT / 8>(qa, Cm + ((b * L + t0) * G + grp) * (int64_t)N, nt, (int64_t)G * N, N);
+    load_slab(0);
+
+    float dq[HT][4], dk[HT][4];  // tokens 16 rb + gr (+ 8), columns NT / 2 nh + 8 j + 2 tg (+ 1)
+#pragma unroll
+    for (int j = 0; j < HT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dq[j][e] = dk[j][e] = 0.f;
+    float kk[4][4], qk[4][4];  // pairs: tokens 16 rb + gr (+ 8) by 32 nh + 8 j + 2 tg (+ 1)
+    float dP[4][4], dM[4][4], dsum = 0.f;
+
+    for (int it = 0; it < total; ++it) {
+        const int h = h_begin + it / nslab, p = it % nslab * 64;
+        if (it + 1 < total) {
+            load_slab(it + 1);
+            cp_wait<1>();
+        } else {
+            cp_wait<0>();
+        }
+        if (p == 0 && tid < kC) {  // this head's scalars
+            const float *scal = reinterpret_cast<const float *>(ws + ((b * H + h) * nc + c) * (int64_t)Lay::bytes + Lay::scal);
+            sm.eg[tid] = scal[tid];
+            sm.ek[tid] = scal[kC + tid];
+            sm.cum[tid] = make_float2(scal[3 * kC + tid], scal[4 * kC + tid]);
+        }
+        __syncthreads();
+        if (it == 0) {  // K K^T and Q K^T, once for the group
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) kk[j][e] = qk[j][e] = 0.f;
+#pragma unroll
+            for (int s = 0; s < NT / 16; ++s) {
+                uint32_t ak[4], aq[4];
+                ldsm4(ak, ka + at16<NT * 2>(16 * rb + (lane & 15), 2 * s + (lane >> 4)));
+                ldsm4(aq, qa + at16<NT * 2>(16 * rb + (lane & 15), 2 * s + (lane >> 4)));
+#pragma unroll
+                for (int jj = 0; jj < 2; ++jj) {
+                    uint32_t f[4];
+                    ldsm4(f, ka + at16<NT * 2>(32 * nh + 16 * jj + (lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1)));
+                    mma(kk[2 * jj], ak, f[0], f[1]);
+                    mma(kk[2 * jj + 1], ak, f[2], f[3]);
+                    mma(qk[2 * jj], aq, f[0], f[1]);
+                    mma(qk[2 * jj + 1], aq, f[2], f[3]);
+                }
+            }
+        }
+        auto &sl = sm.slab[it & 1];
+        const uint32_t sa = smem_addr(sl.s), da = smem_addr(sl.d), ya = smem_addr(sl.dy), ua = smem_addr(sl.u), ra = smem_addr(sl.r);
+        if (p == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dP[j][e] = dM[j][e] = 0.f;
+            dsum = 0.f;
+        }
+        uint32_t ay[4][4], ar[4][4], au[4][4];  // tokens 16 rb ..: left operands over the slab's rows
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const uint32_t off = at16<128>(16 * rb + (lane & 15), 2 * s + (lane >> 4));
+            ldsm4(ay[s], ya + off);
+            ldsm4(ar[s], ra + off);
+            ldsm4(au[s], ua + off);
+        }
+        if (32 * nh <= 16 * rb + 15) {  // pairs up to the diagonal
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int jj = 0; jj < 2; ++jj) {
+                    uint32_t f[4];
+                    ldsm4(f, ua + at16<128>(32 * nh + 16 * jj + (lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1)));
+                    mma(dP[2 * jj], ay[s], f[0], f[1]);
+                    mma(dP[2 * jj + 1], ay[s], f[2], f[3]);
+                    mma(dM[2 * jj], ar[s], f[0], f[1]);
+                    mma(dM[2 * jj + 1], ar[s], f[2], f[3]);
+                }
+        }
+        // the three products with the states, their share of dQ and dK, and their dot products with q and k
+        float rd[2] = {0.f, 0.f}, ud[2] = {0.f, 0.f};
+        const float eg0 = sm.eg[16 * rb + gr], eg1 = sm.eg[16 * rb + gr + 8], ek0 = sm.ek[16 * rb + gr], ek1 = sm.ek[16 * rb + gr + 8];
+#pragma unroll
+        for (int j = 0; j < HT; j += 2) {
+            float ty[2][4], tr[2][4], tu[2][4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ty[n][e] = tr[n][e] = tu[n][e] = 0.f;
+            const int v = nh * HT + j;  // 16-byte vector of the columns
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                uint32_t fs[4], fd[4];
+                const uint32_t off = at16<NT * 2>(16 * s + (lane & 15), v + (lane >> 4));
+                ldsm4t(fs, sa + off);
+                ldsm4t(fd, da + off);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    mma(ty[n], ay[s], fs[2 * n], fs[2 * n + 1]);
+                    mma(tr[n], ar[s], fs[2 * n], fs[2 * n + 1]);
+                    mma(tu[n], au[s], fd[2 * n], fd[2 * n + 1]);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t off = at16<NT * 2>(16 * rb + gr + 8 * r, v + n) + 4 * tg;
+                    const uint32_t kv = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const char *>(sm.k) + off);
+                    const uint32_t qv = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const char *>(sm.q) + off);
+                    const float eg = r ? eg1 : eg0, ek = r ? ek1 : ek0;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float y = eg * ty[n][2 * r + e], rr = eg * tr[n][2 * r + e], uu = ek * tu[n][2 * r + e];
+                        const float kf = e ? high(kv) : low(kv), qf = e ? high(qv) : low(qv);
+                        dq[j + n][2 * r + e] += y;
+                        dk[j + n][2 * r + e] += uu - rr;
+                        rd[r] += y * qf - rr * kf;
+                        ud[r] += uu * kf;
+                    }
+                }
+        }
+        // <D, S>
+        for (int i = tid; i < 64 * NT / 8; i += kGThr) {
+            const uint4 sv = reinterpret_cast<const uint4 *>(sl.s)[i], dv = reinterpret_cast<const uint4 *>(sl.d)[i];
+            const uint32_t a[4] = {sv.x, sv.y, sv.z, sv.w}, d[4] = {dv.x, dv.y, dv.z, dv.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dsum = fmaf(low(a[e]), low(d[e]), fmaf(high(a[e]), high(d[e]), dsum));
+        }
+        // dbeta: four threads per token, 16 rows each
+        float db = 0.f;
+        if (tid / 4 < nt) {
+            const int64_t at = ((b * L + t0 + tid / 4) * H + h) * (int64_t)P + p + (tid & 3) * 16;
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+                if (p + (tid & 3) * 16 + 8 * v < P) {
+                    const uint4 zv = *reinterpret_cast<const uint4 *>(z + at + 8 * v), ev = *reinterpret_cast<const uint4 *>(err + at + 8 * v);
+                    const uint32_t a[4] = {zv.x, zv.y, zv.z, zv.w}, d[4] = {ev.x, ev.y, ev.z, ev.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) db = fmaf(low(a[e]), low(d[e]), fmaf(high(a[e]), high(d[e]), db));
+                }
+        }
+        db += __shfl_xor_sync(0xffffffffu, db, 1);
+        db += __shfl_xor_sync(0xffffffffu, db, 2);
+        if ((tid & 3) == 0) sm.db[tid / 4] = p == 0 ? db : sm.db[tid / 4] + db;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                rd[r] += __shfl_xor_sync(0xffffffffu, rd[r], o);
+                ud[r] += __shfl_xor_sync(0xffffffffu, ud[r], o);
+            }
+            if (tg == 0) {
+                float *ro = &sm.rows[nh][16 * rb + gr + 8 * r], *uo = &sm.U[nh][16 * rb + gr + 8 * r];
+                *ro = p == 0 ? rd[r] : *ro + rd[r];
+                *uo = p == 0 ? ud[r] : *uo + ud[r];
+            }
+        }
+        if (p + 64 >= P) {  // the head's last slab: the pairs
+            float row_sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int jc = 32 * nh + 8 * j + 2 * tg;
+                const float4 cj = *reinterpret_cast<const float4 *>(&sm.cum[jc]);
+                float col[2] = {0.f, 0.f};
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int i = 16 * rb + gr + 8 * r;
+                    const float2 ci = sm.cum[i];
+                    float p2[2], m2[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float ex = jc + e <= i ? decay_between(ci, e ? make_float2(cj.z, cj.w) : make_float2(cj.x, cj.y)) : 0.f;
+                        p2[e] = jc + e <= i ? dP[j][2 * r + e] * ex : 0.f;
+                        m2[e] = jc + e < i ? -dM[j][2 * r + e] * ex : 0.f;
+                        const float pair = p2[e] * qk[j][2 * r + e] + m2[e] * kk[j][2 * r + e];
+                        row_sum[r] += pair;
+                        col[e] += pair;
+                    }
+                    const uint32_t off = at16<128>(i, 4 * nh + j) + 4 * tg;
+                    *reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(sm.dp) + off) = pack(p2[0], p2[1]);
+                    *reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(sm.dm) + off) = pack(m2[0], m2[1]);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) col[e] += __shfl_xor_sync(0xffffffffu, col[e], o);
+                    if (gr == 0) sm.cols[rb][jc + e] = col[e];
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) row_sum[r] += __shfl_xor_sync(0xffffffffu, row_sum[r], o);
+                if (tg == 0) sm.rows[nh][16 * rb + gr + 8 * r] += row_sum[r];
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) dsum += __shfl_xor_sync(0xffffffffu, dsum, o);
+            if (lane == 0) sm.dot[warp] = dsum;
+            __syncthreads();
+            // dQ += dP K; dK += dP^T Q + (dM + dM^T) K
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                uint32_t ap[4], am[4], pt[4], mt[4];
+                const uint32_t off = at16<128>(16 * rb + (lane & 15), 2 * s + (lane >> 4));
+                const uint32_t offt = at16<128>(16 * s + (lane & 7) + ((lane >> 4) << 3), 2 * rb + ((lane >> 3) & 1));
+                if (s <= rb) {
+                    ldsm4(ap, dpa + off);
+                    ldsm4(am, dma + off);
+                }
+                if (s >= rb) {
+                    ldsm4t(pt, dpa + offt);
+                    ldsm4t(mt, dma + offt);
+                }
+#pragma unroll
+                for (int j = 0; j < HT; j += 2) {
+                    uint32_t fk[4], fq[4];
+                    const uint32_t o2 = at16<NT * 2>(16 * s + (lane & 15), nh * HT + j + (lane >> 4));
+                    ldsm4t(fk, ka + o2);
+                    if (s <= rb) {
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            mma(dq[j + n], ap, fk[2 * n], fk[2 * n + 1]);
+                            mma(dk[j + n], am, fk[2 * n], fk[2 * n + 1]);
+                        }
+                    }
+                    if (s >= rb) {
+                        ldsm4t(fq, qa + o2);
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            mma(dk[j + n], pt, fq[2 * n], fq[2 * n + 1]);
+                            mma(dk[j + n], mt, fk[2 * n], fk[2 * n + 1]);
+                        }
+                    }
+                }
+            }
+            if (warp == 0) {  // dg: tokens 2 lane, 2 lane + 1, summed from the chunk's end
+                float d[2], us = 0.f;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = 2 * lane + e;
+                    const float U = sm.U[0][i] + sm.U[1][i];
+                    us += U;
+                    d[e] = sm.rows[0][i] + sm.rows[1][i] - ((sm.cols[0][i] + sm.cols[1][i]) + (sm.cols[2][i] + sm.cols[3][i])) - U;
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) us += __shfl_xor_sync(0xffffffffu, us, o);
+                float end = 0.f;
+                for (int w = 0; w < 8; ++w) end += sm.dot[w];
+                end = us + sm.eg[kC - 1] * end;
+                float s2 = d[0] + d[1];
+                if (lane == 31) s2 += end, d[1] += end;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float up = __shfl_down_sync(0xffffffffu, s2, o);
+                    if (lane + o < 32) s2 += up;
+                }
+                const int64_t at = (b * L + t0 + 2 * lane) * H + h;
+                if (2 * lane < nt) dg[at] = __float2bfloat16_rn(s2), dbeta[at] = __float2bfloat16_rn(sm.db[2 * lane]);
+                if (2 * lane + 1 < nt) dg[at + H] = __float2bfloat16_rn(s2 - d[0]), dbeta[at + H] = __float2bfloat16_rn(sm.db[2 * lane + 1]);
+            }
+        }
+        __syncthreads();  // the slab and the head's sums are free
+    }
+#pragma unroll
+    for (int j = 0; j < HT; ++j)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int t = 16 * rb + gr + 8 * r, n = 8 * (nh * HT + j) + 2 * tg;
+            if (t < nt && n < N) {
+                if (slices == 1) {
+                    const int64_t at = ((b * L + t0 + t) * G + grp) * (int64_t)N + n;
+                    *reinterpret_cast<uint32_t *>(dCm + at) = pack(dq[j][2 * r], dq[j][2 * r + 1]);
+                    *reinterpret_cast<uint32_t *>(dBm + at) = pack(dk[j][2 * r], dk[j][2 * r + 1]);
+                } else {
+                    const int64_t at = ((b * L + t0 + t) * gridDim.y + blockIdx.y) * (int64_t)N + n;
+                    *reinterpret_cast<float2 *>(dC_part + at) = make_float2(dq[j][2 * r], dq[j][2 * r + 1]);
+                    *reinterpret_cast<float2 *>(dB_part + at) = make_float2(dk[j][2 * r], dk[j][2 * r + 1]);
+                }
+            }
+        }
 }
 
 template <int NT, bool BWD>
@@ -612,18 +1170,96 @@ cudaError_t prep_launch(const DeltaProblem &p, char *ws, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <int NT, bool kStore>
+cudaError_t chain_launch(const DeltaProblem &p, const char *ws, const ChainOut &out, cudaStream_t s) {
+    using bf = __nv_bfloat16;
+    constexpr int smem = 2 * sizeof(ChainStage<NT, kStore>);
+    cudaError_t e;
+    if ((e = cudaFuncSetAttribute(k_delta_chain<NT, kStore>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
+    dim3 grid((unsigned)((p.P + kRowsCta - 1) / kRowsCta), (unsigned)p.H, (unsigned)p.B);
+    k_delta_chain<NT, kStore><<<grid, kThr, smem, s>>>(static_cast<const bf *>(p.x), static_cast<const bf *>(p.Bm),
+                                                       static_cast<const bf *>(p.Cm), p.h0, ws, p.L, (int)p.H, (int)p.P,
+                                                       (int)p.G, (int)p.N, out);
+    return cudaGetLastError();
+}
+
 template <int NT>
 cudaError_t fwd_launch(const DeltaProblem &p, char *ws, cudaStream_t s) {
+    const cudaError_t e = prep_launch<NT, false>(p, ws, s);
+    return e ? e : chain_launch<NT, false>(p, ws, ChainOut{static_cast<__nv_bfloat16 *>(p.y), nullptr, nullptr, nullptr, p.h_final}, s);
+}
+
+// Slices of a group's heads in k_delta_grads_mma: the number that makes (waves of CTAs on 148 SMs) x (heads
+// a CTA walks) smallest, the fewest of them on a tie (more than one costs fp32 parts and a second pass).
+int grads_slices(const DeltaProblem &p) {
+    const int64_t units = (p.L + kC - 1) / kC * p.G * p.B, per = p.H / p.G;
+    int best = 1;
+    int64_t cost = (units + 147) / 148 * per;
+    for (int s = 2; s <= per && s <= 16; ++s) {
+        const int64_t here = (units * s + 147) / 148 * ((per + s - 1) / s);
+        if (here * 8 < cost * 7) cost = here, best = s;
+    }
+    return best;
+}
+
+// Workspace of the backward pass, as byte offsets.
+struct BwdLayout {
+    size_t prep, states, cots, err, u, z, dB, dC, total;
+};
+BwdLayout bwd_layout(const DeltaProblem &p) {
+    const size_t chunks = (size_t)(p.B * p.H) * (size_t)((p.L + kC - 1) / kC);
+    const size_t rows = (size_t)(p.B * p.L * p.H * p.P) * 2;
+    const int slices = grads_slices(p);
+    const size_t part = slices > 1 ? (size_t)(p.B * p.L * p.G * slices * p.N) * 4 : 0;
+    BwdLayout l{};
+    size_t at = 0;
+    const auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += align_up(bytes, kWsAlign);
+        return here;
+    };
+    l.prep = take(chunks * Prep<true>::bytes);
+    l.states = take(chunks * (size_t)(p.P * p.N) * 2);
+    l.cots = take(chunks * (size_t)(p.P * p.N) * 2);
+    l.err = take(rows);
+    l.u = take(rows);
+    l.z = take(rows);
+    l.dB = take(part);
+    l.dC = take(part);
+    l.total = at;
+    return l;
+}
+
+template <int NT>
+cudaError_t bwd_launch(const DeltaProblem &p, const DeltaGrads &gr, char *ws, cudaStream_t s) {
     using bf = __nv_bfloat16;
-    cudaError_t e = prep_launch<NT, false>(p, ws, s);
+    const BwdLayout l = bwd_layout(p);
+    bf *states = reinterpret_cast<bf *>(ws + l.states), *cots = reinterpret_cast<bf *>(ws + l.cots);
+    bf *err = reinterpret_cast<bf *>(ws + l.err), *u = reinterpret_cast<bf *>(ws + l.u), *z = reinterpret_cast<bf *>(ws + l.z);
+    float *dB = reinterpret_cast<float *>(ws + l.dB), *dC = reinterpret_cast<float *>(ws + l.dC);
+    const char *prep = ws + l.prep;
+    cudaError_t e = prep_launch<NT, true>(p, ws + l.prep, s);
+    if (!e) e = chain_launch<NT, true>(p, prep, ChainOut{nullptr, states, err, u, nullptr}, s);
     if (e) return e;
-    constexpr int smem = 2 * sizeof(ChainStage<NT>);
-    if ((e = cudaFuncSetAttribute(k_delta_chain<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
+    constexpr int smem = sizeof(ChainBwdSmem<NT>), gsmem = sizeof(GradsSmem<NT>);
+    if ((e = cudaFuncSetAttribute(k_delta_chain_bwd<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
+    if ((e = cudaFuncSetAttribute(k_delta_grads_mma<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, gsmem))) return e;
+    const bf *dy = static_cast<const bf *>(gr.dy), *Bm = static_cast<const bf *>(p.Bm), *Cm = static_cast<const bf *>(p.Cm);
+    bf *dx = static_cast<bf *>(gr.dx);
     dim3 grid((unsigned)((p.P + kRowsCta - 1) / kRowsCta), (unsigned)p.H, (unsigned)p.B);
-    k_delta_chain<NT><<<grid, kThr, smem, s>>>(static_cast<const bf *>(p.x), static_cast<const bf *>(p.Bm),
-                                               static_cast<const bf *>(p.Cm), p.h0, ws, p.L, (int)p.H, (int)p.P, (int)p.G,
-                                               (int)p.N, static_cast<bf *>(p.y), p.h_final);
-    return cudaGetLastError();
+    k_delta_chain_bwd<NT><<<grid, kThr, smem, s>>>(dy, Bm, Cm, gr.dh_final, prep, p.L, (int)p.H, (int)p.P, (int)p.G, (int)p.N,
+                                                   dx, z, cots, gr.dh0);
+    if ((e = cudaGetLastError())) return e;
+    const int slices = grads_slices(p);
+    dim3 ggrid((unsigned)((p.L + kC - 1) / kC), (unsigned)(p.G * slices), (unsigned)p.B);
+    k_delta_grads_mma<NT><<<ggrid, kGThr, gsmem, s>>>(dy, Bm, Cm, prep, states, cots, err, u, z, dx, p.L, (int)p.H, (int)p.P,
+                                                      (int)p.G, (int)p.N, slices, static_cast<bf *>(gr.dBm),
+                                                      static_cast<bf *>(gr.dCm), dB, dC, static_cast<bf *>(gr.dg),
+                                                      static_cast<bf *>(gr.dbeta));
+    if ((e = cudaGetLastError()) || slices == 1) return e;
+    DeltaProblem q = p;  // "heads" of the sum: the slices
+    q.H = p.G * slices;
+    return delta_group_sum_launch(q, dB, dC, gr.dBm, gr.dCm, s);
 }
 
 }  // namespace
@@ -638,6 +1274,13 @@ size_t delta_mma_fwd_workspace_bytes(const DeltaProblem &p) {
 
 cudaError_t delta_mma_fwd(const DeltaProblem &p, void *ws, cudaStream_t s) {
     return p.N <= 64 ? fwd_launch<64>(p, static_cast<char *>(ws), s) : fwd_launch<128>(p, static_cast<char *>(ws), s);
+}
+
+size_t delta_mma_bwd_workspace_bytes(const DeltaProblem &p) { return bwd_layout(p).total; }
+int delta_mma_bwd_kernels(const DeltaProblem &p) { return grads_slices(p) > 1 ? 5 : 4; }
+
+cudaError_t delta_mma_bwd(const DeltaProblem &p, const DeltaGrads &g, void *ws, cudaStream_t s) {
+    return p.N <= 64 ? bwd_launch<64>(p, g, static_cast<char *>(ws), s) : bwd_launch<128>(p, g, static_cast<char *>(ws), s);
 }
 
 }  // namespace ssd
