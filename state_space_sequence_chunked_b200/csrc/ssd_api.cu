@@ -523,7 +523,7 @@ ssd_status_t check_norm(int64_t rows, int64_t dim, int64_t ngroups, ssd_dtype_t 
     const ssd_status_t st = check_dtype(dtype);
     if (st != SSD_OK) return st;
     if (rows < 0 || dim < 1 || ngroups < 1 || dim % ngroups != 0 || !(eps >= 0.f)) return SSD_ERR_INVALID_ARG;
-    if (dim / ngroups > norm_max_group() || dim > 0x7fffffffLL / 4) return SSD_ERR_UNSUPPORTED;
+    if (dim / ngroups > norm_max_group() || dim > 0x7fffffffLL / 4 || rows > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 

@@ -25,33 +25,55 @@ constexpr int kPer = 16;      // channels a thread may hold
 constexpr int kMaxParts = 592;  // partial rows of a column sum: 4 CTAs per SM
 
 struct Geom {
-    int64_t rows;
+    uint32_t rows;  // below 2^31, so that a step past the end does not wrap
     int gs, ngroups, tpg, gpc, rpc;
+    float inv;  // 1 / gs
 };
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + __expf(-v)); }
+// 1 / (1 + 2^(-v log2 e)) by the approximate instructions (2^-22 relative each); 0 where the power
+// overflows.
+__device__ __forceinline__ float sigmoid(float v) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504f * v));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
 
+// V neighbouring channels as they lie in memory (16-byte vectors where V is 8).
 template <typename T, int V>
-__device__ __forceinline__ void load_v(const T *p, float (&f)[V]) {
-    if constexpr (V == 8 && sizeof(T) == 2) {
-        const uint4 r = *reinterpret_cast<const uint4 *>(p);
-        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&r);
+struct Raw {
+    T v[V];
+};
+template <>
+struct Raw<__nv_bfloat16, 8> {
+    uint4 v;
+};
+template <>
+struct Raw<__nv_bfloat16, 2> {
+    __nv_bfloat162 v;
+};
+template <>
+struct Raw<float, 8> {
+    float4 v[2];
+};
+template <>
+struct Raw<float, 2> {
+    float2 v;
+};
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_raw(const T *p) {
+    return *reinterpret_cast<const Raw<T, V> *>(p);
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Raw<T, V> &r, float (&f)[V]) {
+    if constexpr (sizeof(T) == 2) {
+        const T *e = reinterpret_cast<const T *>(&r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 v = __bfloat1622float2(h[i]);
-            f[2 * i] = v.x, f[2 * i + 1] = v.y;
-        }
-    } else if constexpr (V == 8) {
-        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    } else if constexpr (V == 2 && sizeof(T) == 2) {
-        const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p));
-        f[0] = v.x, f[1] = v.y;
-    } else if constexpr (V == 2) {
-        const float2 v = *reinterpret_cast<const float2 *>(p);
-        f[0] = v.x, f[1] = v.y;
+        for (int i = 0; i < V; ++i) f[i] = to_f32(e[i]);
     } else {
-        f[0] = to_f32(p[0]);
+        const float *e = reinterpret_cast<const float *>(&r);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = e[i];
     }
 }
 template <typename T, int V>
@@ -88,9 +110,14 @@ struct Pos {
 };
 
 // Sums of M values over the tpg threads of a group, returned to all of them. Every thread of the CTA
-// calls it (a warp of shared memory per value where a group spans warps).
+// calls it. Where a group spans warps they meet in one of two buffers in turn, so that one barrier a
+// call is enough.
 template <int M>
-__device__ __forceinline__ void group_sum(float (&v)[M], int tpg, float (*buf)[kMaxThr / 32]) {
+struct SumBuf {
+    float v[2][M][kMaxThr / 32];
+};
+template <int M>
+__device__ __forceinline__ void group_sum(float (&v)[M], int tpg, SumBuf<M> &buf, uint32_t &turn) {
     if (tpg <= 32) {
         for (int o = tpg >> 1; o > 0; o >>= 1)
 #pragma unroll
@@ -102,17 +129,21 @@ __device__ __forceinline__ void group_sum(float (&v)[M], int tpg, float (*buf)[k
 #pragma unroll
         for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
     const int warp = threadIdx.x >> 5, wpg = tpg >> 5, first = warp / wpg * wpg;
+    float(&b)[M][kMaxThr / 32] = buf.v[turn];
+    turn ^= 1;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
-        for (int m = 0; m < M; ++m) buf[m][warp] = v[m];
+        for (int m = 0; m < M; ++m) b[m][warp] = v[m];
     __syncthreads();
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-        float s = 0.f;
-        for (int w = 0; w < wpg; ++w) s += buf[m][first + w];
-        v[m] = s;
-    }
-    __syncthreads();
+    for (int m = 0; m < M; ++m) v[m] = lane < wpg ? b[m][first + lane] : 0.f;
+#pragma unroll
+    for (int o = kMaxThr / 64; o > 0; o >>= 1)
+#pragma unroll
+        for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
+#pragma unroll
+    for (int m = 0; m < M; ++m) v[m] = __shfl_sync(0xffffffffu, v[m], 0);
 }
 
 template <int V, int S>
@@ -148,106 +179,163 @@ __device__ __forceinline__ void put_part(const float (&f)[S][V], const Geom &q, 
     }
 }
 
-template <typename T, typename R, int V, int S>
-__global__ void __launch_bounds__(kMaxThr)
+// The rows of one step: U per thread, all of their vectors loaded before any is reduced, so that U times
+// the bytes are in flight and a reduction across warps serves U rows.
+#define SSD_FOR_ROWS(q, U)                                             \
+    for (uint32_t base = blockIdx.y * (uint32_t)(q.rpc * U) + at.row_slot; base - at.row_slot < q.rows; \
+         base += gridDim.y * (uint32_t)(q.rpc * U))
+
+// The forward kernels: 16-byte rows in flight two at a time, at most 80 registers.
+template <typename T, typename R, int V, int S, int U>
+__global__ void __launch_bounds__(V == 8 && S == 1 ? 768 : kMaxThr)
     k_add_rmsnorm(Geom q, const T *x, const R *residual, const float *__restrict__ scale, const float *__restrict__ w,
                   float eps, R *res_out, T *out) {
-    __shared__ float buf[1][kMaxThr / 32];
+    __shared__ SumBuf<U> buf;
+    uint32_t turn = 0;
     const Pos at(q);
     float wv[S][V], sv[S][V];
     load_cols<V, S>(w, q, at, wv, 0.f);
     load_cols<V, S>(scale, q, at, sv, 1.f);
-    for (int64_t base = (int64_t)blockIdx.y * q.rpc; base < q.rows; base += (int64_t)gridDim.y * q.rpc) {
-        const int64_t row = base + at.row_slot;
-        const bool on = at.live && row < q.rows;
-        float r[S][V], sum[1] = {0.f};
+    SSD_FOR_ROWS(q, U) {
+        Raw<T, V> xr[U][S];
+        Raw<R, V> rr[U][S];
+        float sum[U];
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int e = (at.tl + s * q.tpg) * V;
-            if (on && e < q.gs) {
-                load_v<T, V>(x + row * q.gs + e, r[s]);
-                if (residual) {
-                    float o[V];
-                    load_v<R, V>(residual + row * q.gs + e, o);
+        for (int u = 0; u < U; ++u) {
+            const uint32_t row = base + u * q.rpc;
 #pragma unroll
-                    for (int v = 0; v < V; ++v) r[s][v] = scale ? fmaf(sv[s][v], r[s][v], o[v]) : r[s][v] + o[v];
-                } else if (scale) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) r[s][v] *= sv[s][v];
+            for (int s = 0; s < S; ++s) {
+                const int e = (at.tl + s * q.tpg) * V;
+                if (at.live && row < q.rows && e < q.gs) {
+                    xr[u][s] = load_raw<T, V>(x + (int64_t)row * q.gs + e);
+                    if (residual) rr[u][s] = load_raw<R, V>(residual + (int64_t)row * q.gs + e);
                 }
-                if (res_out) store_v<R, V>(res_out + row * q.gs + e, r[s]);
-#pragma unroll
-                for (int v = 0; v < V; ++v) sum[0] = fmaf(r[s][v], r[s][v], sum[0]);
             }
         }
-        group_sum(sum, q.tpg, buf);
-        const float rstd = rsqrtf(sum[0] / (float)q.gs + eps);
+        float r[U][S][V];
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int e = (at.tl + s * q.tpg) * V;
-            if (on && e < q.gs) {
+        for (int u = 0; u < U; ++u) {
+            const uint32_t row = base + u * q.rpc;
+            sum[u] = 0.f;
 #pragma unroll
-                for (int v = 0; v < V; ++v) r[s][v] *= rstd * wv[s][v];
-                store_v<T, V>(out + row * q.gs + e, r[s]);
+            for (int s = 0; s < S; ++s) {
+                const int e = (at.tl + s * q.tpg) * V;
+                if (at.live && row < q.rows && e < q.gs) {
+                    unpack(xr[u][s], r[u][s]);
+                    if (scale) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) r[u][s][v] *= sv[s][v];
+                    }
+                    if (residual) {
+                        float o[V];
+                        unpack(rr[u][s], o);
+#pragma unroll
+                        for (int v = 0; v < V; ++v) r[u][s][v] += o[v];
+                    }
+                    if (res_out) store_v<R, V>(res_out + (int64_t)row * q.gs + e, r[u][s]);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) sum[u] = fmaf(r[u][s][v], r[u][s][v], sum[u]);
+                }
+            }
+        }
+        group_sum(sum, q.tpg, buf, turn);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t row = base + u * q.rpc;
+            const float rstd = rsqrtf(fmaf(sum[u], q.inv, eps));
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const int e = (at.tl + s * q.tpg) * V;
+                if (at.live && row < q.rows && e < q.gs) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) r[u][s][v] *= rstd * wv[s][v];
+                    store_v<T, V>(out + (int64_t)row * q.gs + e, r[u][s]);
+                }
             }
         }
     }
 }
 
+// The backward kernels keep a row as it was loaded (packed) between the two passes over it, the
+// weights in shared memory, and so at most 80 registers where a row is one vector per thread.
 template <typename T, typename R, int V, int S>
-__global__ void __launch_bounds__(kMaxThr)
-    k_add_rmsnorm_bwd(Geom q, const R *__restrict__ r, const float *__restrict__ w, float eps, const T *dout,
-                      const R *dres_in, const T *__restrict__ x, const float *__restrict__ scale, R *dres, T *dx,
-                      float *dw_part, float *ds_part) {
-    extern __shared__ float sm[];
-    __shared__ float buf[2][kMaxThr / 32];
+__global__ void __launch_bounds__(V == 8 && S == 1 ? 768 : kMaxThr)
+    k_add_rmsnorm_bwd(Geom q, const R *r, const float *__restrict__ w, float eps, const T *dout, const R *dres_in, const T *x,
+                      const float *__restrict__ scale, R *dres, T *dx, float *dw_part, float *ds_part) {
+    extern __shared__ __align__(16) float sm[];
+    __shared__ SumBuf<2> buf;
+    uint32_t turn = 0;
     const Pos at(q);
-    float wv[S][V], sv[S][V], dw[S][V], ds[S][V];
-    load_cols<V, S>(w, q, at, wv, 0.f);
-    load_cols<V, S>(scale, q, at, sv, 1.f);
+    float *ws = sm, *ss = sm + q.gs;
+    for (int i = threadIdx.x; i < q.gs; i += blockDim.x) {
+        ws[i] = w[i];
+        ss[i] = scale ? scale[i] : 1.f;
+    }
+    float dw[S][V], ds[S][V];
 #pragma unroll
     for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int v = 0; v < V; ++v) dw[s][v] = ds[s][v] = 0.f;
-    for (int64_t base = (int64_t)blockIdx.y * q.rpc; base < q.rows; base += (int64_t)gridDim.y * q.rpc) {
-        const int64_t row = base + at.row_slot;
+    __syncthreads();
+    SSD_FOR_ROWS(q, 1) {
+        const uint32_t row = base;
         const bool on = at.live && row < q.rows;
-        float rv[S][V], dv[S][V], sum[2] = {0.f, 0.f};
+        Raw<R, V> rr[S], ir[S];
+        Raw<T, V> dr[S], xr[S];
+        float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int e = (at.tl + s * q.tpg) * V;
             if (on && e < q.gs) {
-                load_v<R, V>(r + row * q.gs + e, rv[s]);
-                load_v<T, V>(dout + row * q.gs + e, dv[s]);
+                const int64_t off = (int64_t)row * q.gs + e;
+                rr[s] = load_raw<R, V>(r + off);
+                dr[s] = load_raw<T, V>(dout + off);
+                if (dres_in) ir[s] = load_raw<R, V>(dres_in + off);
+                if (ds_part) xr[s] = load_raw<T, V>(x + off);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int e = (at.tl + s * q.tpg) * V;
+            if (on && e < q.gs) {
+                float rv[V], dv[V], wv[V];
+                unpack(rr[s], rv);
+                unpack(dr[s], dv);
+                unpack(load_raw<float, V>(ws + e), wv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    sum[0] = fmaf(rv[s][v], rv[s][v], sum[0]);
-                    sum[1] = fmaf(wv[s][v] * dv[s][v], rv[s][v], sum[1]);
+                    sum[0] = fmaf(rv[v], rv[v], sum[0]);
+                    sum[1] = fmaf(wv[v] * dv[v], rv[v], sum[1]);
                 }
             }
         }
-        group_sum(sum, q.tpg, buf);
-        const float rstd = rsqrtf(sum[0] / (float)q.gs + eps), mean = sum[1] * rstd / (float)q.gs;
+        group_sum(sum, q.tpg, buf, turn);
+        const float rstd = rsqrtf(fmaf(sum[0], q.inv, eps)), mean = sum[1] * rstd * q.inv;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int e = (at.tl + s * q.tpg) * V;
             if (on && e < q.gs) {
-                float o[V], xv[V];
-                const int64_t off = row * q.gs + e;
-                if (dres_in) load_v<R, V>(dres_in + off, o);
-                if (ds_part) load_v<T, V>(x + off, xv);
+                float rv[V], dv[V], wv[V], o[V], xv[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) o[v] = xv[v] = 0.f;
+                const int64_t off = (int64_t)row * q.gs + e;
+                unpack(rr[s], rv);
+                unpack(dr[s], dv);
+                unpack(load_raw<float, V>(ws + e), wv);
+                if (dres_in) unpack(ir[s], o);
+                if (ds_part) unpack(xr[s], xv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float n = rv[s][v] * rstd;
-                    dw[s][v] = fmaf(dv[s][v], n, dw[s][v]);
-                    const float d = rstd * (wv[s][v] * dv[s][v] - n * mean);
-                    o[v] = dres_in ? o[v] + d : d;
-                    if (ds_part) ds[s][v] = fmaf(o[v], xv[v], ds[s][v]);
+                    const float n = rv[v] * rstd;
+                    dw[s][v] = fmaf(dv[v], n, dw[s][v]);
+                    o[v] = fmaf(rstd, fmaf(-n, mean, wv[v] * dv[v]), o[v]);
+                    ds[s][v] = fmaf(o[v], xv[v], ds[s][v]);
                 }
                 if (dres) store_v<R, V>(dres + off, o);
                 if (dx) {
+                    unpack(load_raw<float, V>(ss + e), wv);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) o[v] *= sv[s][v];
+                    for (int v = 0; v < V; ++v) o[v] *= wv[v];
                     store_v<T, V>(dx + off, o);
                 }
             }
@@ -257,117 +345,159 @@ __global__ void __launch_bounds__(kMaxThr)
     if (ds_part) put_part<V, S>(ds, q, at, sm, ds_part);
 }
 
-template <typename T, int V, int S>
-__global__ void __launch_bounds__(kMaxThr)
-    k_norm_gate(Geom q, const T *y, const T *__restrict__ z, int64_t z_stride, const float *__restrict__ w, float eps,
-                T *out) {
-    __shared__ float buf[1][kMaxThr / 32];
+template <typename T, int V, int S, int U>
+__global__ void __launch_bounds__(V == 8 && S == 1 ? 768 : kMaxThr)
+    k_norm_gate(Geom q, const T *y, const T *z, int64_t z_stride, const float *__restrict__ w, float eps, T *out) {
+    __shared__ SumBuf<U> buf;
+    uint32_t turn = 0;
     const Pos at(q);
-    const int dim = q.gs * q.ngroups;
+    const int dim = q.gs * q.ngroups, col = at.group * q.gs;
     float wv[S][V];
     load_cols<V, S>(w, q, at, wv, 0.f);
-    for (int64_t base = (int64_t)blockIdx.y * q.rpc; base < q.rows; base += (int64_t)gridDim.y * q.rpc) {
-        const int64_t row = base + at.row_slot;
-        const bool on = at.live && row < q.rows;
-        const int col = at.group * q.gs;
-        float f[S][V], zv[S][V], sum[1] = {0.f};
+    SSD_FOR_ROWS(q, U) {
+        Raw<T, V> yr[U][S], zr[U][S];
+        float sum[U];
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int e = (at.tl + s * q.tpg) * V;
-            if (on && e < q.gs) {
-                load_v<T, V>(y + row * dim + col + e, f[s]);
-                load_v<T, V>(z + row * z_stride + col + e, zv[s]);
+        for (int u = 0; u < U; ++u) {
+            const uint32_t row = base + u * q.rpc;
 #pragma unroll
-                for (int v = 0; v < V; ++v) sum[0] = fmaf(f[s][v], f[s][v], sum[0]);
+            for (int s = 0; s < S; ++s) {
+                const int e = (at.tl + s * q.tpg) * V;
+                if (at.live && row < q.rows && e < q.gs) {
+                    yr[u][s] = load_raw<T, V>(y + (int64_t)row * dim + (col + e));
+                    zr[u][s] = load_raw<T, V>(z + (int64_t)row * z_stride + (col + e));
+                }
             }
         }
-        group_sum(sum, q.tpg, buf);
-        const float rstd = rsqrtf(sum[0] / (float)q.gs + eps);
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int e = (at.tl + s * q.tpg) * V;
-            if (on && e < q.gs) {
+        for (int u = 0; u < U; ++u) {
+            const uint32_t row = base + u * q.rpc;
+            sum[u] = 0.f;
 #pragma unroll
-                for (int v = 0; v < V; ++v) f[s][v] *= rstd * wv[s][v] * zv[s][v] * sigmoid(zv[s][v]);
-                store_v<T, V>(out + row * dim + col + e, f[s]);
+            for (int s = 0; s < S; ++s) {
+                const int e = (at.tl + s * q.tpg) * V;
+                if (at.live && row < q.rows && e < q.gs) {
+                    float f[V];
+                    unpack(yr[u][s], f);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) sum[u] = fmaf(f[v], f[v], sum[u]);
+                }
+            }
+        }
+        group_sum(sum, q.tpg, buf, turn);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t row = base + u * q.rpc;
+            const float rstd = rsqrtf(fmaf(sum[u], q.inv, eps));
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const int e = (at.tl + s * q.tpg) * V;
+                if (at.live && row < q.rows && e < q.gs) {
+                    float f[V], zv[V];
+                    unpack(yr[u][s], f);
+                    unpack(zr[u][s], zv);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) f[v] *= (rstd * wv[s][v]) * (zv[v] * sigmoid(zv[v]));
+                    store_v<T, V>(out + (int64_t)row * dim + (col + e), f);
+                }
             }
         }
     }
 }
 
 template <typename T, int V, int S, bool kGateFirst>
-__global__ void __launch_bounds__(kMaxThr)
+__global__ void __launch_bounds__(V == 8 && S == 1 ? 768 : kMaxThr)
     k_gate_bwd(Geom q, const T *y, const T *z, int64_t z_stride, const float *__restrict__ w, float eps, const T *dout, T *dy,
                T *dz, int64_t dz_stride, float *dw_part) {
-    extern __shared__ float sm[];
-    __shared__ float buf[2][kMaxThr / 32];
+    extern __shared__ __align__(16) float sm[];
+    __shared__ SumBuf<2> buf;
+    uint32_t turn = 0;
     const Pos at(q);
-    const int dim = q.gs * q.ngroups;
+    const int dim = q.gs * q.ngroups, col = at.group * q.gs;
     float wv[S][V], dw[S][V];
     load_cols<V, S>(w, q, at, wv, 0.f);
 #pragma unroll
     for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int v = 0; v < V; ++v) dw[s][v] = 0.f;
-    for (int64_t base = (int64_t)blockIdx.y * q.rpc; base < q.rows; base += (int64_t)gridDim.y * q.rpc) {
-        const int64_t row = base + at.row_slot;
+    SSD_FOR_ROWS(q, 1) {
+        const uint32_t row = base;
         const bool on = at.live && row < q.rows;
-        const int col = at.group * q.gs;
-        float yv[S][V], zv[S][V], dv[S][V], sum[2] = {0.f, 0.f};
+        Raw<T, V> yr[S], zr[S], dr[S];
+        float sg[S][V], sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int e = (at.tl + s * q.tpg) * V;
             if (on && e < q.gs) {
-                load_v<T, V>(y + row * dim + col + e, yv[s]);
-                load_v<T, V>(z + row * z_stride + col + e, zv[s]);
-                load_v<T, V>(dout + row * dim + col + e, dv[s]);
+                yr[s] = load_raw<T, V>(y + (int64_t)row * dim + (col + e));
+                zr[s] = load_raw<T, V>(z + (int64_t)row * z_stride + (col + e));
+                dr[s] = load_raw<T, V>(dout + (int64_t)row * dim + (col + e));
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int e = (at.tl + s * q.tpg) * V;
+            if (on && e < q.gs) {
+                float yv[V], zv[V], dv[V];
+                unpack(yr[s], yv);
+                unpack(zr[s], zv);
+                unpack(dr[s], dv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float gate = zv[s][v] * sigmoid(zv[s][v]);
-                    const float a = kGateFirst ? yv[s][v] * gate : yv[s][v];  // what is normalised
-                    const float b = wv[s][v] * dv[s][v] * (kGateFirst ? 1.f : gate);  // its cotangent
+                    sg[s][v] = sigmoid(zv[v]);
+                    const float gate = zv[v] * sg[s][v];
+                    const float a = kGateFirst ? yv[v] * gate : yv[v];             // what is normalised
+                    const float b = wv[s][v] * dv[v] * (kGateFirst ? 1.f : gate);  // its cotangent
                     sum[0] = fmaf(a, a, sum[0]);
                     sum[1] = fmaf(a, b, sum[1]);
                 }
             }
         }
-        group_sum(sum, q.tpg, buf);
-        const float rstd = rsqrtf(sum[0] / (float)q.gs + eps), mean = sum[1] * rstd / (float)q.gs;
+        group_sum(sum, q.tpg, buf, turn);
+        const float rstd = rsqrtf(fmaf(sum[0], q.inv, eps)), mean = sum[1] * rstd * q.inv;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int e = (at.tl + s * q.tpg) * V;
             if (on && e < q.gs) {
-                float oy[V], oz[V];
+                float yv[V], zv[V], dv[V], oy[V], oz[V];
+                unpack(yr[s], yv);
+                unpack(zr[s], zv);
+                unpack(dr[s], dv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float sig = sigmoid(zv[s][v]), gate = zv[s][v] * sig;
-                    const float slope = sig * fmaf(zv[s][v], 1.f - sig, 1.f);
+                    const float sig = sg[s][v], gate = zv[v] * sig;
+                    const float slope = sig * fmaf(zv[v], 1.f - sig, 1.f);
                     if constexpr (kGateFirst) {
-                        const float n = yv[s][v] * gate * rstd, d = rstd * (wv[s][v] * dv[s][v] - n * mean);
-                        dw[s][v] = fmaf(dv[s][v], n, dw[s][v]);
+                        const float n = yv[v] * gate * rstd, d = rstd * (wv[s][v] * dv[v] - n * mean);
+                        dw[s][v] = fmaf(dv[v], n, dw[s][v]);
                         oy[v] = d * gate;
-                        oz[v] = d * yv[s][v] * slope;
+                        oz[v] = d * yv[v] * slope;
                     } else {
-                        const float n = yv[s][v] * rstd, dn = dv[s][v] * n;
+                        const float n = yv[v] * rstd, dn = dv[v] * n;
                         dw[s][v] = fmaf(dn, gate, dw[s][v]);
-                        oy[v] = rstd * (wv[s][v] * dv[s][v] * gate - n * mean);
+                        oy[v] = rstd * (wv[s][v] * dv[v] * gate - n * mean);
                         oz[v] = wv[s][v] * dn * slope;
                     }
                 }
-                store_v<T, V>(dy + row * dim + col + e, oy);
-                store_v<T, V>(dz + row * dz_stride + col + e, oz);
+                store_v<T, V>(dy + (int64_t)row * dim + (col + e), oy);
+                store_v<T, V>(dz + (int64_t)row * dz_stride + (col + e), oz);
             }
         }
     }
     if (dw_part) put_part<V, S>(dw, q, at, sm, dw_part);
 }
 
-// out[c] = sum over the partial rows, in order per thread row. grid (ceil(dim / 32)), (32, 32) threads.
-__global__ void k_col_sum(const float *__restrict__ part, int parts, int dim, float *__restrict__ out) {
+// out[c] = sum over the partial rows, in order per thread row; grid.y picks the first or second sum.
+// grid (ceil(dim / 32), 1 or 2), (32, 32) threads.
+__global__ void k_col_sum(const float *__restrict__ part, int parts, int dim, float *__restrict__ out0,
+                          float *__restrict__ out1) {
     __shared__ float sm[32][33];
+    float *out = blockIdx.y ? out1 : out0;
+    part += (int64_t)blockIdx.y * parts * dim;
     const int c = blockIdx.x * 32 + threadIdx.x;
     float s = 0.f;
     if (c < dim)
+#pragma unroll 4
         for (int r = threadIdx.y; r < parts; r += 32) s += part[(int64_t)r * dim + c];
     sm[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
@@ -393,10 +523,13 @@ struct Launch {
     Geom q;
     dim3 grid;
     int threads;
-    size_t smem;  // of put_part
+    size_t smem;
+    cudaError_t error;
 };
 
-Launch geom(int64_t rows, int gs, int ngroups, int V, int S) {
+// One wave of `kernel`: as many CTAs as fit on the SMs at once, each walking its share of the rows.
+template <typename K>
+Launch geom(K kernel, int64_t rows, int gs, int ngroups, int V, int S, int U, size_t smem) {
     Launch l{};
     const int nvec = (gs + V - 1) / V, need = (nvec + S - 1) / S;
     int tpg = 1;
@@ -410,30 +543,37 @@ Launch geom(int64_t rows, int gs, int ngroups, int V, int S) {
     if (rpc > rows) rpc = (int)rows;
     const int thr = (tpg * gpc * rpc + 31) / 32 * 32;
     const int gx = (ngroups + gpc - 1) / gpc;
-    const int64_t want = 148 * (2048 / thr > 1 ? 2048 / thr : 1), most = (want + gx - 1) / gx;
-    int64_t gy = (rows + rpc - 1) / rpc;
+    // the backward kernels' column sums pass through shared memory, rpc rows of gpc groups
+    l.smem = smem;
+    if (smem && l.smem < (size_t)rpc * gpc * gs * sizeof(float)) l.smem = (size_t)rpc * gpc * gs * sizeof(float);
+    l.error = l.smem > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)l.smem) : cudaSuccess;
+    int fit = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, thr, l.smem) != cudaSuccess || fit < 1) fit = 1;
+    int64_t gy = (rows + rpc * U - 1) / (rpc * U);
+    const int64_t most = 148 * fit / gx > 1 ? 148 * fit / gx : 1;
     if (gy > most) gy = most;
     if (gy > kMaxParts) gy = kMaxParts;
-    l.q = Geom{rows, gs, ngroups, tpg, gpc, rpc};
+    l.q = Geom{(uint32_t)rows, gs, ngroups, tpg, gpc, rpc, (float)(1.0 / gs)};
     l.grid = dim3((unsigned)gx, (unsigned)gy);
     l.threads = thr;
-    l.smem = (size_t)rpc * gpc * gs * sizeof(float);
     return l;
 }
 
-// Calls f with (V, S) as constants: V = 8 holds 1 or 2 vectors, V = 2 eight, V = 1 sixteen.
+// Calls f with (V, S) as constants: as few vectors per thread as the group needs.
 template <int V_, int S_>
 struct VS {
-    static constexpr int V = V_, S = S_;
+    static constexpr int V = V_, S = S_, U = V_ == 8 && S_ == 1 ? 2 : 1;
 };
 template <typename F>
 cudaError_t with_vs(int vec, int gs, F f) {
     if (vec == 8) return gs <= 8 * kMaxThr ? f(VS<8, 1>()) : f(VS<8, 2>());
-    return vec == 2 ? f(VS<2, 8>()) : f(VS<1, 16>());
+    if (vec == 2) return gs <= 4 * kMaxThr ? f(VS<2, 2>()) : f(VS<2, 8>());
+    return gs <= 4 * kMaxThr ? f(VS<1, 4>()) : f(VS<1, 16>());
 }
 
-cudaError_t col_sum(const float *part, int parts, int dim, float *out, cudaStream_t s) {
-    k_col_sum<<<(dim + 31) / 32, dim3(32, 32), 0, s>>>(part, parts, dim, out);
+// Sums of one or two partial arrays that follow one another; out1 may be NULL.
+cudaError_t col_sum(const float *part, int parts, int dim, float *out0, float *out1, cudaStream_t s) {
+    k_col_sum<<<dim3((dim + 31) / 32, out1 ? 2 : 1), dim3(32, 32), 0, s>>>(part, parts, dim, out0, out1);
     return cudaGetLastError();
 }
 
@@ -441,8 +581,10 @@ template <typename T, typename R>
 cudaError_t add_fwd(const AddNormArgs &a, cudaStream_t st) {
     const int vec = vec_of(a.dim, a.dim, a.dim, 4, {a.x, a.residual, a.res_out, a.out});
     return with_vs(vec, (int)a.dim, [&](auto vs) {
-        const Launch l = geom(a.rows, (int)a.dim, 1, vs.V, vs.S);
-        k_add_rmsnorm<T, R, vs.V, vs.S><<<l.grid, l.threads, 0, st>>>(
+        const auto kernel = k_add_rmsnorm<T, R, vs.V, vs.S, vs.U>;
+        const Launch l = geom(kernel, a.rows, (int)a.dim, 1, vs.V, vs.S, vs.U, 0);
+        if (l.error) return l.error;
+        kernel<<<l.grid, l.threads, l.smem, st>>>(
             l.q, static_cast<const T *>(a.x), static_cast<const R *>(a.residual), a.scale, a.weight, a.eps,
             static_cast<R *>(a.res_out), static_cast<T *>(a.out));
         return cudaGetLastError();
@@ -453,15 +595,17 @@ template <typename T, typename R>
 cudaError_t add_bwd(const AddNormArgs &a, const AddNormGrads &g, float *ws, cudaStream_t st) {
     const int vec = vec_of(a.dim, a.dim, a.dim, 4, {a.residual, g.dout, g.dres_in, a.x, g.dres, g.dx});
     return with_vs(vec, (int)a.dim, [&](auto vs) {
-        const Launch l = geom(a.rows, (int)a.dim, 1, vs.V, vs.S);
-        float *dw = g.dw ? ws : nullptr, *ds = g.dscale ? ws + (int64_t)l.grid.y * a.dim : nullptr;
-        k_add_rmsnorm_bwd<T, R, vs.V, vs.S><<<l.grid, l.threads, l.smem, st>>>(
+        const auto kernel = k_add_rmsnorm_bwd<T, R, vs.V, vs.S>;
+        const Launch l = geom(kernel, a.rows, (int)a.dim, 1, vs.V, vs.S, 1, 8 * (size_t)a.dim);
+        if (l.error) return l.error;
+        float *dw = g.dw ? ws : nullptr, *ds = g.dscale ? (dw ? ws + (int64_t)l.grid.y * a.dim : ws) : nullptr;
+        kernel<<<l.grid, l.threads, l.smem, st>>>(
             l.q, static_cast<const R *>(a.residual), a.weight, a.eps, static_cast<const T *>(g.dout),
             static_cast<const R *>(g.dres_in), static_cast<const T *>(a.x), a.scale, static_cast<R *>(g.dres),
             static_cast<T *>(g.dx), dw, ds);
         cudaError_t e = cudaGetLastError();
-        if (!e && dw) e = col_sum(dw, (int)l.grid.y, (int)a.dim, g.dw, st);
-        if (!e && ds) e = col_sum(ds, (int)l.grid.y, (int)a.dim, g.dscale, st);
+        if (!e && (dw || ds))
+            e = col_sum(ws, (int)l.grid.y, (int)a.dim, dw ? g.dw : g.dscale, dw ? g.dscale : nullptr, st);
         return e;
     });
 }
@@ -471,8 +615,10 @@ cudaError_t gate_fwd(const GateNormArgs &a, cudaStream_t st) {
     const int gs = (int)(a.dim / a.ngroups);
     const int vec = vec_of(gs, a.z_stride, gs, sizeof(T), {a.y, a.z, a.out});
     return with_vs(vec, gs, [&](auto vs) {
-        const Launch l = geom(a.rows, gs, (int)a.ngroups, vs.V, vs.S);
-        k_norm_gate<T, vs.V, vs.S><<<l.grid, l.threads, 0, st>>>(l.q, static_cast<const T *>(a.y),
+        const auto kernel = k_norm_gate<T, vs.V, vs.S, vs.U>;
+        const Launch l = geom(kernel, a.rows, gs, (int)a.ngroups, vs.V, vs.S, vs.U, 0);
+        if (l.error) return l.error;
+        kernel<<<l.grid, l.threads, l.smem, st>>>(l.q, static_cast<const T *>(a.y),
                                                                  static_cast<const T *>(a.z), a.z_stride, a.weight, a.eps,
                                                                  static_cast<T *>(a.out));
         return cudaGetLastError();
@@ -484,13 +630,15 @@ cudaError_t gate_bwd(const GateNormArgs &a, const GateNormGrads &g, float *ws, c
     const int gs = (int)(a.dim / a.ngroups);
     const int vec = vec_of(gs, a.z_stride, g.dz_stride, sizeof(T), {a.y, a.z, g.dout, g.dy, g.dz});
     return with_vs(vec, gs, [&](auto vs) {
-        const Launch l = geom(a.rows, gs, (int)a.ngroups, vs.V, vs.S);
+        const auto kernel = k_gate_bwd<T, vs.V, vs.S, kGateFirst>;
+        const Launch l = geom(kernel, a.rows, gs, (int)a.ngroups, vs.V, vs.S, 1, 4);
+        if (l.error) return l.error;
         float *dw = g.dw ? ws : nullptr;
-        k_gate_bwd<T, vs.V, vs.S, kGateFirst><<<l.grid, l.threads, l.smem, st>>>(
+        kernel<<<l.grid, l.threads, l.smem, st>>>(
             l.q, static_cast<const T *>(a.y), static_cast<const T *>(a.z), a.z_stride, a.weight, a.eps,
             static_cast<const T *>(g.dout), static_cast<T *>(g.dy), static_cast<T *>(g.dz), g.dz_stride, dw);
         cudaError_t e = cudaGetLastError();
-        if (!e && dw) e = col_sum(dw, (int)l.grid.y, (int)a.dim, g.dw, st);
+        if (!e && dw) e = col_sum(dw, (int)l.grid.y, (int)a.dim, g.dw, nullptr, st);
         return e;
     });
 }
