@@ -406,39 +406,54 @@ def ssd_gated_rmsnorm(y, z, weight, *, ngroups, eps=1e-5, out=None, stream=None)
 
 
 def _need(name, t, shape, dtype, dev):
-    """t (None passes) has this shape and type, is contiguous and on `dev`."""
-    if t is None:
+    """t (None passes) has this shape and type, is contiguous and on `dev` (a CUDA device's index)."""
+    if t is None or (t.get_device() == dev >= 0 and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
         return
-    if t.device != dev or t.device.type != "cuda":
-        raise ValueError(f"{name}: libssd takes CUDA tensors on one device (got {t.device}, expected {dev})")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name}: libssd takes CUDA tensors on one device (got {t.device})")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: libssd takes contiguous tensors")
+    raise ValueError(f"{name}: libssd takes contiguous tensors")
 
 
 class _On:
-    """The calls within run with `dev` current and allocate on `stream` (None: the device's current
-    stream), so that memory freed afterwards is not handed out again before the kernels are done."""
+    """The calls within run with device `dev` current and allocate on `stream` (None: the device's
+    current stream), so that memory freed afterwards is not handed out again before the kernels are
+    done. Enters with the stream's handle."""
+
+    __slots__ = ("dev", "stream", "ctx")
 
     def __init__(self, dev, stream):
-        self.dev, self.stream = dev, stream
-        self.ctx = None
+        self.dev, self.stream, self.ctx = dev, stream, None
 
     def __enter__(self):
         if self.stream is not None:
             self.ctx = torch.cuda.stream(self.stream)
-        elif self.dev.index is not None and self.dev.index != torch.cuda.current_device():
+        elif self.dev != torch.cuda.current_device():
             self.ctx = torch.cuda.device(self.dev)
         if self.ctx is not None:
             self.ctx.__enter__()
-        return ctypes.c_void_p((self.stream or torch.cuda.current_stream(self.dev)).cuda_stream)
+        if self.stream is not None:
+            return self.stream.cuda_stream
+        return _raw_stream(self.dev)
 
     def __exit__(self, *e):
         if self.ctx is not None:
             self.ctx.__exit__(*e)
+
+
+def _raw_stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# the handle alone where torch offers it: a fifteenth of the time, and it counts for single tokens
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _delta_shape(x, g, beta, B, C, batched):
@@ -446,7 +461,7 @@ def _delta_shape(x, g, beta, B, C, batched):
     lead = x.dim() - 2
     if x.dim() != (4 if batched else 3) or B.dim() != x.dim():
         raise ValueError("x and B: wrong number of dimensions")
-    dev, dt = x.device, x.dtype
+    dev, dt = x.get_device(), x.dtype
     code = _dtype_code(x)
     H, P = x.shape[-2:]
     G, N = B.shape[-2:]
@@ -479,7 +494,7 @@ def delta_bwd_plan(batch, seqlen, nheads, headdim, ngroups, dstate, dtype_code) 
 def _workspace(workspace, need, dev):
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
-    if workspace.device != dev or not workspace.is_contiguous():
+    if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace: a contiguous tensor on the inputs' device")
     return workspace
 
@@ -493,7 +508,7 @@ def ssd_delta_fwd(x, g, beta, B, C, h0=None, *, y=None, h_final=None, return_fin
     """y, h_final of the gated delta rule: x [B,L,H,P], g (log decay) and beta [B,L,H], B (keys) and
     C (queries) [B,L,G,N], h0 [B,H,P,N] f32."""
     shape, code = _delta_shape(x, g, beta, B, C, True)
-    dev = x.device
+    dev = x.get_device()
     state = torch.Size((shape.batch, shape.nheads, shape.headdim, shape.dstate))
     _need("h0", h0, state, torch.float32, dev)
     _need("y", y, x.shape, x.dtype, dev)
@@ -504,8 +519,8 @@ def ssd_delta_fwd(x, g, beta, B, C, h0=None, *, y=None, h_final=None, return_fin
         if h_final is None and return_final_state:
             h_final = torch.empty(state, dtype=torch.float32, device=dev)
         ws = _workspace(workspace, _delta_plan("ssd_delta_fwd_plan", shape, code).workspace_bytes, dev)
-        _check(lib().ssd_delta_fwd(ctypes.byref(shape), code, _ptr(x), _ptr(g), _ptr(beta), _ptr(B), _ptr(C), _ptr(h0),
-                                   _ptr(y), _ptr(h_final), _ptr(ws), _bytes(ws), st), "ssd_delta_fwd")
+        _check(lib().ssd_delta_fwd(ctypes.byref(shape), code, _at(x), _at(g), _at(beta), _at(B), _at(C), _at(h0),
+                                   _at(y), _at(h_final), _at(ws), _bytes(ws), st), "ssd_delta_fwd")
     return y, h_final
 
 
@@ -513,7 +528,7 @@ def ssd_delta_decode_step(state, x, g, beta, B, C, *, state_out=None, y=None, st
     """y [B,H,P] of one token of the gated delta rule; x [B,H,P], g and beta [B,H], B, C [B,G,N]. The
     state [B,H,P,N] f32 is updated in place, or left alone and the new one written to state_out."""
     shape, code = _delta_shape(x, g, beta, B, C, False)
-    dev = x.device
+    dev = x.get_device()
     size = torch.Size((shape.batch, shape.nheads, shape.headdim, shape.dstate))
     _need("state", state, size, torch.float32, dev)
     _need("state_out", state_out, size, torch.float32, dev)
@@ -521,9 +536,9 @@ def ssd_delta_decode_step(state, x, g, beta, B, C, *, state_out=None, y=None, st
     with _On(dev, stream) as st:
         if y is None:
             y = torch.empty_like(x)
-        _check(lib().ssd_delta_decode_step(ctypes.byref(shape), code, _ptr(state),
-                                           _ptr(state if state_out is None else state_out), _ptr(x), _ptr(g), _ptr(beta),
-                                           _ptr(B), _ptr(C), _ptr(y), st), "ssd_delta_decode_step")
+        _check(lib().ssd_delta_decode_step(ctypes.byref(shape), code, _at(state),
+                                           _at(state if state_out is None else state_out), _at(x), _at(g), _at(beta),
+                                           _at(B), _at(C), _at(y), st), "ssd_delta_decode_step")
     return y
 
 
@@ -533,7 +548,7 @@ def ssd_delta_bwd(x, g, beta, B, C, h0, dy, dh_final=None, *, want_dh0: bool = T
     Returns a dict dx, dg, dbeta, dB, dC, dh0 (None unless want_dh0); `out` may supply any of those
     tensors to write into."""
     shape, code = _delta_shape(x, g, beta, B, C, True)
-    dev = x.device
+    dev = x.get_device()
     state = torch.Size((shape.batch, shape.nheads, shape.headdim, shape.dstate))
     _need("h0", h0, state, torch.float32, dev)
     _need("dy", dy, x.shape, x.dtype, dev)
@@ -548,9 +563,9 @@ def ssd_delta_bwd(x, g, beta, B, C, h0, dy, dh_final=None, *, want_dh0: bool = T
         if o.get("dh0") is None:
             o["dh0"] = torch.empty(state, dtype=torch.float32, device=dev) if want_dh0 else None
         ws = _workspace(workspace, _delta_plan("ssd_delta_bwd_plan", shape, code).workspace_bytes, dev)
-        _check(lib().ssd_delta_bwd(ctypes.byref(shape), code, _ptr(x), _ptr(g), _ptr(beta), _ptr(B), _ptr(C), _ptr(h0),
-                                   _ptr(dy), _ptr(dh_final), _ptr(o["dx"]), _ptr(o["dg"]), _ptr(o["dbeta"]), _ptr(o["dB"]),
-                                   _ptr(o["dC"]), _ptr(o["dh0"]), _ptr(ws), _bytes(ws), st), "ssd_delta_bwd")
+        _check(lib().ssd_delta_bwd(ctypes.byref(shape), code, _at(x), _at(g), _at(beta), _at(B), _at(C), _at(h0),
+                                   _at(dy), _at(dh_final), _at(o["dx"]), _at(o["dg"]), _at(o["dbeta"]), _at(o["dB"]),
+                                   _at(o["dC"]), _at(o["dh0"]), _at(ws), _bytes(ws), st), "ssd_delta_bwd")
     return o
 
 
@@ -565,7 +580,7 @@ def ssd_add_rmsnorm(x, residual, weight, *, scale=None, eps=1e-5, res_out=None, 
 
     residual (None = 0) is in x's type or fp32, weight and scale (None = 1) are fp32. res_out may be
     residual itself. want_res=False (and no res_out given) returns None for r."""
-    dev, dim = x.device, x.shape[-1] if x.dim() else 0
+    dev, dim = x.get_device(), x.shape[-1] if x.dim() else 0
     rdt = next((t.dtype for t in (residual, res_out) if t is not None), x.dtype)
     _need("x", x, x.shape, x.dtype, dev)
     _need("residual", residual, x.shape, rdt, dev)
@@ -579,8 +594,8 @@ def ssd_add_rmsnorm(x, residual, weight, *, scale=None, eps=1e-5, res_out=None, 
         if out is None:
             out = torch.empty_like(x)
         _check(lib().ssd_add_rmsnorm(x.numel() // dim if dim else 0, dim, _dtype_code(x), SSD_F32 if rdt == torch.float32 else
-                                     SSD_BF16, _ptr(x), _ptr(residual), _ptr(scale), _ptr(weight), float(eps), _ptr(res_out),
-                                     _ptr(out), st), "ssd_add_rmsnorm")
+                                     SSD_BF16, _at(x), _at(residual), _at(scale), _at(weight), float(eps), _at(res_out),
+                                     _at(out), st), "ssd_add_rmsnorm")
     return res_out, out
 
 
@@ -591,7 +606,7 @@ def ssd_add_rmsnorm_bwd(res, weight, dout, dres_in=None, *, x=None, scale=None, 
     Returns a dict dres (the residual's), dx, dw (None unless want_dw), dscale (None unless scale and
     the forward's x are given); `out` may supply any of those tensors to write into (dres may be
     dres_in, dx may be dout)."""
-    dev, dim = dout.device, dout.shape[-1] if dout.dim() else 0
+    dev, dim = dout.get_device(), dout.shape[-1] if dout.dim() else 0
     _need("dout", dout, dout.shape, dout.dtype, dev)
     _need("res", res, dout.shape, res.dtype, dev)
     _need("dres_in", dres_in, dout.shape, res.dtype, dev)
@@ -610,16 +625,16 @@ def ssd_add_rmsnorm_bwd(res, weight, dout, dres_in=None, *, x=None, scale=None, 
                 o[name] = torch.empty(shape, dtype=dt, device=dev) if want else None
         sums = o["dw"] is not None or o["dscale"] is not None
         ws = _workspace(workspace, norm_bwd_workspace_bytes(rows, dim) if sums else 0, dev)
-        _check(lib().ssd_add_rmsnorm_bwd(rows, dim, code, rcode, _ptr(res), _ptr(weight), float(eps), _ptr(dout),
-                                         _ptr(dres_in), _ptr(x), _ptr(scale), _ptr(o["dres"]), _ptr(o["dx"]), _ptr(o["dw"]),
-                                         _ptr(o["dscale"]), _ptr(ws), _bytes(ws), st), "ssd_add_rmsnorm_bwd")
+        _check(lib().ssd_add_rmsnorm_bwd(rows, dim, code, rcode, _at(res), _at(weight), float(eps), _at(dout),
+                                         _at(dres_in), _at(x), _at(scale), _at(o["dres"]), _at(o["dx"]), _at(o["dw"]),
+                                         _at(o["dscale"]), _at(ws), _bytes(ws), st), "ssd_add_rmsnorm_bwd")
     return o
 
 
 def _rows_view(name, t, like, dev):
     """The row stride of t [..., dim], a column slice of evenly spaced wider rows."""
-    if t.device != dev or t.dtype != like.dtype or t.shape != like.shape:
-        raise ValueError(f"{name}: expected {tuple(like.shape)} {like.dtype} on {dev}")
+    if t.get_device() != dev or t.dtype != like.dtype or t.shape != like.shape:
+        raise ValueError(f"{name}: expected {tuple(like.shape)} {like.dtype} on one device")
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: row views need unit column stride")
     row = None
@@ -636,7 +651,7 @@ def _rows_view(name, t, like, dev):
 def ssd_norm_gate(y, z, weight, *, ngroups, eps=1e-5, out=None, stream=None):
     """out = weight * RMSNorm over `ngroups` groups of y * silu(z) (the norm first, then the gate);
     y [..., dim] contiguous, z [..., dim] may be a column slice of wider rows."""
-    dev, dim = y.device, y.shape[-1] if y.dim() else 0
+    dev, dim = y.get_device(), y.shape[-1] if y.dim() else 0
     _need("y", y, y.shape, y.dtype, dev)
     _need("weight", weight, (dim,), torch.float32, dev)
     _need("out", out, y.shape, y.dtype, dev)
@@ -644,13 +659,13 @@ def ssd_norm_gate(y, z, weight, *, ngroups, eps=1e-5, out=None, stream=None):
     with _On(dev, stream) as st:
         if out is None:
             out = torch.empty_like(y)
-        _check(lib().ssd_norm_gate(y.numel() // dim if dim else 0, dim, ngroups, _dtype_code(y), _ptr(y), _ptr(z), zs,
-                                   _ptr(weight), float(eps), _ptr(out), st), "ssd_norm_gate")
+        _check(lib().ssd_norm_gate(y.numel() // dim if dim else 0, dim, ngroups, _dtype_code(y), _at(y), _at(z), zs,
+                                   _at(weight), float(eps), _at(out), st), "ssd_norm_gate")
     return out
 
 
 def _gate_norm_bwd(fn, y, z, weight, dout, ngroups, eps, want_dw, out, workspace, stream):
-    dev, dim = y.device, y.shape[-1] if y.dim() else 0
+    dev, dim = y.get_device(), y.shape[-1] if y.dim() else 0
     _need("y", y, y.shape, y.dtype, dev)
     _need("weight", weight, (dim,), torch.float32, dev)
     _need("dout", dout, y.shape, y.dtype, dev)
@@ -668,8 +683,8 @@ def _gate_norm_bwd(fn, y, z, weight, dout, ngroups, eps, want_dw, out, workspace
             o["dw"] = torch.empty(dim, dtype=torch.float32, device=dev) if want_dw else None
         dzs = _rows_view("dz", o["dz"], y, dev)
         ws = _workspace(workspace, norm_bwd_workspace_bytes(rows, dim) if o["dw"] is not None else 0, dev)
-        _check(getattr(lib(), fn)(rows, dim, ngroups, _dtype_code(y), _ptr(y), _ptr(z), zs, _ptr(weight), float(eps),
-                                  _ptr(dout), _ptr(o["dy"]), _ptr(o["dz"]), dzs, _ptr(o["dw"]), _ptr(ws), _bytes(ws), st), fn)
+        _check(getattr(lib(), fn)(rows, dim, ngroups, _dtype_code(y), _at(y), _at(z), zs, _at(weight), float(eps),
+                                  _at(dout), _at(o["dy"]), _at(o["dz"]), dzs, _at(o["dw"]), _at(ws), _bytes(ws), st), fn)
     return o
 
 

@@ -190,7 +190,7 @@ def test_binding_refuses_wrong_tensors():
 def test_row_views():
     like = torch.zeros(3, 4, 8)
     wide = torch.zeros(3, 4, 20)
-    cpu = like.device
+    cpu = like.get_device()
     assert B._rows_view("z", wide[..., 5:13], like, cpu) == 20
     assert B._rows_view("z", like, like, cpu) == 8
     assert B._rows_view("z", wide[:1, :1, :8], like[:1, :1], cpu) == 8
