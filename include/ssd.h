@@ -399,11 +399,19 @@ ssd_status_t ssd_gated_rmsnorm(int64_t rows, int64_t dim, int64_t ngroups, ssd_d
  *   y        [B, L, H, P]   dtype          output
  *   h_final  [B, H, P, N]   fp32 or NULL   state after the last token
  * Outputs may not overlap inputs. seqlen == 0 writes only h_final; batch == 0 does nothing.
+ * ssd_delta_fwd_plan: SSD_PATH_TCGEN05 (bf16 with dstate <= 128, dstate and headdim multiples of 8 and
+ * at least 8 tokens: chunks of 64 tokens on tensor cores, what enters the state kept to 2^-16) or
+ * SSD_PATH_SIMT (everything else: token by token in fp32). On SSD_PATH_TCGEN05 the warps of a CTA
+ * wait on one another through bounded waits, as in ssd_fwd; ssd_delta_status, called with the
+ * shape and workspace of an ssd_delta_fwd or ssd_delta_bwd, synchronizes `stream` and returns
+ * SSD_ERR_TIMEOUT if one ran out (outputs are then incomplete), SSD_ERR_CUDA or SSD_OK.
  */
 ssd_status_t ssd_delta_fwd_plan(const ssd_shape_t *shape, ssd_dtype_t dtype, ssd_plan_t *plan);
 ssd_status_t ssd_delta_fwd(const ssd_shape_t *shape, ssd_dtype_t dtype, const void *x, const void *g, const void *beta,
                            const void *Bm, const void *Cm, const float *h0, void *y, float *h_final, void *workspace,
                            size_t workspace_bytes, void *stream);
+
+ssd_status_t ssd_delta_status(const ssd_shape_t *shape, ssd_dtype_t dtype, const void *workspace, void *stream);
 
 /*
  * One generated token of the gated delta rule: state_out = the state after the token, y = its

@@ -63,6 +63,7 @@ _SIGS = {
                 ctypes.c_int),
     "ssd_delta_fwd_plan": ([ctypes.POINTER(ShapeT), ctypes.c_int, ctypes.POINTER(PlanT)], ctypes.c_int),
     "ssd_delta_fwd": ([ctypes.POINTER(ShapeT), ctypes.c_int] + [_vp] * 9 + [_sz, _vp], ctypes.c_int),
+    "ssd_delta_status": ([ctypes.POINTER(ShapeT), ctypes.c_int, _vp, _vp], ctypes.c_int),
     "ssd_delta_decode_step": ([ctypes.POINTER(ShapeT), ctypes.c_int] + [_vp] * 9, ctypes.c_int),
     "ssd_delta_bwd_plan": ([ctypes.POINTER(ShapeT), ctypes.c_int, ctypes.POINTER(PlanT)], ctypes.c_int),
     "ssd_delta_bwd": ([ctypes.POINTER(ShapeT), ctypes.c_int] + [_vp] * 15 + [_sz, _vp], ctypes.c_int),
@@ -430,6 +431,8 @@ class _On:
 
     def __enter__(self):
         if self.stream is not None:
+            if self.stream.device.index != self.dev:
+                raise ValueError("stream: of another device than the tensors")
             self.ctx = torch.cuda.stream(self.stream)
         elif self.dev != torch.cuda.current_device():
             self.ctx = torch.cuda.device(self.dev)
@@ -480,7 +483,7 @@ def _delta_plan(fn, shape, code):
 
 
 def delta_fwd_plan(batch, seqlen, nheads, headdim, ngroups, dstate, dtype_code) -> dict:
-    """{'path': 'simt'|'mma'|'none', 'kernels': launches per call, 'workspace_bytes': int}."""
+    """{'path': 'simt'|'tcgen05'|'none', 'kernels': launches per call, 'workspace_bytes': int}."""
     out = _delta_plan("ssd_delta_fwd_plan", ShapeT(batch, seqlen, nheads, headdim, ngroups, dstate), dtype_code)
     return {"path": PATHS.get(out.path, str(out.path)), "kernels": out.kernels, "workspace_bytes": out.workspace_bytes}
 
@@ -522,6 +525,14 @@ def ssd_delta_fwd(x, g, beta, B, C, h0=None, *, y=None, h_final=None, return_fin
         _check(lib().ssd_delta_fwd(ctypes.byref(shape), code, _at(x), _at(g), _at(beta), _at(B), _at(C), _at(h0),
                                    _at(y), _at(h_final), _at(ws), _bytes(ws), st), "ssd_delta_fwd")
     return y, h_final
+
+
+def delta_status(shape_args, dtype_code, workspace, stream=None) -> int:
+    """Raw ssd_delta_status code for the last ssd_delta_fwd or ssd_delta_bwd on `workspace`
+    (synchronizes the stream). shape_args = (batch, seqlen, nheads, headdim, ngroups, dstate)."""
+    dev = workspace.get_device() if workspace is not None else torch.cuda.current_device()
+    with _On(dev, stream) as st:
+        return lib().ssd_delta_status(ctypes.byref(ShapeT(*shape_args)), dtype_code, _at(workspace), st)
 
 
 def ssd_delta_decode_step(state, x, g, beta, B, C, *, state_out=None, y=None, stream=None):

@@ -401,7 +401,7 @@ ssd_plan_t delta_plan_of(const ssd::DeltaProblem &p, bool backward) {
     if (p.B == 0 || p.L == 0) {
         out.path = SSD_PATH_NONE;
     } else if (delta_mma_supported(p)) {
-        out.path = SSD_PATH_MMA;
+        out.path = SSD_PATH_TCGEN05;
         out.kernels = backward ? delta_mma_bwd_kernels(p) : 2;
         out.workspace_bytes = backward ? delta_mma_bwd_workspace_bytes(p) : delta_mma_fwd_workspace_bytes(p);
     } else {
@@ -437,6 +437,20 @@ SSD_API ssd_status_t ssd_delta_bwd_plan(const ssd_shape_t *shape, ssd_dtype_t dt
     return SSD_OK;
 }
 
+SSD_API ssd_status_t ssd_delta_status(const ssd_shape_t *shape, ssd_dtype_t dtype, const void *workspace, void *stream) {
+    DeltaProblem p;
+    const ssd_status_t st = make_delta(shape, dtype, &p);
+    if (st != SSD_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cudaStreamSynchronize(s) != cudaSuccess) return SSD_ERR_CUDA;
+    if (delta_plan_of(p, false).path != SSD_PATH_TCGEN05) return SSD_OK;  // the other paths have no waits
+    if (!workspace) return SSD_ERR_INVALID_ARG;
+    int32_t word = 0;
+    if (cudaMemcpy(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return SSD_ERR_CUDA;
+    if (word & 1) return SSD_ERR_TIMEOUT;
+    return word ? SSD_ERR_CUDA : SSD_OK;
+}
+
 SSD_API ssd_status_t ssd_delta_fwd(const ssd_shape_t *shape, ssd_dtype_t dtype, const void *x, const void *g,
                                    const void *beta, const void *Bm, const void *Cm, const float *h0, void *y,
                                    float *h_final, void *workspace, size_t workspace_bytes, void *stream) {
@@ -460,7 +474,7 @@ SSD_API ssd_status_t ssd_delta_fwd(const ssd_shape_t *shape, ssd_dtype_t dtype, 
     p.h0 = h0;
     p.y = y;
     p.h_final = h_final;
-    return from_cuda(plan.path == SSD_PATH_MMA ? delta_mma_fwd(p, workspace, s) : delta_seq_fwd(p, s));
+    return from_cuda(plan.path == SSD_PATH_TCGEN05 ? delta_mma_fwd(p, workspace, s) : delta_seq_fwd(p, s));
 }
 
 SSD_API ssd_status_t ssd_delta_decode_step(const ssd_shape_t *shape, ssd_dtype_t dtype, const float *state,
@@ -512,7 +526,7 @@ SSD_API ssd_status_t ssd_delta_bwd(const ssd_shape_t *shape, ssd_dtype_t dtype, 
     p.Cm = Cm;
     p.h0 = h0;
     const DeltaGrads gr{dy, dh_final, dx, dg, dbeta, dBm, dCm, dh0};
-    return from_cuda(plan.path == SSD_PATH_MMA ? delta_mma_bwd(p, gr, workspace, s) : delta_seq_bwd(p, gr, workspace, s));
+    return from_cuda(plan.path == SSD_PATH_TCGEN05 ? delta_mma_bwd(p, gr, workspace, s) : delta_seq_bwd(p, gr, workspace, s));
 }
 
 // ---- norms before and after a block -------------------------------------------------

@@ -45,6 +45,17 @@ size_t delta_mma_bwd_workspace_bytes(const DeltaProblem &p);
 int delta_mma_bwd_kernels(const DeltaProblem &p);
 cudaError_t delta_mma_bwd(const DeltaProblem &p, const DeltaGrads &g, void *ws, cudaStream_t s);
 
+// The chain over the chunks on tcgen05 (ssd_delta_tc.cu), after k_delta_prep. With states set it is the
+// backward pass's recomputation: states [B, H, chunks, P, N], err and u [B, L, H, P], bf16, instead of y.
+struct DeltaChain {
+    const char *prep;
+    int64_t prep_bytes;  // per chunk and head
+    int scal_at, p_at;   // where the scalars and the masked Q K^T stand in it
+    int *status;
+    void *states, *err, *u;
+};
+cudaError_t delta_tc_chain(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s);
+
 // one token (p.L, p.h0, p.h_final unused); state_out may be state_in
 cudaError_t delta_step(const DeltaProblem &p, const float *state_in, float *state_out, cudaStream_t s);
 

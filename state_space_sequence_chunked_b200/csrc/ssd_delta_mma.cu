@@ -198,7 +198,8 @@ __device__ __forceinline__ void put_w(char *out, int at, int lane, const float (
 template <int NT, bool BWD>
 __global__ void __launch_bounds__(kThr)
     k_delta_prep(const __nv_bfloat16 *__restrict__ Bm, const __nv_bfloat16 *__restrict__ Cm, const __nv_bfloat16 *__restrict__ g,
-                 const __nv_bfloat16 *__restrict__ beta, int64_t L, int H, int G, int N, int slices, char *__restrict__ ws) {
+                 const __nv_bfloat16 *__restrict__ beta, int64_t L, int H, int G, int N, int slices, char *__restrict__ ws,
+                 int *__restrict__ status) {
     extern __shared__ __align__(128) char raw[];
     PrepSmem<NT> &sm = *reinterpret_cast<PrepSmem<NT> *>(raw);
     using Lay = Prep<BWD>;
@@ -207,6 +208,7 @@ __global__ void __launch_bounds__(kThr)
     const int grp = blockIdx.y / slices, slice = blockIdx.y % slices, per = H / G;
     const int h_begin = grp * per + per * slice / slices, h_end = grp * per + per * (slice + 1) / slices;
     const uint32_t ka = smem_addr(sm.k), qa = smem_addr(sm.q);
+    if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) *status = 0;
     load_tile<NT / 8>(ka, Bm, b, L, t0, G, grp, N, 0);
     load_tile<NT / 8>(qa, Cm, b, L, t0, G, grp, N, 0);
     cp_commit();
@@ -397,25 +399,6 @@ __global__ void __launch_bounds__(kThr)
     }
 }
 
-// ---------------------------------------------------------------------------------------------
-// k_delta_chain: grid (ceil(P / 64), H, B), a warp per 16 state rows, two stages of a chunk's operands
-// loaded ahead with cp.async. kStore is the backward pass's recomputation: no Y, but the state entering
-// each chunk, err and u, each rounded to bf16 once (they are operands of products there).
-template <int NT, bool kStore>
-struct ChainStage {
-    __nv_bfloat16 k[kC * NT];
-    __nv_bfloat16 q[kC * NT];  // kStore: the entering state on its way out
-    __nv_bfloat16 x[kC * kRowsCta];
-    static constexpr int prep_bytes = kStore ? Prep<true>::WT : Prep<false>::bytes;
-    char prep[prep_bytes];
-};
-
-// What the backward pass keeps per chunk: states [B, H, chunks, P, N], the others [B, L, H, P].
-struct ChainOut {
-    __nv_bfloat16 *y, *states, *err, *u;
-    float *h_final;
-};
-
 // Accumulators T^T (16 state rows x 64 tokens), rounded, over this warp's columns of a [token][row]
 // tile and from there to rows of `dst` ([B, L, H, P]).
 __device__ __forceinline__ void put_tokens(const float (&T)[8][4], char *tile, __nv_bfloat16 *__restrict__ dst, int64_t b,
@@ -513,151 +496,6 @@ __device__ __forceinline__ void rank16(float (&S)[NT / 8][4], const uint32_t (&h
         mma(S[2 * j], hi, f[0], f[1]);
         mma(S[2 * j + 1], hi, f[2], f[3]);
     }
-}
-
-template <int NT, bool kStore>
-__global__ void __launch_bounds__(kThr, 2)
-    k_delta_chain(const __nv_bfloat16 *__restrict__ x, const __nv_bfloat16 *__restrict__ Bm, const __nv_bfloat16 *__restrict__ Cm,
-                  const float *__restrict__ h0, const char *__restrict__ ws, int64_t L, int H, int P, int G, int N,
-                  const ChainOut out) {
-    extern __shared__ __align__(128) char raw[];
-    using Stage = ChainStage<NT, kStore>;
-    using Lay = Prep<kStore>;
-    Stage *stages = reinterpret_cast<Stage *>(raw);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tg = lane & 3;
-    const int h = blockIdx.y, grp = h / (H / G), pc = blockIdx.x * kRowsCta, p0 = pc + 16 * warp;
-    const int64_t b = blockIdx.z, nc = (L + kC - 1) / kC;
-    const bool on = p0 < P;  // a warp with rows
-    const char *prep = ws + (b * H + h) * nc * (int64_t)Lay::bytes;
-
-    const auto load = [&](int64_t c) {
-        Stage &st = stages[c & 1];
-        load_tile<NT / 8>(smem_addr(st.k), Bm, b, L, c * kC, G, grp, N, 0);
-        if constexpr (!kStore) load_tile<NT / 8>(smem_addr(st.q), Cm, b, L, c * kC, G, grp, N, 0);
-        load_tile<kRowsCta / 8>(smem_addr(st.x), x, b, L, c * kC, H, h, P, pc);
-        const uint32_t dst = smem_addr(st.prep);
-        for (int i = tid; i < Stage::prep_bytes / 16; i += kThr) cp16(dst + 16 * i, prep + c * Lay::bytes + 16 * i, true);
-        cp_commit();
-    };
-    load(0);
-
-    // state rows p0 + gr and p0 + gr + 8, columns 8 j + 2 tg and + 1
-    float S[NT / 8][4];
-    const int64_t row = (b * H + h) * (int64_t)P + p0 + gr;
-    load_state<NT>(S, h0, row, P, N, p0 + gr, tg);
-
-    for (int64_t c = 0; c < nc; ++c) {
-        if (c + 1 < nc) {
-            load(c + 1);
-            cp_wait<1>();
-        } else {
-            cp_wait<0>();
-        }
-        __syncthreads();
-        Stage &st = stages[c & 1];
-        if (on) {
-            const uint32_t ka = smem_addr(st.k), qa = smem_addr(st.q), xa = smem_addr(st.x);
-            const uint4 *wf = reinterpret_cast<const uint4 *>(st.prep + Lay::W) + lane;
-            const float *eg = reinterpret_cast<const float *>(st.prep + Lay::scal), *ek = eg + kC, *bt = eg + 2 * kC;
-            if constexpr (kStore)
-                put_state<NT>(S, reinterpret_cast<char *>(st.q), out.states + ((b * H + h) * nc + c) * (int64_t)P * N, P, N, pc, warp, lane);
-            float R[8][4], Y[8][4];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) R[j][e] = Y[j][e] = 0.f;
-            // S K^T and S Q^T
-#pragma unroll
-            for (int s = 0; s < NT / 16; ++s) {
-                uint32_t hi[4], lo[4];
-                split_a(S[2 * s], S[2 * s + 1], hi, lo);
-#pragma unroll
-                for (int jj = 0; jj < 4; ++jj) {
-                    uint32_t bk[4];
-                    const uint32_t off = at16<NT * 2>(16 * jj + (lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1));
-                    ldsm4(bk, ka + off);
-                    mma(R[2 * jj], lo, bk[0], bk[1]);
-                    mma(R[2 * jj + 1], lo, bk[2], bk[3]);
-                    if constexpr (!kStore) {
-                        uint32_t bq[4];
-                        ldsm4(bq, qa + off);
-                        mma(Y[2 * jj], hi, bq[0], bq[1]);
-                        mma(Y[2 * jj + 1], hi, bq[2], bq[3]);
-                    }
-                    mma(R[2 * jj], hi, bk[0], bk[1]);
-                    mma(R[2 * jj + 1], hi, bk[2], bk[3]);
-                }
-            }
-            // R = X - exp(cum) S K^T, and exp(cum) S Q^T
-#pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-                uint32_t xf[4];
-                ldsm4t(xf, xa + at16<kRowsCta * 2>(16 * jj + (lane & 7) + ((lane >> 4) << 3), 2 * warp + ((lane >> 3) & 1)));
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const int j = 2 * jj + n;
-                    const float2 e = *reinterpret_cast<const float2 *>(eg + 8 * j + 2 * tg);
-                    R[j][0] = fmaf(-e.x, R[j][0], low(xf[2 * n]));
-                    R[j][1] = fmaf(-e.y, R[j][1], high(xf[2 * n]));
-                    R[j][2] = fmaf(-e.x, R[j][2], low(xf[2 * n + 1]));
-                    R[j][3] = fmaf(-e.y, R[j][3], high(xf[2 * n + 1]));
-                }
-            }
-            if constexpr (!kStore) scale_tokens(Y, eg, tg);
-            // err = R + W (beta R); beta R is taken of the whole chunk first, so R can take the sums in place
-            uint32_t ah[4][4], al[4][4];
-#pragma unroll
-            for (int bb = 0; bb < 4; ++bb) split_tokens(R, bb, bt, 1.f, tg, ah[bb], al[bb]);
-#pragma unroll
-            for (int a = 0; a < 4; ++a)
-#pragma unroll
-                for (int bb = 0; bb <= a; ++bb) {
-                    const uint4 wh = wf[block_at(a, bb) * 64], wl = wf[block_at(a, bb) * 64 + 32];
-                    mma(R[2 * a], al[bb], wh.x, wh.y);
-                    mma(R[2 * a + 1], al[bb], wh.z, wh.w);
-                    mma(R[2 * a], ah[bb], wl.x, wl.y);
-                    mma(R[2 * a + 1], ah[bb], wl.z, wl.w);
-                    mma(R[2 * a], ah[bb], wh.x, wh.y);
-                    mma(R[2 * a + 1], ah[bb], wh.z, wh.w);
-                }
-            if constexpr (kStore)
-                put_tokens(R, reinterpret_cast<char *>(st.x), out.err, b, L, c * kC, H, h, P, pc, warp, lane);
-            scale_tokens(R, bt, tg);  // u = beta err
-            if constexpr (kStore) {
-                put_tokens(R, reinterpret_cast<char *>(st.x), out.u, b, L, c * kC, H, h, P, pc, warp, lane);
-            } else {  // Y += tril(Q K^T o E) u
-                const uint4 *pf = reinterpret_cast<const uint4 *>(st.prep + Prep<false>::P) + lane;
-#pragma unroll
-                for (int bb = 0; bb < 4; ++bb) {
-                    uint32_t hi[4], lo[4];
-                    split_a(R[2 * bb], R[2 * bb + 1], hi, lo);
-#pragma unroll
-                    for (int a = bb; a < 4; ++a) {
-                        const uint4 f = pf[block_at(a, bb) * 32];
-                        mma(Y[2 * a], lo, f.x, f.y);
-                        mma(Y[2 * a + 1], lo, f.z, f.w);
-                        mma(Y[2 * a], hi, f.x, f.y);
-                        mma(Y[2 * a + 1], hi, f.z, f.w);
-                    }
-                }
-                put_tokens(Y, reinterpret_cast<char *>(st.x), out.y, b, L, c * kC, H, h, P, pc, warp, lane);
-            }
-            // S <- exp(cum_end) S + (exp(cum_end - cum) u)^T K
-            const float gamma = eg[kC - 1];
-#pragma unroll
-            for (int j = 0; j < NT / 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[j][e] *= gamma;
-#pragma unroll
-            for (int bb = 0; bb < 4; ++bb) {
-                uint32_t hi[4], lo[4];
-                split_tokens(R, bb, ek, 1.f, tg, hi, lo);
-                rank16<NT>(S, hi, lo, ka, bb, lane);
-            }
-        }
-        __syncthreads();  // the stage is free
-    }
-    if (out.h_final && on) store_state<NT>(S, out.h_final, row, P, N, p0 + gr, tg);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -1152,7 +990,7 @@ __global__ void __launch_bounds__(kGThr)
 }
 
 template <int NT, bool BWD>
-cudaError_t prep_launch(const DeltaProblem &p, char *ws, cudaStream_t s) {
+cudaError_t prep_launch(const DeltaProblem &p, char *ws, int *status, cudaStream_t s) {
     using bf = __nv_bfloat16;
     const int64_t nc = (p.L + kC - 1) / kC, units = nc * p.G * p.B;
     const int per = (int)(p.H / p.G);
@@ -1166,27 +1004,17 @@ cudaError_t prep_launch(const DeltaProblem &p, char *ws, cudaStream_t s) {
     dim3 grid((unsigned)nc, (unsigned)(p.G * slices), (unsigned)p.B);
     k_delta_prep<NT, BWD><<<grid, kThr, smem, s>>>(static_cast<const bf *>(p.Bm), static_cast<const bf *>(p.Cm),
                                                    static_cast<const bf *>(p.g), static_cast<const bf *>(p.beta), p.L,
-                                                   (int)p.H, (int)p.G, (int)p.N, slices, ws);
+                                                   (int)p.H, (int)p.G, (int)p.N, slices, ws, status);
     return cudaGetLastError();
 }
 
-template <int NT, bool kStore>
-cudaError_t chain_launch(const DeltaProblem &p, const char *ws, const ChainOut &out, cudaStream_t s) {
-    using bf = __nv_bfloat16;
-    constexpr int smem = 2 * sizeof(ChainStage<NT, kStore>);
-    cudaError_t e;
-    if ((e = cudaFuncSetAttribute(k_delta_chain<NT, kStore>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
-    dim3 grid((unsigned)((p.P + kRowsCta - 1) / kRowsCta), (unsigned)p.H, (unsigned)p.B);
-    k_delta_chain<NT, kStore><<<grid, kThr, smem, s>>>(static_cast<const bf *>(p.x), static_cast<const bf *>(p.Bm),
-                                                       static_cast<const bf *>(p.Cm), p.h0, ws, p.L, (int)p.H, (int)p.P,
-                                                       (int)p.G, (int)p.N, out);
-    return cudaGetLastError();
-}
-
+// The workspace begins with the status word of the bounded waits, which k_delta_prep clears.
 template <int NT>
 cudaError_t fwd_launch(const DeltaProblem &p, char *ws, cudaStream_t s) {
-    const cudaError_t e = prep_launch<NT, false>(p, ws, s);
-    return e ? e : chain_launch<NT, false>(p, ws, ChainOut{static_cast<__nv_bfloat16 *>(p.y), nullptr, nullptr, nullptr, p.h_final}, s);
+    using L = Prep<false>;
+    int *status = reinterpret_cast<int *>(ws);
+    const cudaError_t e = prep_launch<NT, false>(p, ws + kWsAlign, status, s);
+    return e ? e : delta_tc_chain(p, DeltaChain{ws + kWsAlign, L::bytes, L::scal, L::P, status, nullptr, nullptr, nullptr}, s);
 }
 
 // Slices of a group's heads in k_delta_grads_mma: the number that makes (waves of CTAs on 148 SMs) x (heads
@@ -1212,7 +1040,7 @@ BwdLayout bwd_layout(const DeltaProblem &p) {
     const int slices = grads_slices(p);
     const size_t part = slices > 1 ? (size_t)(p.B * p.L * p.G * slices * p.N) * 4 : 0;
     BwdLayout l{};
-    size_t at = 0;
+    size_t at = kWsAlign;  // after the status word
     const auto take = [&](size_t bytes) {
         const size_t here = at;
         at += align_up(bytes, kWsAlign);
@@ -1238,8 +1066,12 @@ cudaError_t bwd_launch(const DeltaProblem &p, const DeltaGrads &gr, char *ws, cu
     bf *err = reinterpret_cast<bf *>(ws + l.err), *u = reinterpret_cast<bf *>(ws + l.u), *z = reinterpret_cast<bf *>(ws + l.z);
     float *dB = reinterpret_cast<float *>(ws + l.dB), *dC = reinterpret_cast<float *>(ws + l.dC);
     const char *prep = ws + l.prep;
-    cudaError_t e = prep_launch<NT, true>(p, ws + l.prep, s);
-    if (!e) e = chain_launch<NT, true>(p, prep, ChainOut{nullptr, states, err, u, nullptr}, s);
+    using Lay = Prep<true>;
+    int *status = reinterpret_cast<int *>(ws);
+    cudaError_t e = prep_launch<NT, true>(p, ws + l.prep, status, s);
+    DeltaProblem f = p;  // the states alone: no output, no final state
+    f.h_final = nullptr;
+    if (!e) e = delta_tc_chain(f, DeltaChain{prep, Lay::bytes, Lay::scal, 0, status, states, err, u}, s);
     if (e) return e;
     constexpr int smem = sizeof(ChainBwdSmem<NT>), gsmem = sizeof(GradsSmem<NT>);
     if ((e = cudaFuncSetAttribute(k_delta_chain_bwd<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
@@ -1265,11 +1097,11 @@ cudaError_t bwd_launch(const DeltaProblem &p, const DeltaGrads &gr, char *ws, cu
 }  // namespace
 
 bool delta_mma_supported(const DeltaProblem &p) {
-    return p.dtype == SSD_BF16 && p.N <= 128 && p.N % 8 == 0 && p.P % 8 == 0 && p.L >= 8;
+    return p.dtype == SSD_BF16 && p.N <= 128 && p.N % 8 == 0 && p.P % 8 == 0 && p.L >= 8 && p.L < (1ll << 31);
 }
 
 size_t delta_mma_fwd_workspace_bytes(const DeltaProblem &p) {
-    return (size_t)(p.B * p.H) * (size_t)((p.L + kC - 1) / kC) * Prep<false>::bytes;
+    return kWsAlign + (size_t)(p.B * p.H) * (size_t)((p.L + kC - 1) / kC) * Prep<false>::bytes;
 }
 
 cudaError_t delta_mma_fwd(const DeltaProblem &p, void *ws, cudaStream_t s) {
