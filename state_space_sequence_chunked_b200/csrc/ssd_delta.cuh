@@ -50,7 +50,6 @@ cudaError_t delta_mma_bwd(const DeltaProblem &p, const DeltaGrads &g, void *ws, 
 struct DeltaChain {
     const char *prep;
     int64_t prep_bytes;  // per chunk and head
-    int scal_at, p_at;   // where the scalars and the masked Q K^T stand in it
     int *status;
     void *states, *err, *u;
 };

@@ -34,19 +34,23 @@ constexpr int kRowsCta = 64;     // state rows per CTA of the chain
 constexpr int kBlocks = 10;
 __host__ __device__ constexpr int block_at(int a, int b) { return a * (a + 1) / 2 + b; }
 
-// Per chunk and head, in the workspace: fragments as right operands, one 16-byte vector per lane and
-// block, and the scalars exp(cum), exp(cum_end - cum), beta of the chunk's tokens, then cum as a sum of
-// two floats. The forward has W (hi, lo), the scalars and the masked Q K^T; the backward pass W, the
-// scalars, and both transposed (hi, lo).
-constexpr int kFragBytes = 512;  // one vector per lane
-constexpr int kWBytes = kBlocks * 2 * kFragBytes;
-constexpr int kPBytes = kBlocks * kFragBytes;
+// Per chunk and head, in the workspace. First what k_delta_tc loads in one piece: W (hi, lo), the masked
+// Q K^T (forward only) and the scalars exp(cum), exp(cum_end - cum), beta of the chunk's tokens, then cum as
+// a sum of two floats. The matrices are right operands of tcgen05 products without a swizzle: blocks of
+// 16 x 16 of the lower triangle, by column of blocks, each as 8 x 8 core matrices of 128 contiguous bytes
+// (rows 0-7: two halves of the columns, then rows 8-15). Then, for the backward pass alone, both matrices
+// transposed (hi, lo) as mma.sync fragments, one 16-byte vector per lane and block.
+constexpr int kBlockBytes = 512;
+constexpr int kWBytes = kBlocks * 2 * kBlockBytes;
+constexpr int kPBytes = kBlocks * kBlockBytes;
 constexpr int kScalBytes = 5 * kC * 4;
 template <bool BWD>
 struct Prep {
-    static constexpr int W = 0, scal = kWBytes, P = scal + kScalBytes, WT = scal + kScalBytes, PT = WT + kWBytes;
-    static constexpr int bytes = BWD ? PT + kWBytes : P + kPBytes;
+    static constexpr int W = 0, P = kWBytes, scal = BWD ? kWBytes : P + kPBytes, WT = scal + kScalBytes, PT = WT + kWBytes;
+    static constexpr int bytes = BWD ? PT + kWBytes : scal + kScalBytes;
 };
+// block (a, b) by column of blocks: four of column 0, three of column 1, ...
+__host__ __device__ constexpr int column_at(int a, int b) { return b * 4 - b * (b - 1) / 2 + a - b; }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -177,19 +181,22 @@ __device__ __forceinline__ void block_mma(float (&acc)[2][4], const uint32_t (&a
     }
 }
 
-// Fragments of block `at` of W, and for the backward pass of its transpose.
+// Block (a, b) of W, and for the backward pass its transpose as fragments.
 template <bool BWD>
-__device__ __forceinline__ void put_w(char *out, int at, int lane, const float (&w)[2][4]) {
+__device__ __forceinline__ void put_w(char *out, int a, int b, int lane, const float (&w)[2][4]) {
     uint32_t hi[4], lo[4];  // rows 0-7: two halves of the columns, then rows 8-15
     split(w[0][0], w[0][1], hi[0], lo[0]);
     split(w[1][0], w[1][1], hi[1], lo[1]);
     split(w[0][2], w[0][3], hi[2], lo[2]);
     split(w[1][2], w[1][3], hi[3], lo[3]);
-    uint4 *o = reinterpret_cast<uint4 *>(out + Prep<BWD>::W) + at * 64 + lane;
-    o[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    o[32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    uint32_t *t = reinterpret_cast<uint32_t *>(out + Prep<BWD>::W + column_at(a, b) * kBlockBytes) + lane;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        t[32 * e] = hi[e];
+        t[32 * e + kWBytes / 8] = lo[e];
+    }
     if constexpr (BWD) {
-        o = reinterpret_cast<uint4 *>(out + Prep<BWD>::WT) + at * 64 + lane;
+        uint4 *o = reinterpret_cast<uint4 *>(out + Prep<BWD>::WT) + block_at(a, b) * 64 + lane;
         o[0] = make_uint4(trans8(hi[0]), trans8(hi[2]), trans8(hi[1]), trans8(hi[3]));
         o[32] = make_uint4(trans8(lo[0]), trans8(lo[2]), trans8(lo[1]), trans8(lo[3]));
     }
@@ -303,8 +310,9 @@ __global__ void __launch_bounds__(kThr)
                 o[0] = make_uint4(ph[0], ph[1], ph[2], ph[3]);
                 o[32] = make_uint4(pl[0], pl[1], pl[2], pl[3]);
             } else {
-                reinterpret_cast<uint4 *>(out + Lay::P)[block_at(a, cc) * 32 + lane] =
-                    make_uint4(pack(p[0][0], p[0][1]), pack(p[1][0], p[1][1]), pack(p[0][2], p[0][3]), pack(p[1][2], p[1][3]));
+                uint32_t *o = reinterpret_cast<uint32_t *>(out + Lay::P + column_at(a, cc) * kBlockBytes) + lane;
+                o[0] = pack(p[0][0], p[0][1]), o[32] = pack(p[1][0], p[1][1]);
+                o[64] = pack(p[0][2], p[0][3]), o[96] = pack(p[1][2], p[1][3]);
             }
         };
 #pragma unroll
@@ -356,7 +364,7 @@ __global__ void __launch_bounds__(kThr)
             float m[3][2][4], d[2][4];
             uint32_t mh[3][4], ml[3][4], dh[4], dl[4];
             diag(a, d);
-            put_w<BWD>(out, block_at(a, a), lane, d);
+            put_w<BWD>(out, a, a, lane, d);
             const float s0 = wm.beta[16 * a + gr], s1 = wm.beta[16 * a + gr + 8];
             if (a < 3) split_b(d, s0, s1, bh[block_at(a, a)], bl[block_at(a, a)]);
             if (a == 0) continue;
@@ -391,7 +399,7 @@ __global__ void __launch_bounds__(kThr)
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[n][e] = -w[n][e];
-                put_w<BWD>(out, block_at(a, bb), lane, w);
+                put_w<BWD>(out, a, bb, lane, w);
                 if (a < 3) split_b(w, s0, s1, bh[block_at(a, bb)], bl[block_at(a, bb)]);
             }
         }
@@ -1014,7 +1022,7 @@ cudaError_t fwd_launch(const DeltaProblem &p, char *ws, cudaStream_t s) {
     using L = Prep<false>;
     int *status = reinterpret_cast<int *>(ws);
     const cudaError_t e = prep_launch<NT, false>(p, ws + kWsAlign, status, s);
-    return e ? e : delta_tc_chain(p, DeltaChain{ws + kWsAlign, L::bytes, L::scal, L::P, status, nullptr, nullptr, nullptr}, s);
+    return e ? e : delta_tc_chain(p, DeltaChain{ws + kWsAlign, L::bytes, status, nullptr, nullptr, nullptr}, s);
 }
 
 // Slices of a group's heads in k_delta_grads_mma: the number that makes (waves of CTAs on 148 SMs) x (heads
@@ -1071,7 +1079,7 @@ cudaError_t bwd_launch(const DeltaProblem &p, const DeltaGrads &gr, char *ws, cu
     cudaError_t e = prep_launch<NT, true>(p, ws + l.prep, status, s);
     DeltaProblem f = p;  // the states alone: no output, no final state
     f.h_final = nullptr;
-    if (!e) e = delta_tc_chain(f, DeltaChain{prep, Lay::bytes, Lay::scal, 0, status, states, err, u}, s);
+    if (!e) e = delta_tc_chain(f, DeltaChain{prep, Lay::bytes, status, states, err, u}, s);
     if (e) return e;
     constexpr int smem = sizeof(ChainBwdSmem<NT>), gsmem = sizeof(GradsSmem<NT>);
     if ((e = cudaFuncSetAttribute(k_delta_chain_bwd<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
@@ -1097,7 +1105,8 @@ cudaError_t bwd_launch(const DeltaProblem &p, const DeltaGrads &gr, char *ws, cu
 }  // namespace
 
 bool delta_mma_supported(const DeltaProblem &p) {
-    return p.dtype == SSD_BF16 && p.N <= 128 && p.N % 8 == 0 && p.P % 8 == 0 && p.L >= 8 && p.L < (1ll << 31);
+    return p.dtype == SSD_BF16 && p.N <= 128 && p.N % 8 == 0 && p.P % 8 == 0 && p.L >= 8 && p.L < (1ll << 31) &&
+           p.B * p.H * ((p.L + kC - 1) / kC) < (1ll << 31);
 }
 
 size_t delta_mma_fwd_workspace_bytes(const DeltaProblem &p) {
