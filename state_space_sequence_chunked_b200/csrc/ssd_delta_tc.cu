@@ -27,7 +27,7 @@
 // kStore is the backward pass's recomputation: no Y, but the state entering each chunk, err and u in bf16.
 //
 // Every wait is bounded (tc_ptx.cuh); one that runs out sets bit 0 of the workspace's status word.
-#include <algorithm>
+#include <type_traits>
 
 #include "ssd_delta.cuh"
 #include "tc_ptx.cuh"
@@ -79,28 +79,57 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 // The products are issued by one elected thread, but from code that the whole warp runs: descriptors and
 // TMEM addresses then stay in uniform registers. From inside `if (lane == 0)` each product took about 90
 // cycles to issue, most of them moving its operands into uniform registers.
-__device__ __forceinline__ void mma_el(uint32_t d, uint32_t left, uint64_t right, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "elect.sync _|q, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(left), "l"(right), "r"(id), "r"(acc)
-        : "memory");
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+    return r;
 }
-__device__ __forceinline__ void commit_el(uint64_t *bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "elect.sync _|q, 0xffffffff;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-        : "memory");
+template <bool kAcc>
+__device__ __forceinline__ void mma_el(uint32_t leader, uint32_t d, uint32_t left, uint64_t right, uint32_t id) {
+    if constexpr (kAcc)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(left), "l"(right), "r"(id), "r"(leader)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.ne.b32 p, 0, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(left), "l"(right), "r"(id), "r"(leader)
+            : "memory");
+}
+__device__ __forceinline__ void commit_el(uint32_t leader, uint64_t *bar) {
+    if (leader) mma_commit(bar);
+    __syncwarp();
 }
 
 // hi + lo parts of a pair of fp32 values (lo: what hi leaves, rounded: 2^-18 of the value at worst)
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
     hi = pack_bf16(x, y);
-    lo = pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi));
+    asm("{\n\t.reg .b64 v, h, m;\n\t.reg .f32 a, b;\n\t"
+        "mov.b64 v, {%1, %2};\n\tmov.b64 h, {%3, %4};\n\tmov.b64 m, {%5, %5};\n\t"
+        "fma.rn.f32x2 v, h, m, v;\n\tmov.b64 {a, b}, v;\n\tcvt.rn.bf16x2.f32 %0, b, a;\n\t}"
+        : "=r"(lo)
+        : "f"(x), "f"(y), "f"(bf16_lo(hi)), "f"(bf16_hi(hi)), "f"(-1.f));
 }
+// packed pairs of fp32: a b, and c + a b
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\tmul.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 pair_of(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
 
 template <int NT, bool PAIR, bool kStore>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -120,7 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *rdyR = bar + 6, *rdyE = bar + 7, *rdyS = bar + 8, *rdyQ = bar + 9, *rdyY = bar + 10;  // products done
     uint64_t *sb = bar + 11;     // the state's operands written (T)
     uint64_t *ab = bar + 12;     // beta R written (T)
-    uint64_t *ub = bar + 13;     // u and ek u written (T)
+    uint64_t *ub = bar + 13;     // ek u written (T)
+    uint64_t *yu = bar + 2;      // u (kStore: u and err, to go out) written (T)
     uint64_t *ys = bar + 14;     // Yq scaled (O)
     uint64_t *ofree = bar + 15;  // Y (kStore: err and u) read (O)
     uint64_t *fin = bar + 16;
@@ -146,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(sb, kTWarps);
         mbar_init(ab, kTWarps);
         mbar_init(ub, kTWarps);
+        mbar_init(yu, kTWarps);
         mbar_init(ys, 4);
         mbar_init(ofree, 4);
         mbar_init(fin, 1);
@@ -200,14 +231,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         // A lower triangle as right operand, a column of blocks (16 tokens) at a time, rows from its own block
         // on. No swizzle: core matrices of 128 bytes, the two of a block's row 128 apart, rows of them 256.
-        const auto tri = [&](uint32_t d, uint32_t left, uint32_t tile, uint32_t acc) {
+        const uint32_t el = elect_one();
+        const auto tri = [&](uint32_t d, uint32_t left, uint32_t tile, auto acc) {
             const uint64_t td = (uint64_t)((tile >> 4) & 0x3FFFu) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(256 >> 4) << 32 |
                                 (uint64_t)1 << 46;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                mma_el(d + 16 * i, left + 8 * i, td + (uint64_t)((i * 4 - i * (i - 1) / 2) * 512 >> 4),
-                       idesc(128, 64 - 16 * i, false, false), i > 0 ? 1u : acc);
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t ti = td + (uint64_t)((i * 4 - i * (i - 1) / 2) * 512 >> 4);
+                if (i == 0)
+                    mma_el<decltype(acc)::value>(el, d, left, ti, idesc(128, 64, false, false));
+                else
+                    mma_el<true>(el, d + 16 * i, left + 8 * i, ti, idesc(128, 64 - 16 * i, false, false));
+            }
         };
+        constexpr std::true_type add{};
+        constexpr std::false_type set{};
         for (int c = 0; c < nc; ++c) {
             const int k = c & 1;
             const uint32_t par = (uint32_t)c & 1u;
@@ -219,51 +257,63 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < NT / 16; ++kk) {
                 const uint64_t off = (uint64_t)(((kk >> 2) * kPanel + (kk & 3) * 32) >> 4);
-                mma_el(tm + kTmR, tm + kTmLo + 8 * kk, kd + off, id_ks, kk > 0);
-                mma_el(tm + kTmR, tm + kTmHi + 8 * kk, kd + off, id_ks, 1);
+                if (kk == 0)
+                    mma_el<false>(el, tm + kTmR, tm + kTmLo, kd, id_ks);
+                else
+                    mma_el<true>(el, tm + kTmR, tm + kTmLo + 8 * kk, kd + off, id_ks);
+                mma_el<true>(el, tm + kTmR, tm + kTmHi + 8 * kk, kd + off, id_ks);
             }
-            commit_el(rdyR);
+            commit_el(el, rdyR);
             if constexpr (!kStore) {
                 if (c > 0 && !wait_warp(ofree, par ^ 1u, abort_flag, status)) break;
                 tc_fence_after();
                 const uint64_t qd = sdesc(st + Z::q, 16, 1024);
 #pragma unroll
-                for (int kk = 0; kk < NT / 16; ++kk)
-                    mma_el(tm + kTmY, tm + kTmHi + 8 * kk, qd + (uint64_t)(((kk >> 2) * kPanel + (kk & 3) * 32) >> 4), id_ks, kk > 0);
-                commit_el(rdyQ);
+                for (int kk = 0; kk < NT / 16; ++kk) {
+                    const uint64_t off = (uint64_t)(((kk >> 2) * kPanel + (kk & 3) * 32) >> 4);
+                    if (kk == 0)
+                        mma_el<false>(el, tm + kTmY, tm + kTmHi, qd, id_ks);
+                    else
+                        mma_el<true>(el, tm + kTmY, tm + kTmHi + 8 * kk, qd + off, id_ks);
+                }
+                commit_el(el, rdyQ);
             }
             if (!wait_warp(ab, par, abort_flag, status)) break;
             tc_fence_after();
 #pragma unroll
             for (int e = 0; e < HB; ++e) {
                 const uint32_t wh = st + Z::w + e * Z::head;
-                tri(tm + kTmR, tm + kTmAl + 32 * e, wh, e);
-                tri(tm + kTmR, tm + kTmA + 32 * e, wh + kTri, 1);
-                tri(tm + kTmR, tm + kTmA + 32 * e, wh, 1);
+                if (e == 0)
+                    tri(tm + kTmR, tm + kTmAl, wh, set);
+                else
+                    tri(tm + kTmR, tm + kTmAl + 32 * e, wh, add);
+                tri(tm + kTmR, tm + kTmA + 32 * e, wh + kTri, add);
+                tri(tm + kTmR, tm + kTmA + 32 * e, wh, add);
             }
-            commit_el(rdyE);
+            commit_el(el, rdyE);
             if (!wait_warp(ub, par, abort_flag, status)) break;
             tc_fence_after();
             const uint64_t ks = sdesc(st + Z::k, kPanel, 1024);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-                mma_el(tm + kTmS, tm + kEkl + 8 * kk, ks + 128 * kk, id_s, 1);
-                mma_el(tm + kTmS, tm + kEk + 8 * kk, ks + 128 * kk, id_s, 1);
+                mma_el<true>(el, tm + kTmS, tm + kEkl + 8 * kk, ks + 128 * kk, id_s);
+                mma_el<true>(el, tm + kTmS, tm + kEk + 8 * kk, ks + 128 * kk, id_s);
             }
-            commit_el(rdyS);
+            commit_el(el, rdyS);
             if constexpr (!kStore) {
                 if (!wait_warp(ys, par, abort_flag, status)) break;
+                if (!wait_warp(yu, par, abort_flag, status)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int e = 0; e < HB; ++e) {
-                    tri(tm + kTmY, tm + kTmAl + 32 * e, st + Z::w + e * Z::head + Z::p, 1);
-                    tri(tm + kTmY, tm + kTmA + 32 * e, st + Z::w + e * Z::head + Z::p, 1);
+                    tri(tm + kTmY, tm + kTmAl + 32 * e, st + Z::w + e * Z::head + Z::p, add);
+                    tri(tm + kTmY, tm + kTmA + 32 * e, st + Z::w + e * Z::head + Z::p, add);
                 }
-                commit_el(rdyY);
+                commit_el(el, rdyY);
             }
-            commit_el(&sfree[k]);
+            commit_el(el, &sfree[k]);
         }
-        commit_el(fin);
+        commit_el(el, fin);
     } else if (warp < 4) {
         // (idle: a T or O warp's TMEM lanes are those of its number modulo 4)
     } else if (warp < kOWarp) {
@@ -290,42 +340,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (kStore && !wait_warp(ofree, par ^ 1u, abort_flag, status)) break;
                 tc_fence_after();
             }
-            {  // the state: its operands, and itself times exp(cum_end) for the product to add to
-                const float gamma = eg[kC - 1];
+            // The state's operands; then, while S K^T runs, the state times exp(cum_end) for the next product to
+            // add to, and X.
+            float R[16];
+            {
+                uint32_t s[SC];
 #pragma unroll
                 for (int j = 0; j < SC; j += 16) {
-                    uint32_t s[16], hi[8], lw[8];
+                    uint32_t v[16];
                     if (c > 0) {
-                        tmem_ld16(lo_ + kTmS + n0 + j, s);
+                        tmem_ld16(lo_ + kTmS + n0 + j, v);
                         tmem_wait_ld();
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
                             if (a.h0 && p < a.P && n0 + j + 4 * i < a.N)
-                                v = *reinterpret_cast<const float4 *>(a.h0 + srow * a.N + n0 + j + 4 * i);
-                            s[4 * i] = __float_as_uint(v.x), s[4 * i + 1] = __float_as_uint(v.y);
-                            s[4 * i + 2] = __float_as_uint(v.z), s[4 * i + 3] = __float_as_uint(v.w);
+                                f = *reinterpret_cast<const float4 *>(a.h0 + srow * a.N + n0 + j + 4 * i);
+                            v[4 * i] = __float_as_uint(f.x), v[4 * i + 1] = __float_as_uint(f.y);
+                            v[4 * i + 2] = __float_as_uint(f.z), v[4 * i + 3] = __float_as_uint(f.w);
                         }
                     }
+                    uint32_t hi[8], lw[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        split2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]), hi[i], lw[i]);
-                        s[2 * i] = __float_as_uint(gamma * __uint_as_float(s[2 * i]));
-                        s[2 * i + 1] = __float_as_uint(gamma * __uint_as_float(s[2 * i + 1]));
-                    }
+                    for (int i = 0; i < 8; ++i) split2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), hi[i], lw[i]);
                     tmem_st8(lo_ + kTmHi + (n0 + j) / 2, hi);
                     tmem_st8(lo_ + kTmLo + (n0 + j) / 2, lw);
-                    tmem_st16(lo_ + kTmS + n0 + j, s);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[j + i] = v[i];
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sb);
+                const float gamma = eg[kC - 1];
+#pragma unroll
+                for (int j = 0; j < SC; j += 16) {
+                    uint32_t v[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 g = mul2(make_float2(gamma, gamma), pair_of(s[j + 2 * i], s[j + 2 * i + 1]));
+                        v[2 * i] = __float_as_uint(g.x), v[2 * i + 1] = __float_as_uint(g.y);
+                    }
+                    tmem_st16(lo_ + kTmS + n0 + j, v);
+                }
             }
-            // R = X - eg S K^T; beta R as left operand. This warp: tokens tk0 .. + 15.
-            float R[16];
             const unsigned char *xt = sm + k * Z::stage + Z::x + (qtr >> 1) * kPanel;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                R[i] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(xt + swz(tk0 + i, pp >> 3) + 2 * (pp & 7)));
+            // R = X - eg S K^T; beta R as left operand. This warp: tokens tk0 .. + 15.
             if (!wait_warp(rdyR, par, abort_flag, status)) break;
             tc_fence_after();
             {
@@ -336,16 +400,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 16; i += 4) {
                     const int t = tk0 + i;
                     const float4 g4 = *reinterpret_cast<const float4 *>(eg + t), b4 = *reinterpret_cast<const float4 *>(bt + t);
-                    float xv[4];
+                    const float2 gg[2] = {make_float2(-g4.x, -g4.y), make_float2(-g4.z, -g4.w)};
+                    const float2 bb[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
 #pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        xv[v] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(xt + swz(t + v, pp >> 3) + 2 * (pp & 7)));
-                    R[i] = fmaf(-g4.x, __uint_as_float(r[i]), xv[0]);
-                    R[i + 1] = fmaf(-g4.y, __uint_as_float(r[i + 1]), xv[1]);
-                    R[i + 2] = fmaf(-g4.z, __uint_as_float(r[i + 2]), xv[2]);
-                    R[i + 3] = fmaf(-g4.w, __uint_as_float(r[i + 3]), xv[3]);
-                    split2(b4.x * R[i], b4.y * R[i + 1], hi[i / 2], lw[i / 2]);
-                    split2(b4.z * R[i + 2], b4.w * R[i + 3], hi[i / 2 + 1], lw[i / 2 + 1]);
+                    for (int v = 0; v < 2; ++v) {
+                        const int o = i + 2 * v;
+                        const float2 rr = fma2(gg[v], pair_of(r[o], r[o + 1]), make_float2(R[o], R[o + 1]));
+                        R[o] = rr.x, R[o + 1] = rr.y;
+                        const float2 br = mul2(bb[v], rr);
+                        split2(br.x, br.y, hi[o / 2], lw[o / 2]);
+                    }
                 }
                 tmem_st8(lo_ + kTmA + 32 * e + 8 * sub, hi);
                 tmem_st8(lo_ + kTmAl + 32 * e + 8 * sub, lw);
@@ -354,40 +418,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(ab);
             }
-            // err = R + E, u = beta err, and ek u
+            // err = R + E, u = beta err; ek u first, which the state waits for
             if (!wait_warp(rdyE, par, abort_flag, status)) break;
             tc_fence_after();
             {
-                uint32_t r[16], hi[8], lw[8], ehi[8], elw[8];
+                uint32_t r[16], hi[8], lw[8];
                 tmem_ld16(lo_ + kTmR + tk0, r);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
-                    const int t = tk0 + i;
-                    const float4 k4 = *reinterpret_cast<const float4 *>(ek + t), b4 = *reinterpret_cast<const float4 *>(bt + t);
-                    float u[4];
+                    const float4 k4 = *reinterpret_cast<const float4 *>(ek + tk0 + i), b4 = *reinterpret_cast<const float4 *>(bt + tk0 + i);
+                    const float2 kk[2] = {make_float2(k4.x, k4.y), make_float2(k4.z, k4.w)};
+                    const float2 bb[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) R[i + v] += __uint_as_float(r[i + v]);
-                    u[0] = b4.x * R[i], u[1] = b4.y * R[i + 1], u[2] = b4.z * R[i + 2], u[3] = b4.w * R[i + 3];
-                    split2(k4.x * u[0], k4.y * u[1], ehi[i / 2], elw[i / 2]);
-                    split2(k4.z * u[2], k4.w * u[3], ehi[i / 2 + 1], elw[i / 2 + 1]);
-                    if constexpr (kStore) {  // u and err go out rounded; no product here takes u itself
-                        hi[i / 2] = pack_bf16(u[0], u[1]), hi[i / 2 + 1] = pack_bf16(u[2], u[3]);
-                        lw[i / 2] = pack_bf16(R[i], R[i + 1]), lw[i / 2 + 1] = pack_bf16(R[i + 2], R[i + 3]);
-                    } else {
-                        split2(u[0], u[1], hi[i / 2], lw[i / 2]);
-                        split2(u[2], u[3], hi[i / 2 + 1], lw[i / 2 + 1]);
+                    for (int v = 0; v < 2; ++v) {
+                        const int o = i + 2 * v;
+                        R[o] += __uint_as_float(r[o]), R[o + 1] += __uint_as_float(r[o + 1]);
+                        const float2 u = mul2(bb[v], make_float2(R[o], R[o + 1])), eu = mul2(kk[v], u);
+                        if constexpr (!kStore) r[o] = __float_as_uint(u.x), r[o + 1] = __float_as_uint(u.y);
+                        else r[o / 2] = pack_bf16(u.x, u.y);
+                        split2(eu.x, eu.y, hi[o / 2], lw[o / 2]);
                     }
                 }
-                tmem_st8(lo_ + kEk + 8 * sub, ehi);
-                tmem_st8(lo_ + kEkl + 8 * sub, elw);
-                if constexpr (kStore) {
-                    tmem_st8(lo_ + kTmY + 8 * sub, hi);
-                    tmem_st8(lo_ + kTmY + 32 + 8 * sub, lw);
-                } else {
-                    tmem_st8(lo_ + kTmA + 32 * e + 8 * sub, hi);
-                    tmem_st8(lo_ + kTmAl + 32 * e + 8 * sub, lw);
-                }
+                tmem_st8(lo_ + kEk + 8 * sub, hi);
+                tmem_st8(lo_ + kEkl + 8 * sub, lw);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -395,6 +449,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(ub);
                     mbar_arrive(&sfree[k]);
                 }
+                if constexpr (kStore) {  // u and err go out rounded; no product here takes u itself
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) hi[i] = r[i], lw[i] = pack_bf16(R[2 * i], R[2 * i + 1]);
+                    tmem_st8(lo_ + kTmY + 8 * sub, hi);
+                    tmem_st8(lo_ + kTmY + 32 + 8 * sub, lw);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) split2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), hi[i], lw[i]);
+                    tmem_st8(lo_ + kTmA + 32 * e + 8 * sub, hi);
+                    tmem_st8(lo_ + kTmAl + 32 * e + 8 * sub, lw);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(yu);
             }
         }
         if (a.h_final && wait_warp(rdyS, (uint32_t)(nc - 1) & 1u, abort_flag, status)) {
@@ -473,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (64 * pn < a.N) tma_store_4d(&tm_s, stage2 + pn * 4096, 64 * pn, p0, unit, 0, pol);
                     bulk_commit();
                 }
-                if (!wait_warp(ub, par, abort_flag, status)) break;
+                if (!wait_warp(yu, par, abort_flag, status)) break;
             }
             tc_fence_after();
             if (lane == 0) bulk_wait_read();
