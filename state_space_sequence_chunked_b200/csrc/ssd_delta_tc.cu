@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *sb = bar + 11;     // the state's operands written (T)
     uint64_t *ab = bar + 12;     // beta R written (T)
     uint64_t *ub = bar + 13;     // ek u written (T)
+    uint64_t *ost = bar + 3;     // kStore: S hi read (O)
     uint64_t *yu = bar + 2;      // u (kStore: u and err, to go out) written (T)
     uint64_t *ys = bar + 14;     // Yq scaled (O)
     uint64_t *ofree = bar + 15;  // Y (kStore: err and u) read (O)
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(yu, kTWarps);
         mbar_init(ys, 4);
         mbar_init(ofree, 4);
+        mbar_init(ost, 4);
         mbar_init(fin, 1);
         abort_flag[0] = 0;
         abort_flag[1] = a.wait_us;
@@ -337,37 +339,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float *eg = scal_of(k, e), *ek = eg + kC, *bt = eg + 2 * kC;
             if (c > 0) {
                 if (!wait_warp(rdyS, par ^ 1u, abort_flag, status)) break;
-                if (kStore && !wait_warp(ofree, par ^ 1u, abort_flag, status)) break;
+                if (kStore && !wait_warp(ost, par ^ 1u, abort_flag, status)) break;
                 tc_fence_after();
             }
             // The state's operands; then, while S K^T runs, the state times exp(cum_end) for the next product to
-            // add to, and X.
-            float R[16];
+            // add to, and what beta R = beta X - beta eg S K^T needs. This warp: tokens tk0 .. + 15.
+            float bx[16], be[16];
+            const unsigned char *xt = sm + k * Z::stage + Z::x + (qtr >> 1) * kPanel;
+            const auto x_at = [&](int i) {
+                return __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(xt + swz(tk0 + i, pp >> 3) + 2 * (pp & 7)));
+            };
             {
                 uint32_t s[SC];
+                if (c > 0) {
+                    if constexpr (SC == 32) {
+                        tmem_ld32(lo_ + kTmS + n0, s);
+                        tmem_wait_ld(s);
+                    } else {
+                        tmem_ld16(lo_ + kTmS + n0, s);
+                        tmem_wait_ld();
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < SC; i += 4) {
+                        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (a.h0 && p < a.P && n0 + i < a.N) f = *reinterpret_cast<const float4 *>(a.h0 + srow * a.N + n0 + i);
+                        s[i] = __float_as_uint(f.x), s[i + 1] = __float_as_uint(f.y);
+                        s[i + 2] = __float_as_uint(f.z), s[i + 3] = __float_as_uint(f.w);
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < SC; j += 16) {
-                    uint32_t v[16];
-                    if (c > 0) {
-                        tmem_ld16(lo_ + kTmS + n0 + j, v);
-                        tmem_wait_ld();
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (a.h0 && p < a.P && n0 + j + 4 * i < a.N)
-                                f = *reinterpret_cast<const float4 *>(a.h0 + srow * a.N + n0 + j + 4 * i);
-                            v[4 * i] = __float_as_uint(f.x), v[4 * i + 1] = __float_as_uint(f.y);
-                            v[4 * i + 2] = __float_as_uint(f.z), v[4 * i + 3] = __float_as_uint(f.w);
-                        }
-                    }
                     uint32_t hi[8], lw[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) split2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), hi[i], lw[i]);
+                    for (int i = 0; i < 8; ++i)
+                        split2(__uint_as_float(s[j + 2 * i]), __uint_as_float(s[j + 2 * i + 1]), hi[i], lw[i]);
                     tmem_st8(lo_ + kTmHi + (n0 + j) / 2, hi);
                     tmem_st8(lo_ + kTmLo + (n0 + j) / 2, lw);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) s[j + i] = v[i];
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -385,31 +393,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st16(lo_ + kTmS + n0 + j, v);
                 }
             }
-            const unsigned char *xt = sm + k * Z::stage + Z::x + (qtr >> 1) * kPanel;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                R[i] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(xt + swz(tk0 + i, pp >> 3) + 2 * (pp & 7)));
-            // R = X - eg S K^T; beta R as left operand. This warp: tokens tk0 .. + 15.
+            for (int i = 0; i < 16; i += 4) {
+                const float4 g4 = *reinterpret_cast<const float4 *>(eg + tk0 + i), b4 = *reinterpret_cast<const float4 *>(bt + tk0 + i);
+                be[i] = -b4.x * g4.x, be[i + 1] = -b4.y * g4.y, be[i + 2] = -b4.z * g4.z, be[i + 3] = -b4.w * g4.w;
+                bx[i] = b4.x * x_at(i), bx[i + 1] = b4.y * x_at(i + 1), bx[i + 2] = b4.z * x_at(i + 2), bx[i + 3] = b4.w * x_at(i + 3);
+            }
             if (!wait_warp(rdyR, par, abort_flag, status)) break;
             tc_fence_after();
+            float R[16];
             {
                 uint32_t r[16], hi[8], lw[8];
                 tmem_ld16(lo_ + kTmR + tk0, r);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const int t = tk0 + i;
-                    const float4 g4 = *reinterpret_cast<const float4 *>(eg + t), b4 = *reinterpret_cast<const float4 *>(bt + t);
-                    const float2 gg[2] = {make_float2(-g4.x, -g4.y), make_float2(-g4.z, -g4.w)};
-                    const float2 bb[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const int o = i + 2 * v;
-                        const float2 rr = fma2(gg[v], pair_of(r[o], r[o + 1]), make_float2(R[o], R[o + 1]));
-                        R[o] = rr.x, R[o + 1] = rr.y;
-                        const float2 br = mul2(bb[v], rr);
-                        split2(br.x, br.y, hi[o / 2], lw[o / 2]);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const float2 br = fma2(make_float2(be[2 * i], be[2 * i + 1]), pair_of(r[2 * i], r[2 * i + 1]),
+                                           make_float2(bx[2 * i], bx[2 * i + 1]));
+                    split2(br.x, br.y, hi[i], lw[i]);
                 }
                 tmem_st8(lo_ + kTmA + 32 * e + 8 * sub, hi);
                 tmem_st8(lo_ + kTmAl + 32 * e + 8 * sub, lw);
@@ -417,6 +418,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(ab);
+                // while W (beta R) runs: R itself, and ek beta
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 g4 = *reinterpret_cast<const float4 *>(eg + tk0 + i), b4 = *reinterpret_cast<const float4 *>(bt + tk0 + i);
+                    const float4 k4 = *reinterpret_cast<const float4 *>(ek + tk0 + i);
+                    R[i] = fmaf(-g4.x, __uint_as_float(r[i]), x_at(i)), R[i + 1] = fmaf(-g4.y, __uint_as_float(r[i + 1]), x_at(i + 1));
+                    R[i + 2] = fmaf(-g4.z, __uint_as_float(r[i + 2]), x_at(i + 2));
+                    R[i + 3] = fmaf(-g4.w, __uint_as_float(r[i + 3]), x_at(i + 3));
+                    be[i] = k4.x * b4.x, be[i + 1] = k4.y * b4.y, be[i + 2] = k4.z * b4.z, be[i + 3] = k4.w * b4.w;
+                }
             }
             // err = R + E, u = beta err; ek u first, which the state waits for
             if (!wait_warp(rdyE, par, abort_flag, status)) break;
@@ -426,44 +437,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld16(lo_ + kTmR + tk0, r);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const float4 k4 = *reinterpret_cast<const float4 *>(ek + tk0 + i), b4 = *reinterpret_cast<const float4 *>(bt + tk0 + i);
-                    const float2 kk[2] = {make_float2(k4.x, k4.y), make_float2(k4.z, k4.w)};
-                    const float2 bb[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const int o = i + 2 * v;
-                        R[o] += __uint_as_float(r[o]), R[o + 1] += __uint_as_float(r[o + 1]);
-                        const float2 u = mul2(bb[v], make_float2(R[o], R[o + 1])), eu = mul2(kk[v], u);
-                        if constexpr (!kStore) r[o] = __float_as_uint(u.x), r[o + 1] = __float_as_uint(u.y);
-                        else r[o / 2] = pack_bf16(u.x, u.y);
-                        split2(eu.x, eu.y, hi[o / 2], lw[o / 2]);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    R[2 * i] += __uint_as_float(r[2 * i]), R[2 * i + 1] += __uint_as_float(r[2 * i + 1]);
+                    const float2 eu = mul2(make_float2(be[2 * i], be[2 * i + 1]), make_float2(R[2 * i], R[2 * i + 1]));
+                    split2(eu.x, eu.y, hi[i], lw[i]);
                 }
                 tmem_st8(lo_ + kEk + 8 * sub, hi);
                 tmem_st8(lo_ + kEkl + 8 * sub, lw);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(ub);
-                    mbar_arrive(&sfree[k]);
+                if (lane == 0) mbar_arrive(ub);
+                if constexpr (kStore) {  // the last chunk's u and err have left
+                    if (c > 0 && !wait_warp(ofree, par ^ 1u, abort_flag, status)) break;
                 }
-                if constexpr (kStore) {  // u and err go out rounded; no product here takes u itself
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) hi[i] = r[i], lw[i] = pack_bf16(R[2 * i], R[2 * i + 1]);
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 b4 = *reinterpret_cast<const float4 *>(bt + tk0 + i);
+                    const float u[4] = {b4.x * R[i], b4.y * R[i + 1], b4.z * R[i + 2], b4.w * R[i + 3]};
+                    if constexpr (kStore) {  // u and err go out rounded; no product here takes u itself
+                        hi[i / 2] = pack_bf16(u[0], u[1]), hi[i / 2 + 1] = pack_bf16(u[2], u[3]);
+                        lw[i / 2] = pack_bf16(R[i], R[i + 1]), lw[i / 2 + 1] = pack_bf16(R[i + 2], R[i + 3]);
+                    } else {
+                        split2(u[0], u[1], hi[i / 2], lw[i / 2]);
+                        split2(u[2], u[3], hi[i / 2 + 1], lw[i / 2 + 1]);
+                    }
+                }
+                if constexpr (kStore) {
                     tmem_st8(lo_ + kTmY + 8 * sub, hi);
                     tmem_st8(lo_ + kTmY + 32 + 8 * sub, lw);
                 } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) split2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), hi[i], lw[i]);
                     tmem_st8(lo_ + kTmA + 32 * e + 8 * sub, hi);
                     tmem_st8(lo_ + kTmAl + 32 * e + 8 * sub, lw);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(yu);
+                if (lane == 0) {
+                    mbar_arrive(yu);
+                    mbar_arrive(&sfree[k]);
+                }
             }
         }
         if (a.h_final && wait_warp(rdyS, (uint32_t)(nc - 1) & 1u, abort_flag, status)) {
@@ -534,8 +547,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4 *>(stage2 + pn * 4096 + swz(lane, i)) =
                             make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 }
+                tc_fence_before();
                 fence_proxy_async();
                 __syncwarp();
+                if (lane == 0) mbar_arrive(ost);
                 if (lane == 0 && p0 < a.P) {
                     const int unit = (b * a.H + h + e) * nc + c;
                     for (int pn = 0; pn < NT / 64; ++pn)
