@@ -50,9 +50,12 @@ cudaError_t delta_mma_bwd(const DeltaProblem &p, const DeltaGrads &g, void *ws, 
 struct DeltaChain {
     const char *prep;
     int64_t prep_bytes;  // per chunk and head
-    int *status;
+    int *status, *flags;  // cleared before: the status word, a counter per CTA
+    float *hand;          // delta_tc_hand_bytes
     void *states, *err, *u;
 };
+int delta_tc_grid(const DeltaProblem &p);
+size_t delta_tc_hand_bytes(const DeltaProblem &p);
 cudaError_t delta_tc_chain(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s);
 
 // one token (p.L, p.h0, p.h_final unused); state_out may be state_in

@@ -206,7 +206,7 @@ template <int NT, bool BWD>
 __global__ void __launch_bounds__(kThr)
     k_delta_prep(const __nv_bfloat16 *__restrict__ Bm, const __nv_bfloat16 *__restrict__ Cm, const __nv_bfloat16 *__restrict__ g,
                  const __nv_bfloat16 *__restrict__ beta, int64_t L, int H, int G, int N, int slices, char *__restrict__ ws,
-                 int *__restrict__ status) {
+                 int *__restrict__ clear, int nclear) {
     extern __shared__ __align__(128) char raw[];
     PrepSmem<NT> &sm = *reinterpret_cast<PrepSmem<NT> *>(raw);
     using Lay = Prep<BWD>;
@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(kThr)
     const int grp = blockIdx.y / slices, slice = blockIdx.y % slices, per = H / G;
     const int h_begin = grp * per + per * slice / slices, h_end = grp * per + per * (slice + 1) / slices;
     const uint32_t ka = smem_addr(sm.k), qa = smem_addr(sm.q);
-    if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) *status = 0;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+        for (int i = tid; i < nclear; i += kThr) clear[i] = 0;
     load_tile<NT / 8>(ka, Bm, b, L, t0, G, grp, N, 0);
     load_tile<NT / 8>(qa, Cm, b, L, t0, G, grp, N, 0);
     cp_commit();
@@ -998,7 +999,7 @@ __global__ void __launch_bounds__(kGThr)
 }
 
 template <int NT, bool BWD>
-cudaError_t prep_launch(const DeltaProblem &p, char *ws, int *status, cudaStream_t s) {
+cudaError_t prep_launch(const DeltaProblem &p, char *ws, int *clear, int nclear, cudaStream_t s) {
     using bf = __nv_bfloat16;
     const int64_t nc = (p.L + kC - 1) / kC, units = nc * p.G * p.B;
     const int per = (int)(p.H / p.G);
@@ -1012,17 +1013,25 @@ cudaError_t prep_launch(const DeltaProblem &p, char *ws, int *status, cudaStream
     dim3 grid((unsigned)nc, (unsigned)(p.G * slices), (unsigned)p.B);
     k_delta_prep<NT, BWD><<<grid, kThr, smem, s>>>(static_cast<const bf *>(p.Bm), static_cast<const bf *>(p.Cm),
                                                    static_cast<const bf *>(p.g), static_cast<const bf *>(p.beta), p.L,
-                                                   (int)p.H, (int)p.G, (int)p.N, slices, ws, status);
+                                                   (int)p.H, (int)p.G, (int)p.N, slices, ws, clear, nclear);
     return cudaGetLastError();
 }
 
-// The workspace begins with the status word of the bounded waits, which k_delta_prep clears.
+// The workspace begins with the status word of the bounded waits and, 256 bytes on, the chain's counters,
+// a CTA each; k_delta_prep clears both.
+size_t head_bytes(const DeltaProblem &p) { return kWsAlign + align_up((size_t)delta_tc_grid(p) * sizeof(int), kWsAlign); }
+
 template <int NT>
 cudaError_t fwd_launch(const DeltaProblem &p, char *ws, cudaStream_t s) {
     using L = Prep<false>;
     int *status = reinterpret_cast<int *>(ws);
-    const cudaError_t e = prep_launch<NT, false>(p, ws + kWsAlign, status, s);
-    return e ? e : delta_tc_chain(p, DeltaChain{ws + kWsAlign, L::bytes, status, nullptr, nullptr, nullptr}, s);
+    const size_t at = head_bytes(p);
+    char *prep = ws + at + align_up(delta_tc_hand_bytes(p), kWsAlign);
+    const cudaError_t e = prep_launch<NT, false>(p, prep, status, (int)(at / sizeof(int)), s);
+    return e ? e
+             : delta_tc_chain(p, DeltaChain{prep, L::bytes, status, status + kWsAlign / sizeof(int),
+                                            reinterpret_cast<float *>(ws + at), nullptr, nullptr, nullptr},
+                              s);
 }
 
 // Slices of a group's heads in k_delta_grads_mma: the number that makes (waves of CTAs on 148 SMs) x (heads
@@ -1040,7 +1049,7 @@ int grads_slices(const DeltaProblem &p) {
 
 // Workspace of the backward pass, as byte offsets.
 struct BwdLayout {
-    size_t prep, states, cots, err, u, z, dB, dC, total;
+    size_t hand, prep, states, cots, err, u, z, dB, dC, total;
 };
 BwdLayout bwd_layout(const DeltaProblem &p) {
     const size_t chunks = (size_t)(p.B * p.H) * (size_t)((p.L + kC - 1) / kC);
@@ -1048,12 +1057,13 @@ BwdLayout bwd_layout(const DeltaProblem &p) {
     const int slices = grads_slices(p);
     const size_t part = slices > 1 ? (size_t)(p.B * p.L * p.G * slices * p.N) * 4 : 0;
     BwdLayout l{};
-    size_t at = kWsAlign;  // after the status word
+    size_t at = head_bytes(p);
     const auto take = [&](size_t bytes) {
         const size_t here = at;
         at += align_up(bytes, kWsAlign);
         return here;
     };
+    l.hand = take(delta_tc_hand_bytes(p));
     l.prep = take(chunks * Prep<true>::bytes);
     l.states = take(chunks * (size_t)(p.P * p.N) * 2);
     l.cots = take(chunks * (size_t)(p.P * p.N) * 2);
@@ -1076,10 +1086,12 @@ cudaError_t bwd_launch(const DeltaProblem &p, const DeltaGrads &gr, char *ws, cu
     const char *prep = ws + l.prep;
     using Lay = Prep<true>;
     int *status = reinterpret_cast<int *>(ws);
-    cudaError_t e = prep_launch<NT, true>(p, ws + l.prep, status, s);
+    cudaError_t e = prep_launch<NT, true>(p, ws + l.prep, status, (int)(head_bytes(p) / sizeof(int)), s);
     DeltaProblem f = p;  // the states alone: no output, no final state
     f.h_final = nullptr;
-    if (!e) e = delta_tc_chain(f, DeltaChain{prep, Lay::bytes, status, states, err, u}, s);
+    if (!e) e = delta_tc_chain(f, DeltaChain{prep, Lay::bytes, status, status + kWsAlign / sizeof(int), reinterpret_cast<float *>(ws + l.hand),
+                                         states, err, u},
+                           s);
     if (e) return e;
     constexpr int smem = sizeof(ChainBwdSmem<NT>), gsmem = sizeof(GradsSmem<NT>);
     if ((e = cudaFuncSetAttribute(k_delta_chain_bwd<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
@@ -1104,13 +1116,19 @@ cudaError_t bwd_launch(const DeltaProblem &p, const DeltaGrads &gr, char *ws, cu
 
 }  // namespace
 
+// From 24 tokens on, or from 10 where there are more than 4 CTAs of the sequential kernel for each SM: its
+// time is that of its token chain, 0.5 us a token where they all run at once (96 CTAs, 24 tokens: 14.5
+// against 18.0 us here, 32 tokens: 17.6 against 18.1; 768 CTAs, 8 tokens: 17.5 against 18.7, 16 tokens: 27.2
+// against 18.7).
 bool delta_mma_supported(const DeltaProblem &p) {
-    return p.dtype == SSD_BF16 && p.N <= 128 && p.N % 8 == 0 && p.P % 8 == 0 && p.L >= 8 && p.L < (1ll << 31) &&
+    if (p.L < (p.B * p.H * ((p.P + 15) / 16) > 4 * 148 ? 10 : 24)) return false;
+    return p.dtype == SSD_BF16 && p.N <= 128 && p.N % 8 == 0 && p.P % 8 == 0 && p.L < (1ll << 31) &&
            p.B * p.H * ((p.L + kC - 1) / kC) < (1ll << 31);
 }
 
 size_t delta_mma_fwd_workspace_bytes(const DeltaProblem &p) {
-    return kWsAlign + (size_t)(p.B * p.H) * (size_t)((p.L + kC - 1) / kC) * Prep<false>::bytes;
+    return head_bytes(p) + align_up(delta_tc_hand_bytes(p), kWsAlign) +
+           (size_t)(p.B * p.H) * (size_t)((p.L + kC - 1) / kC) * Prep<false>::bytes;
 }
 
 cudaError_t delta_mma_fwd(const DeltaProblem &p, void *ws, cudaStream_t s) {

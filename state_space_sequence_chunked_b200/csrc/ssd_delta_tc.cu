@@ -63,12 +63,55 @@ struct ChainArgs {
     const float *h0;
     const char *prep;
     int64_t prep_bytes;  // per chunk and head
-    int64_t L;
-    int H, P, G, N;
+    int nc, H, P, G, N;
+    int tiles, streams;  // of 128 rows per head; (tiles x heads or head pairs x batch)
     float *h_final;
+    float *hand;  // [CTA][128 rows][NT]: states handed on to the next CTA
+    int *flags;   // [CTA]: T warps that have written theirs
     int *status;
     int wait_us;
 };
+
+// The chunks of all streams, in order, are cut into equal contiguous shares, one per CTA. A share may
+// begin and end inside a stream; its last, begun stream runs first and its first, begun by the CTA
+// before, runs last, so that a state handed on is ready long before it is read. Shares are no shorter
+// than a stream, so a stream is cut at most once.
+struct Seg {
+    int stream, c0, c1;
+};
+struct Share {
+    int64_t lo, hi;
+    int nc, head, full0, full, n;
+    __device__ __forceinline__ Share(int64_t total, int nc_, int i, int grid) : nc(nc_) {
+        lo = total * i / grid, hi = total * (i + 1) / grid;
+        head = (int)(hi % nc);
+        full0 = (int)((lo + nc - 1) / nc);
+        full = (int)(hi / nc) - full0;
+        n = (head ? 1 : 0) + full + (lo % nc ? 1 : 0);
+    }
+    __device__ __forceinline__ Seg at(int j) const {
+        if (head && j == 0) return Seg{full0 + full, 0, head};
+        j -= head ? 1 : 0;
+        return j < full ? Seg{full0 + j, 0, nc} : Seg{full0 - 1, (int)(lo % nc), nc};
+    }
+};
+
+// Bounded wait for `want` arrivals on a counter in global memory.
+__device__ __noinline__ bool wait_count(const int *flag, int want, volatile int *abort_flag, int *status) {
+    const unsigned long long t0 = now_ns(), lim = wait_limit_ns(abort_flag);
+    for (;;) {
+        int v;
+        asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+        if (v >= want) return true;
+        if (*abort_flag) return false;
+        if (now_ns() - t0 > lim) {
+            *abort_flag = 1;
+            atomicOr(status, 1);
+            return false;
+        }
+        __nanosleep(200);
+    }
+}
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
@@ -160,9 +203,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     int *status = a.status;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.y * HB, grp = h / (a.H / a.G), b = blockIdx.z;
-    const int pc = PAIR ? 0 : blockIdx.x * 128;
-    const int nc = (int)((a.L + kC - 1) / kC);
+    const int nc = a.nc;
+    const Share share((int64_t)a.streams * nc, nc, blockIdx.x, gridDim.x);
+    const int steps = (int)(share.hi - share.lo);
+    // batch row, first head and first state row of a stream
+    const auto place = [&](int stream, int &b, int &h, int &pc) {
+        const int tile = stream % a.tiles, hy = stream / a.tiles % (a.H / HB);
+        b = stream / a.tiles / (a.H / HB), h = hy * HB, pc = 128 * tile;
+    };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -201,28 +249,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------- loads
         if (lane == 0) {
             const uint64_t keep = policy_evict_last(), stream = policy_evict_first();
-            int c = 0;
-            for (; c < nc; ++c) {
-                const int k = c & 1;
-                if (c >= 2 && !wait_phase(&sfree[k], (uint32_t)((c - 2) >> 1) & 1u, abort_flag, status)) break;
-                unsigned char *st = sm + k * Z::stage;
-                mbar_arrive_tx(&full[k], Z::tx);
-                for (int pn = 0; pn < NT / 64; ++pn)
-                    tma_load_4d_hint(st + Z::k + pn * kPanel, &tm_k, &full[k], 64 * pn, grp, c * kC, b, keep);
-                for (int pn = 0; pn < 2; ++pn)
-                    tma_load_4d_hint(st + Z::x + pn * kPanel, &tm_x, &full[k], PAIR ? 0 : pc + 64 * pn, PAIR ? h + pn : h, c * kC, b,
-                                     stream);
-                for (int e = 0; e < HB; ++e)
-                    bulk_load(st + Z::w + e * Z::head, a.prep + (((int64_t)b * a.H + h + e) * nc + c) * a.prep_bytes, Z::head, &full[k]);
-                if constexpr (!kStore)
+            int it = 0;
+            bool ok = true;
+            for (int j = 0; ok && j < share.n; ++j) {
+                const Seg sg = share.at(j);
+                int b, h, pc;
+                place(sg.stream, b, h, pc);
+                const int grp = h / (a.H / a.G);
+                for (int c = sg.c0; c < sg.c1; ++c, ++it) {
+                    const int k = it & 1;
+                    if (it >= 2 && !(ok = wait_phase(&sfree[k], (uint32_t)((it - 2) >> 1) & 1u, abort_flag, status))) break;
+                    unsigned char *st = sm + k * Z::stage;
+                    mbar_arrive_tx(&full[k], Z::tx);
                     for (int pn = 0; pn < NT / 64; ++pn)
-                        tma_load_4d_hint(st + Z::q + pn * kPanel, &tm_q, &full[k], 64 * pn, grp, c * kC, b, keep);
+                        tma_load_4d_hint(st + Z::k + pn * kPanel, &tm_k, &full[k], 64 * pn, grp, c * kC, b, keep);
+                    for (int pn = 0; pn < 2; ++pn)
+                        tma_load_4d_hint(st + Z::x + pn * kPanel, &tm_x, &full[k], PAIR ? 0 : pc + 64 * pn, PAIR ? h + pn : h, c * kC,
+                                         b, stream);
+                    for (int e = 0; e < HB; ++e)
+                        bulk_load(st + Z::w + e * Z::head, a.prep + (((int64_t)b * a.H + h + e) * nc + c) * a.prep_bytes, Z::head,
+                                  &full[k]);
+                    if constexpr (!kStore)
+                        for (int pn = 0; pn < NT / 64; ++pn)
+                            tma_load_4d_hint(st + Z::q + pn * kPanel, &tm_q, &full[k], 64 * pn, grp, c * kC, b, keep);
+                }
             }
             // loads in flight land before the CTA exits
             for (int i = 1; i <= 2; ++i) {
-                if (c - i < 0) continue;
+                if (it - i < 0) continue;
                 const unsigned long long w0 = now_ns();
-                while (!mbar_try(&full[(c - i) & 1], (uint32_t)((c - i) >> 1) & 1u) && now_ns() - w0 < kWaitNs) {
+                while (!mbar_try(&full[(it - i) & 1], (uint32_t)((it - i) >> 1) & 1u) && now_ns() - w0 < kWaitNs) {
                 }
             }
         }
@@ -248,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         constexpr std::true_type add{};
         constexpr std::false_type set{};
-        for (int c = 0; c < nc; ++c) {
+        for (int c = 0; c < steps; ++c) {
             const int k = c & 1;
             const uint32_t par = (uint32_t)c & 1u;
             const uint32_t st = smem_u32(sm) + k * Z::stage;
@@ -323,8 +379,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int qtr = warp & 3, sub = (warp - 4) >> 2, e = PAIR ? qtr >> 1 : 0;
         const uint32_t lo_ = tmem + ((uint32_t)(32 * qtr) << 16);  // this warp's lanes
         const int pp = (qtr & 1) * 32 + lane;                      // row within the x panel qtr >> 1
-        const int p = PAIR ? pp : pc + 32 * qtr + lane;            // state row of the head
-        const int64_t srow = ((int64_t)b * a.H + h + e) * a.P + p;
         constexpr int SC = NT / 4;  // state columns of this warp, from n0 on
         const int n0 = sub * SC, tk0 = 16 * sub;  // and tokens
         if constexpr (PAIR) {  // zeros in the other head's tokens
@@ -332,12 +386,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st8(lo_ + kTmA + 32 * (1 - e) + 8 * sub, zero);
             tmem_st8(lo_ + kTmAl + 32 * (1 - e) + 8 * sub, zero);
         }
-        for (int c = 0; c < nc; ++c) {
-            const int k = c & 1;
-            const uint32_t par = (uint32_t)c & 1u;
-            if (!wait_warp(&full[k], (uint32_t)(c >> 1) & 1u, abort_flag, status)) break;
+        int it = 0;
+        bool ok = true;
+        for (int j = 0; ok && j < share.n; ++j) {
+        const Seg sg = share.at(j);
+        int b, h, pc;
+        place(sg.stream, b, h, pc);
+        const int p = PAIR ? pp : pc + 32 * qtr + lane;  // state row of the head
+        const int64_t srow = ((int64_t)b * a.H + h + e) * a.P + p;
+        if (sg.c0 > 0 && !(ok = __all_sync(0xffffffffu, wait_count(a.flags + blockIdx.x - 1, kTWarps, abort_flag, status)))) break;
+        int c = sg.c0;
+        for (; c < sg.c1; ++c, ++it) {
+            const int k = it & 1;
+            const uint32_t par = (uint32_t)it & 1u;
+            if (!wait_warp(&full[k], (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
             const float *eg = scal_of(k, e), *ek = eg + kC, *bt = eg + 2 * kC;
-            if (c > 0) {
+            if (it > 0) {
                 if (!wait_warp(rdyS, par ^ 1u, abort_flag, status)) break;
                 if (kStore && !wait_warp(ost, par ^ 1u, abort_flag, status)) break;
                 tc_fence_after();
@@ -351,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             {
                 uint32_t s[SC];
-                if (c > 0) {
+                if (c > sg.c0) {
                     if constexpr (SC == 32) {
                         tmem_ld32(lo_ + kTmS + n0, s);
                         tmem_wait_ld(s);
@@ -363,7 +427,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < SC; i += 4) {
                         float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (a.h0 && p < a.P && n0 + i < a.N) f = *reinterpret_cast<const float4 *>(a.h0 + srow * a.N + n0 + i);
+                        if (c > 0)
+                            f = __ldcg(reinterpret_cast<const float4 *>(a.hand + ((int64_t)(blockIdx.x - 1) * 128 + 32 * qtr + lane) * NT + n0 + i));
+                        else if (a.h0 && p < a.P && n0 + i < a.N)
+                            f = *reinterpret_cast<const float4 *>(a.h0 + srow * a.N + n0 + i);
                         s[i] = __float_as_uint(f.x), s[i + 1] = __float_as_uint(f.y);
                         s[i + 2] = __float_as_uint(f.z), s[i + 3] = __float_as_uint(f.w);
                     }
@@ -449,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(ub);
                 if constexpr (kStore) {  // the last chunk's u and err have left
-                    if (c > 0 && !wait_warp(ofree, par ^ 1u, abort_flag, status)) break;
+                    if (it > 0 && !wait_warp(ofree, par ^ 1u, abort_flag, status)) break;
                 }
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
@@ -479,34 +546,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (a.h_final && wait_warp(rdyS, (uint32_t)(nc - 1) & 1u, abort_flag, status)) {
-            tc_fence_after();
+        // the segment's end: the final state, or the state for the CTA that goes on
+        if (c < sg.c1 || !wait_warp(rdyS, (uint32_t)(it - 1) & 1u, abort_flag, status)) break;
+        tc_fence_after();
+        float *dst = sg.c1 < nc ? a.hand + ((int64_t)blockIdx.x * 128 + 32 * qtr + lane) * NT
+                                : a.h_final && p < a.P ? a.h_final + srow * a.N : nullptr;
+        const int cols = sg.c1 < nc ? NT : a.N;
 #pragma unroll
-            for (int j = 0; j < SC; j += 16) {
-                uint32_t s[16];
-                tmem_ld16(lo_ + kTmS + n0 + j, s);
-                tmem_wait_ld();
-                if (p < a.P)
+        for (int jj = 0; jj < SC; jj += 16) {
+            uint32_t s[16];
+            tmem_ld16(lo_ + kTmS + n0 + jj, s);
+            tmem_wait_ld();
+            if (dst)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (n0 + j + 4 * i < a.N)
-                            *reinterpret_cast<uint4 *>(a.h_final + srow * a.N + n0 + j + 4 * i) =
-                                make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
-            }
+                for (int i = 0; i < 4; ++i)
+                    if (n0 + jj + 4 * i < cols)
+                        *reinterpret_cast<uint4 *>(dst + n0 + jj + 4 * i) = make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+        }
+        if (sg.c1 < nc) {
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(a.flags + blockIdx.x) : "memory");
+        }
         }
     } else {
         // ------------------------------------------------------------- O: outputs, 32 state rows x 64 tokens per warp
         const int qtr = warp & 3, e = PAIR ? qtr >> 1 : 0;
         const uint32_t lo_ = tmem + ((uint32_t)(32 * qtr) << 16);
-        const int p0 = PAIR ? (qtr & 1) * 32 : pc + 32 * qtr;  // first state row of the head
         unsigned char *stage0 = sm + Z::out + qtr * 4096, *stage1 = stage0 + 4 * 4096;  // [64 tokens][32 rows]
         unsigned char *stage2 = sm + Z::out + 8 * 4096 + qtr * 64 * NT;  // kStore: [columns / 64][32 rows][128 B], swizzled
         const uint64_t pol = policy_evict_first();
-        for (int c = 0; c < nc; ++c) {
-            const int k = c & 1;
-            const uint32_t par = (uint32_t)c & 1u;
+        int it = 0;
+        bool ok = true;
+        for (int j = 0; ok && j < share.n; ++j) {
+        const Seg sg = share.at(j);
+        int b, h, pc;
+        place(sg.stream, b, h, pc);
+        const int p0 = PAIR ? (qtr & 1) * 32 : pc + 32 * qtr;  // first state row of the head
+        int c = sg.c0;
+        for (; c < sg.c1; ++c, ++it) {
+            const int k = it & 1;
+            const uint32_t par = (uint32_t)it & 1u;
             if constexpr (!kStore) {
-                if (!wait_warp(&full[k], (uint32_t)(c >> 1) & 1u, abort_flag, status)) break;
+                if (!wait_warp(&full[k], (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
                 if (!wait_warp(rdyQ, par, abort_flag, status)) break;
                 tc_fence_after();
                 const float *eg = scal_of(k, e);
@@ -593,6 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bulk_commit();
             }
         }
+        ok = c == sg.c1;
+        }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
     }
@@ -637,6 +721,11 @@ bool encode_states(CUtensorMap *m, const void *base, int64_t N, int64_t P, int64
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Two heads of a group side by side where each fits 64 rows: half the streams, and K, Q loaded once for
+// both.
+bool pairs(const DeltaProblem &p) { return p.P <= 64 && (p.H / p.G) % 2 == 0; }
+int64_t streams_of(const DeltaProblem &p) { return pairs(p) ? p.B * (p.H / 2) : p.B * p.H * ((p.P + 127) / 128); }
+
 template <int NT, bool PAIR, bool kStore>
 cudaError_t launch(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s) {
     CUtensorMap tk, tq, tx, t0, t1, ts;
@@ -646,24 +735,47 @@ cudaError_t launch(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s) 
         !encode_out(&t0, kStore ? ch.u : p.y, p.P, p.H, p.L, p.B) || !encode_out(&t1, kStore ? ch.err : p.y, p.P, p.H, p.L, p.B))
         return cudaErrorInvalidValue;
     if (kStore ? !encode_states(&ts, ch.states, p.N, p.P, p.B * p.H * nc) : (ts = t0, false)) return cudaErrorInvalidValue;
-    const ChainArgs a{p.h0, ch.prep, ch.prep_bytes, p.L, (int)p.H, (int)p.P, (int)p.G, (int)p.N,
-                      p.h_final, ch.status, wait_limit_us()};
+    const int tiles = PAIR ? 1 : (int)((p.P + 127) / 128);
+    const int64_t streams = streams_of(p);
+    const int grid = delta_tc_grid(p);
+    const ChainArgs a{p.h0,   ch.prep,   ch.prep_bytes, (int)nc,  (int)p.H,  (int)p.P,        (int)p.G, (int)p.N,
+                      tiles,  (int)streams, p.h_final,  ch.hand, ch.flags, ch.status, wait_limit_us()};
     constexpr int smem = Lay<NT, PAIR, kStore>::bytes;
     const auto kernel = k_delta_tc<NT, PAIR, kStore>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e) return e;
-    const dim3 grid(PAIR ? 1u : (unsigned)((p.P + 127) / 128), (unsigned)(PAIR ? p.H / 2 : p.H), (unsigned)p.B);
-    kernel<<<grid, kThreads, smem, s>>>(tk, tq, tx, t0, t1, ts, a);
-    return cudaGetLastError();
+    // Where a stream is cut its CTAs have to be resident together, which a cooperative launch guarantees.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = streams > grid ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, tk, tq, tx, t0, t1, ts, a);
 }
 
 template <int NT, bool kStore>
 cudaError_t launch_pair(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s) {
-    // two heads of a group side by side where each fits 64 rows: half the CTAs, and K, Q loaded once for both
-    return p.P <= 64 && (p.H / p.G) % 2 == 0 ? launch<NT, true, kStore>(p, ch, s) : launch<NT, false, kStore>(p, ch, s);
+    return pairs(p) ? launch<NT, true, kStore>(p, ch, s) : launch<NT, false, kStore>(p, ch, s);
 }
 
 }  // namespace
+
+// One CTA per SM (it takes all of TMEM), or per stream where there are fewer.
+int delta_tc_grid(const DeltaProblem &p) {
+    const int sms = num_sms() > 0 ? num_sms() : 148;
+    const int64_t streams = streams_of(p);
+    return (int)(streams < sms ? streams : sms);
+}
+
+size_t delta_tc_hand_bytes(const DeltaProblem &p) {
+    const int grid = delta_tc_grid(p);
+    return streams_of(p) > grid ? (size_t)grid * 128 * (p.N <= 64 ? 64 : 128) * sizeof(float) : 0;
+}
 
 cudaError_t delta_tc_chain(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s) {
     const bool store = ch.states != nullptr;

@@ -310,3 +310,34 @@ def test_two_streams_at_once(cuda_device):
     for round_ in got:
         for g, w in zip(round_, want):
             assert all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(g, w))
+
+
+CUT = [(2, 130, 160, 16, 1, 64), (1, 200, 152, 72, 2, 64), (3, 100, 50, 136, 5, 128), (5, 330, 60, 64, 1, 128)]
+
+
+@pytest.mark.parametrize("shape", CUT, ids=str)
+def test_more_streams_than_sms(cuda_device, shape):
+    """More head pairs (or heads) than SMs: streams are cut between CTAs and their state handed on."""
+    d = draw(*shape, "bf16", seed=91)
+    check_fwd(d, cuda_device, "bf16")
+    check_bwd(d, cuda_device, "bf16")
+
+
+def test_waits_that_run_out(cuda_device):
+    """With a limit of 1 us some wait between the warps runs out: the call comes back, says so, and the
+    next one at the normal limit is right."""
+    shape = CUT[0]
+    d = draw(*shape, "bf16", seed=92)
+    a = on(d, cuda_device)
+    n = ssd.delta_fwd_plan(*shape, ssd.SSD_BF16)["workspace_bytes"]
+    ws = torch.empty(n, dtype=torch.uint8, device=cuda_device)
+    ssd.ssd_delta_fwd(*a, workspace=ws)
+    assert ssd.delta_status(shape, ssd.SSD_BF16, ws) == 0
+    try:
+        ssd.set_wait_limit_us(1)
+        ssd.ssd_delta_fwd(*a, workspace=ws)
+        assert ssd.delta_status(shape, ssd.SSD_BF16, ws) == 6  # SSD_ERR_TIMEOUT
+    finally:
+        ssd.set_wait_limit_us(0)
+    check_fwd(d, cuda_device, "bf16")
+    assert ssd.delta_status((1, 4, 2, 64, 1, 64), ssd.SSD_BF16, None) == 0  # a path without waits
