@@ -461,19 +461,19 @@ def _at(t):
 
 def _delta_shape(x, g, beta, B, C, batched):
     """(ShapeT, dtype code) of the delta rule's inputs, checked against one another."""
-    lead = x.dim() - 2
-    if x.dim() != (4 if batched else 3) or B.dim() != x.dim():
-        raise ValueError("x and B: wrong number of dimensions")
-    dev, dt = x.get_device(), x.dtype
-    code = _dtype_code(x)
-    H, P = x.shape[-2:]
-    G, N = B.shape[-2:]
-    _need("x", x, x.shape, dt, dev)
-    _need("g", g, x.shape[:lead + 1], dt, dev)
-    _need("beta", beta, x.shape[:lead + 1], dt, dev)
-    _need("B", B, (*x.shape[:lead], G, N), dt, dev)
-    _need("C", C, (*x.shape[:lead], G, N), dt, dev)
-    return ShapeT(x.shape[0], x.shape[1] if batched else 1, H, P, G, N), code
+    xs, bs, gs, dev, dt = x.shape, B.shape, g.shape, x.get_device(), x.dtype
+    # all in one expression: for single tokens the checks cost as much as the launch
+    if not (len(xs) == len(bs) == (4 if batched else 3) and xs[:-2] == bs[:-2] and gs == xs[:-1] and beta.shape == gs
+            and C.shape == bs and dev >= 0 and g.get_device() == dev and beta.get_device() == dev and B.get_device() == dev
+            and C.get_device() == dev and g.dtype is dt and beta.dtype is dt and B.dtype is dt and C.dtype is dt
+            and x.is_contiguous() and g.is_contiguous() and beta.is_contiguous() and B.is_contiguous() and C.is_contiguous()):
+        if len(xs) != (4 if batched else 3) or len(bs) != len(xs):
+            raise ValueError("x and B: wrong number of dimensions")
+        for name, t, shape in (("x", x, xs), ("g", g, xs[:-1]), ("beta", beta, xs[:-1]), ("B", B, (*xs[:-2], *bs[-2:])),
+                               ("C", C, (*xs[:-2], *bs[-2:]))):
+            _need(name, t, torch.Size(shape), dt, dev)
+        raise ValueError("x, g, beta, B, C do not fit one another")
+    return ShapeT(xs[0], xs[1] if batched else 1, xs[-2], xs[-1], bs[-2], bs[-1]), _dtype_code(x)
 
 
 def _delta_plan(fn, shape, code):
@@ -512,7 +512,7 @@ def ssd_delta_fwd(x, g, beta, B, C, h0=None, *, y=None, h_final=None, return_fin
     C (queries) [B,L,G,N], h0 [B,H,P,N] f32."""
     shape, code = _delta_shape(x, g, beta, B, C, True)
     dev = x.get_device()
-    state = torch.Size((shape.batch, shape.nheads, shape.headdim, shape.dstate))
+    state = (x.shape[0], *x.shape[2:], B.shape[-1])
     _need("h0", h0, state, torch.float32, dev)
     _need("y", y, x.shape, x.dtype, dev)
     _need("h_final", h_final, state, torch.float32, dev)
@@ -540,7 +540,7 @@ def ssd_delta_decode_step(state, x, g, beta, B, C, *, state_out=None, y=None, st
     state [B,H,P,N] f32 is updated in place, or left alone and the new one written to state_out."""
     shape, code = _delta_shape(x, g, beta, B, C, False)
     dev = x.get_device()
-    size = torch.Size((shape.batch, shape.nheads, shape.headdim, shape.dstate))
+    size = (*x.shape, B.shape[-1])
     _need("state", state, size, torch.float32, dev)
     _need("state_out", state_out, size, torch.float32, dev)
     _need("y", y, x.shape, x.dtype, dev)
@@ -560,7 +560,7 @@ def ssd_delta_bwd(x, g, beta, B, C, h0, dy, dh_final=None, *, want_dh0: bool = T
     tensors to write into."""
     shape, code = _delta_shape(x, g, beta, B, C, True)
     dev = x.get_device()
-    state = torch.Size((shape.batch, shape.nheads, shape.headdim, shape.dstate))
+    state = (x.shape[0], *x.shape[2:], B.shape[-1])
     _need("h0", h0, state, torch.float32, dev)
     _need("dy", dy, x.shape, x.dtype, dev)
     _need("dh_final", dh_final, state, torch.float32, dev)
