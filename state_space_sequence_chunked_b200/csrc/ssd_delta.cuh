@@ -45,18 +45,21 @@ size_t delta_mma_bwd_workspace_bytes(const DeltaProblem &p);
 int delta_mma_bwd_kernels(const DeltaProblem &p);
 cudaError_t delta_mma_bwd(const DeltaProblem &p, const DeltaGrads &g, void *ws, cudaStream_t s);
 
-// The chain over the chunks on tcgen05 (ssd_delta_tc.cu), after k_delta_prep. With states set it is the
-// backward pass's recomputation: states [B, H, chunks, P, N], err and u [B, L, H, P], bf16, instead of y.
+// The chains over the chunks on tcgen05 (ssd_delta_tc.cu), after k_delta_prep: the forward's, or the
+// backward pass's recomputation and reverse chain together. states and cots [B, H, chunks, P, N], err, u
+// and z [B, L, H, P], bf16, are the latter's.
 struct DeltaChain {
     const char *prep;
-    int64_t prep_bytes;  // per chunk and head
-    int *status, *flags;  // cleared before: the status word, a counter per CTA
-    float *hand;          // delta_tc_hand_bytes
-    void *states, *err, *u;
+    int64_t prep_bytes;    // per chunk and head
+    int scal_at, rows_at;  // the backward pass: the scalars; W and P by rows of blocks
+    int *status, *flags;   // cleared before: the status word, a counter per CTA
+    float *hand;           // delta_tc_hand_bytes
+    void *states, *err, *u, *cots, *z;
 };
-int delta_tc_grid(const DeltaProblem &p);
-size_t delta_tc_hand_bytes(const DeltaProblem &p);
-cudaError_t delta_tc_chain(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s);
+int delta_tc_grid(const DeltaProblem &p, bool backward);
+size_t delta_tc_hand_bytes(const DeltaProblem &p, bool backward);
+cudaError_t delta_tc_fwd(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s);
+cudaError_t delta_tc_bwd(const DeltaProblem &p, const DeltaGrads &g, const DeltaChain &ch, cudaStream_t s);
 
 // one token (p.L, p.h0, p.h_final unused); state_out may be state_in
 cudaError_t delta_step(const DeltaProblem &p, const float *state_in, float *state_out, cudaStream_t s);

@@ -38,16 +38,17 @@ __host__ __device__ constexpr int block_at(int a, int b) { return a * (a + 1) / 
 // Q K^T (forward only) and the scalars exp(cum), exp(cum_end - cum), beta of the chunk's tokens, then cum as
 // a sum of two floats. The matrices are right operands of tcgen05 products without a swizzle: blocks of
 // 16 x 16 of the lower triangle, by column of blocks, each as 8 x 8 core matrices of 128 contiguous bytes
-// (rows 0-7: two halves of the columns, then rows 8-15). Then, for the backward pass alone, both matrices
-// transposed (hi, lo) as mma.sync fragments, one 16-byte vector per lane and block.
+// (rows 0-7: two halves of the columns, then rows 8-15). Then, for the backward pass alone, W and the masked
+// Q K^T (hi, lo each) by row of blocks, for products that sum over their rows (columns 0-7: the two
+// halves of the rows, then columns 8-15).
 constexpr int kBlockBytes = 512;
 constexpr int kWBytes = kBlocks * 2 * kBlockBytes;
 constexpr int kPBytes = kBlocks * kBlockBytes;
 constexpr int kScalBytes = 5 * kC * 4;
 template <bool BWD>
 struct Prep {
-    static constexpr int W = 0, P = kWBytes, scal = BWD ? kWBytes : P + kPBytes, WT = scal + kScalBytes, PT = WT + kWBytes;
-    static constexpr int bytes = BWD ? PT + kWBytes : scal + kScalBytes;
+    static constexpr int W = 0, P = kWBytes, scal = BWD ? kWBytes : P + kPBytes, Wr = scal + kScalBytes, Pr = Wr + kWBytes;
+    static constexpr int bytes = BWD ? Pr + kWBytes : scal + kScalBytes;
 };
 // block (a, b) by column of blocks: four of column 0, three of column 1, ...
 __host__ __device__ constexpr int column_at(int a, int b) { return b * 4 - b * (b - 1) / 2 + a - b; }
@@ -181,7 +182,18 @@ __device__ __forceinline__ void block_mma(float (&acc)[2][4], const uint32_t (&a
     }
 }
 
-// Block (a, b) of W, and for the backward pass its transpose as fragments.
+// Block (a, b) by row of blocks, hi and lo (fragments: rows 0-7, two halves of the columns, then rows 8-15).
+__device__ __forceinline__ void put_rows(char *out, int a, int b, int lane, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
+    uint32_t *t = reinterpret_cast<uint32_t *>(out + block_at(a, b) * kBlockBytes) + lane;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int at = 32 * ((e & 1) * 2 + (e >> 1));  // columns first
+        t[at] = hi[e];
+        t[at + kWBytes / 8] = lo[e];
+    }
+}
+
+// Block (a, b) of W.
 template <bool BWD>
 __device__ __forceinline__ void put_w(char *out, int a, int b, int lane, const float (&w)[2][4]) {
     uint32_t hi[4], lo[4];  // rows 0-7: two halves of the columns, then rows 8-15
@@ -195,11 +207,7 @@ __device__ __forceinline__ void put_w(char *out, int a, int b, int lane, const f
         t[32 * e] = hi[e];
         t[32 * e + kWBytes / 8] = lo[e];
     }
-    if constexpr (BWD) {
-        uint4 *o = reinterpret_cast<uint4 *>(out + Prep<BWD>::WT) + block_at(a, b) * 64 + lane;
-        o[0] = make_uint4(trans8(hi[0]), trans8(hi[2]), trans8(hi[1]), trans8(hi[3]));
-        o[32] = make_uint4(trans8(lo[0]), trans8(lo[2]), trans8(lo[1]), trans8(lo[3]));
-    }
+    if constexpr (BWD) put_rows(out + Prep<BWD>::Wr, a, b, lane, hi, lo);
 }
 
 template <int NT, bool BWD>
@@ -306,10 +314,11 @@ __global__ void __launch_bounds__(kThr)
             }
             if constexpr (BWD) {
                 uint32_t ph[4], pl[4];
-                split_b(p, 1.f, 1.f, ph, pl);
-                uint4 *o = reinterpret_cast<uint4 *>(out + Lay::PT) + block_at(a, cc) * 64 + lane;
-                o[0] = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-                o[32] = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+                split(p[0][0], p[0][1], ph[0], pl[0]);
+                split(p[1][0], p[1][1], ph[1], pl[1]);
+                split(p[0][2], p[0][3], ph[2], pl[2]);
+                split(p[1][2], p[1][3], ph[3], pl[3]);
+                put_rows(out + Lay::Pr, a, cc, lane, ph, pl);
             } else {
                 uint32_t *o = reinterpret_cast<uint32_t *>(out + Lay::P + column_at(a, cc) * kBlockBytes) + lane;
                 o[0] = pack(p[0][0], p[0][1]), o[32] = pack(p[1][0], p[1][1]);
@@ -406,244 +415,6 @@ __global__ void __launch_bounds__(kThr)
         }
         __syncwarp();
     }
-}
-
-// Accumulators T^T (16 state rows x 64 tokens), rounded, over this warp's columns of a [token][row]
-// tile and from there to rows of `dst` ([B, L, H, P]).
-__device__ __forceinline__ void put_tokens(const float (&T)[8][4], char *tile, __nv_bfloat16 *__restrict__ dst, int64_t b,
-                                           int64_t L, int64_t t0, int H, int h, int P, int pc, int warp, int lane) {
-    const uint32_t ta = smem_addr(tile);
-#pragma unroll
-    for (int jj = 0; jj < 4; ++jj)
-        stsm4t(ta + at16<kRowsCta * 2>(16 * jj + (lane & 7) + ((lane >> 4) << 3), 2 * warp + ((lane >> 3) & 1)),
-               pack(T[2 * jj][0], T[2 * jj][1]), pack(T[2 * jj][2], T[2 * jj][3]), pack(T[2 * jj + 1][0], T[2 * jj + 1][1]),
-               pack(T[2 * jj + 1][2], T[2 * jj + 1][3]));
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = 16 * i + (lane >> 1), v = 2 * warp + (lane & 1);
-        if (t0 + t < L && pc + 8 * v < P)
-            *reinterpret_cast<uint4 *>(dst + ((b * L + t0 + t) * H + h) * (int64_t)P + pc + 8 * v) =
-                *reinterpret_cast<const uint4 *>(tile + at16<kRowsCta * 2>(t, v));
-    }
-    __syncwarp();
-}
-
-// A state (16 rows of N columns per warp), rounded, through `tile` to [P, N] rows at dst.
-template <int NT>
-__device__ __forceinline__ void put_state(const float (&S)[NT / 8][4], char *tile, __nv_bfloat16 *__restrict__ dst, int P, int N,
-                                          int pc, int warp, int lane) {
-    const uint32_t ta = smem_addr(tile);
-#pragma unroll
-    for (int s = 0; s < NT / 16; ++s)
-        stsm4(ta + at16<NT * 2>(16 * warp + (lane & 15), 2 * s + (lane >> 4)), pack(S[2 * s][0], S[2 * s][1]),
-              pack(S[2 * s][2], S[2 * s][3]), pack(S[2 * s + 1][0], S[2 * s + 1][1]), pack(S[2 * s + 1][2], S[2 * s + 1][3]));
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < NT / 16; ++i) {
-        const int r = 16 * warp + (i * 32 + lane) / (NT / 8), v = (i * 32 + lane) % (NT / 8);
-        if (pc + r < P && 8 * v < N)
-            *reinterpret_cast<uint4 *>(dst + (int64_t)(pc + r) * N + 8 * v) =
-                *reinterpret_cast<const uint4 *>(tile + at16<NT * 2>(r, v));
-    }
-    __syncwarp();
-}
-
-template <int NT>
-__device__ __forceinline__ void load_state(float (&S)[NT / 8][4], const float *__restrict__ src, int64_t row, int P, int N, int p,
-                                           int tg) {
-#pragma unroll
-    for (int j = 0; j < NT / 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int n = 8 * j + 2 * tg + (e & 1), r = 8 * (e >> 1);
-            S[j][e] = src && n < N && p + r < P ? src[(row + r) * N + n] : 0.f;
-        }
-}
-template <int NT>
-__device__ __forceinline__ void store_state(const float (&S)[NT / 8][4], float *__restrict__ dst, int64_t row, int P, int N, int p,
-                                            int tg) {
-#pragma unroll
-    for (int j = 0; j < NT / 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int n = 8 * j + 2 * tg + (e & 1), r = 8 * (e >> 1);
-            if (n < N && p + r < P) dst[(row + r) * N + n] = S[j][e];
-        }
-}
-
-// T *= per-token factors (tokens are the columns)
-__device__ __forceinline__ void scale_tokens(float (&T)[8][4], const float *f, int tg) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float2 e = *reinterpret_cast<const float2 *>(f + 8 * j + 2 * tg);
-        T[j][0] *= e.x, T[j][1] *= e.y, T[j][2] *= e.x, T[j][3] *= e.y;
-    }
-}
-// left operand (hi, lo) of tokens 16 k .. + 15 of T, scaled per token
-__device__ __forceinline__ void split_tokens(const float (&T)[8][4], int k, const float *f, float sign, int tg, uint32_t (&hi)[4],
-                                             uint32_t (&lo)[4]) {
-    float t[2][4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        const float2 e = *reinterpret_cast<const float2 *>(f + 16 * k + 8 * n + 2 * tg);
-        const float x = sign * e.x, y = sign * e.y;
-        t[n][0] = x * T[2 * k + n][0], t[n][1] = y * T[2 * k + n][1], t[n][2] = x * T[2 * k + n][2], t[n][3] = y * T[2 * k + n][3];
-    }
-    split_a(t[0], t[1], hi, lo);
-}
-// S += (the left operand of tokens 16 k .. + 15) times those rows of a [token][column] tile
-template <int NT>
-__device__ __forceinline__ void rank16(float (&S)[NT / 8][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], uint32_t tile, int k,
-                                       int lane) {
-#pragma unroll
-    for (int j = 0; j < NT / 16; ++j) {
-        uint32_t f[4];
-        ldsm4t(f, tile + at16<NT * 2>(16 * k + (lane & 15), 2 * j + (lane >> 4)));
-        mma(S[2 * j], lo, f[0], f[1]);
-        mma(S[2 * j + 1], lo, f[2], f[3]);
-        mma(S[2 * j], hi, f[0], f[1]);
-        mma(S[2 * j + 1], hi, f[2], f[3]);
-    }
-}
-
-// ---------------------------------------------------------------------------------------------
-// k_delta_chain_bwd: the chain in reverse, laid out like the forward one. With D the cotangent of the
-// state leaving a chunk,
-//     F = tril(Q K^T o E)^T dY + (exp(cum_end - cum) K) D^T,   z = F + W^T (beta F),   r = beta z = dX,
-//     D <- exp(cum_end) D + (exp(cum) dY)^T Q - (exp(cum) r)^T K.
-// D of every chunk goes out in bf16 (an operand of k_delta_grads_mma), z too.
-template <int NT>
-struct ChainBwdStage {
-    __nv_bfloat16 k[kC * NT], q[kC * NT], dy[kC * kRowsCta];
-    char prep[Prep<true>::bytes - Prep<true>::scal];
-};
-template <int NT>
-struct ChainBwdSmem {
-    ChainBwdStage<NT> stage[2];
-    __nv_bfloat16 out[kRowsCta * NT];
-};
-
-template <int NT>
-__global__ void __launch_bounds__(kThr, 1)
-    k_delta_chain_bwd(const __nv_bfloat16 *__restrict__ dy, const __nv_bfloat16 *__restrict__ Bm,
-                      const __nv_bfloat16 *__restrict__ Cm, const float *__restrict__ dh_final, const char *__restrict__ ws,
-                      int64_t L, int H, int P, int G, int N, __nv_bfloat16 *__restrict__ dx, __nv_bfloat16 *__restrict__ z,
-                      __nv_bfloat16 *__restrict__ cots, float *__restrict__ dh0) {
-    extern __shared__ __align__(128) char raw[];
-    using Lay = Prep<true>;
-    ChainBwdSmem<NT> &sm = *reinterpret_cast<ChainBwdSmem<NT> *>(raw);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tg = lane & 3;
-    const int h = blockIdx.y, grp = h / (H / G), pc = blockIdx.x * kRowsCta, p0 = pc + 16 * warp;
-    const int64_t b = blockIdx.z, nc = (L + kC - 1) / kC;
-    const bool on = p0 < P;
-    const char *prep = ws + (b * H + h) * nc * (int64_t)Lay::bytes + Lay::scal;
-
-    const auto load = [&](int64_t c) {
-        ChainBwdStage<NT> &st = sm.stage[c & 1];
-        load_tile<NT / 8>(smem_addr(st.k), Bm, b, L, c * kC, G, grp, N, 0);
-        load_tile<NT / 8>(smem_addr(st.q), Cm, b, L, c * kC, G, grp, N, 0);
-        load_tile<kRowsCta / 8>(smem_addr(st.dy), dy, b, L, c * kC, H, h, P, pc);
-        const uint32_t dst = smem_addr(st.prep);
-        for (int i = tid; i < (int)sizeof(st.prep) / 16; i += kThr) cp16(dst + 16 * i, prep + c * Lay::bytes + 16 * i, true);
-        cp_commit();
-    };
-    load(nc - 1);
-
-    float D[NT / 8][4];
-    const int64_t row = (b * H + h) * (int64_t)P + p0 + gr;
-    load_state<NT>(D, dh_final, row, P, N, p0 + gr, tg);
-
-    for (int64_t c = nc - 1; c >= 0; --c) {
-        if (c > 0) {
-            load(c - 1);
-            cp_wait<1>();
-        } else {
-            cp_wait<0>();
-        }
-        __syncthreads();
-        ChainBwdStage<NT> &st = sm.stage[c & 1];
-        if (on) {
-            const uint32_t ka = smem_addr(st.k), qa = smem_addr(st.q), ya = smem_addr(st.dy);
-            const float *eg = reinterpret_cast<const float *>(st.prep), *ek = eg + kC, *bt = eg + 2 * kC;
-            const uint4 *wf = reinterpret_cast<const uint4 *>(st.prep + Lay::WT - Lay::scal) + lane;
-            const uint4 *pf = reinterpret_cast<const uint4 *>(st.prep + Lay::PT - Lay::scal) + lane;
-            put_state<NT>(D, reinterpret_cast<char *>(sm.out), cots + ((b * H + h) * nc + c) * (int64_t)P * N, P, N, pc, warp, lane);
-            float F[8][4];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) F[j][e] = 0.f;
-#pragma unroll
-            for (int s = 0; s < NT / 16; ++s) {  // D K^T
-                uint32_t hi[4], lo[4];
-                split_a(D[2 * s], D[2 * s + 1], hi, lo);
-#pragma unroll
-                for (int jj = 0; jj < 4; ++jj) {
-                    uint32_t bk[4];
-                    ldsm4(bk, ka + at16<NT * 2>(16 * jj + (lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1)));
-                    mma(F[2 * jj], lo, bk[0], bk[1]);
-                    mma(F[2 * jj + 1], lo, bk[2], bk[3]);
-                    mma(F[2 * jj], hi, bk[0], bk[1]);
-                    mma(F[2 * jj + 1], hi, bk[2], bk[3]);
-                }
-            }
-            scale_tokens(F, ek, tg);
-            uint32_t yf[4][4];  // dY^T as left operand, exact
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                ldsm4t(yf[k], ya + at16<kRowsCta * 2>(16 * k + (lane & 7) + ((lane >> 4) << 3), 2 * warp + ((lane >> 3) & 1)));
-#pragma unroll
-                for (int a = 0; a <= k; ++a) {  // tokens of block a gather from tokens of blocks k >= a
-                    const uint4 ph = pf[block_at(k, a) * 64], pl = pf[block_at(k, a) * 64 + 32];
-                    mma(F[2 * a], yf[k], pl.x, pl.y);
-                    mma(F[2 * a + 1], yf[k], pl.z, pl.w);
-                    mma(F[2 * a], yf[k], ph.x, ph.y);
-                    mma(F[2 * a + 1], yf[k], ph.z, ph.w);
-                }
-            }
-            uint32_t ah[4][4], al[4][4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) split_tokens(F, k, bt, 1.f, tg, ah[k], al[k]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int a = 0; a <= k; ++a) {
-                    const uint4 wh = wf[block_at(k, a) * 64], wl = wf[block_at(k, a) * 64 + 32];
-                    mma(F[2 * a], al[k], wh.x, wh.y);
-                    mma(F[2 * a + 1], al[k], wh.z, wh.w);
-                    mma(F[2 * a], ah[k], wl.x, wl.y);
-                    mma(F[2 * a + 1], ah[k], wl.z, wl.w);
-                    mma(F[2 * a], ah[k], wh.x, wh.y);
-                    mma(F[2 * a + 1], ah[k], wh.z, wh.w);
-                }
-            put_tokens(F, reinterpret_cast<char *>(st.dy), z, b, L, c * kC, H, h, P, pc, warp, lane);
-            scale_tokens(F, bt, tg);
-            put_tokens(F, reinterpret_cast<char *>(st.dy), dx, b, L, c * kC, H, h, P, pc, warp, lane);
-            const float gamma = eg[kC - 1];
-#pragma unroll
-            for (int j = 0; j < NT / 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) D[j][e] *= gamma;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t hi[4], lo[4];
-                split_tokens(F, k, eg, -1.f, tg, hi, lo);
-                rank16<NT>(D, hi, lo, ka, k, lane);
-                float t[2][4];  // exp(cum) dY
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float2 e = *reinterpret_cast<const float2 *>(eg + 16 * k + 8 * n + 2 * tg);
-                    t[n][0] = e.x * low(yf[k][2 * n]), t[n][1] = e.y * high(yf[k][2 * n]);
-                    t[n][2] = e.x * low(yf[k][2 * n + 1]), t[n][3] = e.y * high(yf[k][2 * n + 1]);
-                }
-                split_a(t[0], t[1], hi, lo);
-                rank16<NT>(D, hi, lo, qa, k, lane);
-            }
-        }
-        __syncthreads();
-    }
-    if (dh0 && on) store_state<NT>(D, dh0, row, P, N, p0 + gr, tg);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -1019,19 +790,21 @@ cudaError_t prep_launch(const DeltaProblem &p, char *ws, int *clear, int nclear,
 
 // The workspace begins with the status word of the bounded waits and, 256 bytes on, the chain's counters,
 // a CTA each; k_delta_prep clears both.
-size_t head_bytes(const DeltaProblem &p) { return kWsAlign + align_up((size_t)delta_tc_grid(p) * sizeof(int), kWsAlign); }
+size_t head_bytes(const DeltaProblem &p, bool backward) {
+    return kWsAlign + align_up((size_t)delta_tc_grid(p, backward) * sizeof(int), kWsAlign);
+}
 
 template <int NT>
 cudaError_t fwd_launch(const DeltaProblem &p, char *ws, cudaStream_t s) {
     using L = Prep<false>;
     int *status = reinterpret_cast<int *>(ws);
-    const size_t at = head_bytes(p);
-    char *prep = ws + at + align_up(delta_tc_hand_bytes(p), kWsAlign);
+    const size_t at = head_bytes(p, false);
+    char *prep = ws + at + align_up(delta_tc_hand_bytes(p, false), kWsAlign);
     const cudaError_t e = prep_launch<NT, false>(p, prep, status, (int)(at / sizeof(int)), s);
     return e ? e
-             : delta_tc_chain(p, DeltaChain{prep, L::bytes, status, status + kWsAlign / sizeof(int),
-                                            reinterpret_cast<float *>(ws + at), nullptr, nullptr, nullptr},
-                              s);
+             : delta_tc_fwd(p, DeltaChain{prep, L::bytes, L::scal, 0, status, status + kWsAlign / sizeof(int),
+                                          reinterpret_cast<float *>(ws + at), nullptr, nullptr, nullptr, nullptr, nullptr},
+                            s);
 }
 
 // Slices of a group's heads in k_delta_grads_mma: the number that makes (waves of CTAs on 148 SMs) x (heads
@@ -1057,13 +830,13 @@ BwdLayout bwd_layout(const DeltaProblem &p) {
     const int slices = grads_slices(p);
     const size_t part = slices > 1 ? (size_t)(p.B * p.L * p.G * slices * p.N) * 4 : 0;
     BwdLayout l{};
-    size_t at = head_bytes(p);
+    size_t at = head_bytes(p, true);
     const auto take = [&](size_t bytes) {
         const size_t here = at;
         at += align_up(bytes, kWsAlign);
         return here;
     };
-    l.hand = take(delta_tc_hand_bytes(p));
+    l.hand = take(delta_tc_hand_bytes(p, true));
     l.prep = take(chunks * Prep<true>::bytes);
     l.states = take(chunks * (size_t)(p.P * p.N) * 2);
     l.cots = take(chunks * (size_t)(p.P * p.N) * 2);
@@ -1086,22 +859,16 @@ cudaError_t bwd_launch(const DeltaProblem &p, const DeltaGrads &gr, char *ws, cu
     const char *prep = ws + l.prep;
     using Lay = Prep<true>;
     int *status = reinterpret_cast<int *>(ws);
-    cudaError_t e = prep_launch<NT, true>(p, ws + l.prep, status, (int)(head_bytes(p) / sizeof(int)), s);
-    DeltaProblem f = p;  // the states alone: no output, no final state
-    f.h_final = nullptr;
-    if (!e) e = delta_tc_chain(f, DeltaChain{prep, Lay::bytes, status, status + kWsAlign / sizeof(int), reinterpret_cast<float *>(ws + l.hand),
-                                         states, err, u},
-                           s);
+    cudaError_t e = prep_launch<NT, true>(p, ws + l.prep, status, (int)(head_bytes(p, true) / sizeof(int)), s);
+    if (!e)
+        e = delta_tc_bwd(p, gr, DeltaChain{prep, Lay::bytes, Lay::scal, Lay::Wr, status, status + kWsAlign / sizeof(int),
+                                           reinterpret_cast<float *>(ws + l.hand), states, err, u, cots, z},
+                         s);
     if (e) return e;
-    constexpr int smem = sizeof(ChainBwdSmem<NT>), gsmem = sizeof(GradsSmem<NT>);
-    if ((e = cudaFuncSetAttribute(k_delta_chain_bwd<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
+    constexpr int gsmem = sizeof(GradsSmem<NT>);
     if ((e = cudaFuncSetAttribute(k_delta_grads_mma<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, gsmem))) return e;
     const bf *dy = static_cast<const bf *>(gr.dy), *Bm = static_cast<const bf *>(p.Bm), *Cm = static_cast<const bf *>(p.Cm);
-    bf *dx = static_cast<bf *>(gr.dx);
-    dim3 grid((unsigned)((p.P + kRowsCta - 1) / kRowsCta), (unsigned)p.H, (unsigned)p.B);
-    k_delta_chain_bwd<NT><<<grid, kThr, smem, s>>>(dy, Bm, Cm, gr.dh_final, prep, p.L, (int)p.H, (int)p.P, (int)p.G, (int)p.N,
-                                                   dx, z, cots, gr.dh0);
-    if ((e = cudaGetLastError())) return e;
+    const bf *dx = static_cast<const bf *>(gr.dx);
     const int slices = grads_slices(p);
     dim3 ggrid((unsigned)((p.L + kC - 1) / kC), (unsigned)(p.G * slices), (unsigned)p.B);
     k_delta_grads_mma<NT><<<ggrid, kGThr, gsmem, s>>>(dy, Bm, Cm, prep, states, cots, err, u, z, dx, p.L, (int)p.H, (int)p.P,
@@ -1127,7 +894,7 @@ bool delta_mma_supported(const DeltaProblem &p) {
 }
 
 size_t delta_mma_fwd_workspace_bytes(const DeltaProblem &p) {
-    return head_bytes(p) + align_up(delta_tc_hand_bytes(p), kWsAlign) +
+    return head_bytes(p, false) + align_up(delta_tc_hand_bytes(p, false), kWsAlign) +
            (size_t)(p.B * p.H) * (size_t)((p.L + kC - 1) / kC) * Prep<false>::bytes;
 }
 
@@ -1136,7 +903,7 @@ cudaError_t delta_mma_fwd(const DeltaProblem &p, void *ws, cudaStream_t s) {
 }
 
 size_t delta_mma_bwd_workspace_bytes(const DeltaProblem &p) { return bwd_layout(p).total; }
-int delta_mma_bwd_kernels(const DeltaProblem &p) { return grads_slices(p) > 1 ? 5 : 4; }
+int delta_mma_bwd_kernels(const DeltaProblem &p) { return grads_slices(p) > 1 ? 4 : 3; }
 
 cudaError_t delta_mma_bwd(const DeltaProblem &p, const DeltaGrads &g, void *ws, cudaStream_t s) {
     return p.N <= 64 ? bwd_launch<64>(p, g, static_cast<char *>(ws), s) : bwd_launch<128>(p, g, static_cast<char *>(ws), s);

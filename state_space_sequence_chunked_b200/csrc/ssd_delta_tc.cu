@@ -40,6 +40,7 @@ using namespace tc;
 constexpr int kC = kDeltaChunk;
 constexpr int kTWarps = 16, kOWarp = 4 + kTWarps, kThreads = 32 * (kOWarp + 4);
 constexpr int kPanel = kC * 128;   // bytes of 64 rows of 64 bf16
+constexpr int kTriLbo = 128, kTriSbo = 256;  // see tri_rows
 constexpr int kTri = 10 * 512;     // bytes of a 64 x 64 lower triangle of 16 x 16 blocks, bf16
 constexpr int kTmS = 0, kTmHi = 128, kTmLo = 192, kTmR = 256, kTmY = 320, kTmA = 384, kTmAl = 448;
 constexpr int kEk = kTmLo, kEkl = kTmLo + 32;  // ek u over S lo
@@ -63,6 +64,7 @@ struct ChainArgs {
     const float *h0;
     const char *prep;
     int64_t prep_bytes;  // per chunk and head
+    int scal_at, rows_at;  // reverse chain: the scalars; W and P by rows of blocks (hi, lo each)
     int nc, H, P, G, N;
     int tiles, streams;  // of 128 rows per head; (tiles x heads or head pairs x batch)
     float *h_final;
@@ -174,11 +176,115 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 pair_of(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
 
+// What a chain begins with: barriers (count of arrivals each), TMEM, the abort flag.
+struct Setup {
+    uint32_t tmem;
+    volatile int *abort_flag;
+};
+template <int M>
+__device__ __forceinline__ Setup set_up(uint64_t *bar, const int (&counts)[M], int wait_us, int warp) {
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + M);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bar + M + 1);
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 0; i < M; ++i) mbar_init(bar + i, counts[i]);
+        abort_flag[0] = 0;
+        abort_flag[1] = wait_us;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    return Setup{*tmem_slot, abort_flag};
+}
+// And ends with: every issued product has completed (fin) before TMEM is released.
+__device__ __forceinline__ void tear_down(uint32_t tmem, uint64_t *fin, int warp, int lane) {
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        if (lane == 0) {
+            const unsigned long long t0 = now_ns();
+            while (!mbar_try(fin, 0) && now_ns() - t0 < kWaitNs) {
+            }
+        }
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+// Loads in flight land before the CTA exits: the last two uses of the stages' barriers.
+__device__ __forceinline__ void drain_loads(uint64_t *full, int it) {
+    for (int i = 1; i <= 2; ++i) {
+        if (it - i < 0) continue;
+        const unsigned long long w0 = now_ns();
+        while (!mbar_try(&full[(it - i) & 1], (uint32_t)((it - i) >> 1) & 1u) && now_ns() - w0 < kWaitNs) {
+        }
+    }
+}
+
+// State rows as they enter a segment, SC columns from n0 on: handed on by CTA `from`, or the initial state.
+template <int SC>
+__device__ __forceinline__ void load_rows(uint32_t (&s)[SC], const ChainArgs &a, int from, int p, int64_t srow, int n0, int row, int nt) {
+#pragma unroll
+    for (int i = 0; i < SC; i += 4) {
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (from >= 0)
+            f = __ldcg(reinterpret_cast<const float4 *>(a.hand + ((int64_t)from * 128 + row) * nt + n0 + i));
+        else if (a.h0 && p < a.P && n0 + i < a.N)
+            f = *reinterpret_cast<const float4 *>(a.h0 + srow * a.N + n0 + i);
+        s[i] = __float_as_uint(f.x), s[i + 1] = __float_as_uint(f.y);
+        s[i + 2] = __float_as_uint(f.z), s[i + 3] = __float_as_uint(f.w);
+    }
+}
+// And as they leave it: for the CTA that goes on, or the final state.
+template <int SC>
+__device__ __forceinline__ void store_rows(uint32_t taddr, const ChainArgs &a, bool hand_on, int cta, int p, int64_t srow, int n0,
+                                           int row, int nt) {
+    float *dst = hand_on ? a.hand + ((int64_t)cta * 128 + row) * nt : a.h_final && p < a.P ? a.h_final + srow * a.N : nullptr;
+    const int cols = hand_on ? nt : a.N;
+#pragma unroll
+    for (int j = 0; j < SC; j += 16) {
+        uint32_t s[16];
+        tmem_ld16(taddr + n0 + j, s);
+        tmem_wait_ld();
+        if (dst)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (n0 + j + 4 * i < cols)
+                    *reinterpret_cast<uint4 *>(dst + n0 + j + 4 * i) = make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+    }
+}
+// 32 rows of a bf16 state in TMEM to panels of 64 columns, [32 rows][128 B], swizzled.
+template <int NT>
+__device__ __forceinline__ void put_state(uint32_t taddr, unsigned char *stage, int lane) {
+#pragma unroll
+    for (int pn = 0; pn < NT / 64; ++pn) {
+        uint32_t v[32];
+        tmem_ld32(taddr + 32 * pn, v);
+        tmem_wait_ld(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4 *>(stage + pn * 4096 + swz(lane, i)) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+}
+// Pairs of tokens of one row per lane to [64 tokens][32 rows].
+__device__ __forceinline__ void put_pairs(const uint32_t (&o)[32], unsigned char *stage, int lane) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        *reinterpret_cast<uint16_t *>(stage + (2 * i) * 64 + 2 * lane) = (uint16_t)(o[i] & 0xffffu);
+        *reinterpret_cast<uint16_t *>(stage + (2 * i + 1) * 64 + 2 * lane) = (uint16_t)(o[i] >> 16);
+    }
+}
+
 template <int NT, bool PAIR, bool kStore>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_delta_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
-               const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_o0,
-               const __grid_constant__ CUtensorMap tm_o1, const __grid_constant__ CUtensorMap tm_s, const ChainArgs a) {
+__device__ __forceinline__ void chain_fwd(const CUtensorMap &tm_k, const CUtensorMap &tm_q, const CUtensorMap &tm_x,
+                                          const CUtensorMap &tm_o0, const CUtensorMap &tm_o1, const CUtensorMap &tm_s,
+                                          const ChainArgs &a, int cta, int ctas) {
     using Z = Lay<NT, PAIR, kStore>;
     constexpr int HB = Z::HB;
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -198,13 +304,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *ys = bar + 14;     // Yq scaled (O)
     uint64_t *ofree = bar + 15;  // Y (kStore: err and u) read (O)
     uint64_t *fin = bar + 16;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 17);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(bar + 18);
     int *status = a.status;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nc = a.nc;
-    const Share share((int64_t)a.streams * nc, nc, blockIdx.x, gridDim.x);
+    const Share share((int64_t)a.streams * nc, nc, cta, ctas);
     const int steps = (int)(share.hi - share.lo);
     // batch row, first head and first state row of a stream
     const auto place = [&](int stream, int &b, int &h, int &pc) {
@@ -212,37 +316,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         b = stream / a.tiles / (a.H / HB), h = hy * HB, pc = 128 * tile;
     };
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&sfree[i], 1 + kTWarps + (kStore ? 0 : 4));  // the products, T, O
-        }
-        mbar_init(rdyR, 1);
-        mbar_init(rdyE, 1);
-        mbar_init(rdyS, 1);
-        mbar_init(rdyQ, 1);
-        mbar_init(rdyY, 1);
-        mbar_init(sb, kTWarps);
-        mbar_init(ab, kTWarps);
-        mbar_init(ub, kTWarps);
-        mbar_init(yu, kTWarps);
-        mbar_init(ys, 4);
-        mbar_init(ofree, 4);
-        mbar_init(ost, 4);
-        mbar_init(fin, 1);
-        abort_flag[0] = 0;
-        abort_flag[1] = a.wait_us;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    constexpr int kReaders = 1 + kTWarps + (kStore ? 0 : 4);  // of a stage: the products, T, O
+    // in the order above: full, yu, ost, sfree, the five products, sb, ab, ub, ys, ofree, fin
+    constexpr int counts[17] = {1, 1, kTWarps, 4, kReaders, kReaders, 1, 1, 1, 1, 1, kTWarps, kTWarps, kTWarps, 4, 4, 1};
+    const Setup su = set_up(bar, counts, a.wait_us, warp);
+    const uint32_t tmem = su.tmem;
+    volatile int *abort_flag = su.abort_flag;
     const auto scal_of = [&](int k, int e) { return reinterpret_cast<const float *>(sm + k * Z::stage + Z::w + e * Z::head + Z::scal); };
 
     if (warp == 0) {
@@ -274,13 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tma_load_4d_hint(st + Z::q + pn * kPanel, &tm_q, &full[k], 64 * pn, grp, c * kC, b, keep);
                 }
             }
-            // loads in flight land before the CTA exits
-            for (int i = 1; i <= 2; ++i) {
-                if (it - i < 0) continue;
-                const unsigned long long w0 = now_ns();
-                while (!mbar_try(&full[(it - i) & 1], (uint32_t)((it - i) >> 1) & 1u) && now_ns() - w0 < kWaitNs) {
-                }
-            }
+            drain_loads(full, it);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -389,185 +462,163 @@ __global__ void __launch_bounds__(kThreads, 1)
         int it = 0;
         bool ok = true;
         for (int j = 0; ok && j < share.n; ++j) {
-        const Seg sg = share.at(j);
-        int b, h, pc;
-        place(sg.stream, b, h, pc);
-        const int p = PAIR ? pp : pc + 32 * qtr + lane;  // state row of the head
-        const int64_t srow = ((int64_t)b * a.H + h + e) * a.P + p;
-        if (sg.c0 > 0 && !(ok = __all_sync(0xffffffffu, wait_count(a.flags + blockIdx.x - 1, kTWarps, abort_flag, status)))) break;
-        int c = sg.c0;
-        for (; c < sg.c1; ++c, ++it) {
-            const int k = it & 1;
-            const uint32_t par = (uint32_t)it & 1u;
-            if (!wait_warp(&full[k], (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
-            const float *eg = scal_of(k, e), *ek = eg + kC, *bt = eg + 2 * kC;
-            if (it > 0) {
-                if (!wait_warp(rdyS, par ^ 1u, abort_flag, status)) break;
-                if (kStore && !wait_warp(ost, par ^ 1u, abort_flag, status)) break;
-                tc_fence_after();
-            }
-            // The state's operands; then, while S K^T runs, the state times exp(cum_end) for the next product to
-            // add to, and what beta R = beta X - beta eg S K^T needs. This warp: tokens tk0 .. + 15.
-            float bx[16], be[16];
-            const unsigned char *xt = sm + k * Z::stage + Z::x + (qtr >> 1) * kPanel;
-            const auto x_at = [&](int i) {
-                return __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(xt + swz(tk0 + i, pp >> 3) + 2 * (pp & 7)));
-            };
-            {
-                uint32_t s[SC];
-                if (c > sg.c0) {
-                    if constexpr (SC == 32) {
-                        tmem_ld32(lo_ + kTmS + n0, s);
-                        tmem_wait_ld(s);
+            const Seg sg = share.at(j);
+            int b, h, pc;
+            place(sg.stream, b, h, pc);
+            const int p = PAIR ? pp : pc + 32 * qtr + lane;  // state row of the head
+            const int64_t srow = ((int64_t)b * a.H + h + e) * a.P + p;
+            if (sg.c0 > 0 && !(ok = __all_sync(0xffffffffu, wait_count(a.flags + cta - 1, kTWarps, abort_flag, status)))) break;
+            int c = sg.c0;
+            for (; c < sg.c1; ++c, ++it) {
+                const int k = it & 1;
+                const uint32_t par = (uint32_t)it & 1u;
+                if (!wait_warp(&full[k], (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
+                const float *eg = scal_of(k, e), *ek = eg + kC, *bt = eg + 2 * kC;
+                if (it > 0) {
+                    if (!wait_warp(rdyS, par ^ 1u, abort_flag, status)) break;
+                    if (kStore && !wait_warp(ost, par ^ 1u, abort_flag, status)) break;
+                    tc_fence_after();
+                }
+                // The state's operands; then, while S K^T runs, the state times exp(cum_end) for the next product to
+                // add to, and what beta R = beta X - beta eg S K^T needs. This warp: tokens tk0 .. + 15.
+                float bx[16], be[16];
+                const unsigned char *xt = sm + k * Z::stage + Z::x + (qtr >> 1) * kPanel;
+                const auto x_at = [&](int i) {
+                    return __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(xt + swz(tk0 + i, pp >> 3) + 2 * (pp & 7)));
+                };
+                {
+                    uint32_t s[SC];
+                    if (c > sg.c0) {
+                        if constexpr (SC == 32) {
+                            tmem_ld32(lo_ + kTmS + n0, s);
+                            tmem_wait_ld(s);
+                        } else {
+                            tmem_ld16(lo_ + kTmS + n0, s);
+                            tmem_wait_ld();
+                        }
                     } else {
-                        tmem_ld16(lo_ + kTmS + n0, s);
-                        tmem_wait_ld();
+                        load_rows<SC>(s, a, c > 0 ? cta - 1 : -1, p, srow, n0, 32 * qtr + lane, NT);
                     }
-                } else {
 #pragma unroll
-                    for (int i = 0; i < SC; i += 4) {
-                        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (c > 0)
-                            f = __ldcg(reinterpret_cast<const float4 *>(a.hand + ((int64_t)(blockIdx.x - 1) * 128 + 32 * qtr + lane) * NT + n0 + i));
-                        else if (a.h0 && p < a.P && n0 + i < a.N)
-                            f = *reinterpret_cast<const float4 *>(a.h0 + srow * a.N + n0 + i);
-                        s[i] = __float_as_uint(f.x), s[i + 1] = __float_as_uint(f.y);
-                        s[i + 2] = __float_as_uint(f.z), s[i + 3] = __float_as_uint(f.w);
+                    for (int j = 0; j < SC; j += 16) {
+                        uint32_t hi[8], lw[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            split2(__uint_as_float(s[j + 2 * i]), __uint_as_float(s[j + 2 * i + 1]), hi[i], lw[i]);
+                        tmem_st8(lo_ + kTmHi + (n0 + j) / 2, hi);
+                        tmem_st8(lo_ + kTmLo + (n0 + j) / 2, lw);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sb);
+                    const float gamma = eg[kC - 1];
+#pragma unroll
+                    for (int j = 0; j < SC; j += 16) {
+                        uint32_t v[16];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 g = mul2(make_float2(gamma, gamma), pair_of(s[j + 2 * i], s[j + 2 * i + 1]));
+                            v[2 * i] = __float_as_uint(g.x), v[2 * i + 1] = __float_as_uint(g.y);
+                        }
+                        tmem_st16(lo_ + kTmS + n0 + j, v);
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < SC; j += 16) {
-                    uint32_t hi[8], lw[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        split2(__uint_as_float(s[j + 2 * i]), __uint_as_float(s[j + 2 * i + 1]), hi[i], lw[i]);
-                    tmem_st8(lo_ + kTmHi + (n0 + j) / 2, hi);
-                    tmem_st8(lo_ + kTmLo + (n0 + j) / 2, lw);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sb);
-                const float gamma = eg[kC - 1];
-#pragma unroll
-                for (int j = 0; j < SC; j += 16) {
-                    uint32_t v[16];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 g = mul2(make_float2(gamma, gamma), pair_of(s[j + 2 * i], s[j + 2 * i + 1]));
-                        v[2 * i] = __float_as_uint(g.x), v[2 * i + 1] = __float_as_uint(g.y);
-                    }
-                    tmem_st16(lo_ + kTmS + n0 + j, v);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const float4 g4 = *reinterpret_cast<const float4 *>(eg + tk0 + i), b4 = *reinterpret_cast<const float4 *>(bt + tk0 + i);
-                be[i] = -b4.x * g4.x, be[i + 1] = -b4.y * g4.y, be[i + 2] = -b4.z * g4.z, be[i + 3] = -b4.w * g4.w;
-                bx[i] = b4.x * x_at(i), bx[i + 1] = b4.y * x_at(i + 1), bx[i + 2] = b4.z * x_at(i + 2), bx[i + 3] = b4.w * x_at(i + 3);
-            }
-            if (!wait_warp(rdyR, par, abort_flag, status)) break;
-            tc_fence_after();
-            float R[16];
-            {
-                uint32_t r[16], hi[8], lw[8];
-                tmem_ld16(lo_ + kTmR + tk0, r);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 br = fma2(make_float2(be[2 * i], be[2 * i + 1]), pair_of(r[2 * i], r[2 * i + 1]),
-                                           make_float2(bx[2 * i], bx[2 * i + 1]));
-                    split2(br.x, br.y, hi[i], lw[i]);
-                }
-                tmem_st8(lo_ + kTmA + 32 * e + 8 * sub, hi);
-                tmem_st8(lo_ + kTmAl + 32 * e + 8 * sub, lw);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(ab);
-                // while W (beta R) runs: R itself, and ek beta
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
                     const float4 g4 = *reinterpret_cast<const float4 *>(eg + tk0 + i), b4 = *reinterpret_cast<const float4 *>(bt + tk0 + i);
-                    const float4 k4 = *reinterpret_cast<const float4 *>(ek + tk0 + i);
-                    R[i] = fmaf(-g4.x, __uint_as_float(r[i]), x_at(i)), R[i + 1] = fmaf(-g4.y, __uint_as_float(r[i + 1]), x_at(i + 1));
-                    R[i + 2] = fmaf(-g4.z, __uint_as_float(r[i + 2]), x_at(i + 2));
-                    R[i + 3] = fmaf(-g4.w, __uint_as_float(r[i + 3]), x_at(i + 3));
-                    be[i] = k4.x * b4.x, be[i + 1] = k4.y * b4.y, be[i + 2] = k4.z * b4.z, be[i + 3] = k4.w * b4.w;
+                    be[i] = -b4.x * g4.x, be[i + 1] = -b4.y * g4.y, be[i + 2] = -b4.z * g4.z, be[i + 3] = -b4.w * g4.w;
+                    bx[i] = b4.x * x_at(i), bx[i + 1] = b4.y * x_at(i + 1), bx[i + 2] = b4.z * x_at(i + 2), bx[i + 3] = b4.w * x_at(i + 3);
                 }
-            }
-            // err = R + E, u = beta err; ek u first, which the state waits for
-            if (!wait_warp(rdyE, par, abort_flag, status)) break;
-            tc_fence_after();
-            {
-                uint32_t r[16], hi[8], lw[8];
-                tmem_ld16(lo_ + kTmR + tk0, r);
-                tmem_wait_ld();
+                if (!wait_warp(rdyR, par, abort_flag, status)) break;
+                tc_fence_after();
+                float R[16];
+                {
+                    uint32_t r[16], hi[8], lw[8];
+                    tmem_ld16(lo_ + kTmR + tk0, r);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    R[2 * i] += __uint_as_float(r[2 * i]), R[2 * i + 1] += __uint_as_float(r[2 * i + 1]);
-                    const float2 eu = mul2(make_float2(be[2 * i], be[2 * i + 1]), make_float2(R[2 * i], R[2 * i + 1]));
-                    split2(eu.x, eu.y, hi[i], lw[i]);
-                }
-                tmem_st8(lo_ + kEk + 8 * sub, hi);
-                tmem_st8(lo_ + kEkl + 8 * sub, lw);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(ub);
-                if constexpr (kStore) {  // the last chunk's u and err have left
-                    if (it > 0 && !wait_warp(ofree, par ^ 1u, abort_flag, status)) break;
-                }
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const float4 b4 = *reinterpret_cast<const float4 *>(bt + tk0 + i);
-                    const float u[4] = {b4.x * R[i], b4.y * R[i + 1], b4.z * R[i + 2], b4.w * R[i + 3]};
-                    if constexpr (kStore) {  // u and err go out rounded; no product here takes u itself
-                        hi[i / 2] = pack_bf16(u[0], u[1]), hi[i / 2 + 1] = pack_bf16(u[2], u[3]);
-                        lw[i / 2] = pack_bf16(R[i], R[i + 1]), lw[i / 2 + 1] = pack_bf16(R[i + 2], R[i + 3]);
-                    } else {
-                        split2(u[0], u[1], hi[i / 2], lw[i / 2]);
-                        split2(u[2], u[3], hi[i / 2 + 1], lw[i / 2 + 1]);
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 br = fma2(make_float2(be[2 * i], be[2 * i + 1]), pair_of(r[2 * i], r[2 * i + 1]),
+                                               make_float2(bx[2 * i], bx[2 * i + 1]));
+                        split2(br.x, br.y, hi[i], lw[i]);
                     }
-                }
-                if constexpr (kStore) {
-                    tmem_st8(lo_ + kTmY + 8 * sub, hi);
-                    tmem_st8(lo_ + kTmY + 32 + 8 * sub, lw);
-                } else {
                     tmem_st8(lo_ + kTmA + 32 * e + 8 * sub, hi);
                     tmem_st8(lo_ + kTmAl + 32 * e + 8 * sub, lw);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ab);
+                    // while W (beta R) runs: R itself, and ek beta
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 g4 = *reinterpret_cast<const float4 *>(eg + tk0 + i), b4 = *reinterpret_cast<const float4 *>(bt + tk0 + i);
+                        const float4 k4 = *reinterpret_cast<const float4 *>(ek + tk0 + i);
+                        R[i] = fmaf(-g4.x, __uint_as_float(r[i]), x_at(i)), R[i + 1] = fmaf(-g4.y, __uint_as_float(r[i + 1]), x_at(i + 1));
+                        R[i + 2] = fmaf(-g4.z, __uint_as_float(r[i + 2]), x_at(i + 2));
+                        R[i + 3] = fmaf(-g4.w, __uint_as_float(r[i + 3]), x_at(i + 3));
+                        be[i] = k4.x * b4.x, be[i + 1] = k4.y * b4.y, be[i + 2] = k4.z * b4.z, be[i + 3] = k4.w * b4.w;
+                    }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(yu);
-                    mbar_arrive(&sfree[k]);
+                // err = R + E, u = beta err; ek u first, which the state waits for
+                if (!wait_warp(rdyE, par, abort_flag, status)) break;
+                tc_fence_after();
+                {
+                    uint32_t r[16], hi[8], lw[8];
+                    tmem_ld16(lo_ + kTmR + tk0, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        R[2 * i] += __uint_as_float(r[2 * i]), R[2 * i + 1] += __uint_as_float(r[2 * i + 1]);
+                        const float2 eu = mul2(make_float2(be[2 * i], be[2 * i + 1]), make_float2(R[2 * i], R[2 * i + 1]));
+                        split2(eu.x, eu.y, hi[i], lw[i]);
+                    }
+                    tmem_st8(lo_ + kEk + 8 * sub, hi);
+                    tmem_st8(lo_ + kEkl + 8 * sub, lw);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ub);
+                    if constexpr (kStore) {  // the last chunk's u and err have left
+                        if (it > 0 && !wait_warp(ofree, par ^ 1u, abort_flag, status)) break;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 b4 = *reinterpret_cast<const float4 *>(bt + tk0 + i);
+                        const float u[4] = {b4.x * R[i], b4.y * R[i + 1], b4.z * R[i + 2], b4.w * R[i + 3]};
+                        if constexpr (kStore) {  // u and err go out rounded; no product here takes u itself
+                            hi[i / 2] = pack_bf16(u[0], u[1]), hi[i / 2 + 1] = pack_bf16(u[2], u[3]);
+                            lw[i / 2] = pack_bf16(R[i], R[i + 1]), lw[i / 2 + 1] = pack_bf16(R[i + 2], R[i + 3]);
+                        } else {
+                            split2(u[0], u[1], hi[i / 2], lw[i / 2]);
+                            split2(u[2], u[3], hi[i / 2 + 1], lw[i / 2 + 1]);
+                        }
+                    }
+                    if constexpr (kStore) {
+                        tmem_st8(lo_ + kTmY + 8 * sub, hi);
+                        tmem_st8(lo_ + kTmY + 32 + 8 * sub, lw);
+                    } else {
+                        tmem_st8(lo_ + kTmA + 32 * e + 8 * sub, hi);
+                        tmem_st8(lo_ + kTmAl + 32 * e + 8 * sub, lw);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(yu);
+                        mbar_arrive(&sfree[k]);
+                    }
                 }
             }
-        }
-        // the segment's end: the final state, or the state for the CTA that goes on
-        if (c < sg.c1 || !wait_warp(rdyS, (uint32_t)(it - 1) & 1u, abort_flag, status)) break;
-        tc_fence_after();
-        float *dst = sg.c1 < nc ? a.hand + ((int64_t)blockIdx.x * 128 + 32 * qtr + lane) * NT
-                                : a.h_final && p < a.P ? a.h_final + srow * a.N : nullptr;
-        const int cols = sg.c1 < nc ? NT : a.N;
-#pragma unroll
-        for (int jj = 0; jj < SC; jj += 16) {
-            uint32_t s[16];
-            tmem_ld16(lo_ + kTmS + n0 + jj, s);
-            tmem_wait_ld();
-            if (dst)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (n0 + jj + 4 * i < cols)
-                        *reinterpret_cast<uint4 *>(dst + n0 + jj + 4 * i) = make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
-        }
-        if (sg.c1 < nc) {
-            __threadfence();
-            __syncwarp();
-            if (lane == 0) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(a.flags + blockIdx.x) : "memory");
-        }
+            // the segment's end: the final state, or the state for the CTA that goes on
+            if (c < sg.c1 || !wait_warp(rdyS, (uint32_t)(it - 1) & 1u, abort_flag, status)) break;
+            tc_fence_after();
+            store_rows<SC>(lo_ + kTmS, a, sg.c1 < nc, cta, p, srow, n0, 32 * qtr + lane, NT);
+            if (sg.c1 < nc) {
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(a.flags + cta) : "memory");
+            }
         }
     } else {
         // ------------------------------------------------------------- O: outputs, 32 state rows x 64 tokens per warp
@@ -579,56 +630,504 @@ __global__ void __launch_bounds__(kThreads, 1)
         int it = 0;
         bool ok = true;
         for (int j = 0; ok && j < share.n; ++j) {
-        const Seg sg = share.at(j);
-        int b, h, pc;
-        place(sg.stream, b, h, pc);
-        const int p0 = PAIR ? (qtr & 1) * 32 : pc + 32 * qtr;  // first state row of the head
-        int c = sg.c0;
-        for (; c < sg.c1; ++c, ++it) {
+            const Seg sg = share.at(j);
+            int b, h, pc;
+            place(sg.stream, b, h, pc);
+            const int p0 = PAIR ? (qtr & 1) * 32 : pc + 32 * qtr;  // first state row of the head
+            int c = sg.c0;
+            for (; c < sg.c1; ++c, ++it) {
+                const int k = it & 1;
+                const uint32_t par = (uint32_t)it & 1u;
+                if constexpr (!kStore) {
+                    if (!wait_warp(&full[k], (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
+                    if (!wait_warp(rdyQ, par, abort_flag, status)) break;
+                    tc_fence_after();
+                    const float *eg = scal_of(k, e);
+#pragma unroll
+                    for (int j = 0; j < 64; j += 16) {
+                        uint32_t r[16];
+                        tmem_ld16(lo_ + kTmY + j, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 g4 = *reinterpret_cast<const float4 *>(eg + j + i);
+                            r[i] = __float_as_uint(g4.x * __uint_as_float(r[i])), r[i + 1] = __float_as_uint(g4.y * __uint_as_float(r[i + 1]));
+                            r[i + 2] = __float_as_uint(g4.z * __uint_as_float(r[i + 2]));
+                            r[i + 3] = __float_as_uint(g4.w * __uint_as_float(r[i + 3]));
+                        }
+                        tmem_st16(lo_ + kTmY + j, r);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(ys);
+                        mbar_arrive(&sfree[k]);
+                    }
+                    if (!wait_warp(rdyY, par, abort_flag, status)) break;
+                } else {  // the entering state, as S hi holds it
+                    if (!wait_warp(sb, par, abort_flag, status)) break;
+                    tc_fence_after();
+                    if (lane == 0) bulk_wait_read();  // the staging's last store has read it
+                    __syncwarp();
+                    put_state<NT>(lo_ + kTmHi, stage2, lane);
+                    tc_fence_before();
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ost);
+                    if (lane == 0 && p0 < a.P) {
+                        const int unit = (b * a.H + h + e) * nc + c;
+                        for (int pn = 0; pn < NT / 64; ++pn)
+                            if (64 * pn < a.N) tma_store_4d(&tm_s, stage2 + pn * 4096, 64 * pn, p0, unit, 0, pol);
+                        bulk_commit();
+                    }
+                    if (!wait_warp(yu, par, abort_flag, status)) break;
+                }
+                tc_fence_after();
+                if (lane == 0) bulk_wait_read();
+                __syncwarp();
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t o[32];
+                    tmem_ld32(lo_ + kTmY + 32 * half, o);
+                    tmem_wait_ld(o);
+                    if (half) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(ofree);
+                    }
+                    if constexpr (kStore) {  // pairs of tokens: u, then err
+                        put_pairs(o, half ? stage1 : stage0, lane);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            reinterpret_cast<__nv_bfloat16 *>(stage0 + (32 * half + i) * 64)[lane] = __float2bfloat16_rn(__uint_as_float(o[i]));
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0 && p0 < a.P) {
+                    tma_store_4d(&tm_o0, stage0, p0, h + e, c * kC, b, pol);
+                    if constexpr (kStore) tma_store_4d(&tm_o1, stage1, p0, h + e, c * kC, b, pol);
+                    bulk_commit();
+                }
+            }
+            ok = c == sg.c1;
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+
+    tear_down(tmem, fin, warp, lane);
+}
+
+// ---------------------------------------------------------------------------------------------
+// The chain in reverse, for the backward pass. With D the cotangent of the state leaving a chunk,
+//   per chunk                left                      right                               into
+//   Z  = P^T dY              dY (shared memory)        P hi, lo  (rows = the sum's tokens)  Z   64 columns
+//   F0 = D K^T               D hi, lo (TMEM)           K                                   R   64
+//   E  = W^T (beta F)        beta F hi, lo (TMEM)      W hi, lo                            R   (over F0)
+//   D += (eg dY)^T Q         eg dY hi, lo (sh. mem.)   Q, columns contiguous               D   N, fp32
+//   D -= (eg r)^T K          -eg r hi, lo (TMEM)       K                                   D
+// with F = Z + ek F0, z = F + E, r = beta z = dX. Rows, tokens and warps as above, plus warps 2-3, which
+// form eg dY. In a PAIR the left operands of Z come with a panel of zeros for the other head's rows.
+// z and dX go out in bf16, and D hi of every chunk (an operand of k_delta_grads_mma).
+template <int NT, bool PAIR>
+struct RevLay {
+    static constexpr int HB = PAIR ? 2 : 1;
+    static constexpr int kBytes = NT / 64 * kPanel;
+    static constexpr int k = 0, q = k + 2 * kBytes;                // two stages each
+    static constexpr int dy0 = q + 2 * kBytes, zero = dy0 + 2 * kPanel, dy1 = zero + (PAIR ? kPanel : 0);
+    static constexpr int e = dy1 + 2 * kPanel;                     // eg dY: hi, lo, two panels each
+    static constexpr int out = e + 4 * kPanel;                     // O warps: two buffers of 4 KB each
+    static constexpr int w = out + 4 * 8192, p = w + HB * 2 * kTri;  // W hi, lo per head; P hi, lo per head
+    static constexpr int scal = p + HB * 2 * kTri;                 // two stages
+    static constexpr int bar = scal + 2 * HB * 3 * kC * 4;
+    static constexpr int bytes = bar + 256;
+    static constexpr int tx = 2 * kBytes + 2 * kPanel + HB * 3 * kC * 4;
+};
+
+// Lower triangle by rows of blocks, as right operand whose sum runs over its rows: core matrices of 8 rows by
+// 8 columns, the next 8 columns 256 bytes on, the next 8 rows 128.
+__device__ __forceinline__ uint64_t tri_rows(uint32_t tile, int a) {
+    return (uint64_t)(((tile + 512 * (a * (a + 1) / 2)) >> 4) & 0x3FFFu) | (uint64_t)(kTriLbo >> 4) << 16 |
+           (uint64_t)(kTriSbo >> 4) << 32 | (uint64_t)1 << 46;
+}
+__device__ __forceinline__ void mma_ss_el(uint32_t leader, uint32_t d, uint64_t left, uint64_t right, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(left), "l"(right), "r"(id), "r"(leader), "r"(acc)
+        : "memory");
+}
+
+template <int NT, bool PAIR>
+__device__ __forceinline__ void chain_rev(const CUtensorMap &tm_k, const CUtensorMap &tm_q, const CUtensorMap &tm_dy,
+                                          const CUtensorMap &tm_z, const CUtensorMap &tm_dx, const CUtensorMap &tm_d,
+                                          const ChainArgs &a, int cta, int ctas) {
+    using Z = RevLay<NT, PAIR>;
+    constexpr int HB = Z::HB;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    if ((smem_u32(sm) & 1023u) != 0) {
+        if (threadIdx.x == 0) atomicOr(a.status, 2);
+        return;
+    }
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + Z::bar);
+    uint64_t *full = bar, *sfree = bar + 2;                    // [2] a stage's loads landed; its readers done
+    uint64_t *wfull = bar + 4, *wfree = bar + 5;               // W landed; read
+    uint64_t *pfull = bar + 6, *pfree = bar + 7;               // P landed; read
+    uint64_t *rdyZ = bar + 8, *rdyR = bar + 9, *rdyE = bar + 10, *rdyS = bar + 11;  // products done
+    uint64_t *sb = bar + 12, *ab = bar + 13, *ub = bar + 14, *yu = bar + 15;        // T: D's operands, beta F, eg r; z and dX
+    uint64_t *eb = bar + 16;                                   // eg dY written
+    uint64_t *ost = bar + 17, *ofree = bar + 18;               // O: D hi read; z and dX read
+    uint64_t *fin = bar + 19;
+    int *status = a.status;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nc = a.nc;
+    const Share share((int64_t)a.streams * nc, nc, cta, ctas);
+    const int steps = (int)(share.hi - share.lo);
+    const auto place = [&](int stream, int &b, int &h, int &pc) {
+        const int tile = stream % a.tiles, hy = stream / a.tiles % (a.H / HB);
+        b = stream / a.tiles / (a.H / HB), h = hy * HB, pc = 128 * tile;
+    };
+    if constexpr (PAIR) {
+        for (int i = threadIdx.x; i < kPanel / 16; i += kThreads)
+            reinterpret_cast<uint4 *>(sm + Z::zero)[i] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async();
+    }
+    constexpr int counts[20] = {1, 1, 1 + kTWarps, 1 + kTWarps, 1, 1, 1, 1, 1, 1, 1, 1, kTWarps, kTWarps, kTWarps, kTWarps, 2, 4, 4, 1};
+    const Setup su = set_up(bar, counts, a.wait_us, warp);
+    const uint32_t tmem = su.tmem;
+    volatile int *abort_flag = su.abort_flag;
+    const auto scal_of = [&](int k, int e) { return reinterpret_cast<const float *>(sm + Z::scal + (k * HB + e) * 3 * kC * 4); };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------- loads
+        if (lane == 0) {
+            const uint64_t keep = policy_evict_last(), stream = policy_evict_first();
+            int it = 0, wp = 0;  // uses of the stages; of W and P
+            bool ok = true;
+            for (int j = 0; ok && j < share.n; ++j) {
+                const Seg sg = share.at(j);
+                int b, h, pc;
+                place(sg.stream, b, h, pc);
+                const int grp = h / (a.H / a.G);
+                for (int t = sg.c0; t < sg.c1; ++t) {
+                    const int c = nc - 1 - t, k = it & 1;
+                    const auto prep = [&](int e) { return a.prep + (((int64_t)b * a.H + h + e) * nc + c) * a.prep_bytes; };
+                    if (it >= 2 && !(ok = wait_phase(&sfree[k], (uint32_t)((it - 2) >> 1) & 1u, abort_flag, status))) break;
+                    mbar_arrive_tx(&full[k], Z::tx);
+                    for (int pn = 0; pn < 2; ++pn)
+                        tma_load_4d_hint(sm + (pn ? Z::dy1 : Z::dy0) + k * kPanel, &tm_dy, &full[k], PAIR ? 0 : pc + 64 * pn,
+                                         PAIR ? h + pn : h, c * kC, b, stream);
+                    for (int e = 0; e < HB; ++e)
+                        bulk_load(sm + Z::scal + (k * HB + e) * 3 * kC * 4, prep(e) + a.scal_at, 3 * kC * 4, &full[k]);
+                    for (int pn = 0; pn < NT / 64; ++pn) {
+                        tma_load_4d_hint(sm + Z::k + k * Z::kBytes + pn * kPanel, &tm_k, &full[k], 64 * pn, grp, c * kC, b, keep);
+                        tma_load_4d_hint(sm + Z::q + k * Z::kBytes + pn * kPanel, &tm_q, &full[k], 64 * pn, grp, c * kC, b, keep);
+                    }
+                    ++it;
+                    if (wp > 0 && !(ok = wait_phase(pfree, (uint32_t)(wp - 1) & 1u, abort_flag, status))) break;
+                    if (wp > 0 && !(ok = wait_phase(wfree, (uint32_t)(wp - 1) & 1u, abort_flag, status))) break;
+                    mbar_arrive_tx(pfull, HB * 2 * kTri);
+                    mbar_arrive_tx(wfull, HB * 2 * kTri);
+                    for (int e = 0; e < HB; ++e) {
+                        bulk_load(sm + Z::p + e * 2 * kTri, prep(e) + a.rows_at + 2 * kTri, 2 * kTri, pfull);
+                        bulk_load(sm + Z::w + e * 2 * kTri, prep(e) + a.rows_at, 2 * kTri, wfull);
+                    }
+                    ++wp;
+                }
+            }
+            drain_loads(full, it);
+            if (wp > 0) {
+                const unsigned long long w0 = now_ns();
+                while (!(mbar_try(pfull, (uint32_t)(wp - 1) & 1u) && mbar_try(wfull, (uint32_t)(wp - 1) & 1u)) &&
+                       now_ns() - w0 < kWaitNs) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------- products
+        constexpr uint32_t id_ks = idesc(128, 64, false, false), id_s = idesc(128, NT, false, true), id_eq = idesc(128, NT, true, true);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t el = elect_one(), base = smem_u32(sm);
+        for (int it = 0; it < steps; ++it) {
             const int k = it & 1;
             const uint32_t par = (uint32_t)it & 1u;
-            if constexpr (!kStore) {
-                if (!wait_warp(&full[k], (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
-                if (!wait_warp(rdyQ, par, abort_flag, status)) break;
-                tc_fence_after();
-                const float *eg = scal_of(k, e);
+            const uint32_t ka = base + Z::k + k * Z::kBytes, qa = base + Z::q + k * Z::kBytes;
+            if (!wait_warp(&full[k], (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
+            if (!wait_warp(pfull, par, abort_flag, status)) break;
+            if (it > 0 && !wait_warp(ofree, par ^ 1u, abort_flag, status)) break;
+            tc_fence_after();
 #pragma unroll
-                for (int j = 0; j < 64; j += 16) {
-                    uint32_t r[16];
-                    tmem_ld16(lo_ + kTmY + j, r);
+            for (int e = 0; e < HB; ++e) {
+                const uint32_t y0 = base + Z::dy0 + k * kPanel, y1 = base + Z::dy1 + k * kPanel, zr = base + Z::zero;
+                const uint64_t ya = !PAIR ? sdesc(y0, y1 - y0, 1024) : e == 0 ? sdesc(y0, zr - y0, 1024) : sdesc(zr, y1 - zr, 1024);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int i = 3; i >= 0; --i)
+                        mma_ss_el(el, tm + kTmY, ya + 128 * i, tri_rows(base + Z::p + (2 * e + 1 - part) * kTri, i),
+                                  idesc(128, 16 * (i + 1), true, true), e > 0 || part > 0 || i < 3);
+            }
+            commit_el(el, rdyZ);
+            commit_el(el, pfree);
+            if (!wait_warp(sb, par, abort_flag, status)) break;
+            tc_fence_after();
+            const uint64_t kd = sdesc(ka, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < NT / 16; ++kk) {
+                const uint64_t off = (uint64_t)(((kk >> 2) * kPanel + (kk & 3) * 32) >> 4);
+                if (kk == 0)
+                    mma_el<false>(el, tm + kTmR, tm + kTmLo, kd, id_ks);
+                else
+                    mma_el<true>(el, tm + kTmR, tm + kTmLo + 8 * kk, kd + off, id_ks);
+                mma_el<true>(el, tm + kTmR, tm + kTmHi + 8 * kk, kd + off, id_ks);
+            }
+            commit_el(el, rdyR);
+            if (!wait_warp(wfull, par, abort_flag, status)) break;
+            if (!wait_warp(ab, par, abort_flag, status)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int e = 0; e < HB; ++e)
+#pragma unroll
+                for (int part = 0; part < 3; ++part)  // lo W hi, hi W lo, hi W hi
+#pragma unroll
+                    for (int i = 3; i >= 0; --i) {
+                        const uint32_t left = tm + (part == 0 ? kTmAl : kTmA) + 32 * e + 8 * i;
+                        const uint64_t right = tri_rows(base + Z::w + (2 * e + (part == 1 ? 1 : 0)) * kTri, i);
+                        const uint32_t id = idesc(128, 16 * (i + 1), false, true);
+                        if (e == 0 && part == 0 && i == 3)
+                            mma_el<false>(el, tm + kTmR, left, right, id);
+                        else
+                            mma_el<true>(el, tm + kTmR, left, right, id);
+                    }
+            commit_el(el, rdyE);
+            commit_el(el, wfree);
+            if (!wait_warp(eb, par, abort_flag, status)) break;
+            tc_fence_after();
+            const uint64_t qs = sdesc(qa, kPanel, 1024), ks = sdesc(ka, kPanel, 1024), ed = sdesc(base + Z::e, kPanel, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                mma_ss_el(el, tm + kTmS, ed + 128 * kk + (uint64_t)(2 * kPanel >> 4), qs + 128 * kk, id_eq, 1);
+                mma_ss_el(el, tm + kTmS, ed + 128 * kk, qs + 128 * kk, id_eq, 1);
+            }
+            if (!wait_warp(ub, par, abort_flag, status)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                mma_el<true>(el, tm + kTmS, tm + kEkl + 8 * kk, ks + 128 * kk, id_s);
+                mma_el<true>(el, tm + kTmS, tm + kEk + 8 * kk, ks + 128 * kk, id_s);
+            }
+            commit_el(el, rdyS);
+            commit_el(el, &sfree[k]);
+        }
+        commit_el(el, fin);
+    } else if (warp < 4) {
+        // ------------------------------------------------------------- eg dY, hi and lo, 16 bytes of a token at a time
+        for (int it = 0; it < steps; ++it) {
+            const int k = it & 1;
+            if (!wait_warp(&full[k], (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
+            if (it > 0 && !wait_warp(rdyS, ((uint32_t)it & 1u) ^ 1u, abort_flag, status)) break;
+#pragma unroll 4
+            for (int v = 0; v < 16; ++v) {
+                const int i = v * 64 + (warp & 1) * 32 + lane, pn = i >> 9, t = (i >> 3) & 63;
+                const uint32_t at = swz(t, i & 7);
+                const uint4 y = *reinterpret_cast<const uint4 *>(sm + (pn ? Z::dy1 : Z::dy0) + k * kPanel + at);
+                const float g = scal_of(k, PAIR ? pn : 0)[t];
+                const uint32_t in[4] = {y.x, y.y, y.z, y.w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split2(g * bf16_lo(in[e]), g * bf16_hi(in[e]), hi[e], lo[e]);
+                *reinterpret_cast<uint4 *>(sm + Z::e + pn * kPanel + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(sm + Z::e + (2 + pn) * kPanel + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(eb);
+        }
+    } else if (warp < kOWarp) {
+        // ------------------------------------------------------------- T
+        const int qtr = warp & 3, sub = (warp - 4) >> 2, e = PAIR ? qtr >> 1 : 0;
+        const uint32_t lo_ = tmem + ((uint32_t)(32 * qtr) << 16);
+        constexpr int SC = NT / 4;
+        const int n0 = sub * SC, tk0 = 16 * sub;
+        if constexpr (PAIR) {  // zeros in the other head's tokens
+            const uint32_t none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            tmem_st8(lo_ + kTmA + 32 * (1 - e) + 8 * sub, none);
+            tmem_st8(lo_ + kTmAl + 32 * (1 - e) + 8 * sub, none);
+        }
+        int it = 0;
+        bool ok = true;
+        for (int j = 0; ok && j < share.n; ++j) {
+            const Seg sg = share.at(j);
+            int b, h, pc;
+            place(sg.stream, b, h, pc);
+            const int p = PAIR ? (qtr & 1) * 32 + lane : pc + 32 * qtr + lane;
+            const int64_t srow = ((int64_t)b * a.H + h + e) * a.P + p;
+            if (sg.c0 > 0 && !(ok = __all_sync(0xffffffffu, wait_count(a.flags + cta - 1, kTWarps, abort_flag, status)))) break;
+            int t = sg.c0;
+            for (; t < sg.c1; ++t, ++it) {
+                const int k = it & 1;
+                const uint32_t par = (uint32_t)it & 1u;
+                if (!wait_warp(&full[k], (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
+                const float *eg = scal_of(k, e), *ek = eg + kC, *bt = eg + 2 * kC;
+                if (it > 0) {
+                    if (!wait_warp(rdyS, par ^ 1u, abort_flag, status)) break;
+                    if (!wait_warp(ost, par ^ 1u, abort_flag, status)) break;
+                    tc_fence_after();
+                }
+                {  // D's operands; then D times exp(cum_end)
+                    uint32_t s[SC];
+                    if (t > sg.c0) {
+                        if constexpr (SC == 32) {
+                            tmem_ld32(lo_ + kTmS + n0, s);
+                            tmem_wait_ld(s);
+                        } else {
+                            tmem_ld16(lo_ + kTmS + n0, s);
+                            tmem_wait_ld();
+                        }
+                    } else {
+                        load_rows<SC>(s, a, t > 0 ? cta - 1 : -1, p, srow, n0, 32 * qtr + lane, NT);
+                    }
+#pragma unroll
+                    for (int i0 = 0; i0 < SC; i0 += 16) {
+                        uint32_t hi[8], lw[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            split2(__uint_as_float(s[i0 + 2 * i]), __uint_as_float(s[i0 + 2 * i + 1]), hi[i], lw[i]);
+                        tmem_st8(lo_ + kTmHi + (n0 + i0) / 2, hi);
+                        tmem_st8(lo_ + kTmLo + (n0 + i0) / 2, lw);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sb);
+                    const float gamma = eg[kC - 1];
+#pragma unroll
+                    for (int i0 = 0; i0 < SC; i0 += 16) {
+                        uint32_t v[16];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 g = mul2(make_float2(gamma, gamma), pair_of(s[i0 + 2 * i], s[i0 + 2 * i + 1]));
+                            v[2 * i] = __float_as_uint(g.x), v[2 * i + 1] = __float_as_uint(g.y);
+                        }
+                        tmem_st16(lo_ + kTmS + n0 + i0, v);
+                    }
+                }
+                // beta F = beta Z + beta ek D K^T
+                float F[16], be[16];
+                if (!wait_warp(rdyZ, par, abort_flag, status)) break;
+                tc_fence_after();
+                uint32_t zf[16];
+                tmem_ld16(lo_ + kTmY + tk0, zf);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 k4 = *reinterpret_cast<const float4 *>(ek + tk0 + i), b4 = *reinterpret_cast<const float4 *>(bt + tk0 + i);
+                    be[i] = b4.x * k4.x, be[i + 1] = b4.y * k4.y, be[i + 2] = b4.z * k4.z, be[i + 3] = b4.w * k4.w;
+                    F[i] = b4.x * __uint_as_float(zf[i]), F[i + 1] = b4.y * __uint_as_float(zf[i + 1]);
+                    F[i + 2] = b4.z * __uint_as_float(zf[i + 2]), F[i + 3] = b4.w * __uint_as_float(zf[i + 3]);
+                }
+                if (!wait_warp(rdyR, par, abort_flag, status)) break;
+                tc_fence_after();
+                {
+                    uint32_t r[16], hi[8], lw[8];
+                    tmem_ld16(lo_ + kTmR + tk0, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 g4 = *reinterpret_cast<const float4 *>(eg + j + i);
-                        r[i] = __float_as_uint(g4.x * __uint_as_float(r[i])), r[i + 1] = __float_as_uint(g4.y * __uint_as_float(r[i + 1]));
-                        r[i + 2] = __float_as_uint(g4.z * __uint_as_float(r[i + 2]));
-                        r[i + 3] = __float_as_uint(g4.w * __uint_as_float(r[i + 3]));
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 bf = fma2(make_float2(be[2 * i], be[2 * i + 1]), pair_of(r[2 * i], r[2 * i + 1]),
+                                               make_float2(F[2 * i], F[2 * i + 1]));
+                        split2(bf.x, bf.y, hi[i], lw[i]);
                     }
-                    tmem_st16(lo_ + kTmY + j, r);
+                    tmem_st8(lo_ + kTmA + 32 * e + 8 * sub, hi);
+                    tmem_st8(lo_ + kTmAl + 32 * e + 8 * sub, lw);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ab);
+                    // while W^T (beta F) runs: F itself, and -eg beta
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 g4 = *reinterpret_cast<const float4 *>(eg + tk0 + i), b4 = *reinterpret_cast<const float4 *>(bt + tk0 + i);
+                        const float4 k4 = *reinterpret_cast<const float4 *>(ek + tk0 + i);
+                        F[i] = fmaf(k4.x, __uint_as_float(r[i]), __uint_as_float(zf[i]));
+                        F[i + 1] = fmaf(k4.y, __uint_as_float(r[i + 1]), __uint_as_float(zf[i + 1]));
+                        F[i + 2] = fmaf(k4.z, __uint_as_float(r[i + 2]), __uint_as_float(zf[i + 2]));
+                        F[i + 3] = fmaf(k4.w, __uint_as_float(r[i + 3]), __uint_as_float(zf[i + 3]));
+                        be[i] = -g4.x * b4.x, be[i + 1] = -g4.y * b4.y, be[i + 2] = -g4.z * b4.z, be[i + 3] = -g4.w * b4.w;
+                    }
                 }
-                tmem_wait_st();
-                tc_fence_before();
+                // z = F + E, r = beta z; -eg r first, which D waits for
+                if (!wait_warp(rdyE, par, abort_flag, status)) break;
+                tc_fence_after();
+                {
+                    uint32_t r[16], hi[8], lw[8];
+                    tmem_ld16(lo_ + kTmR + tk0, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        F[2 * i] += __uint_as_float(r[2 * i]), F[2 * i + 1] += __uint_as_float(r[2 * i + 1]);
+                        const float2 er = mul2(make_float2(be[2 * i], be[2 * i + 1]), make_float2(F[2 * i], F[2 * i + 1]));
+                        split2(er.x, er.y, hi[i], lw[i]);
+                    }
+                    tmem_st8(lo_ + kEk + 8 * sub, hi);
+                    tmem_st8(lo_ + kEkl + 8 * sub, lw);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ub);
+                    // z and dX, rounded, over Z (which every T warp has read by now)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 b4 = *reinterpret_cast<const float4 *>(bt + tk0 + i);
+                        hi[i / 2] = pack_bf16(F[i], F[i + 1]), hi[i / 2 + 1] = pack_bf16(F[i + 2], F[i + 3]);
+                        lw[i / 2] = pack_bf16(b4.x * F[i], b4.y * F[i + 1]), lw[i / 2 + 1] = pack_bf16(b4.z * F[i + 2], b4.w * F[i + 3]);
+                    }
+                    tmem_st8(lo_ + kTmY + 8 * sub, hi);
+                    tmem_st8(lo_ + kTmY + 32 + 8 * sub, lw);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(yu);
+                        mbar_arrive(&sfree[k]);
+                    }
+                }
+            }
+            if (t < sg.c1 || !wait_warp(rdyS, (uint32_t)(it - 1) & 1u, abort_flag, status)) break;
+            tc_fence_after();
+            store_rows<SC>(lo_ + kTmS, a, sg.c1 < nc, cta, p, srow, n0, 32 * qtr + lane, NT);
+            if (sg.c1 < nc) {
+                __threadfence();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(ys);
-                    mbar_arrive(&sfree[k]);
-                }
-                if (!wait_warp(rdyY, par, abort_flag, status)) break;
-            } else {  // the entering state, as S hi holds it
+                if (lane == 0) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(a.flags + cta) : "memory");
+            }
+        }
+    } else {
+        // ------------------------------------------------------------- O
+        const int qtr = warp & 3, e = PAIR ? qtr >> 1 : 0;
+        const uint32_t lo_ = tmem + ((uint32_t)(32 * qtr) << 16);
+        unsigned char *stage = sm + Z::out + qtr * 8192;  // D hi: [64 columns][32 rows][128 B]; z, dX: [64 tokens][32 rows]
+        const uint64_t pol = policy_evict_first();
+        int it = 0;
+        bool ok = true;
+        for (int j = 0; ok && j < share.n; ++j) {
+            const Seg sg = share.at(j);
+            int b, h, pc;
+            place(sg.stream, b, h, pc);
+            const int p0 = PAIR ? (qtr & 1) * 32 : pc + 32 * qtr;
+            int t = sg.c0;
+            for (; t < sg.c1; ++t, ++it) {
+                const int c = nc - 1 - t;
+                const uint32_t par = (uint32_t)it & 1u;
                 if (!wait_warp(sb, par, abort_flag, status)) break;
                 tc_fence_after();
-                if (lane == 0) bulk_wait_read();  // the staging's last store has read it
+                if (lane == 0) bulk_wait_read();
                 __syncwarp();
-#pragma unroll
-                for (int pn = 0; pn < NT / 64; ++pn) {
-                    uint32_t v[32];
-                    tmem_ld32(lo_ + kTmHi + 32 * pn, v);
-                    tmem_wait_ld(v);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint4 *>(stage2 + pn * 4096 + swz(lane, i)) =
-                            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                }
+                put_state<NT>(lo_ + kTmHi, stage, lane);
                 tc_fence_before();
                 fence_proxy_async();
                 __syncwarp();
@@ -636,63 +1135,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0 && p0 < a.P) {
                     const int unit = (b * a.H + h + e) * nc + c;
                     for (int pn = 0; pn < NT / 64; ++pn)
-                        if (64 * pn < a.N) tma_store_4d(&tm_s, stage2 + pn * 4096, 64 * pn, p0, unit, 0, pol);
+                        if (64 * pn < a.N) tma_store_4d(&tm_d, stage + pn * 4096, 64 * pn, p0, unit, 0, pol);
                     bulk_commit();
                 }
                 if (!wait_warp(yu, par, abort_flag, status)) break;
-            }
-            tc_fence_after();
-            if (lane == 0) bulk_wait_read();
-            __syncwarp();
+                tc_fence_after();
+                if (lane == 0) bulk_wait_read();
+                __syncwarp();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t o[32];
-                tmem_ld32(lo_ + kTmY + 32 * half, o);
-                tmem_wait_ld(o);
-                if (half) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(ofree);
-                }
-                if constexpr (kStore) {  // pairs of tokens: u, then err
-                    unsigned char *st = half ? stage1 : stage0;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        *reinterpret_cast<uint16_t *>(st + (2 * i) * 64 + 2 * lane) = (uint16_t)(o[i] & 0xffffu);
-                        *reinterpret_cast<uint16_t *>(st + (2 * i + 1) * 64 + 2 * lane) = (uint16_t)(o[i] >> 16);
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t o[32];
+                    tmem_ld32(lo_ + kTmY + 32 * half, o);
+                    tmem_wait_ld(o);
+                    if (half) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(ofree);
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        reinterpret_cast<__nv_bfloat16 *>(stage0 + (32 * half + i) * 64)[lane] = __float2bfloat16_rn(__uint_as_float(o[i]));
+                    put_pairs(o, stage + 4096 * half, lane);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0 && p0 < a.P) {
+                    tma_store_4d(&tm_z, stage, p0, h + e, c * kC, b, pol);
+                    tma_store_4d(&tm_dx, stage + 4096, p0, h + e, c * kC, b, pol);
+                    bulk_commit();
                 }
             }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0 && p0 < a.P) {
-                tma_store_4d(&tm_o0, stage0, p0, h + e, c * kC, b, pol);
-                if constexpr (kStore) tma_store_4d(&tm_o1, stage1, p0, h + e, c * kC, b, pol);
-                bulk_commit();
-            }
-        }
-        ok = c == sg.c1;
+            ok = t == sg.c1;
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
     }
+    tear_down(tmem, fin, warp, lane);
+}
 
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 1) {
-        if (lane == 0) {  // every issued product has completed before TMEM is released
-            const unsigned long long t0 = now_ns();
-            while (!mbar_try(fin, 0) && now_ns() - t0 < kWaitNs) {
-            }
-        }
-        __syncwarp();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
-    }
+struct Maps {
+    CUtensorMap k, q, x, o0, o1, s;
+};
+
+template <int NT, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1) k_delta_tc(const __grid_constant__ Maps m, const __grid_constant__ ChainArgs a) {
+    chain_fwd<NT, PAIR, false>(m.k, m.q, m.x, m.o0, m.o1, m.s, a, blockIdx.x, gridDim.x);
+}
+
+// Both chains of the backward pass, which do not depend on one another: the first half of the CTAs
+// recomputes the states, the other half walks back.
+template <int NT, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_delta_tc_bwd(const __grid_constant__ Maps mf, const __grid_constant__ Maps mr, const __grid_constant__ ChainArgs f,
+                   const __grid_constant__ ChainArgs r) {
+    const int half = gridDim.x / 2;
+    if ((int)blockIdx.x < half)
+        chain_fwd<NT, PAIR, true>(mf.k, mf.q, mf.x, mf.o0, mf.o1, mf.s, f, blockIdx.x, half);
+    else
+        chain_rev<NT, PAIR>(mr.k, mr.q, mr.x, mr.o0, mr.o1, mr.s, r, blockIdx.x - half, half);
 }
 
 // [B, L, X, inner] bf16, boxes of 32 columns by 64 tokens, not swizzled (the O warps' staging).
@@ -726,22 +1223,18 @@ bool encode_states(CUtensorMap *m, const void *base, int64_t N, int64_t P, int64
 bool pairs(const DeltaProblem &p) { return p.P <= 64 && (p.H / p.G) % 2 == 0; }
 int64_t streams_of(const DeltaProblem &p) { return pairs(p) ? p.B * (p.H / 2) : p.B * p.H * ((p.P + 127) / 128); }
 
-template <int NT, bool PAIR, bool kStore>
-cudaError_t launch(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s) {
-    CUtensorMap tk, tq, tx, t0, t1, ts;
-    const int64_t nc = (p.L + kC - 1) / kC;
-    if (!encode_4d(&tk, p.Bm, p.N, p.G, p.L, p.B, kC) || !encode_4d(&tq, p.Cm, p.N, p.G, p.L, p.B, kC) ||
-        !encode_4d(&tx, p.x, p.P, p.H, p.L, p.B, kC) ||
-        !encode_out(&t0, kStore ? ch.u : p.y, p.P, p.H, p.L, p.B) || !encode_out(&t1, kStore ? ch.err : p.y, p.P, p.H, p.L, p.B))
-        return cudaErrorInvalidValue;
-    if (kStore ? !encode_states(&ts, ch.states, p.N, p.P, p.B * p.H * nc) : (ts = t0, false)) return cudaErrorInvalidValue;
-    const int tiles = PAIR ? 1 : (int)((p.P + 127) / 128);
-    const int64_t streams = streams_of(p);
-    const int grid = delta_tc_grid(p);
-    const ChainArgs a{p.h0,   ch.prep,   ch.prep_bytes, (int)nc,  (int)p.H,  (int)p.P,        (int)p.G, (int)p.N,
-                      tiles,  (int)streams, p.h_final,  ch.hand, ch.flags, ch.status, wait_limit_us()};
-    constexpr int smem = Lay<NT, PAIR, kStore>::bytes;
-    const auto kernel = k_delta_tc<NT, PAIR, kStore>;
+bool encode_maps(Maps *m, const DeltaProblem &p, const void *x, const void *o0, const void *o1, const void *states) {
+    const int64_t units = p.B * p.H * ((p.L + kC - 1) / kC);
+    if (!encode_4d(&m->k, p.Bm, p.N, p.G, p.L, p.B, kC) || !encode_4d(&m->q, p.Cm, p.N, p.G, p.L, p.B, kC) ||
+        !encode_4d(&m->x, x, p.P, p.H, p.L, p.B, kC) || !encode_out(&m->o0, o0, p.P, p.H, p.L, p.B))
+        return false;
+    m->o1 = m->o0;
+    m->s = m->o0;
+    return !states || (encode_out(&m->o1, o1, p.P, p.H, p.L, p.B) && encode_states(&m->s, states, p.N, p.P, units));
+}
+
+template <typename K, typename... A>
+cudaError_t launch(K kernel, int grid, int smem, bool cut, cudaStream_t s, const A &...args) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e) return e;
     // Where a stream is cut its CTAs have to be resident together, which a cooperative launch guarantees.
@@ -754,33 +1247,60 @@ cudaError_t launch(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s) 
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = streams > grid ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, tk, tq, tx, t0, t1, ts, a);
+    cfg.numAttrs = cut ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int NT, bool kStore>
-cudaError_t launch_pair(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s) {
-    return pairs(p) ? launch<NT, true, kStore>(p, ch, s) : launch<NT, false, kStore>(p, ch, s);
+ChainArgs args_of(const DeltaProblem &p, const DeltaChain &ch, const float *first, float *last, int cta0) {
+    const int tiles = pairs(p) ? 1 : (int)((p.P + 127) / 128);
+    return ChainArgs{first, ch.prep, ch.prep_bytes, ch.scal_at, ch.rows_at, (int)((p.L + kC - 1) / kC), (int)p.H, (int)p.P,
+                     (int)p.G, (int)p.N, tiles, (int)streams_of(p), last, ch.hand + (int64_t)cta0 * 128 * (p.N <= 64 ? 64 : 128),
+                     ch.flags + cta0, ch.status, wait_limit_us()};
+}
+
+template <int NT, bool PAIR>
+cudaError_t fwd(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s) {
+    Maps m;
+    if (!encode_maps(&m, p, p.x, p.y, nullptr, nullptr)) return cudaErrorInvalidValue;
+    const int grid = delta_tc_grid(p, false);
+    return launch(k_delta_tc<NT, PAIR>, grid, Lay<NT, PAIR, false>::bytes, streams_of(p) > grid, s, m,
+                  args_of(p, ch, p.h0, p.h_final, 0));
+}
+
+template <int NT, bool PAIR>
+cudaError_t bwd(const DeltaProblem &p, const DeltaGrads &g, const DeltaChain &ch, cudaStream_t s) {
+    Maps mf, mr;
+    if (!encode_maps(&mf, p, p.x, ch.u, ch.err, ch.states) || !encode_maps(&mr, p, g.dy, ch.z, g.dx, ch.cots))
+        return cudaErrorInvalidValue;
+    const int grid = delta_tc_grid(p, true);
+    constexpr int f = Lay<NT, PAIR, true>::bytes, r = RevLay<NT, PAIR>::bytes;
+    return launch(k_delta_tc_bwd<NT, PAIR>, grid, f > r ? f : r, streams_of(p) > grid / 2, s, mf, mr,
+                  args_of(p, ch, p.h0, nullptr, 0), args_of(p, ch, g.dh_final, g.dh0, grid / 2));
 }
 
 }  // namespace
 
-// One CTA per SM (it takes all of TMEM), or per stream where there are fewer.
-int delta_tc_grid(const DeltaProblem &p) {
-    const int sms = num_sms() > 0 ? num_sms() : 148;
+// One CTA per SM (it takes all of TMEM), or per stream where there are fewer; half of them for each of
+// the backward pass's two chains.
+int delta_tc_grid(const DeltaProblem &p, bool backward) {
+    const int sms = num_sms() > 0 ? num_sms() : 148, most = backward ? sms / 2 : sms;
     const int64_t streams = streams_of(p);
-    return (int)(streams < sms ? streams : sms);
+    return (int)(streams < most ? streams : most) * (backward ? 2 : 1);
 }
 
-size_t delta_tc_hand_bytes(const DeltaProblem &p) {
-    const int grid = delta_tc_grid(p);
-    return streams_of(p) > grid ? (size_t)grid * 128 * (p.N <= 64 ? 64 : 128) * sizeof(float) : 0;
+size_t delta_tc_hand_bytes(const DeltaProblem &p, bool backward) {
+    const int grid = delta_tc_grid(p, backward);
+    return streams_of(p) > (backward ? grid / 2 : grid) ? (size_t)grid * 128 * (p.N <= 64 ? 64 : 128) * sizeof(float) : 0;
 }
 
-cudaError_t delta_tc_chain(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s) {
-    const bool store = ch.states != nullptr;
-    if (p.N <= 64) return store ? launch_pair<64, true>(p, ch, s) : launch_pair<64, false>(p, ch, s);
-    return store ? launch_pair<128, true>(p, ch, s) : launch_pair<128, false>(p, ch, s);
+cudaError_t delta_tc_fwd(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s) {
+    if (p.N <= 64) return pairs(p) ? fwd<64, true>(p, ch, s) : fwd<64, false>(p, ch, s);
+    return pairs(p) ? fwd<128, true>(p, ch, s) : fwd<128, false>(p, ch, s);
+}
+
+cudaError_t delta_tc_bwd(const DeltaProblem &p, const DeltaGrads &g, const DeltaChain &ch, cudaStream_t s) {
+    if (p.N <= 64) return pairs(p) ? bwd<64, true>(p, g, ch, s) : bwd<64, false>(p, g, ch, s);
+    return pairs(p) ? bwd<128, true>(p, g, ch, s) : bwd<128, false>(p, g, ch, s);
 }
 
 }  // namespace ssd
