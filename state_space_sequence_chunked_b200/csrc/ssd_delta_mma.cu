@@ -141,8 +141,14 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16 *__r
 // in fp32 (a lane per column), then the rows of blocks below, on tensor cores with every fp32 operand
 // in two bf16 parts:
 //     W_ab = -(I + W_aa diag(beta_a)) (M_ab (I + diag(beta_b) W_bb) + sum_{b<c<a} M_ac diag(beta_c) W_cb).
-constexpr int kLd = kC + 4;  // padded row of the fp32 tiles
-constexpr int kDl = 20;      // padded row of a diagonal block
+constexpr int kDl = 20;  // padded row of a diagonal block
+// The fp32 products are kept up to the diagonal block: row i of block row a has 16 (a + 1) columns and a
+// pad of 8 (a half warp's pairs then fall in different banks).
+__device__ __forceinline__ int tri_at(int i) {
+    const int a = i >> 4;
+    return 16 * (4 * a * (2 * a + 4)) + (i & 15) * (16 * a + 24);
+}
+constexpr int kTriFloats = 16 * (24 + 40 + 56 + 72);
 
 struct PrepWarp {
     float diag[4][16 * kDl];
@@ -150,12 +156,12 @@ struct PrepWarp {
     float beta[kC];
 };
 template <int NT>
-struct PrepSmem {
-    float kk[kC * kLd], qk[kC * kLd];
-    union {
-        struct {
-            __nv_bfloat16 k[kC * NT], q[kC * NT];
-        };
+union PrepSmem {
+    struct {
+        __nv_bfloat16 k[kC * NT], q[kC * NT];
+    };
+    struct {  // once K and Q are done with
+        float kk[kTriFloats], qk[kTriFloats];
         PrepWarp w[4];
     };
 };
@@ -211,7 +217,7 @@ __device__ __forceinline__ void put_w(char *out, int a, int b, int lane, const f
 }
 
 template <int NT, bool BWD>
-__global__ void __launch_bounds__(kThr)
+__global__ void __launch_bounds__(kThr, 4)
     k_delta_prep(const __nv_bfloat16 *__restrict__ Bm, const __nv_bfloat16 *__restrict__ Cm, const __nv_bfloat16 *__restrict__ g,
                  const __nv_bfloat16 *__restrict__ beta, int64_t L, int H, int G, int N, int slices, char *__restrict__ ws,
                  int *__restrict__ clear, int nclear) {
@@ -254,26 +260,31 @@ __global__ void __launch_bounds__(kThr)
                 }
             }
         }
+        __syncthreads();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             if (j < 2 * warp + 2) {
-                const int i = 16 * warp + gr, col = 8 * j + 2 * tg;
-                *reinterpret_cast<float2 *>(&sm.kk[i * kLd + col]) = make_float2(kk[j][0], kk[j][1]);
-                *reinterpret_cast<float2 *>(&sm.kk[(i + 8) * kLd + col]) = make_float2(kk[j][2], kk[j][3]);
-                *reinterpret_cast<float2 *>(&sm.qk[i * kLd + col]) = make_float2(qk[j][0], qk[j][1]);
-                *reinterpret_cast<float2 *>(&sm.qk[(i + 8) * kLd + col]) = make_float2(qk[j][2], qk[j][3]);
+                const int r0 = tri_at(16 * warp + gr) + 8 * j + 2 * tg, r1 = tri_at(16 * warp + gr + 8) + 8 * j + 2 * tg;
+                *reinterpret_cast<float2 *>(&sm.kk[r0]) = make_float2(kk[j][0], kk[j][1]);
+                *reinterpret_cast<float2 *>(&sm.kk[r1]) = make_float2(kk[j][2], kk[j][3]);
+                *reinterpret_cast<float2 *>(&sm.qk[r0]) = make_float2(qk[j][0], qk[j][1]);
+                *reinterpret_cast<float2 *>(&sm.qk[r1]) = make_float2(qk[j][2], qk[j][3]);
             }
         }
     }
-    __syncthreads();  // K and Q are done with: the warps' own memory lies over them
+    __syncthreads();
     PrepWarp &wm = sm.w[warp];
+    const bool in0 = t0 + 2 * lane < L, in1 = t0 + 2 * lane + 1 < L;  // 2 tokens per lane
+    const auto token = [&](const __nv_bfloat16 *src, int h, int o) {
+        return (o ? in1 : in0) && h < h_end ? to_f32(src[(b * L + t0 + 2 * lane + o) * H + h]) : 0.f;
+    };
+    float next[4] = {token(g, h_begin + warp, 0), token(g, h_begin + warp, 1), token(beta, h_begin + warp, 0), token(beta, h_begin + warp, 1)};
     for (int h = h_begin + warp; h < h_end; h += 4) {
         char *out = ws + ((b * H + h) * nc + c) * (int64_t)Lay::bytes;
         {  // cumulated log decay: 2 tokens per lane, fp64
-            const int64_t at = (b * L + t0 + 2 * lane) * H + h;
-            const bool in0 = t0 + 2 * lane < L, in1 = t0 + 2 * lane + 1 < L;
-            const double g0 = in0 ? clamp_log_decay(to_f32(g[at])) : 0.0, g1 = in1 ? clamp_log_decay(to_f32(g[at + H])) : 0.0;
-            const float b0 = in0 ? to_f32(beta[at]) : 0.f, b1 = in1 ? to_f32(beta[at + H]) : 0.f;
+            const double g0 = clamp_log_decay(next[0]), g1 = clamp_log_decay(next[1]);
+            const float b0 = next[2], b1 = next[3];
+            next[0] = token(g, h + 4, 0), next[1] = token(g, h + 4, 1), next[2] = token(beta, h + 4, 0), next[3] = token(beta, h + 4, 1);
             double sum = g0 + g1;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -304,8 +315,9 @@ __global__ void __launch_bounds__(kThr)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int i = 16 * a + gr + 8 * r;
-                    const float2 kk = *reinterpret_cast<const float2 *>(&sm.kk[i * kLd + j]);
-                    const float2 qk = *reinterpret_cast<const float2 *>(&sm.qk[i * kLd + j]);
+                    const int at = tri_at(i) + j;
+                    const float2 kk = *reinterpret_cast<const float2 *>(&sm.kk[at]);
+                    const float2 qk = *reinterpret_cast<const float2 *>(&sm.qk[at]);
                     const float e0 = j <= i ? decay_between(ri[r], make_float2(cj.x, cj.y)) : 0.f;
                     const float e1 = j + 1 <= i ? decay_between(ri[r], make_float2(cj.z, cj.w)) : 0.f;
                     m[n][2 * r] = j < i ? kk.x * e0 : 0.f, m[n][2 * r + 1] = j + 1 < i ? kk.y * e1 : 0.f;
@@ -774,9 +786,9 @@ cudaError_t prep_launch(const DeltaProblem &p, char *ws, int *clear, int nclear,
     using bf = __nv_bfloat16;
     const int64_t nc = (p.L + kC - 1) / kC, units = nc * p.G * p.B;
     const int per = (int)(p.H / p.G);
-    // a CTA walks all heads of a group while that leaves 3 CTAs (what fits) for every SM, and
+    // a CTA walks all heads of a group while that leaves 4 CTAs (what fits) for every SM, and
     // four heads at least, one per warp
-    int slices = units >= 148 * 3 ? 1 : (int)((148 * 3 + units - 1) / units);
+    int slices = units >= 148 * 4 ? 1 : (int)((148 * 4 + units - 1) / units);
     if (slices > (per + 3) / 4) slices = (per + 3) / 4;
     cudaError_t e;
     constexpr int smem = sizeof(PrepSmem<NT>);
