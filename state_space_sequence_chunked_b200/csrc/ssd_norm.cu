@@ -256,10 +256,10 @@ __global__ void __launch_bounds__(V == 8 && S == 1 ? 768 : kMaxThr)
     }
 }
 
-// The backward kernels keep a row as it was loaded (packed) between the two passes over it, the
-// weights in shared memory, and so at most 80 registers where a row is one vector per thread.
+// The other kernels keep a row as it was loaded (packed) between the two passes over it, and load the next
+// row before they begin on it, so that loads are in flight all the time.
 template <typename T, typename R, int V, int S>
-__global__ void __launch_bounds__(V == 8 && S == 1 ? 768 : kMaxThr)
+__global__ void __launch_bounds__(V == 8 && S == 1 ? 640 : kMaxThr)
     k_add_rmsnorm_bwd(Geom q, const R *r, const float *__restrict__ w, float eps, const T *dout, const R *dres_in, const T *x,
                       const float *__restrict__ scale, R *dres, T *dx, float *dw_part, float *ds_part) {
     extern __shared__ __align__(16) float sm[];
@@ -277,30 +277,44 @@ __global__ void __launch_bounds__(V == 8 && S == 1 ? 768 : kMaxThr)
 #pragma unroll
         for (int v = 0; v < V; ++v) dw[s][v] = ds[s][v] = 0.f;
     __syncthreads();
+    struct Row {
+        Raw<R, V> r[S], i[S];
+        Raw<T, V> d[S], x[S];
+    };
+    const auto load = [&](Row &to, uint32_t row) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int e = (at.tl + s * q.tpg) * V;
+            if (at.live && row < q.rows && e < q.gs) {
+                const int64_t off = (int64_t)row * q.gs + e;
+                to.r[s] = load_raw<R, V>(r + off);
+                to.d[s] = load_raw<T, V>(dout + off);
+                if (dres_in) to.i[s] = load_raw<R, V>(dres_in + off);
+                if (ds_part) to.x[s] = load_raw<T, V>(x + off);
+            }
+        }
+    };
+    constexpr bool kAhead = V == 8 && S == 1;
+    Row next;
+    if (kAhead) load(next, blockIdx.y * (uint32_t)q.rpc + at.row_slot);
     SSD_FOR_ROWS(q, 1) {
         const uint32_t row = base;
         const bool on = at.live && row < q.rows;
-        Raw<R, V> rr[S], ir[S];
-        Raw<T, V> dr[S], xr[S];
+        Row now;
+        if (kAhead) {
+            now = next;
+            load(next, row + gridDim.y * (uint32_t)q.rpc);
+        } else {
+            load(now, row);
+        }
         float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int e = (at.tl + s * q.tpg) * V;
             if (on && e < q.gs) {
-                const int64_t off = (int64_t)row * q.gs + e;
-                rr[s] = load_raw<R, V>(r + off);
-                dr[s] = load_raw<T, V>(dout + off);
-                if (dres_in) ir[s] = load_raw<R, V>(dres_in + off);
-                if (ds_part) xr[s] = load_raw<T, V>(x + off);
-            }
-        }
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int e = (at.tl + s * q.tpg) * V;
-            if (on && e < q.gs) {
                 float rv[V], dv[V], wv[V];
-                unpack(rr[s], rv);
-                unpack(dr[s], dv);
+                unpack(now.r[s], rv);
+                unpack(now.d[s], dv);
                 unpack(load_raw<float, V>(ws + e), wv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
@@ -319,11 +333,11 @@ __global__ void __launch_bounds__(V == 8 && S == 1 ? 768 : kMaxThr)
 #pragma unroll
                 for (int v = 0; v < V; ++v) o[v] = xv[v] = 0.f;
                 const int64_t off = (int64_t)row * q.gs + e;
-                unpack(rr[s], rv);
-                unpack(dr[s], dv);
+                unpack(now.r[s], rv);
+                unpack(now.d[s], dv);
                 unpack(load_raw<float, V>(ws + e), wv);
-                if (dres_in) unpack(ir[s], o);
-                if (ds_part) unpack(xr[s], xv);
+                if (dres_in) unpack(now.i[s], o);
+                if (ds_part) unpack(now.x[s], xv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const float n = rv[v] * rstd;
@@ -345,68 +359,71 @@ __global__ void __launch_bounds__(V == 8 && S == 1 ? 768 : kMaxThr)
     if (ds_part) put_part<V, S>(ds, q, at, sm, ds_part);
 }
 
-template <typename T, int V, int S, int U>
-__global__ void __launch_bounds__(V == 8 && S == 1 ? 768 : kMaxThr)
+template <typename T, int V, int S>
+__global__ void __launch_bounds__(V == 8 && S == 1 ? 1024 : kMaxThr)
     k_norm_gate(Geom q, const T *y, const T *z, int64_t z_stride, const float *__restrict__ w, float eps, T *out) {
-    __shared__ SumBuf<U> buf;
+    __shared__ SumBuf<1> buf;
     uint32_t turn = 0;
     const Pos at(q);
     const int dim = q.gs * q.ngroups, col = at.group * q.gs;
     float wv[S][V];
     load_cols<V, S>(w, q, at, wv, 0.f);
-    SSD_FOR_ROWS(q, U) {
-        Raw<T, V> yr[U][S], zr[U][S];
-        float sum[U];
+    struct Row {
+        Raw<T, V> y[S], z[S];
+    };
+    const auto load = [&](Row &to, uint32_t row) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t row = base + u * q.rpc;
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const int e = (at.tl + s * q.tpg) * V;
-                if (at.live && row < q.rows && e < q.gs) {
-                    yr[u][s] = load_raw<T, V>(y + (int64_t)row * dim + (col + e));
-                    zr[u][s] = load_raw<T, V>(z + (int64_t)row * z_stride + (col + e));
-                }
+        for (int s = 0; s < S; ++s) {
+            const int e = (at.tl + s * q.tpg) * V;
+            if (at.live && row < q.rows && e < q.gs) {
+                to.y[s] = load_raw<T, V>(y + (int64_t)row * dim + (col + e));
+                to.z[s] = load_raw<T, V>(z + (int64_t)row * z_stride + (col + e));
             }
         }
+    };
+    constexpr bool kAhead = V == 8 && S == 1;
+    Row next;
+    if (kAhead) load(next, blockIdx.y * (uint32_t)q.rpc + at.row_slot);
+    SSD_FOR_ROWS(q, 1) {
+        const uint32_t row = base;
+        const bool on = at.live && row < q.rows;
+        Row now;
+        if (kAhead) {
+            now = next;
+            load(next, row + gridDim.y * (uint32_t)q.rpc);
+        } else {
+            load(now, row);
+        }
+        float sum[1] = {0.f};
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t row = base + u * q.rpc;
-            sum[u] = 0.f;
+        for (int s = 0; s < S; ++s) {
+            const int e = (at.tl + s * q.tpg) * V;
+            if (on && e < q.gs) {
+                float f[V];
+                unpack(now.y[s], f);
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const int e = (at.tl + s * q.tpg) * V;
-                if (at.live && row < q.rows && e < q.gs) {
-                    float f[V];
-                    unpack(yr[u][s], f);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) sum[u] = fmaf(f[v], f[v], sum[u]);
-                }
+                for (int v = 0; v < V; ++v) sum[0] = fmaf(f[v], f[v], sum[0]);
             }
         }
         group_sum(sum, q.tpg, buf, turn);
+        const float rstd = rsqrtf(fmaf(sum[0], q.inv, eps));
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t row = base + u * q.rpc;
-            const float rstd = rsqrtf(fmaf(sum[u], q.inv, eps));
+        for (int s = 0; s < S; ++s) {
+            const int e = (at.tl + s * q.tpg) * V;
+            if (on && e < q.gs) {
+                float f[V], zv[V];
+                unpack(now.y[s], f);
+                unpack(now.z[s], zv);
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const int e = (at.tl + s * q.tpg) * V;
-                if (at.live && row < q.rows && e < q.gs) {
-                    float f[V], zv[V];
-                    unpack(yr[u][s], f);
-                    unpack(zr[u][s], zv);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) f[v] *= (rstd * wv[s][v]) * (zv[v] * sigmoid(zv[v]));
-                    store_v<T, V>(out + (int64_t)row * dim + (col + e), f);
-                }
+                for (int v = 0; v < V; ++v) f[v] *= (rstd * wv[s][v]) * (zv[v] * sigmoid(zv[v]));
+                store_v<T, V>(out + (int64_t)row * dim + (col + e), f);
             }
         }
     }
 }
 
 template <typename T, int V, int S, bool kGateFirst>
-__global__ void __launch_bounds__(V == 8 && S == 1 ? 768 : kMaxThr)
+__global__ void __launch_bounds__(V == 8 && S == 1 ? 640 : kMaxThr)
     k_gate_bwd(Geom q, const T *y, const T *z, int64_t z_stride, const float *__restrict__ w, float eps, const T *dout, T *dy,
                T *dz, int64_t dz_stride, float *dw_part) {
     extern __shared__ __align__(16) float sm[];
@@ -420,28 +437,42 @@ __global__ void __launch_bounds__(V == 8 && S == 1 ? 768 : kMaxThr)
     for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int v = 0; v < V; ++v) dw[s][v] = 0.f;
+    struct Row {
+        Raw<T, V> y[S], z[S], d[S];
+    };
+    const auto load = [&](Row &to, uint32_t row) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int e = (at.tl + s * q.tpg) * V;
+            if (at.live && row < q.rows && e < q.gs) {
+                to.y[s] = load_raw<T, V>(y + (int64_t)row * dim + (col + e));
+                to.z[s] = load_raw<T, V>(z + (int64_t)row * z_stride + (col + e));
+                to.d[s] = load_raw<T, V>(dout + (int64_t)row * dim + (col + e));
+            }
+        }
+    };
+    constexpr bool kAhead = V == 8 && S == 1;
+    Row next;
+    if (kAhead) load(next, blockIdx.y * (uint32_t)q.rpc + at.row_slot);
     SSD_FOR_ROWS(q, 1) {
         const uint32_t row = base;
         const bool on = at.live && row < q.rows;
-        Raw<T, V> yr[S], zr[S], dr[S];
+        Row now;
+        if (kAhead) {
+            now = next;
+            load(next, row + gridDim.y * (uint32_t)q.rpc);
+        } else {
+            load(now, row);
+        }
         float sg[S][V], sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int e = (at.tl + s * q.tpg) * V;
             if (on && e < q.gs) {
-                yr[s] = load_raw<T, V>(y + (int64_t)row * dim + (col + e));
-                zr[s] = load_raw<T, V>(z + (int64_t)row * z_stride + (col + e));
-                dr[s] = load_raw<T, V>(dout + (int64_t)row * dim + (col + e));
-            }
-        }
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int e = (at.tl + s * q.tpg) * V;
-            if (on && e < q.gs) {
                 float yv[V], zv[V], dv[V];
-                unpack(yr[s], yv);
-                unpack(zr[s], zv);
-                unpack(dr[s], dv);
+                unpack(now.y[s], yv);
+                unpack(now.z[s], zv);
+                unpack(now.d[s], dv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     sg[s][v] = sigmoid(zv[v]);
@@ -460,9 +491,9 @@ __global__ void __launch_bounds__(V == 8 && S == 1 ? 768 : kMaxThr)
             const int e = (at.tl + s * q.tpg) * V;
             if (on && e < q.gs) {
                 float yv[V], zv[V], dv[V], oy[V], oz[V];
-                unpack(yr[s], yv);
-                unpack(zr[s], zv);
-                unpack(dr[s], dv);
+                unpack(now.y[s], yv);
+                unpack(now.z[s], zv);
+                unpack(now.d[s], dv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const float sig = sg[s][v], gate = zv[v] * sig;
@@ -615,8 +646,8 @@ cudaError_t gate_fwd(const GateNormArgs &a, cudaStream_t st) {
     const int gs = (int)(a.dim / a.ngroups);
     const int vec = vec_of(gs, a.z_stride, gs, sizeof(T), {a.y, a.z, a.out});
     return with_vs(vec, gs, [&](auto vs) {
-        const auto kernel = k_norm_gate<T, vs.V, vs.S, vs.U>;
-        const Launch l = geom(kernel, a.rows, gs, (int)a.ngroups, vs.V, vs.S, vs.U, 0);
+        const auto kernel = k_norm_gate<T, vs.V, vs.S>;
+        const Launch l = geom(kernel, a.rows, gs, (int)a.ngroups, vs.V, vs.S, 1, 0);
         if (l.error) return l.error;
         kernel<<<l.grid, l.threads, l.smem, st>>>(l.q, static_cast<const T *>(a.y),
                                                                  static_cast<const T *>(a.z), a.z_stride, a.weight, a.eps,
