@@ -60,6 +60,11 @@ int delta_tc_grid(const DeltaProblem &p, bool backward);
 size_t delta_tc_hand_bytes(const DeltaProblem &p, bool backward);
 cudaError_t delta_tc_fwd(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s);
 cudaError_t delta_tc_bwd(const DeltaProblem &p, const DeltaGrads &g, const DeltaChain &ch, cudaStream_t s);
+// After both chains (ssd_delta_grads.cu): dBm, dCm, dg, dbeta. With more than one slice of a group's heads
+// the keys' and queries' gradients are fp32 parts [B, L, G * slices, N], to be summed.
+int delta_grads_slices(const DeltaProblem &p);
+cudaError_t delta_grads(const DeltaProblem &p, const DeltaGrads &g, const DeltaChain &ch, float *dB_part, float *dC_part,
+                        cudaStream_t s);
 
 // one token (p.L, p.h0, p.h_final unused); state_out may be state_in
 cudaError_t delta_step(const DeltaProblem &p, const float *state_in, float *state_out, cudaStream_t s);

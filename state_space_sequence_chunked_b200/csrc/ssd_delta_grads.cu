@@ -1,0 +1,477 @@
+// The gradients of the gated delta rule that sum over the rows of the state, on tcgen05, after both chains.
+// Per chunk and head, with S the state entering the chunk, D the cotangent leaving it, E_ij =
+// exp(cum_i - cum_j) for i >= j, eg = exp(cum), ek = exp(cum_end - cum), u = beta err, r = beta z:
+//     dP = tril((dY u^T) o E),   dM = -tril((r u^T) o E, -1),
+//     dQ = eg dY S + dP K,
+//     dK = -eg r S + ek u D + dM K + dP^T Q + dM^T K,
+//     dbeta_i = z_i.err_i,   dg = the sum from i to the chunk's end of
+//         rows - columns of (dP o Q K^T + dM o K K^T) + eg dY_i.S q_i - eg r_i.S k_i - U_i,
+//         U_i = ek_i u_i.D k_i, and at the last token + sum U + exp(cum_end) <D, S>.
+// No sum runs across chunks, and each pair of tokens enters once, in fp32.
+//
+// A CTA takes a chunk of a group and walks its heads (of its slice), 64 state rows at a time. dQ and dK of
+// the chunk stand in TMEM for all of them, tokens by lane (dQ in lanes 0-63, dK in 64-127), and every term is
+// a product with 128 rows that adds to both or, with a panel of zeros, to dK alone:
+//     [eg dY; -eg r] S,  [0; ek u] D,  [dP; dM] K,  [0; dP^T] Q,  [0; dM^T] K
+// so that the CUDA cores only scale the left operands, form dP and dM out of [dY; r] u^T, and take the
+// dot products of dg with [Q; K] S^T and [Q; K] D^T. Operands are rounded to bf16 once each; sums are fp32, in
+// a fixed order (no atomics).
+//
+// Warps (640 threads): 0 loads (TMA, two stages), 1 issues the products, 2 ends a head (dg, dbeta), 4-19 the
+// elementwise work, four per 32 lanes with a quarter of the columns each.
+//
+// Bound by the elementwise warps: about 2500 issue slots per head and SM against 1400 cycles of products.
+// The same sums with mma.sync in registers (64 tokens by half or a quarter of the columns per warp) took 212 us
+// on the 130M-like backward, 23800 instructions a head.
+//
+// Every wait is bounded (tc_ptx.cuh); one that runs out sets bit 0 of the workspace's status word.
+#include "delta_tc.cuh"
+
+namespace ssd {
+namespace {
+
+using namespace tc;
+
+constexpr int kCWarps = 16, kThreads = 32 * (4 + kCWarps);
+constexpr int kTmG = 0, kTmP = 128, kTmS = 192, kTmD = 256, kTmConst = 320;
+
+struct HeadSums {
+    float rows[4][128];  // by column quarter: dQ-side and dK-side tokens
+    float cols[4][kC];   // by lane quarter
+    float U[4][kC];
+    float dot[kCWarps], db[kC];
+};
+
+template <int NT>
+struct Lay {
+    static constexpr int pn = NT / 64;
+    static constexpr int qk = 0;                                  // [panel][Q 64 rows, K 64 rows]
+    static constexpr int x1 = qk + pn * 2 * kPanel;               // [eg dY; -eg r]
+    static constexpr int zero = x1 + 2 * kPanel, x2 = zero + kPanel;  // [0; ek u]
+    static constexpr int dp = x2 + kPanel;                        // [dP; dM]
+    static constexpr int s = 0, d = pn * kPanel, dy = 2 * pn * kPanel, r = dy + kPanel, u = r + kPanel, stage = u + kPanel;
+    static constexpr int stages = dp + 2 * kPanel;
+    static constexpr int scal = stages + 2 * stage;               // [2][eg, ek, beta, cum as two floats][64]
+    static constexpr int sums = scal + 2 * 5 * kC * 4;
+    static constexpr int bar = sums + 2 * (int)sizeof(HeadSums);
+    static constexpr int bytes = bar + 256;
+    static constexpr int tx = stage;
+};
+
+struct GradArgs {
+    const char *prep;
+    int64_t prep_bytes;
+    int scal_at, nc, L, H, P, G, N, slices;
+    const __nv_bfloat16 *z, *err;
+    __nv_bfloat16 *dBm, *dCm, *dg, *dbeta;
+    float *dB_part, *dC_part;
+    int *status;
+    int wait_us;
+};
+struct Maps {
+    CUtensorMap k, q, dy, r, u, s, d;
+};
+
+__device__ __forceinline__ uint32_t scale_pair(float f, uint32_t v) { return pack_bf16(f * bf16_lo(v), f * bf16_hi(v)); }
+__device__ __forceinline__ uint4 scale8(float f, uint4 v) {
+    return make_uint4(scale_pair(f, v.x), scale_pair(f, v.y), scale_pair(f, v.z), scale_pair(f, v.w));
+}
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = fmaf(bf16_lo(x[i]), bf16_lo(y[i]), fmaf(bf16_hi(x[i]), bf16_hi(y[i]), s));
+    return s;
+}
+// sum of v over p of a TMEM row piece (16 columns) and the same columns of a bf16 row
+__device__ __forceinline__ float dot16(const uint32_t (&v)[16], uint4 a, uint4 b) {
+    const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float s = 0.f, t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        s = fmaf(__uint_as_float(v[2 * i]), bf16_lo(x[i]), s);
+        t = fmaf(__uint_as_float(v[2 * i + 1]), bf16_hi(x[i]), t);
+    }
+    return s + t;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const __grid_constant__ Maps m, const __grid_constant__ GradArgs a) {
+    using Z = Lay<NT>;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    if ((smem_u32(sm) & 1023u) != 0) {
+        if (threadIdx.x == 0) atomicOr(a.status, 2);
+        return;
+    }
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + Z::bar);
+    uint64_t *full = bar, *sfree = bar + 2;      // [2] a stage's loads landed; its readers done
+    uint64_t *rdyC = bar + 4, *rdyD = bar + 5;   // Q K^T and K K^T; a step's products to be read
+    uint64_t *done = bar + 6;                    // a step's products into dQ, dK
+    uint64_t *dfree = bar + 7;                   // the products read
+    uint64_t *xb = bar + 8, *pb = bar + 9;       // left operands written: scaled rows; dP, dM
+    uint64_t *hd = bar + 10, *hfree = bar + 12;  // [2] a head's sums written; read
+    uint64_t *fin = bar + 14;
+    int *status = a.status;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x, b = blockIdx.z, t0 = c * kC, nt = a.L - t0 < kC ? a.L - t0 : kC;
+    const int grp = blockIdx.y / a.slices, slice = blockIdx.y % a.slices, per = a.H / a.G;
+    const int h_begin = grp * per + per * slice / a.slices, h_end = grp * per + per * (slice + 1) / a.slices;
+    const int nslab = (a.P + 63) / 64, steps = (h_end - h_begin) * nslab;
+    for (int i = threadIdx.x; i < kPanel / 16; i += kThreads) reinterpret_cast<uint4 *>(sm + Z::zero)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async();
+    constexpr int counts[15] = {1, 1, 1 + kCWarps, 1 + kCWarps, 1, 1, 1, kCWarps, kCWarps, kCWarps, kCWarps, kCWarps, 1, 1, 1};
+    const Setup su = set_up(bar, counts, a.wait_us, warp);
+    const uint32_t tmem = su.tmem;
+    volatile int *abort_flag = su.abort_flag;
+    const auto stage_of = [&](int k) { return sm + Z::stages + k * Z::stage; };
+    const auto scal_of = [&](int k) { return reinterpret_cast<const float *>(sm + Z::scal + k * 5 * kC * 4); };
+    const auto sums_of = [&](int turn) { return reinterpret_cast<HeadSums *>(sm + Z::sums) + (turn & 1); };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------- loads
+        if (lane == 0) {
+            const uint64_t once = policy_evict_first();
+            int it = 0;
+            for (; it < steps; ++it) {
+                const int k = it & 1, h = h_begin + it / nslab, p = it % nslab * 64;
+                if (it >= 2 && !wait_phase(&sfree[k], (uint32_t)((it - 2) >> 1) & 1u, abort_flag, status)) break;
+                unsigned char *st = stage_of(k);
+                mbar_arrive_tx(&full[k], Z::tx + 5 * kC * 4 + (it == 0 ? Z::pn * 2 * kPanel : 0));
+                if (it == 0)
+                    for (int pn = 0; pn < Z::pn; ++pn) {
+                        tma_load_4d(sm + Z::qk + pn * 2 * kPanel, &m.q, &full[k], 64 * pn, grp, t0, b);
+                        tma_load_4d(sm + Z::qk + pn * 2 * kPanel + kPanel, &m.k, &full[k], 64 * pn, grp, t0, b);
+                    }
+                const int unit = (b * a.H + h) * a.nc + c;
+                bulk_load(sm + Z::scal + k * 5 * kC * 4, a.prep + (int64_t)unit * a.prep_bytes + a.scal_at, 5 * kC * 4, &full[k]);
+                tma_load_4d_hint(st + Z::dy, &m.dy, &full[k], p, h, t0, b, once);
+                tma_load_4d_hint(st + Z::r, &m.r, &full[k], p, h, t0, b, once);
+                tma_load_4d_hint(st + Z::u, &m.u, &full[k], p, h, t0, b, once);
+                for (int pn = 0; pn < Z::pn; ++pn) {
+                    tma_load_4d_hint(st + Z::s + pn * kPanel, &m.s, &full[k], 64 * pn, p, unit, 0, once);
+                    tma_load_4d_hint(st + Z::d + pn * kPanel, &m.d, &full[k], 64 * pn, p, unit, 0, once);
+                }
+            }
+            drain_loads(full, it);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------- products
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t el = elect_one(), base = smem_u32(sm);
+        constexpr uint32_t id64 = idesc(128, 64, false, false);                // K-major both, N = 64
+        constexpr uint32_t idn = idesc(128, NT, false, true), idt = idesc(128, NT, true, true);  // into dQ, dK
+        const uint64_t qk = sdesc(base + Z::qk, 16, 1024), kr = sdesc(base + Z::qk + kPanel, 16, 1024);
+        const uint64_t qn = sdesc(base + Z::qk, 2 * kPanel, 1024), kn = sdesc(base + Z::qk + kPanel, 2 * kPanel, 1024);
+        const uint64_t x1 = sdesc(base + Z::x1, 16, 1024), x2 = sdesc(base + Z::zero, 16, 1024), dp = sdesc(base + Z::dp, 16, 1024);
+        const uint64_t dpt = sdesc(base + Z::zero, Z::dp - Z::zero, 1024), dmt = sdesc(base + Z::zero, Z::dp + kPanel - Z::zero, 1024);
+        for (int it = 0; it < steps; ++it) {
+            const int k = it & 1, slab = it % nslab;
+            const uint32_t par = (uint32_t)it & 1u, st = base + Z::stages + k * Z::stage;
+            if (!wait_warp(&full[k], (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
+            if (it == 0) {
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < NT / 16; ++kk) {
+                    const uint64_t off = (uint64_t)(((kk >> 2) * 2 * kPanel + (kk & 3) * 32) >> 4);
+                    mma_ss_el(el, tm + kTmConst, qk + off, kr + off, id64, kk > 0);
+                }
+                commit_el(el, rdyC);
+            }
+            if (it > 0 && !wait_warp(dfree, par ^ 1u, abort_flag, status)) break;
+            tc_fence_after();
+            const uint64_t dyr = sdesc(st + Z::dy, 16, 1024), ur = sdesc(st + Z::u, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mma_ss_el(el, tm + kTmP, dyr + 2 * kk, ur + 2 * kk, id64, slab > 0 || kk > 0);
+            const uint64_t sr = sdesc(st + Z::s, 16, 1024), dr = sdesc(st + Z::d, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < NT / 16; ++kk) {
+                const uint64_t offa = (uint64_t)(((kk >> 2) * 2 * kPanel + (kk & 3) * 32) >> 4);
+                const uint64_t offb = (uint64_t)(((kk >> 2) * kPanel + (kk & 3) * 32) >> 4);
+                mma_ss_el(el, tm + kTmS, qk + offa, sr + offb, id64, kk > 0);
+                mma_ss_el(el, tm + kTmD, qk + offa, dr + offb, id64, kk > 0);
+            }
+            commit_el(el, rdyD);
+            if (!wait_warp(xb, par, abort_flag, status)) break;
+            tc_fence_after();
+            const uint64_t sn = sdesc(st + Z::s, kPanel, 1024), dn = sdesc(st + Z::d, kPanel, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                mma_ss_el(el, tm + kTmG, x1 + 2 * kk, sn + 128 * kk, idn, it > 0 || kk > 0);
+                mma_ss_el(el, tm + kTmG, x2 + 2 * kk, dn + 128 * kk, idn, 1);
+            }
+            if (!wait_warp(pb, par, abort_flag, status)) break;
+            if (slab == nslab - 1) {
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    mma_ss_el(el, tm + kTmG, dp + 2 * kk, kn + 128 * kk, idn, 1);
+                    mma_ss_el(el, tm + kTmG, dpt + 128 * kk, qn + 128 * kk, idt, 1);
+                    mma_ss_el(el, tm + kTmG, dmt + 128 * kk, kn + 128 * kk, idt, 1);
+                }
+            }
+            commit_el(el, done);
+            commit_el(el, &sfree[k]);
+        }
+        commit_el(el, fin);
+    } else if (warp == 2) {
+        // ------------------------------------------------------------- a head's end: dg and dbeta, 2 tokens per lane
+        for (int turn = 0; turn < h_end - h_begin; ++turn) {
+            if (!wait_warp(&hd[turn & 1], (uint32_t)(turn >> 1) & 1u, abort_flag, status)) break;
+            const HeadSums &s = *sums_of(turn);
+            float d[2], us = 0.f, end = lane < kCWarps ? s.dot[lane] : 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e;
+                us += (s.U[0][i] + s.U[1][i]) + (s.U[2][i] + s.U[3][i]);
+                d[e] = 0.f;
+#pragma unroll
+                for (int o = 0; o < 4; ++o) d[e] += (s.rows[o][i] + s.rows[o][64 + i]) - s.cols[o][i];
+            }
+            const float b0 = s.db[2 * lane], b1 = s.db[2 * lane + 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&hfree[turn & 1]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                us += __shfl_xor_sync(0xffffffffu, us, o);
+                end += __shfl_xor_sync(0xffffffffu, end, o);
+            }
+            float s2 = d[0] + d[1];
+            if (lane == 31) s2 += us + end;  // (dot comes with exp(cum_end))
+            const float odd = lane == 31 ? d[1] + us + end : d[1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float up = __shfl_down_sync(0xffffffffu, s2, o);
+                if (lane + o < 32) s2 += up;
+            }
+            // s2: from token 2 lane on; the next lane's from 2 lane + 2 on
+            const float nxt = __shfl_down_sync(0xffffffffu, s2, 1);
+            const int64_t at = ((int64_t)b * a.L + t0 + 2 * lane) * a.H + h_begin + turn;
+            if (2 * lane < nt) a.dg[at] = __float2bfloat16_rn(s2), a.dbeta[at] = __float2bfloat16_rn(b0);
+            if (2 * lane + 1 < nt)
+                a.dg[at + a.H] = __float2bfloat16_rn(odd + (lane < 31 ? nxt : 0.f)), a.dbeta[at + a.H] = __float2bfloat16_rn(b1);
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------- elementwise
+        const int qtr = warp & 3, sub = (warp - 4) >> 2;
+        const uint32_t lo_ = tmem + ((uint32_t)(32 * qtr) << 16);
+        const int row = 32 * qtr + lane, i = row & 63;  // lane of TMEM; its token
+        const bool upper = row >= 64;                   // (warp-uniform) the rows of dK
+        const int ct = (warp - 4) * 32 + lane, lt = ct >> 3, lc = ct & 7;  // and by 16-byte vector: token, vector
+        float rowsum = 0.f, usum = 0.f, dots = 0.f, db = 0.f;
+        const auto vec = [&](const __nv_bfloat16 *src, int it) {
+            const int h = h_begin + it / nslab, p = it % nslab * 64 + 8 * lc;
+            return lt < nt && p < a.P && it < steps
+                       ? __ldg(reinterpret_cast<const uint4 *>(src + (((int64_t)b * a.L + t0 + lt) * a.H + h) * a.P + p))
+                       : make_uint4(0, 0, 0, 0);
+        };
+        uint4 zv = vec(a.z, 0), ev = vec(a.err, 0);
+        bool ok = true;
+        for (int it = 0; it < steps; ++it) {
+            const int k = it & 1, turn = it / nslab, slab = it % nslab;
+            const uint32_t par = (uint32_t)it & 1u;
+            ok = false;
+            if (!wait_warp(&full[k], (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
+            const unsigned char *st = stage_of(k);
+            const float *eg = scal_of(k), *ek = eg + kC, *ch = eg + 3 * kC, *cl = eg + 4 * kC;
+            if (it > 0 && !wait_warp(done, par ^ 1u, abort_flag, status)) break;  // the left operands are free
+            {
+                const uint32_t at = swz(lt, lc);
+                const float g = eg[lt], kf = ek[lt];
+                *reinterpret_cast<uint4 *>(sm + Z::x1 + at) = scale8(g, *reinterpret_cast<const uint4 *>(st + Z::dy + at));
+                *reinterpret_cast<uint4 *>(sm + Z::x1 + kPanel + at) = scale8(-g, *reinterpret_cast<const uint4 *>(st + Z::r + at));
+                *reinterpret_cast<uint4 *>(sm + Z::x2 + at) = scale8(kf, *reinterpret_cast<const uint4 *>(st + Z::u + at));
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(xb);
+            }
+            if (it == 0 && !wait_warp(rdyC, 0, abort_flag, status)) break;
+            if (slab == 0) {
+                rowsum = usum = dots = db = 0.f;
+                // the sums of the head before last have been read
+                if (turn >= 2 && !wait_warp(&hfree[turn & 1], (uint32_t)((turn - 2) >> 1) & 1u, abort_flag, status)) break;
+            }
+            if (!wait_warp(rdyD, par, abort_flag, status)) break;
+            tc_fence_after();
+            HeadSums &s = *sums_of(turn);
+            if (slab == nslab - 1) {  // the pairs: tokens 16 sub .. + 15 of this row
+                uint32_t v[16], w[16];
+                tmem_ld16(lo_ + kTmP + 16 * sub, v);
+                tmem_ld16(lo_ + kTmConst + 16 * sub, w);
+                tmem_wait_ld(v);
+                tmem_wait_ld(w);
+                const float ih = ch[i], il = cl[i];
+                float pr[16];
+                uint32_t o[8];
+                if (16 * sub > (i | 31)) {  // (warp-uniform) above the diagonal
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) pr[j] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[j] = 0;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        const int jj = 16 * sub + j;
+                        const float4 h4 = *reinterpret_cast<const float4 *>(ch + jj), l4 = *reinterpret_cast<const float4 *>(cl + jj);
+                        const float hj[4] = {h4.x, h4.y, h4.z, h4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
+                        float x[4];
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            const bool in = upper ? jj + n < i : jj + n <= i;
+                            const float ex = ex2(1.44269504f * ((ih - hj[n]) + (il - lj[n])));
+                            x[n] = in ? (upper ? -ex : ex) * __uint_as_float(v[j + n]) : 0.f;
+                            pr[j + n] = x[n] * __uint_as_float(w[j + n]);
+                            rowsum += pr[j + n];
+                        }
+                        o[j / 2] = pack_bf16(x[0], x[1]), o[j / 2 + 1] = pack_bf16(x[2], x[3]);
+                    }
+                }
+                *reinterpret_cast<uint4 *>(sm + Z::dp + swz(row, 2 * sub)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(sm + Z::dp + swz(row, 2 * sub + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pb);
+                // columns: halves exchanged and added, so that lane l ends with column l >> 1
+#pragma unroll
+                for (int w2 = 8, x = 16; w2 >= 1; w2 >>= 1, x >>= 1)
+#pragma unroll
+                    for (int j = 0; j < w2; ++j) {
+                        const bool up = lane & x;
+                        const float send = up ? pr[j] : pr[j + w2], keep = up ? pr[j + w2] : pr[j];
+                        pr[j] = keep + __shfl_xor_sync(0xffffffffu, send, x);
+                    }
+                pr[0] += __shfl_xor_sync(0xffffffffu, pr[0], 1);
+                if ((lane & 1) == 0) s.cols[qtr][16 * sub + (lane >> 1)] = pr[0];
+            } else if (lane == 0) {
+                mbar_arrive(pb);
+            }
+            {  // dot products of dg, columns (state rows) 16 sub .. + 15 of the slab
+                uint32_t v[16], w[16];
+                tmem_ld16(lo_ + kTmS + 16 * sub, v);
+                tmem_ld16(lo_ + kTmD + 16 * sub, w);
+                tmem_wait_ld(v);
+                tmem_wait_ld(w);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(dfree);
+                const unsigned char *rw = st + Z::dy;  // [dY; r], 128 rows
+                const float d1 = dot16(v, *reinterpret_cast<const uint4 *>(rw + swz(row, 2 * sub)),
+                                       *reinterpret_cast<const uint4 *>(rw + swz(row, 2 * sub + 1)));
+                if (upper) {
+                    const float d2 = dot16(w, *reinterpret_cast<const uint4 *>(st + Z::u + swz(i, 2 * sub)),
+                                           *reinterpret_cast<const uint4 *>(st + Z::u + swz(i, 2 * sub + 1)));
+                    const float U = ek[i] * d2;
+                    usum += U;
+                    rowsum -= eg[i] * d1 + U;
+                } else {
+                    rowsum += eg[i] * d1;
+                }
+            }
+            // <D, S> and dbeta
+#pragma unroll
+            for (int v = 0; v < Z::pn; ++v)
+                dots = dot8(reinterpret_cast<const uint4 *>(st + Z::s)[ct + 512 * v], reinterpret_cast<const uint4 *>(st + Z::d)[ct + 512 * v], dots);
+            db = dot8(zv, ev, db);
+            zv = vec(a.z, it + 1), ev = vec(a.err, it + 1);
+            if (slab == nslab - 1) {
+                s.rows[sub][row] = rowsum;
+                if (upper) s.U[sub][i] = usum;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) dots += __shfl_xor_sync(0xffffffffu, dots, o);
+                if (lane == 0) s.dot[warp - 4] = eg[kC - 1] * dots;
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) db += __shfl_xor_sync(0xffffffffu, db, o);
+                if (lc == 0) s.db[lt] = db;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&hd[turn & 1]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sfree[k]);
+            ok = true;
+        }
+        if (ok && wait_warp(done, (uint32_t)(steps - 1) & 1u, abort_flag, status)) {  // dQ and dK
+            tc_fence_after();
+            constexpr int W = NT / 4;
+            const bool live = i < nt;
+            const int64_t tok = (int64_t)b * a.L + t0 + i;
+#pragma unroll
+            for (int j = 0; j < W; j += 16) {
+                uint32_t v[16];
+                tmem_ld16(lo_ + kTmG + W * sub + j, v);
+                tmem_wait_ld(v);
+#pragma unroll
+                for (int n = 0; n < 16; n += 8) {
+                    const int col = W * sub + j + n;
+                    if (!live || col >= a.N) continue;
+                    const float *f = reinterpret_cast<const float *>(v + n);
+                    if (a.slices == 1) {
+                        __nv_bfloat16 *dst = (upper ? a.dBm : a.dCm) + (tok * a.G + grp) * a.N + col;
+                        *reinterpret_cast<uint4 *>(dst) =
+                            make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+                    } else {
+                        float *dst = (upper ? a.dB_part : a.dC_part) + (tok * gridDim.y + blockIdx.y) * a.N + col;
+                        reinterpret_cast<float4 *>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
+                        reinterpret_cast<float4 *>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
+                    }
+                }
+            }
+        }
+    }
+    tear_down(tmem, fin, warp, lane);
+}
+
+// [units, P, N] bf16 states, boxes of 64 columns by 64 rows, 128-byte swizzle.
+bool encode_state_tiles(CUtensorMap *m, const void *base, int64_t N, int64_t P, int64_t units) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)N, (cuuint64_t)P, (cuuint64_t)units, 1};
+    const cuuint64_t strides[3] = {(cuuint64_t)(N * 2), (cuuint64_t)(P * N * 2), (cuuint64_t)(units * P * N * 2)};
+    const cuuint32_t box[4] = {64, 64, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT>
+cudaError_t launch(const DeltaProblem &p, const DeltaGrads &g, const DeltaChain &ch, float *dB_part, float *dC_part, cudaStream_t s) {
+    using bf = __nv_bfloat16;
+    const int64_t nc = (p.L + kC - 1) / kC, units = p.B * p.H * nc;
+    Maps m;
+    if (!encode_4d(&m.k, p.Bm, p.N, p.G, p.L, p.B, kC) || !encode_4d(&m.q, p.Cm, p.N, p.G, p.L, p.B, kC) ||
+        !encode_4d(&m.dy, g.dy, p.P, p.H, p.L, p.B, kC) || !encode_4d(&m.r, g.dx, p.P, p.H, p.L, p.B, kC) ||
+        !encode_4d(&m.u, ch.u, p.P, p.H, p.L, p.B, kC) || !encode_state_tiles(&m.s, ch.states, p.N, p.P, units) ||
+        !encode_state_tiles(&m.d, ch.cots, p.N, p.P, units))
+        return cudaErrorInvalidValue;
+    const int slices = delta_grads_slices(p);
+    const GradArgs a{ch.prep, ch.prep_bytes, ch.scal_at, (int)nc, (int)p.L, (int)p.H, (int)p.P, (int)p.G, (int)p.N, slices,
+                     static_cast<const bf *>(ch.z), static_cast<const bf *>(ch.err), static_cast<bf *>(g.dBm), static_cast<bf *>(g.dCm),
+                     static_cast<bf *>(g.dg), static_cast<bf *>(g.dbeta), dB_part, dC_part, ch.status, wait_limit_us()};
+    constexpr int smem = Lay<NT>::bytes;
+    const cudaError_t e = cudaFuncSetAttribute(k_delta_grads<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e) return e;
+    k_delta_grads<NT><<<dim3((unsigned)nc, (unsigned)(p.G * slices), (unsigned)p.B), kThreads, smem, s>>>(m, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Slices of a group's heads: the number that makes (waves of CTAs on 148 SMs) x (heads a CTA walks)
+// smallest, the fewest of them unless more save an eighth (more than one costs fp32 parts and a second
+// pass).
+int delta_grads_slices(const DeltaProblem &p) {
+    const int64_t units = (p.L + kC - 1) / kC * p.G * p.B, per = p.H / p.G;
+    int best = 1;
+    int64_t cost = (units + 147) / 148 * per;
+    for (int s = 2; s <= per && s <= 16; ++s) {
+        const int64_t here = (units * s + 147) / 148 * ((per + s - 1) / s);
+        if (here * 8 < cost * 7) cost = here, best = s;
+    }
+    return best;
+}
+
+cudaError_t delta_grads(const DeltaProblem &p, const DeltaGrads &g, const DeltaChain &ch, float *dB_part, float *dC_part,
+                        cudaStream_t s) {
+    return p.N <= 64 ? launch<64>(p, g, ch, dB_part, dC_part, s) : launch<128>(p, g, ch, dB_part, dC_part, s);
+}
+
+}  // namespace ssd

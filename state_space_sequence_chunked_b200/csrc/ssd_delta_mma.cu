@@ -429,358 +429,6 @@ __global__ void __launch_bounds__(kThr, 4)
     }
 }
 
-// ---------------------------------------------------------------------------------------------
-// k_delta_grads_mma: grid (chunks, G * slices, B), 8 warps; everything that sums over the state rows. With S
-// the state entering the chunk and D the cotangent leaving it, per head
-//     dP = tril((dY u^T) o E),   dM = -tril((r u^T) o E, -1),
-//     dQ = exp(cum) dY S + dP K,
-//     dK = dP^T Q + (dM + dM^T) K + exp(cum_end - cum) u D - exp(cum) r S,
-//     dbeta_i = z_i.err_i,   dg = the sum from i to the chunk's end of
-//         rows - columns of (dP o Q K^T + dM o K K^T) + exp(cum) dY_i.S q_i - exp(cum) r_i.S k_i - U_i,
-//         U_i = exp(cum_end - cum_i) u_i.D k_i, and at the last token + sum U + exp(cum_end) <D, S>.
-// No sum runs across chunks, and each pair of tokens enters once, in fp32. A CTA walks the heads of its
-// slice with dQ, dK in fp32 accumulators (no atomics), slabs of 64 state rows at a time; a warp holds 16
-// tokens by half of the columns (of dQ, dK, and of the pairs).
-constexpr int kGThr = 256;
-template <int NT>
-struct GradsSmem {
-    __nv_bfloat16 k[kC * NT], q[kC * NT];
-    struct Slab {
-        __nv_bfloat16 s[64 * NT], d[64 * NT], dy[kC * 64], u[kC * 64], r[kC * 64];
-    } slab[2];
-    __nv_bfloat16 dp[kC * kC], dm[kC * kC];  // dP; dM (strictly lower)
-    float2 cum[kC];
-    float eg[kC], ek[kC];
-    float rows[2][kC], cols[4][kC];  // sums by warp column half, by warp row block
-    float U[2][kC];
-    float dot[8], db[kC];
-};
-
-// As load_tile with kGThr threads, rows of [B, L, X, D].
-template <int NV>
-__device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16 *__restrict__ src, int64_t rows, int64_t stride, int cols) {
-    for (int i = threadIdx.x; i < 64 * NV; i += kGThr) {
-        const int t = i / NV, c = i % NV;
-        const bool in = t < rows && 8 * c < cols;
-        cp16(dst + at16<NV * 16>(t, c), in ? src + t * stride + 8 * c : src, in);
-    }
-}
-
-template <int NT>
-__global__ void __launch_bounds__(kGThr)
-    k_delta_grads_mma(const __nv_bfloat16 *__restrict__ dy, const __nv_bfloat16 *__restrict__ Bm,
-                      const __nv_bfloat16 *__restrict__ Cm, const char *__restrict__ ws, const __nv_bfloat16 *__restrict__ states,
-                      const __nv_bfloat16 *__restrict__ cots, const __nv_bfloat16 *__restrict__ err,
-                      const __nv_bfloat16 *__restrict__ u, const __nv_bfloat16 *__restrict__ z, const __nv_bfloat16 *__restrict__ dx,
-                      int64_t L, int H, int P, int G, int N, int slices, __nv_bfloat16 *__restrict__ dBm,
-                      __nv_bfloat16 *__restrict__ dCm, float *__restrict__ dB_part, float *__restrict__ dC_part,
-                      __nv_bfloat16 *__restrict__ dg, __nv_bfloat16 *__restrict__ dbeta) {
-    extern __shared__ __align__(128) char raw[];
-    using Lay = Prep<true>;
-    GradsSmem<NT> &sm = *reinterpret_cast<GradsSmem<NT> *>(raw);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tg = lane & 3;
-    const int rb = warp & 3, nh = warp >> 2;  // 16-token block of rows; half of the columns
-    constexpr int HT = NT / 16;               // 8-column tiles in half of the columns
-    const int64_t c = blockIdx.x, nc = gridDim.x, b = blockIdx.z, t0 = c * kC;
-    const int64_t nt = L - t0 < kC ? L - t0 : kC;
-    const int grp = blockIdx.y / slices, slice = blockIdx.y % slices, per = H / G;
-    const int h_begin = grp * per + per * slice / slices, h_end = grp * per + per * (slice + 1) / slices;
-    const int nslab = (P + 63) / 64, total = (h_end - h_begin) * nslab;
-    const uint32_t ka = smem_addr(sm.k), qa = smem_addr(sm.q), dpa = smem_addr(sm.dp), dma = smem_addr(sm.dm);
-
-    const auto load_slab = [&](int it) {
-        const int h = h_begin + it / nslab, p = it % nslab * 64;
-        auto &sl = sm.slab[it & 1];
-        const int64_t st = (((b * H + h) * nc + c) * (int64_t)P + p) * N, at = ((b * L + t0) * H + h) * (int64_t)P + p;
-        load_rows<NT / 8>(smem_addr(sl.s), states + st, P - p, N, N);
-        load_rows<NT / 8>(smem_addr(sl.d), cots + st, P - p, N, N);
-        load_rows<8>(smem_addr(sl.dy), dy + at, nt, (int64_t)H * P, P - p);
-        load_rows<8>(smem_addr(sl.u), u + at, nt, (int64_t)H * P, P - p);
-        load_rows<8>(smem_addr(sl.r), dx + at, nt, (int64_t)H * P, P - p);
-        cp_commit();
-    };
-    load_rows<NT / 8>(ka, Bm + ((b * L + t0) * G + grp) * (int64_t)N, nt, (int64_t)G * N, N);
-    load_rows<NT / 8>(qa, Cm + ((b * L + t0) * G + grp) * (int64_t)N, nt, (int64_t)G * N, N);
-    load_slab(0);
-
-    float dq[HT][4], dk[HT][4];  // tokens 16 rb + gr (+ 8), columns NT / 2 nh + 8 j + 2 tg (+ 1)
-#pragma unroll
-    for (int j = 0; j < HT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dq[j][e] = dk[j][e] = 0.f;
-    float kk[4][4], qk[4][4];  // pairs: tokens 16 rb + gr (+ 8) by 32 nh + 8 j + 2 tg (+ 1)
-    float dP[4][4], dM[4][4], dsum = 0.f;
-
-    for (int it = 0; it < total; ++it) {
-        const int h = h_begin + it / nslab, p = it % nslab * 64;
-        if (it + 1 < total) {
-            load_slab(it + 1);
-            cp_wait<1>();
-        } else {
-            cp_wait<0>();
-        }
-        if (p == 0 && tid < kC) {  // this head's scalars
-            const float *scal = reinterpret_cast<const float *>(ws + ((b * H + h) * nc + c) * (int64_t)Lay::bytes + Lay::scal);
-            sm.eg[tid] = scal[tid];
-            sm.ek[tid] = scal[kC + tid];
-            sm.cum[tid] = make_float2(scal[3 * kC + tid], scal[4 * kC + tid]);
-        }
-        __syncthreads();
-        if (it == 0) {  // K K^T and Q K^T, once for the group
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) kk[j][e] = qk[j][e] = 0.f;
-#pragma unroll
-            for (int s = 0; s < NT / 16; ++s) {
-                uint32_t ak[4], aq[4];
-                ldsm4(ak, ka + at16<NT * 2>(16 * rb + (lane & 15), 2 * s + (lane >> 4)));
-                ldsm4(aq, qa + at16<NT * 2>(16 * rb + (lane & 15), 2 * s + (lane >> 4)));
-#pragma unroll
-                for (int jj = 0; jj < 2; ++jj) {
-                    uint32_t f[4];
-                    ldsm4(f, ka + at16<NT * 2>(32 * nh + 16 * jj + (lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1)));
-                    mma(kk[2 * jj], ak, f[0], f[1]);
-                    mma(kk[2 * jj + 1], ak, f[2], f[3]);
-                    mma(qk[2 * jj], aq, f[0], f[1]);
-                    mma(qk[2 * jj + 1], aq, f[2], f[3]);
-                }
-            }
-        }
-        auto &sl = sm.slab[it & 1];
-        const uint32_t sa = smem_addr(sl.s), da = smem_addr(sl.d), ya = smem_addr(sl.dy), ua = smem_addr(sl.u), ra = smem_addr(sl.r);
-        if (p == 0) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) dP[j][e] = dM[j][e] = 0.f;
-            dsum = 0.f;
-        }
-        uint32_t ay[4][4], ar[4][4], au[4][4];  // tokens 16 rb ..: left operands over the slab's rows
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const uint32_t off = at16<128>(16 * rb + (lane & 15), 2 * s + (lane >> 4));
-            ldsm4(ay[s], ya + off);
-            ldsm4(ar[s], ra + off);
-            ldsm4(au[s], ua + off);
-        }
-        if (32 * nh <= 16 * rb + 15) {  // pairs up to the diagonal
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int jj = 0; jj < 2; ++jj) {
-                    uint32_t f[4];
-                    ldsm4(f, ua + at16<128>(32 * nh + 16 * jj + (lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1)));
-                    mma(dP[2 * jj], ay[s], f[0], f[1]);
-                    mma(dP[2 * jj + 1], ay[s], f[2], f[3]);
-                    mma(dM[2 * jj], ar[s], f[0], f[1]);
-                    mma(dM[2 * jj + 1], ar[s], f[2], f[3]);
-                }
-        }
-        // the three products with the states, their share of dQ and dK, and their dot products with q and k
-        float rd[2] = {0.f, 0.f}, ud[2] = {0.f, 0.f};
-        const float eg0 = sm.eg[16 * rb + gr], eg1 = sm.eg[16 * rb + gr + 8], ek0 = sm.ek[16 * rb + gr], ek1 = sm.ek[16 * rb + gr + 8];
-#pragma unroll
-        for (int j = 0; j < HT; j += 2) {
-            float ty[2][4], tr[2][4], tu[2][4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) ty[n][e] = tr[n][e] = tu[n][e] = 0.f;
-            const int v = nh * HT + j;  // 16-byte vector of the columns
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                uint32_t fs[4], fd[4];
-                const uint32_t off = at16<NT * 2>(16 * s + (lane & 15), v + (lane >> 4));
-                ldsm4t(fs, sa + off);
-                ldsm4t(fd, da + off);
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    mma(ty[n], ay[s], fs[2 * n], fs[2 * n + 1]);
-                    mma(tr[n], ar[s], fs[2 * n], fs[2 * n + 1]);
-                    mma(tu[n], au[s], fd[2 * n], fd[2 * n + 1]);
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint32_t off = at16<NT * 2>(16 * rb + gr + 8 * r, v + n) + 4 * tg;
-                    const uint32_t kv = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const char *>(sm.k) + off);
-                    const uint32_t qv = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const char *>(sm.q) + off);
-                    const float eg = r ? eg1 : eg0, ek = r ? ek1 : ek0;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float y = eg * ty[n][2 * r + e], rr = eg * tr[n][2 * r + e], uu = ek * tu[n][2 * r + e];
-                        const float kf = e ? high(kv) : low(kv), qf = e ? high(qv) : low(qv);
-                        dq[j + n][2 * r + e] += y;
-                        dk[j + n][2 * r + e] += uu - rr;
-                        rd[r] += y * qf - rr * kf;
-                        ud[r] += uu * kf;
-                    }
-                }
-        }
-        // <D, S>
-        for (int i = tid; i < 64 * NT / 8; i += kGThr) {
-            const uint4 sv = reinterpret_cast<const uint4 *>(sl.s)[i], dv = reinterpret_cast<const uint4 *>(sl.d)[i];
-            const uint32_t a[4] = {sv.x, sv.y, sv.z, sv.w}, d[4] = {dv.x, dv.y, dv.z, dv.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dsum = fmaf(low(a[e]), low(d[e]), fmaf(high(a[e]), high(d[e]), dsum));
-        }
-        // dbeta: four threads per token, 16 rows each
-        float db = 0.f;
-        if (tid / 4 < nt) {
-            const int64_t at = ((b * L + t0 + tid / 4) * H + h) * (int64_t)P + p + (tid & 3) * 16;
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-                if (p + (tid & 3) * 16 + 8 * v < P) {
-                    const uint4 zv = *reinterpret_cast<const uint4 *>(z + at + 8 * v), ev = *reinterpret_cast<const uint4 *>(err + at + 8 * v);
-                    const uint32_t a[4] = {zv.x, zv.y, zv.z, zv.w}, d[4] = {ev.x, ev.y, ev.z, ev.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) db = fmaf(low(a[e]), low(d[e]), fmaf(high(a[e]), high(d[e]), db));
-                }
-        }
-        db += __shfl_xor_sync(0xffffffffu, db, 1);
-        db += __shfl_xor_sync(0xffffffffu, db, 2);
-        if ((tid & 3) == 0) sm.db[tid / 4] = p == 0 ? db : sm.db[tid / 4] + db;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                rd[r] += __shfl_xor_sync(0xffffffffu, rd[r], o);
-                ud[r] += __shfl_xor_sync(0xffffffffu, ud[r], o);
-            }
-            if (tg == 0) {
-                float *ro = &sm.rows[nh][16 * rb + gr + 8 * r], *uo = &sm.U[nh][16 * rb + gr + 8 * r];
-                *ro = p == 0 ? rd[r] : *ro + rd[r];
-                *uo = p == 0 ? ud[r] : *uo + ud[r];
-            }
-        }
-        if (p + 64 >= P) {  // the head's last slab: the pairs
-            float row_sum[2] = {0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int jc = 32 * nh + 8 * j + 2 * tg;
-                const float4 cj = *reinterpret_cast<const float4 *>(&sm.cum[jc]);
-                float col[2] = {0.f, 0.f};
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int i = 16 * rb + gr + 8 * r;
-                    const float2 ci = sm.cum[i];
-                    float p2[2], m2[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float ex = jc + e <= i ? decay_between(ci, e ? make_float2(cj.z, cj.w) : make_float2(cj.x, cj.y)) : 0.f;
-                        p2[e] = jc + e <= i ? dP[j][2 * r + e] * ex : 0.f;
-                        m2[e] = jc + e < i ? -dM[j][2 * r + e] * ex : 0.f;
-                        const float pair = p2[e] * qk[j][2 * r + e] + m2[e] * kk[j][2 * r + e];
-                        row_sum[r] += pair;
-                        col[e] += pair;
-                    }
-                    const uint32_t off = at16<128>(i, 4 * nh + j) + 4 * tg;
-                    *reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(sm.dp) + off) = pack(p2[0], p2[1]);
-                    *reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(sm.dm) + off) = pack(m2[0], m2[1]);
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) col[e] += __shfl_xor_sync(0xffffffffu, col[e], o);
-                    if (gr == 0) sm.cols[rb][jc + e] = col[e];
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-#pragma unroll
-                for (int o = 1; o < 4; o <<= 1) row_sum[r] += __shfl_xor_sync(0xffffffffu, row_sum[r], o);
-                if (tg == 0) sm.rows[nh][16 * rb + gr + 8 * r] += row_sum[r];
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) dsum += __shfl_xor_sync(0xffffffffu, dsum, o);
-            if (lane == 0) sm.dot[warp] = dsum;
-            __syncthreads();
-            // dQ += dP K; dK += dP^T Q + (dM + dM^T) K
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                uint32_t ap[4], am[4], pt[4], mt[4];
-                const uint32_t off = at16<128>(16 * rb + (lane & 15), 2 * s + (lane >> 4));
-                const uint32_t offt = at16<128>(16 * s + (lane & 7) + ((lane >> 4) << 3), 2 * rb + ((lane >> 3) & 1));
-                if (s <= rb) {
-                    ldsm4(ap, dpa + off);
-                    ldsm4(am, dma + off);
-                }
-                if (s >= rb) {
-                    ldsm4t(pt, dpa + offt);
-                    ldsm4t(mt, dma + offt);
-                }
-#pragma unroll
-                for (int j = 0; j < HT; j += 2) {
-                    uint32_t fk[4], fq[4];
-                    const uint32_t o2 = at16<NT * 2>(16 * s + (lane & 15), nh * HT + j + (lane >> 4));
-                    ldsm4t(fk, ka + o2);
-                    if (s <= rb) {
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            mma(dq[j + n], ap, fk[2 * n], fk[2 * n + 1]);
-                            mma(dk[j + n], am, fk[2 * n], fk[2 * n + 1]);
-                        }
-                    }
-                    if (s >= rb) {
-                        ldsm4t(fq, qa + o2);
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            mma(dk[j + n], pt, fq[2 * n], fq[2 * n + 1]);
-                            mma(dk[j + n], mt, fk[2 * n], fk[2 * n + 1]);
-                        }
-                    }
-                }
-            }
-            if (warp == 0) {  // dg: tokens 2 lane, 2 lane + 1, summed from the chunk's end
-                float d[2], us = 0.f;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int i = 2 * lane + e;
-                    const float U = sm.U[0][i] + sm.U[1][i];
-                    us += U;
-                    d[e] = sm.rows[0][i] + sm.rows[1][i] - ((sm.cols[0][i] + sm.cols[1][i]) + (sm.cols[2][i] + sm.cols[3][i])) - U;
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) us += __shfl_xor_sync(0xffffffffu, us, o);
-                float end = 0.f;
-                for (int w = 0; w < 8; ++w) end += sm.dot[w];
-                end = us + sm.eg[kC - 1] * end;
-                float s2 = d[0] + d[1];
-                if (lane == 31) s2 += end, d[1] += end;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float up = __shfl_down_sync(0xffffffffu, s2, o);
-                    if (lane + o < 32) s2 += up;
-                }
-                const int64_t at = (b * L + t0 + 2 * lane) * H + h;
-                if (2 * lane < nt) dg[at] = __float2bfloat16_rn(s2), dbeta[at] = __float2bfloat16_rn(sm.db[2 * lane]);
-                if (2 * lane + 1 < nt) dg[at + H] = __float2bfloat16_rn(s2 - d[0]), dbeta[at + H] = __float2bfloat16_rn(sm.db[2 * lane + 1]);
-            }
-        }
-        __syncthreads();  // the slab and the head's sums are free
-    }
-#pragma unroll
-    for (int j = 0; j < HT; ++j)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int t = 16 * rb + gr + 8 * r, n = 8 * (nh * HT + j) + 2 * tg;
-            if (t < nt && n < N) {
-                if (slices == 1) {
-                    const int64_t at = ((b * L + t0 + t) * G + grp) * (int64_t)N + n;
-                    *reinterpret_cast<uint32_t *>(dCm + at) = pack(dq[j][2 * r], dq[j][2 * r + 1]);
-                    *reinterpret_cast<uint32_t *>(dBm + at) = pack(dk[j][2 * r], dk[j][2 * r + 1]);
-                } else {
-                    const int64_t at = ((b * L + t0 + t) * gridDim.y + blockIdx.y) * (int64_t)N + n;
-                    *reinterpret_cast<float2 *>(dC_part + at) = make_float2(dq[j][2 * r], dq[j][2 * r + 1]);
-                    *reinterpret_cast<float2 *>(dB_part + at) = make_float2(dk[j][2 * r], dk[j][2 * r + 1]);
-                }
-            }
-        }
-}
-
 template <int NT, bool BWD>
 cudaError_t prep_launch(const DeltaProblem &p, char *ws, int *clear, int nclear, cudaStream_t s) {
     using bf = __nv_bfloat16;
@@ -819,19 +467,6 @@ cudaError_t fwd_launch(const DeltaProblem &p, char *ws, cudaStream_t s) {
                             s);
 }
 
-// Slices of a group's heads in k_delta_grads_mma: the number that makes (waves of CTAs on 148 SMs) x (heads
-// a CTA walks) smallest, the fewest of them on a tie (more than one costs fp32 parts and a second pass).
-int grads_slices(const DeltaProblem &p) {
-    const int64_t units = (p.L + kC - 1) / kC * p.G * p.B, per = p.H / p.G;
-    int best = 1;
-    int64_t cost = (units + 147) / 148 * per;
-    for (int s = 2; s <= per && s <= 16; ++s) {
-        const int64_t here = (units * s + 147) / 148 * ((per + s - 1) / s);
-        if (here * 8 < cost * 7) cost = here, best = s;
-    }
-    return best;
-}
-
 // Workspace of the backward pass, as byte offsets.
 struct BwdLayout {
     size_t hand, prep, states, cots, err, u, z, dB, dC, total;
@@ -839,7 +474,7 @@ struct BwdLayout {
 BwdLayout bwd_layout(const DeltaProblem &p) {
     const size_t chunks = (size_t)(p.B * p.H) * (size_t)((p.L + kC - 1) / kC);
     const size_t rows = (size_t)(p.B * p.L * p.H * p.P) * 2;
-    const int slices = grads_slices(p);
+    const int slices = delta_grads_slices(p);
     const size_t part = slices > 1 ? (size_t)(p.B * p.L * p.G * slices * p.N) * 4 : 0;
     BwdLayout l{};
     size_t at = head_bytes(p, true);
@@ -872,22 +507,12 @@ cudaError_t bwd_launch(const DeltaProblem &p, const DeltaGrads &gr, char *ws, cu
     using Lay = Prep<true>;
     int *status = reinterpret_cast<int *>(ws);
     cudaError_t e = prep_launch<NT, true>(p, ws + l.prep, status, (int)(head_bytes(p, true) / sizeof(int)), s);
-    if (!e)
-        e = delta_tc_bwd(p, gr, DeltaChain{prep, Lay::bytes, Lay::scal, Lay::Wr, status, status + kWsAlign / sizeof(int),
-                                           reinterpret_cast<float *>(ws + l.hand), states, err, u, cots, z},
-                         s);
-    if (e) return e;
-    constexpr int gsmem = sizeof(GradsSmem<NT>);
-    if ((e = cudaFuncSetAttribute(k_delta_grads_mma<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, gsmem))) return e;
-    const bf *dy = static_cast<const bf *>(gr.dy), *Bm = static_cast<const bf *>(p.Bm), *Cm = static_cast<const bf *>(p.Cm);
-    const bf *dx = static_cast<const bf *>(gr.dx);
-    const int slices = grads_slices(p);
-    dim3 ggrid((unsigned)((p.L + kC - 1) / kC), (unsigned)(p.G * slices), (unsigned)p.B);
-    k_delta_grads_mma<NT><<<ggrid, kGThr, gsmem, s>>>(dy, Bm, Cm, prep, states, cots, err, u, z, dx, p.L, (int)p.H, (int)p.P,
-                                                      (int)p.G, (int)p.N, slices, static_cast<bf *>(gr.dBm),
-                                                      static_cast<bf *>(gr.dCm), dB, dC, static_cast<bf *>(gr.dg),
-                                                      static_cast<bf *>(gr.dbeta));
-    if ((e = cudaGetLastError()) || slices == 1) return e;
+    const DeltaChain ch{prep, Lay::bytes, Lay::scal, Lay::Wr, status, status + kWsAlign / sizeof(int),
+                        reinterpret_cast<float *>(ws + l.hand), states, err, u, cots, z};
+    if (!e) e = delta_tc_bwd(p, gr, ch, s);
+    if (!e) e = delta_grads(p, gr, ch, dB, dC, s);
+    const int slices = delta_grads_slices(p);
+    if (e || slices == 1) return e;
     DeltaProblem q = p;  // "heads" of the sum: the slices
     q.H = p.G * slices;
     return delta_group_sum_launch(q, dB, dC, gr.dBm, gr.dCm, s);
@@ -915,7 +540,7 @@ cudaError_t delta_mma_fwd(const DeltaProblem &p, void *ws, cudaStream_t s) {
 }
 
 size_t delta_mma_bwd_workspace_bytes(const DeltaProblem &p) { return bwd_layout(p).total; }
-int delta_mma_bwd_kernels(const DeltaProblem &p) { return grads_slices(p) > 1 ? 4 : 3; }
+int delta_mma_bwd_kernels(const DeltaProblem &p) { return delta_grads_slices(p) > 1 ? 4 : 3; }
 
 cudaError_t delta_mma_bwd(const DeltaProblem &p, const DeltaGrads &g, void *ws, cudaStream_t s) {
     return p.N <= 64 ? bwd_launch<64>(p, g, static_cast<char *>(ws), s) : bwd_launch<128>(p, g, static_cast<char *>(ws), s);

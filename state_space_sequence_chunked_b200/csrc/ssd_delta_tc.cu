@@ -27,19 +27,14 @@
 // kStore is the backward pass's recomputation: no Y, but the state entering each chunk, err and u in bf16.
 //
 // Every wait is bounded (tc_ptx.cuh); one that runs out sets bit 0 of the workspace's status word.
-#include <type_traits>
-
-#include "ssd_delta.cuh"
-#include "tc_ptx.cuh"
+#include "delta_tc.cuh"
 
 namespace ssd {
 namespace {
 
 using namespace tc;
 
-constexpr int kC = kDeltaChunk;
 constexpr int kTWarps = 16, kOWarp = 4 + kTWarps, kThreads = 32 * (kOWarp + 4);
-constexpr int kPanel = kC * 128;   // bytes of 64 rows of 64 bf16
 constexpr int kTriLbo = 128, kTriSbo = 256;  // see tri_rows
 constexpr int kTri = 10 * 512;     // bytes of a 64 x 64 lower triangle of 16 x 16 blocks, bf16
 constexpr int kTmS = 0, kTmHi = 128, kTmLo = 192, kTmR = 256, kTmY = 320, kTmA = 384, kTmAl = 448;
@@ -112,118 +107,6 @@ __device__ __noinline__ bool wait_count(const int *flag, int want, volatile int 
             return false;
         }
         __nanosleep(200);
-    }
-}
-
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
-// The products are issued by one elected thread, but from code that the whole warp runs: descriptors and
-// TMEM addresses then stay in uniform registers. From inside `if (lane == 0)` each product took about 90
-// cycles to issue, most of them moving its operands into uniform registers.
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
-    return r;
-}
-template <bool kAcc>
-__device__ __forceinline__ void mma_el(uint32_t leader, uint32_t d, uint32_t left, uint64_t right, uint32_t id) {
-    if constexpr (kAcc)
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.eq.b32 p, 0, 0;\n\t"
-            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-            "r"(left), "l"(right), "r"(id), "r"(leader)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.ne.b32 p, 0, 0;\n\t"
-            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-            "r"(left), "l"(right), "r"(id), "r"(leader)
-            : "memory");
-}
-__device__ __forceinline__ void commit_el(uint32_t leader, uint64_t *bar) {
-    if (leader) mma_commit(bar);
-    __syncwarp();
-}
-
-// hi + lo parts of a pair of fp32 values (lo: what hi leaves, rounded: 2^-18 of the value at worst)
-__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
-    hi = pack_bf16(x, y);
-    asm("{\n\t.reg .b64 v, h, m;\n\t.reg .f32 a, b;\n\t"
-        "mov.b64 v, {%1, %2};\n\tmov.b64 h, {%3, %4};\n\tmov.b64 m, {%5, %5};\n\t"
-        "fma.rn.f32x2 v, h, m, v;\n\tmov.b64 {a, b}, v;\n\tcvt.rn.bf16x2.f32 %0, b, a;\n\t}"
-        : "=r"(lo)
-        : "f"(x), "f"(y), "f"(bf16_lo(hi)), "f"(bf16_hi(hi)), "f"(-1.f));
-}
-// packed pairs of fp32: a b, and c + a b
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\tmul.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
-        "fma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-__device__ __forceinline__ float2 pair_of(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
-
-// What a chain begins with: barriers (count of arrivals each), TMEM, the abort flag.
-struct Setup {
-    uint32_t tmem;
-    volatile int *abort_flag;
-};
-template <int M>
-__device__ __forceinline__ Setup set_up(uint64_t *bar, const int (&counts)[M], int wait_us, int warp) {
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + M);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(bar + M + 1);
-    if (threadIdx.x == 0) {
-#pragma unroll
-        for (int i = 0; i < M; ++i) mbar_init(bar + i, counts[i]);
-        abort_flag[0] = 0;
-        abort_flag[1] = wait_us;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    return Setup{*tmem_slot, abort_flag};
-}
-// And ends with: every issued product has completed (fin) before TMEM is released.
-__device__ __forceinline__ void tear_down(uint32_t tmem, uint64_t *fin, int warp, int lane) {
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 1) {
-        if (lane == 0) {
-            const unsigned long long t0 = now_ns();
-            while (!mbar_try(fin, 0) && now_ns() - t0 < kWaitNs) {
-            }
-        }
-        __syncwarp();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
-    }
-}
-// Loads in flight land before the CTA exits: the last two uses of the stages' barriers.
-__device__ __forceinline__ void drain_loads(uint64_t *full, int it) {
-    for (int i = 1; i <= 2; ++i) {
-        if (it - i < 0) continue;
-        const unsigned long long w0 = now_ns();
-        while (!mbar_try(&full[(it - i) & 1], (uint32_t)((it - i) >> 1) & 1u) && now_ns() - w0 < kWaitNs) {
-        }
     }
 }
 
@@ -753,14 +636,6 @@ __device__ __forceinline__ uint64_t tri_rows(uint32_t tile, int a) {
     return (uint64_t)(((tile + 512 * (a * (a + 1) / 2)) >> 4) & 0x3FFFu) | (uint64_t)(kTriLbo >> 4) << 16 |
            (uint64_t)(kTriSbo >> 4) << 32 | (uint64_t)1 << 46;
 }
-__device__ __forceinline__ void mma_ss_el(uint32_t leader, uint32_t d, uint64_t left, uint64_t right, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(left), "l"(right), "r"(id), "r"(leader), "r"(acc)
-        : "memory");
-}
-
 template <int NT, bool PAIR>
 __device__ __forceinline__ void chain_rev(const CUtensorMap &tm_k, const CUtensorMap &tm_q, const CUtensorMap &tm_dy,
                                           const CUtensorMap &tm_z, const CUtensorMap &tm_dx, const CUtensorMap &tm_d,
