@@ -33,13 +33,14 @@ namespace {
 using namespace tc;
 
 constexpr int kCWarps = 16, kThreads = 32 * (4 + kCWarps);
+constexpr float kLog2e = 1.44269504f;
 constexpr int kTmG = 0, kTmP = 128, kTmS = 192, kTmD = 256, kTmConst = 320;
 
 struct HeadSums {
     float rows[4][128];  // by column quarter: dQ-side and dK-side tokens
     float cols[4][kC];   // by lane quarter
     float U[4][kC];
-    float dot[kCWarps], db[kC];
+    float dot[kCWarps / 2], db[kC];
 };
 
 template <int NT>
@@ -72,26 +73,28 @@ struct Maps {
     CUtensorMap k, q, dy, r, u, s, d;
 };
 
-__device__ __forceinline__ uint32_t scale_pair(float f, uint32_t v) { return pack_bf16(f * bf16_lo(v), f * bf16_hi(v)); }
+__device__ __forceinline__ uint32_t scale_pair(float f, uint32_t v) {
+    const float2 m = mul2(make_float2(f, f), make_float2(bf16_lo(v), bf16_hi(v)));
+    return pack_bf16(m.x, m.y);
+}
 __device__ __forceinline__ uint4 scale8(float f, uint4 v) {
     return make_uint4(scale_pair(f, v.x), scale_pair(f, v.y), scale_pair(f, v.z), scale_pair(f, v.w));
 }
-__device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
+// s + the products of two rows of eight, lanes of s apart
+__device__ __forceinline__ float2 dot8(uint4 a, uint4 b, float2 s) {
     const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s = fmaf(bf16_lo(x[i]), bf16_lo(y[i]), fmaf(bf16_hi(x[i]), bf16_hi(y[i]), s));
+    for (int i = 0; i < 4; ++i)
+        s = fma2(make_float2(bf16_lo(x[i]), bf16_hi(x[i])), make_float2(bf16_lo(y[i]), bf16_hi(y[i])), s);
     return s;
 }
-// sum of v over p of a TMEM row piece (16 columns) and the same columns of a bf16 row
+// a TMEM row piece (16 columns) by the same columns of a bf16 row
 __device__ __forceinline__ float dot16(const uint32_t (&v)[16], uint4 a, uint4 b) {
     const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    float s = 0.f, t = 0.f;
+    float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        s = fmaf(__uint_as_float(v[2 * i]), bf16_lo(x[i]), s);
-        t = fmaf(__uint_as_float(v[2 * i + 1]), bf16_hi(x[i]), t);
-    }
-    return s + t;
+    for (int i = 0; i < 8; ++i) s = fma2(pair_of(v[2 * i], v[2 * i + 1]), make_float2(bf16_lo(x[i]), bf16_hi(x[i])), s);
+    return s.x + s.y;
 }
 
 template <int NT>
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const __grid_consta
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + Z::bar);
     uint64_t *full = bar, *sfree = bar + 2;      // [2] a stage's loads landed; its readers done
     uint64_t *rdyC = bar + 4, *rdyD = bar + 5;   // Q K^T and K K^T; a step's products to be read
-    uint64_t *done = bar + 6;                    // a step's products into dQ, dK
+    uint64_t *done = bar + 6, *xdone = bar + 15; // a step's products into dQ, dK; those with the scaled rows
     uint64_t *dfree = bar + 7;                   // the products read
     uint64_t *xb = bar + 8, *pb = bar + 9;       // left operands written: scaled rows; dP, dM
     uint64_t *hd = bar + 10, *hfree = bar + 12;  // [2] a head's sums written; read
@@ -118,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const __grid_consta
     const int nslab = (a.P + 63) / 64, steps = (h_end - h_begin) * nslab;
     for (int i = threadIdx.x; i < kPanel / 16; i += kThreads) reinterpret_cast<uint4 *>(sm + Z::zero)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async();
-    constexpr int counts[15] = {1, 1, 1 + kCWarps, 1 + kCWarps, 1, 1, 1, kCWarps, kCWarps, kCWarps, kCWarps, kCWarps, 1, 1, 1};
+    constexpr int counts[16] = {1, 1, 1 + kCWarps, 1 + kCWarps, 1, 1, 1, kCWarps, kCWarps, kCWarps, kCWarps, kCWarps, 1, 1, 1, 1};
     const Setup su = set_up(bar, counts, a.wait_us, warp);
     const uint32_t tmem = su.tmem;
     volatile int *abort_flag = su.abort_flag;
@@ -131,8 +134,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const __grid_consta
         if (lane == 0) {
             const uint64_t once = policy_evict_first();
             int it = 0;
-            for (; it < steps; ++it) {
-                const int k = it & 1, h = h_begin + it / nslab, p = it % nslab * 64;
+            for (int h = h_begin, p = 0; it < steps; ++it, p += 64) {
+                if (p >= a.P) p = 0, ++h;
+                const int k = it & 1;
                 if (it >= 2 && !wait_phase(&sfree[k], (uint32_t)((it - 2) >> 1) & 1u, abort_flag, status)) break;
                 unsigned char *st = stage_of(k);
                 mbar_arrive_tx(&full[k], Z::tx + 5 * kC * 4 + (it == 0 ? Z::pn * 2 * kPanel : 0));
@@ -164,8 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const __grid_consta
         const uint64_t qn = sdesc(base + Z::qk, 2 * kPanel, 1024), kn = sdesc(base + Z::qk + kPanel, 2 * kPanel, 1024);
         const uint64_t x1 = sdesc(base + Z::x1, 16, 1024), x2 = sdesc(base + Z::zero, 16, 1024), dp = sdesc(base + Z::dp, 16, 1024);
         const uint64_t dpt = sdesc(base + Z::zero, Z::dp - Z::zero, 1024), dmt = sdesc(base + Z::zero, Z::dp + kPanel - Z::zero, 1024);
-        for (int it = 0; it < steps; ++it) {
-            const int k = it & 1, slab = it % nslab;
+        for (int it = 0, slab = -1; it < steps; ++it) {
+            if (++slab == nslab) slab = 0;
+            const int k = it & 1;
             const uint32_t par = (uint32_t)it & 1u, st = base + Z::stages + k * Z::stage;
             if (!wait_warp(&full[k], (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
             if (it == 0) {
@@ -199,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const __grid_consta
                 mma_ss_el(el, tm + kTmG, x1 + 2 * kk, sn + 128 * kk, idn, it > 0 || kk > 0);
                 mma_ss_el(el, tm + kTmG, x2 + 2 * kk, dn + 128 * kk, idn, 1);
             }
+            commit_el(el, xdone);
             if (!wait_warp(pb, par, abort_flag, status)) break;
             if (slab == nslab - 1) {
                 tc_fence_after();
@@ -218,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const __grid_consta
         for (int turn = 0; turn < h_end - h_begin; ++turn) {
             if (!wait_warp(&hd[turn & 1], (uint32_t)(turn >> 1) & 1u, abort_flag, status)) break;
             const HeadSums &s = *sums_of(turn);
-            float d[2], us = 0.f, end = lane < kCWarps ? s.dot[lane] : 0.f;
+            float d[2], us = 0.f, end = lane < kCWarps / 2 ? s.dot[lane] : 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 2 * lane + e;
@@ -257,23 +263,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const __grid_consta
         const int row = 32 * qtr + lane, i = row & 63;  // lane of TMEM; its token
         const bool upper = row >= 64;                   // (warp-uniform) the rows of dK
         const int ct = (warp - 4) * 32 + lane, lt = ct >> 3, lc = ct & 7;  // and by 16-byte vector: token, vector
-        float rowsum = 0.f, usum = 0.f, dots = 0.f, db = 0.f;
-        const auto vec = [&](const __nv_bfloat16 *src, int it) {
-            const int h = h_begin + it / nslab, p = it % nslab * 64 + 8 * lc;
-            return lt < nt && p < a.P && it < steps
-                       ? __ldg(reinterpret_cast<const uint4 *>(src + (((int64_t)b * a.L + t0 + lt) * a.H + h) * a.P + p))
-                       : make_uint4(0, 0, 0, 0);
+        float rowsum = 0.f, usum = 0.f;
+        float2 dots = make_float2(0.f, 0.f), db = dots;
+        // z and err of a step, one vector per thread; the next step's are asked for while this one's are used
+        const int64_t zat = (((int64_t)b * a.L + t0 + lt) * a.H + h_begin) * a.P + 8 * lc;
+        const __nv_bfloat16 *zp = a.z + zat, *ep = a.err + zat;
+        const auto vec = [&](const __nv_bfloat16 *src, int p) {
+            return lt < nt && p + 8 * lc < a.P ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
         };
-        uint4 zv = vec(a.z, 0), ev = vec(a.err, 0);
+        uint4 zv = vec(zp, 0), ev = vec(ep, 0);
         bool ok = true;
-        for (int it = 0; it < steps; ++it) {
-            const int k = it & 1, turn = it / nslab, slab = it % nslab;
+        for (int it = 0, turn = 0, slab = -1; it < steps; ++it) {
+            const int k = it & 1;
+            if (++slab == nslab) slab = 0, ++turn;
             const uint32_t par = (uint32_t)it & 1u;
             ok = false;
             if (!wait_warp(&full[k], (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
             const unsigned char *st = stage_of(k);
             const float *eg = scal_of(k), *ek = eg + kC, *ch = eg + 3 * kC, *cl = eg + 4 * kC;
-            if (it > 0 && !wait_warp(done, par ^ 1u, abort_flag, status)) break;  // the left operands are free
+            if (it > 0 && !wait_warp(xdone, par ^ 1u, abort_flag, status)) break;  // the last step's were read
             {
                 const uint32_t at = swz(lt, lc);
                 const float g = eg[lt], kf = ek[lt];
@@ -285,8 +293,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const __grid_consta
                 if (lane == 0) mbar_arrive(xb);
             }
             if (it == 0 && !wait_warp(rdyC, 0, abort_flag, status)) break;
+            if (it > 0 && !wait_warp(done, par ^ 1u, abort_flag, status)) break;  // dP and dM were read
             if (slab == 0) {
-                rowsum = usum = dots = db = 0.f;
+                rowsum = usum = 0.f;
+                dots = db = make_float2(0.f, 0.f);
                 // the sums of the head before last have been read
                 if (turn >= 2 && !wait_warp(&hfree[turn & 1], (uint32_t)((turn - 2) >> 1) & 1u, abort_flag, status)) break;
             }
@@ -299,7 +309,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const __grid_consta
                 tmem_ld16(lo_ + kTmConst + 16 * sub, w);
                 tmem_wait_ld(v);
                 tmem_wait_ld(w);
-                const float ih = ch[i], il = cl[i];
+                const float ih = ch[i], il = cl[i], sign = upper ? -1.f : 1.f;
+                const int last = upper ? i - 1 : i;
+                const float2 minus = make_float2(-1.f, -1.f);
                 float pr[16];
                 uint32_t o[8];
                 if (16 * sub > (i | 31)) {  // (warp-uniform) above the diagonal
@@ -312,15 +324,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const __grid_consta
                     for (int j = 0; j < 16; j += 4) {
                         const int jj = 16 * sub + j;
                         const float4 h4 = *reinterpret_cast<const float4 *>(ch + jj), l4 = *reinterpret_cast<const float4 *>(cl + jj);
-                        const float hj[4] = {h4.x, h4.y, h4.z, h4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
+                        const float2 hj[2] = {make_float2(h4.x, h4.y), make_float2(h4.z, h4.w)};
+                        const float2 lj[2] = {make_float2(l4.x, l4.y), make_float2(l4.z, l4.w)};
                         float x[4];
 #pragma unroll
-                        for (int n = 0; n < 4; ++n) {
-                            const bool in = upper ? jj + n < i : jj + n <= i;
-                            const float ex = ex2(1.44269504f * ((ih - hj[n]) + (il - lj[n])));
-                            x[n] = in ? (upper ? -ex : ex) * __uint_as_float(v[j + n]) : 0.f;
-                            pr[j + n] = x[n] * __uint_as_float(w[j + n]);
-                            rowsum += pr[j + n];
+                        for (int n = 0; n < 4; n += 2) {
+                            // log2(e) ((h_i - h_j) + (l_i - l_j)): the difference of the large parts first
+                            float2 d = fma2(hj[n / 2], minus, make_float2(ih, ih));
+                            d = mul2(make_float2(kLog2e, kLog2e), fma2(make_float2(1.f, 1.f), d, fma2(lj[n / 2], minus, make_float2(il, il))));
+                            const float2 ex = mul2(make_float2(sign, sign), make_float2(ex2(d.x), ex2(d.y)));
+                            const float2 m = mul2(ex, pair_of(v[j + n], v[j + n + 1]));
+                            x[n] = jj + n <= last ? m.x : 0.f, x[n + 1] = jj + n + 1 <= last ? m.y : 0.f;
+                            const float2 pq = mul2(make_float2(x[n], x[n + 1]), pair_of(w[j + n], w[j + n + 1]));
+                            pr[j + n] = pq.x, pr[j + n + 1] = pq.y;
+                            rowsum += pq.x + pq.y;
                         }
                         o[j / 2] = pack_bf16(x[0], x[1]), o[j / 2 + 1] = pack_bf16(x[2], x[3]);
                     }
@@ -367,20 +384,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const __grid_consta
                 }
             }
             // <D, S> and dbeta
+            if ((qtr & 1) == 0)  // half of these warps' pairs lie above the diagonal
 #pragma unroll
-            for (int v = 0; v < Z::pn; ++v)
-                dots = dot8(reinterpret_cast<const uint4 *>(st + Z::s)[ct + 512 * v], reinterpret_cast<const uint4 *>(st + Z::d)[ct + 512 * v], dots);
+                for (int v = 0; v < 2 * Z::pn; ++v) {
+                    const int at = (sub * 2 + (qtr >> 1)) * 32 + lane + 256 * v;
+                    dots = dot8(reinterpret_cast<const uint4 *>(st + Z::s)[at], reinterpret_cast<const uint4 *>(st + Z::d)[at], dots);
+                }
             db = dot8(zv, ev, db);
-            zv = vec(a.z, it + 1), ev = vec(a.err, it + 1);
+            if (it + 1 < steps) {
+                // the next slab of the head, or the next head (rows of P, heads side by side)
+                const bool more = slab + 1 < nslab;
+                const int step = more ? 64 : a.P - 64 * slab;
+                zp += step, ep += step;
+                zv = vec(zp, more ? 64 * (slab + 1) : 0), ev = vec(ep, more ? 64 * (slab + 1) : 0);
+            }
             if (slab == nslab - 1) {
                 s.rows[sub][row] = rowsum;
                 if (upper) s.U[sub][i] = usum;
+                float ds = dots.x + dots.y, zs = db.x + db.y;
+                if ((qtr & 1) == 0) {
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) dots += __shfl_xor_sync(0xffffffffu, dots, o);
-                if (lane == 0) s.dot[warp - 4] = eg[kC - 1] * dots;
+                    for (int o = 16; o > 0; o >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, o);
+                    if (lane == 0) s.dot[sub * 2 + (qtr >> 1)] = eg[kC - 1] * ds;
+                }
 #pragma unroll
-                for (int o = 1; o < 8; o <<= 1) db += __shfl_xor_sync(0xffffffffu, db, o);
-                if (lc == 0) s.db[lt] = db;
+                for (int o = 1; o < 8; o <<= 1) zs += __shfl_xor_sync(0xffffffffu, zs, o);
+                if (lc == 0) s.db[lt] = zs;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&hd[turn & 1]);
             }
