@@ -400,7 +400,7 @@ ssd_plan_t delta_plan_of(const ssd::DeltaProblem &p, bool backward) {
     ssd_plan_t out{};
     if (p.B == 0 || p.L == 0) {
         out.path = SSD_PATH_NONE;
-    } else if (delta_mma_supported(p)) {
+    } else if (delta_mma_supported(p, backward)) {
         out.path = SSD_PATH_TCGEN05;
         out.kernels = backward ? delta_mma_bwd_kernels(p) : 2;
         out.workspace_bytes = backward ? delta_mma_bwd_workspace_bytes(p) : delta_mma_fwd_workspace_bytes(p);
@@ -443,8 +443,10 @@ SSD_API ssd_status_t ssd_delta_status(const ssd_shape_t *shape, ssd_dtype_t dtyp
     if (st != SSD_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(s) != cudaSuccess) return SSD_ERR_CUDA;
-    if (delta_plan_of(p, false).path != SSD_PATH_TCGEN05) return SSD_OK;  // the other paths have no waits
-    if (!workspace) return SSD_ERR_INVALID_ARG;
+    // Only the tensor-core path has waits. Every forward call that takes it has a workspace, and so has every
+    // such backward call, for more shapes.
+    if (!workspace) return delta_plan_of(p, false).path == SSD_PATH_TCGEN05 ? SSD_ERR_INVALID_ARG : SSD_OK;
+    if (delta_plan_of(p, true).path != SSD_PATH_TCGEN05) return SSD_OK;
     int32_t word = 0;
     if (cudaMemcpy(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return SSD_ERR_CUDA;
     if (word & 1) return SSD_ERR_TIMEOUT;

@@ -4,10 +4,11 @@
 // The rows p of the state are independent given k and q: a row is h_t[p, :] = a_t h[p, :] + u_t[p] k_t,
 // so a warp keeps whole rows in registers and nothing crosses warps.
 //
-//   k_delta_seq       token by token, a lane holding dstate / 32 columns of 2 rows. Both dot products of
-//                     a token are of the state before it: y_t = a (h q) + u (k.q), so that the chain
-//                     per token is one reduction and one update. For the backward pass it also
-//                     leaves err and the state entering each segment of kSeg tokens.
+//   k_delta_seq       four tokens at a time, a row in 8 lanes. All dot products of the four, h k_i and h q_i,
+//                     are of the state before them; what tokens j < i of the four add is a
+//                     combination of the products k_j.k_i and k_j.q_i, which the staging warps
+//                     form beside: one reduction and one update of the state per four tokens. For the
+//                     backward pass it also leaves err and the state entering each segment of kSeg.
 //   k_delta_seq_bwd   the same walk in reverse: with D the cotangent of h_t,
 //                     D += dy_t q_t^T, z_t = D k_t, dx_t = beta_t z_t, D <- a_t (D - dx_t k_t^T).
 //                     It needs no state; it leaves z and the cotangent leaving each segment.
@@ -23,8 +24,8 @@ namespace ssd {
 namespace {
 
 constexpr int kThr = 256, kWarps = kThr / 32;
-constexpr int kRows = 2;  // state rows per warp of the sequential kernels
-constexpr int kTb = 16;   // tokens staged at a time
+constexpr int kR = 1, kSeqRows = 16;  // state rows per lane and per CTA of the sequential kernels
+constexpr int kSeqWalk = kSeqRows / kR * 8, kSeqThr = kSeqWalk + 128;  // threads that walk, and with those that stage
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -32,187 +33,337 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Stages kTb tokens from t0 (zeros past L): keys, queries as fp32 rows of NJ * 32 columns.
+// Tokens of the sequential kernels in shared memory, as fp32, a block of 4 at a time with the products of its
+// keys and queries. Past L: zeros, a = 1, beta = 0 (such a token leaves the state as it is).
+template <int NJ>
+struct SeqStage {
+    static constexpr int tb = NJ < 8 ? 16 : 8, cols = 32 * NJ;
+    float4 k[tb * cols / 4], q[tb * cols / 4];
+    float x[kSeqRows][tb];      // of the rows: x, or dy
+    float a[tb], beta[tb];
+    float qk[tb / 4][4][4];     // q_i.k_j, j <= i
+    float kk[tb / 4][8];        // k_i.k_j, j < i: (1,0) (2,0) (2,1) (3,0) (3,1) (3,2)
+};
+
+// Four warps stage tokens: those after the next ones are on their way in registers while the next ones are written.
+// `rows` is x or dy.
 template <typename T, int NJ>
-__device__ __forceinline__ void stage_rows(const T *__restrict__ src, int64_t L, int64_t t0, int G, int N, int b, int grp,
-                                           float *dst) {
-    for (int i = threadIdx.x; i < kTb * NJ * 32; i += kThr) {
-        const int t = i / (NJ * 32), n = i % (NJ * 32);
-        const int64_t tt = t0 + t;
-        dst[i] = n < N && tt < L ? to_f32(src[(((int64_t)b * L + tt) * G + grp) * N + n]) : 0.f;
+struct SeqLoad {
+    using S = SeqStage<NJ>;
+    static constexpr int kM = S::tb * S::cols / 128, kX = S::tb * kSeqRows / 128;
+    T k[kM], q[kM], x[kX], gv, bv;
+    __device__ __forceinline__ void fetch(const T *__restrict__ rows, const T *__restrict__ g, const T *__restrict__ beta,
+                                          const T *__restrict__ Bm, const T *__restrict__ Cm, int64_t L, int64_t t0, int H, int P,
+                                          int G, int N, int b, int h, int pc, int tid) {
+        const T zero = T(0.f);
+        const int64_t base = (((int64_t)b * L + t0) * G + h / (H / G)) * N;
+        const int left = L - t0 < S::tb ? (int)(L - t0) : S::tb;
+#pragma unroll
+        for (int m = 0; m < kM; ++m) {
+            const int i = tid + 128 * m, t = i / S::cols, n = i % S::cols;
+            const bool in = n < N && t < left;
+            const int64_t at = in ? base + (int64_t)t * G * N + n : 0;
+            k[m] = in ? Bm[at] : zero;
+            q[m] = in && Cm ? Cm[at] : zero;
+        }
+#pragma unroll
+        for (int m = 0; m < kX; ++m) {
+            const int i = tid + 128 * m, t = i / kSeqRows, r = i % kSeqRows;
+            x[m] = t < left && pc + r < P ? rows[(((int64_t)b * L + t0 + t) * H + h) * P + pc + r] : zero;
+        }
+        const int64_t at = ((int64_t)b * L + t0 + tid) * H + h;
+        gv = tid < left ? g[at] : zero;
+        bv = tid < left ? beta[at] : zero;
+    }
+    __device__ __forceinline__ void put(S &st, int tid) const {
+#pragma unroll
+        for (int m = 0; m < kM; ++m) {
+            reinterpret_cast<float *>(st.k)[tid + 128 * m] = to_f32(k[m]);
+            reinterpret_cast<float *>(st.q)[tid + 128 * m] = to_f32(q[m]);
+        }
+#pragma unroll
+        for (int m = 0; m < kX; ++m) st.x[(tid + 128 * m) % kSeqRows][(tid + 128 * m) / kSeqRows] = to_f32(x[m]);
+        if (tid < S::tb) st.a[tid] = expf(to_f32(gv)), st.beta[tid] = to_f32(bv);
+    }
+};
+// What of a block's tokens meets: all by the staging warps, after their writes.
+template <int NJ>
+__device__ __forceinline__ void seq_pairs(SeqStage<NJ> &st, int tid) {
+    using S = SeqStage<NJ>;
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    // 10 + 6 products of a block, 8 lanes each
+    const int item = tid >> 3, l8 = tid & 7, m = item < 10 ? item : item - 10;
+    const int r = (m >= 1) + (m >= 3) + (m >= 6), j = m - r * (r + 1) / 2, i = item < 10 ? r : r + 1;
+    const float4 *left = item < 10 ? st.q : st.k;
+#pragma unroll
+    for (int blk = 0; blk < S::tb / 4; ++blk) {
+        float d = 0.f;
+#pragma unroll
+        for (int v = 0; v < NJ; ++v) {
+            const float4 f = left[(4 * blk + i) * (S::cols / 4) + 8 * v + l8], w = st.k[(4 * blk + j) * (S::cols / 4) + 8 * v + l8];
+            d = fmaf(f.x, w.x, fmaf(f.y, w.y, fmaf(f.z, w.z, fmaf(f.w, w.w, d))));
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        if (l8 == 0) (item < 10 ? st.qk[blk][i][j] : st.kk[blk][m]) = d;
     }
 }
 
-// grid (ceil(P / 16), H, B).
-template <typename T, int NJ>
-__global__ void __launch_bounds__(kThr)
+// Staging and walking warps meet here once per stage, each from its own loop.
+__device__ __forceinline__ void seq_sync() { asm volatile("bar.sync 2, %0;" ::"n"(kSeqThr) : "memory"); }
+
+// A row of the state, 4 NJ columns per lane: columns 32 v + 4 l8 ..
+template <int NJ>
+__device__ __forceinline__ void row_load(float2 (&s)[NJ][2], const float *src, bool live, int l8, int N) {
+#pragma unroll
+    for (int v = 0; v < NJ; ++v) {
+        const int n = 32 * v + 4 * l8;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            s[v][e] = make_float2(live && n + 2 * e < N ? src[n + 2 * e] : 0.f, live && n + 2 * e + 1 < N ? src[n + 2 * e + 1] : 0.f);
+    }
+}
+template <int NJ>
+__device__ __forceinline__ void row_store(const float2 (&s)[NJ][2], float *dst, int l8, int N) {
+#pragma unroll
+    for (int v = 0; v < NJ; ++v) {
+        const int n = 32 * v + 4 * l8;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (n + 2 * e < N) dst[n + 2 * e] = s[v][e].x;
+            if (n + 2 * e + 1 < N) dst[n + 2 * e + 1] = s[v][e].y;
+        }
+    }
+}
+__device__ __forceinline__ float2 low2(float4 v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ float2 high2(float4 v) { return make_float2(v.z, v.w); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+template <int NJ>
+__device__ __forceinline__ float row_dot(const float2 (&s)[NJ][2], const float4 *w, int l8) {
+    float2 d0 = both(0.f), d1 = d0;
+#pragma unroll
+    for (int v = 0; v < NJ; ++v) {
+        const float4 f = w[8 * v + l8];
+        d0 = fma2(s[v][0], low2(f), d0);
+        d1 = fma2(s[v][1], high2(f), d1);
+    }
+    return (d0.x + d1.x) + (d0.y + d1.y);
+}
+template <int NJ>
+__device__ __forceinline__ void row_add(float2 (&s)[NJ][2], float c, const float4 *w, int l8) {
+#pragma unroll
+    for (int v = 0; v < NJ; ++v) {
+        const float4 f = w[8 * v + l8];
+        s[v][0] = fma2(both(c), low2(f), s[v][0]);
+        s[v][1] = fma2(both(c), high2(f), s[v][1]);
+    }
+}
+template <int NJ>
+__device__ __forceinline__ void row_scale(float2 (&s)[NJ][2], float c) {
+#pragma unroll
+    for (int v = 0; v < NJ; ++v) s[v][0] = mul2(both(c), s[v][0]), s[v][1] = mul2(both(c), s[v][1]);
+}
+// Eight values per lane, each to be summed over eight neighbouring lanes: halves are exchanged, so that lane l
+// ends with the sum of value l.
+__device__ __forceinline__ float sums8(float (&v)[8], int lane) {
+    int x = 4;
+#pragma unroll
+    for (int w = 4; w >= 1; w >>= 1, x >>= 1)
+#pragma unroll
+        for (int j = 0; j < w; ++j) {
+            const bool up = lane & x;
+            const float send = up ? v[j] : v[j + w], keep = up ? v[j + w] : v[j];
+            v[j] = keep + __shfl_xor_sync(0xffffffffu, send, x);
+        }
+    return v[0];
+}
+
+// grid (ceil(P / 16), H, B), 2 warps that walk the tokens and 4 that stage the next ones.
+template <typename T, int NJ, bool kY>
+__global__ void __launch_bounds__(kSeqThr, NJ < 8 ? 2 : 1)
     k_delta_seq(const T *__restrict__ x, const T *__restrict__ g, const T *__restrict__ beta, const T *__restrict__ Bm,
                 const T *__restrict__ Cm, const float *__restrict__ h0, int64_t L, int H, int P, int G, int N,
                 T *__restrict__ y, float *__restrict__ h_final, float *__restrict__ seg_states,
                 float *__restrict__ err_out) {
-    __shared__ float ks[kTb * NJ * 32], qs[kTb * NJ * 32], xs[kTb * kWarps * kRows], as[kTb], bs[kTb], kqs[kTb];
-    const int h = blockIdx.y, b = blockIdx.z, grp = h / (H / G);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int pc = blockIdx.x * kWarps * kRows, p0 = pc + warp * kRows;
-    const int64_t row0 = ((int64_t)b * H + h) * P, ns = (L + kSeg - 1) / kSeg;
-    float s[kRows][NJ];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int n = lane + 32 * j;
-            s[r][j] = h0 && p0 + r < P && n < N ? h0[(row0 + p0 + r) * N + n] : 0.f;
+    using S = SeqStage<NJ>;
+    __shared__ S st[2];
+    const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l8 = lane & 7;
+    const int pc = blockIdx.x * kSeqRows, r0 = (warp * 4 + (lane >> 3)) * kR, p0 = pc + r0;
+    
+    const int64_t row = ((int64_t)b * H + h) * P + p0, ns = (L + kSeg - 1) / kSeg;
+    if (tid >= kSeqWalk) {
+        SeqLoad<T, NJ> in;
+        const auto fetch = [&](int64_t t0) { in.fetch(x, g, beta, Bm, Cm, L, t0, H, P, G, N, b, h, pc, tid - kSeqWalk); };
+        fetch(0);
+        for (int64_t t0 = 0; t0 < L; t0 += S::tb) {
+            in.put(st[t0 / S::tb & 1], tid - kSeqWalk);
+            if (t0 + S::tb < L) fetch(t0 + S::tb);
+            seq_pairs<NJ>(st[t0 / S::tb & 1], tid - kSeqWalk);
+            seq_sync();  // these tokens are there, and the others' place is free
         }
-    for (int64_t t0 = 0; t0 < L; t0 += kTb) {
-        __syncthreads();
-        stage_rows<T, NJ>(Bm, L, t0, G, N, b, grp, ks);
-        if (Cm) stage_rows<T, NJ>(Cm, L, t0, G, N, b, grp, qs);
-        for (int i = tid; i < kTb * kWarps * kRows; i += kThr) {
-            const int t = i / (kWarps * kRows), p = pc + i % (kWarps * kRows);
-            xs[i] = t0 + t < L && p < P ? to_f32(x[(((int64_t)b * L + t0 + t) * H + h) * P + p]) : 0.f;
-        }
-        if (tid < kTb && t0 + tid < L) {
-            as[tid] = expf(to_f32(g[((int64_t)b * L + t0 + tid) * H + h]));
-            bs[tid] = to_f32(beta[((int64_t)b * L + t0 + tid) * H + h]);
-        }
-        __syncthreads();
-        if (Cm) {
-            for (int t = warp; t < kTb; t += kWarps) {
-                float d = 0.f;
+        return;
+    }
+    float2 s[kR][NJ][2];
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
-                    d = fmaf(ks[t * NJ * 32 + lane + 32 * j], qs[t * NJ * 32 + lane + 32 * j], d);
-                d = warp_sum(d);
-                if (lane == 0) kqs[t] = d;
-            }
-            __syncthreads();
-        }
-        const int nt = L - t0 < kTb ? (int)(L - t0) : kTb;
-        for (int t = 0; t < nt; ++t) {
-            if (seg_states && (t0 + t) % kSeg == 0) {
-                const int64_t c = (t0 + t) / kSeg;
+    for (int e = 0; e < kR; ++e) row_load<NJ>(s[e], h0 + (row + e) * N, h0 && p0 + e < P, l8, N);
+    for (int64_t t0 = 0; t0 < L; t0 += S::tb) {
+        const S &c = st[t0 / S::tb & 1];
+        seq_sync();
+        for (int blk = 0; blk < S::tb / 4 && t0 + 4 * blk < L; ++blk) {
+            const int64_t t = t0 + 4 * blk;
+            if (seg_states && t % kSeg == 0)
 #pragma unroll
-                for (int r = 0; r < kRows; ++r)
+                for (int e = 0; e < kR; ++e)
+                    if (p0 + e < P) row_store<NJ>(s[e], seg_states + ((((int64_t)b * H + h) * ns + t / kSeg) * P + p0 + e) * N, l8, N);
+            const float4 *k = c.k + blk * S::cols, *q = c.q + blk * S::cols;
+            float own[kR];  // h.k of token l8, or h.q of token l8 - 4
+            {
+                float d[kR][8];
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        const int n = lane + 32 * j;
-                        if (p0 + r < P && n < N)
-                            seg_states[((((int64_t)b * H + h) * ns + c) * P + p0 + r) * N + n] = s[r][j];
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int e = 0; e < kR; ++e) {
+                        d[e][i] = row_dot<NJ>(s[e], k + i * (S::cols / 4), l8);
+                        d[e][4 + i] = kY ? row_dot<NJ>(s[e], q + i * (S::cols / 4), l8) : 0.f;
                     }
+                }
+#pragma unroll
+                for (int e = 0; e < kR; ++e) own[e] = sums8(d[e], lane);
             }
-            const float a = as[t], bt = bs[t];
-            float pk[kRows], pq[kRows];
+            const float4 a4 = *reinterpret_cast<const float4 *>(&c.a[4 * blk]), b4 = *reinterpret_cast<const float4 *>(&c.beta[4 * blk]);
+            const float a[4] = {a4.x, a4.y, a4.z, a4.w}, bt[4] = {b4.x, b4.y, b4.z, b4.w};
+            const float4 m0 = *reinterpret_cast<const float4 *>(&c.kk[blk][0]), m1 = *reinterpret_cast<const float4 *>(&c.kk[blk][4]);
+            const float kk[6] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y};
+            const float4 qr = *reinterpret_cast<const float4 *>(&c.qk[blk][l8 & 3][0]);
+            const float qk[4] = {qr.x, qr.y, qr.z, qr.w};
+            float u[kR][4];
+            const int64_t tt = t + (l8 & 3), at = (((int64_t)b * L + tt) * H + h) * P + p0;
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                pk[r] = pq[r] = 0.f;
+            for (int e = 0; e < kR; ++e) {
+                const float4 x4 = *reinterpret_cast<const float4 *>(&c.x[r0 + e][4 * blk]);
+                const float xv[4] = {x4.x, x4.y, x4.z, x4.w};
+                float err[4], yv = own[e];
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    pk[r] = fmaf(s[r][j], ks[t * NJ * 32 + lane + 32 * j], pk[r]);
-                    if (Cm) pq[r] = fmaf(s[r][j], qs[t * NJ * 32 + lane + 32 * j], pq[r]);
+                for (int i = 0; i < 4; ++i) {  // h' k_i: the block's earlier tokens by their keys' products
+                    float v = __shfl_sync(0xffffffffu, own[e], (lane & 24) + i);
+#pragma unroll
+                    for (int j = 0; j < i; ++j) v = fmaf(u[e][j], kk[i * (i - 1) / 2 + j], a[j] * v);
+                    err[i] = xv[i] - a[i] * v;
+                    u[e][i] = bt[i] * err[i];
+                    const float n = fmaf(u[e][i], qk[i], a[i] * yv);
+                    yv = i <= (l8 & 3) ? n : yv;
+                }
+                if (p0 + e < P && tt < L) {
+                    if (l8 >= 4) {
+                        if (kY) store_as(y + at + e, yv);
+                    } else if (err_out) {
+                        err_out[at + e] = (l8 & 2) ? (l8 & 1 ? err[3] : err[2]) : (l8 & 1 ? err[1] : err[0]);
+                    }
                 }
             }
+            const float c2 = a[3], c1 = c2 * a[2], c0 = c1 * a[1], ci[4] = {c0, c1, c2, 1.f};
+            for (int e = 0; e < kR; ++e) row_scale<NJ>(s[e], c0 * a[0]);
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const float err = xs[t * kWarps * kRows + warp * kRows + r] - a * warp_sum(pk[r]);
-                const float u = bt * err;
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) s[r][j] = fmaf(a, s[r][j], u * ks[t * NJ * 32 + lane + 32 * j]);
-                const int64_t at = (((int64_t)b * L + t0 + t) * H + h) * P + p0 + r;
-                if (Cm) {
-                    const float yv = a * warp_sum(pq[r]) + u * kqs[t];
-                    if (lane == 0 && p0 + r < P) store_as(y + at, yv);
-                }
-                if (err_out && lane == 0 && p0 + r < P) err_out[at] = err;
-            }
+            for (int i = 0; i < 4; ++i) for (int e = 0; e < kR; ++e) row_add<NJ>(s[e], ci[i] * u[e][i], k + i * (S::cols / 4), l8);
         }
     }
-    if (h_final) {
+    if (h_final)
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int n = lane + 32 * j;
-                if (p0 + r < P && n < N) h_final[(row0 + p0 + r) * N + n] = s[r][j];
-            }
-    }
+        for (int e = 0; e < kR; ++e)
+            if (p0 + e < P) row_store<NJ>(s[e], h_final + (row + e) * N, l8, N);
 }
 
-// grid (ceil(P / 16), H, B).
+// grid (ceil(P / 16), H, B), warps as above.
 template <typename T, int NJ>
-__global__ void __launch_bounds__(kThr)
+__global__ void __launch_bounds__(kSeqThr, NJ < 8 ? 2 : 1)
     k_delta_seq_bwd(const T *__restrict__ dy, const float *__restrict__ dh_final, const T *__restrict__ g,
                     const T *__restrict__ beta, const T *__restrict__ Bm, const T *__restrict__ Cm, int64_t L, int H, int P,
                     int G, int N, T *__restrict__ dx, float *__restrict__ z_out, float *__restrict__ seg_cot,
                     float *__restrict__ dh0) {
-    __shared__ float ks[kTb * NJ * 32], qs[kTb * NJ * 32], ys[kTb * kWarps * kRows], as[kTb], bs[kTb];
-    const int h = blockIdx.y, b = blockIdx.z, grp = h / (H / G);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int pc = blockIdx.x * kWarps * kRows, p0 = pc + warp * kRows;
-    const int64_t row0 = ((int64_t)b * H + h) * P, ns = (L + kSeg - 1) / kSeg;
-    float s[kRows][NJ];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int n = lane + 32 * j;
-            s[r][j] = dh_final && p0 + r < P && n < N ? dh_final[(row0 + p0 + r) * N + n] : 0.f;
+    using S = SeqStage<NJ>;
+    __shared__ S st[2];
+    const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l8 = lane & 7;
+    const int pc = blockIdx.x * kSeqRows, r0 = (warp * 4 + (lane >> 3)) * kR, p0 = pc + r0;
+    
+    const int64_t row = ((int64_t)b * H + h) * P + p0, ns = (L + kSeg - 1) / kSeg, first = (L - 1) / S::tb * S::tb;
+    if (tid >= kSeqWalk) {
+        SeqLoad<T, NJ> in;
+        const auto fetch = [&](int64_t t0) { in.fetch(dy, g, beta, Bm, Cm, L, t0, H, P, G, N, b, h, pc, tid - kSeqWalk); };
+        fetch(first);
+        for (int64_t t0 = first; t0 >= 0; t0 -= S::tb) {
+            in.put(st[t0 / S::tb & 1], tid - kSeqWalk);
+            if (t0 > 0) fetch(t0 - S::tb);
+            seq_pairs<NJ>(st[t0 / S::tb & 1], tid - kSeqWalk);
+            seq_sync();
         }
-    for (int64_t t0 = (L - 1) / kTb * kTb; t0 >= 0; t0 -= kTb) {
-        __syncthreads();
-        stage_rows<T, NJ>(Bm, L, t0, G, N, b, grp, ks);
-        stage_rows<T, NJ>(Cm, L, t0, G, N, b, grp, qs);
-        for (int i = tid; i < kTb * kWarps * kRows; i += kThr) {
-            const int t = i / (kWarps * kRows), p = pc + i % (kWarps * kRows);
-            ys[i] = t0 + t < L && p < P ? to_f32(dy[(((int64_t)b * L + t0 + t) * H + h) * P + p]) : 0.f;
-        }
-        if (tid < kTb && t0 + tid < L) {
-            as[tid] = expf(to_f32(g[((int64_t)b * L + t0 + tid) * H + h]));
-            bs[tid] = to_f32(beta[((int64_t)b * L + t0 + tid) * H + h]);
-        }
-        __syncthreads();
-        for (int t = (L - t0 < kTb ? (int)(L - t0) : kTb) - 1; t >= 0; --t) {
-            const int64_t tt = t0 + t;
-            if (tt == L - 1 || (tt + 1) % kSeg == 0) {
-                const int64_t c = tt / kSeg;
+        return;
+    }
+    float2 s[kR][NJ][2];
 #pragma unroll
-                for (int r = 0; r < kRows; ++r)
+    for (int e = 0; e < kR; ++e) row_load<NJ>(s[e], dh_final + (row + e) * N, dh_final && p0 + e < P, l8, N);
+    for (int64_t t0 = first; t0 >= 0; t0 -= S::tb) {
+        const S &c = st[t0 / S::tb & 1];
+        seq_sync();
+        for (int blk = S::tb / 4 - 1; blk >= 0; --blk) {
+            const int64_t t = t0 + 4 * blk;
+            if (t >= L) continue;
+            if (t + 4 >= L || (t + 4) % kSeg == 0)
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        const int n = lane + 32 * j;
-                        if (p0 + r < P && n < N)
-                            seg_cot[((((int64_t)b * H + h) * ns + c) * P + p0 + r) * N + n] = s[r][j];
-                    }
+                for (int e = 0; e < kR; ++e)
+                    if (p0 + e < P) row_store<NJ>(s[e], seg_cot + ((((int64_t)b * H + h) * ns + t / kSeg) * P + p0 + e) * N, l8, N);
+            const float4 *k = c.k + blk * S::cols, *q = c.q + blk * S::cols;
+            float own;  // D k of token l8 & 3, rows l8 >> 2
+            {
+                float d[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    d[i] = row_dot<NJ>(s[0], k + i * (S::cols / 4), l8);
+                    d[4 + i] = kR > 1 ? row_dot<NJ>(s[kR - 1], k + i * (S::cols / 4), l8) : 0.f;
+                }
+                own = sums8(d, lane);
             }
-            const float a = as[t], bt = bs[t];
+            const float4 a4 = *reinterpret_cast<const float4 *>(&c.a[4 * blk]), b4 = *reinterpret_cast<const float4 *>(&c.beta[4 * blk]);
+            const float a[4] = {a4.x, a4.y, a4.z, a4.w}, bt[4] = {b4.x, b4.y, b4.z, b4.w};
+            const float4 m0 = *reinterpret_cast<const float4 *>(&c.kk[blk][0]), m1 = *reinterpret_cast<const float4 *>(&c.kk[blk][4]);
+            const float kk[6] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y};
+            float dv[kR][4], yv[kR][4], zi = 0.f;
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const float d = ys[t * kWarps * kRows + warp * kRows + r];
-                float pk = 0.f;
+            for (int e = 0; e < kR; ++e) {
+                const float4 y4 = *reinterpret_cast<const float4 *>(&c.x[r0 + e][4 * blk]);
+                yv[e][0] = y4.x, yv[e][1] = y4.y, yv[e][2] = y4.z, yv[e][3] = y4.w;
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    s[r][j] = fmaf(d, qs[t * NJ * 32 + lane + 32 * j], s[r][j]);
-                    pk = fmaf(s[r][j], ks[t * NJ * 32 + lane + 32 * j], pk);
+                for (int i = 3; i >= 0; --i) {  // D k_i: the later tokens of the block by their products with k_i
+                    float v = __shfl_sync(0xffffffffu, own, (lane & 24) + 4 * e + i);
+#pragma unroll
+                    for (int j = 3; j > i; --j)
+                        v = a[j] * fmaf(yv[e][j], c.qk[blk][j][i], fmaf(-dv[e][j], kk[j * (j - 1) / 2 + i], v));
+                    const float z = fmaf(yv[e][i], c.qk[blk][i][i], v);
+                    dv[e][i] = bt[i] * z;
+                    if (l8 == 4 * e + i) zi = z;
                 }
-                const float z = warp_sum(pk), dv = bt * z;
+            }
+            const float c1 = a[0] * a[1], c2 = c1 * a[2], c3 = c2 * a[3], ci[4] = {a[0], c1, c2, c3};
+            for (int e = 0; e < kR; ++e) row_scale<NJ>(s[e], c3);
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) s[r][j] = a * fmaf(-dv, ks[t * NJ * 32 + lane + 32 * j], s[r][j]);
-                const int64_t at = (((int64_t)b * L + tt) * H + h) * P + p0 + r;
-                if (lane == 0 && p0 + r < P) {
-                    store_as(dx + at, dv);
-                    z_out[at] = z;
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int e = 0; e < kR; ++e) {
+                    row_add<NJ>(s[e], ci[i] * yv[e][i], q + i * (S::cols / 4), l8);
+                    row_add<NJ>(s[e], -ci[i] * dv[e][i], k + i * (S::cols / 4), l8);
                 }
+            }
+            const int i = l8 & 3, e = l8 >> 2;
+            const int64_t at = (((int64_t)b * L + t + i) * H + h) * P + p0 + e;
+            if (e < kR && p0 + e < P && t + i < L) {
+                z_out[at] = zi;
+                store_as(dx + at, c.beta[4 * blk + i] * zi);
             }
         }
     }
-    if (dh0) {
+    if (dh0)
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int n = lane + 32 * j;
-                if (p0 + r < P && n < N) dh0[(row0 + p0 + r) * N + n] = s[r][j];
-            }
-    }
+        for (int e = 0; e < kR; ++e)
+            if (p0 + e < P) row_store<NJ>(s[e], dh0 + (row + e) * N, l8, N);
 }
 
 // One segment of one head: grid (segments, H, B). With S the entering state, D the leaving cotangent,
@@ -470,11 +621,11 @@ __global__ void __launch_bounds__(kThr)
 
 template <typename T, int NJ>
 cudaError_t seq_launch(const DeltaProblem &p, float *seg_states, float *err, cudaStream_t s) {
-    dim3 grid((unsigned)((p.P + kWarps * kRows - 1) / (kWarps * kRows)), (unsigned)p.H, (unsigned)p.B);
-    k_delta_seq<T, NJ><<<grid, kThr, 0, s>>>(static_cast<const T *>(p.x), static_cast<const T *>(p.g),
-                                             static_cast<const T *>(p.beta), static_cast<const T *>(p.Bm),
-                                             p.y ? static_cast<const T *>(p.Cm) : nullptr, p.h0, p.L, (int)p.H, (int)p.P,
-                                             (int)p.G, (int)p.N, static_cast<T *>(p.y), p.h_final, seg_states, err);
+    dim3 grid((unsigned)((p.P + kSeqRows - 1) / kSeqRows), (unsigned)p.H, (unsigned)p.B);
+    const auto kernel = p.y ? k_delta_seq<T, NJ, true> : k_delta_seq<T, NJ, false>;
+    kernel<<<grid, kSeqThr, 0, s>>>(static_cast<const T *>(p.x), static_cast<const T *>(p.g), static_cast<const T *>(p.beta),
+                                    static_cast<const T *>(p.Bm), p.y ? static_cast<const T *>(p.Cm) : nullptr, p.h0, p.L,
+                                    (int)p.H, (int)p.P, (int)p.G, (int)p.N, static_cast<T *>(p.y), p.h_final, seg_states, err);
     return cudaGetLastError();
 }
 
@@ -488,8 +639,8 @@ cudaError_t seq_typed(const DeltaProblem &p, float *seg_states, float *err, cuda
 
 template <typename T, int NJ>
 cudaError_t seq_bwd_launch(const DeltaProblem &p, const DeltaGrads &gr, float *z, float *seg_cot, cudaStream_t s) {
-    dim3 grid((unsigned)((p.P + kWarps * kRows - 1) / (kWarps * kRows)), (unsigned)p.H, (unsigned)p.B);
-    k_delta_seq_bwd<T, NJ><<<grid, kThr, 0, s>>>(static_cast<const T *>(gr.dy), gr.dh_final, static_cast<const T *>(p.g),
+    dim3 grid((unsigned)((p.P + kSeqRows - 1) / kSeqRows), (unsigned)p.H, (unsigned)p.B);
+    k_delta_seq_bwd<T, NJ><<<grid, kSeqThr, 0, s>>>(static_cast<const T *>(gr.dy), gr.dh_final, static_cast<const T *>(p.g),
                                                  static_cast<const T *>(p.beta), static_cast<const T *>(p.Bm),
                                                  static_cast<const T *>(p.Cm), p.L, (int)p.H, (int)p.P, (int)p.G, (int)p.N,
                                                  static_cast<T *>(gr.dx), z, seg_cot, gr.dh0);

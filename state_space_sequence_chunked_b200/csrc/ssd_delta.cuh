@@ -38,7 +38,7 @@ cudaError_t delta_group_sum_launch(const DeltaProblem &p, const float *dB_part, 
                                    cudaStream_t s);
 // ---- chunked tensor-core path (bf16, dstate <= 128, dstate and headdim multiples of 8) ----
 constexpr int kDeltaChunk = 64;
-bool delta_mma_supported(const DeltaProblem &p);
+bool delta_mma_supported(const DeltaProblem &p, bool backward);
 size_t delta_mma_fwd_workspace_bytes(const DeltaProblem &p);
 cudaError_t delta_mma_fwd(const DeltaProblem &p, void *ws, cudaStream_t s);
 size_t delta_mma_bwd_workspace_bytes(const DeltaProblem &p);
@@ -68,5 +68,22 @@ cudaError_t delta_grads(const DeltaProblem &p, const DeltaGrads &g, const DeltaC
 
 // one token (p.L, p.h0, p.h_final unused); state_out may be state_in
 cudaError_t delta_step(const DeltaProblem &p, const float *state_in, float *state_out, cudaStream_t s);
+
+// packed pairs of fp32: a b, and c + a b
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\tmul.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
 
 }  // namespace ssd

@@ -520,12 +520,14 @@ cudaError_t bwd_launch(const DeltaProblem &p, const DeltaGrads &gr, char *ws, cu
 
 }  // namespace
 
-// From 24 tokens on, or from 10 where there are more than 4 CTAs of the sequential kernel for each SM: its
-// time is that of its token chain, 0.5 us a token where they all run at once (96 CTAs, 24 tokens: 14.5
-// against 18.0 us here, 32 tokens: 17.6 against 18.1; 768 CTAs, 8 tokens: 17.5 against 18.7, 16 tokens: 27.2
-// against 18.7).
-bool delta_mma_supported(const DeltaProblem &p) {
-    if (p.L < (p.B * p.H * ((p.P + 15) / 16) > 4 * 148 ? 10 : 24)) return false;
+// The sequential kernel takes as long as its token chain (0.2 us a token and CTA; n CTAs of 16 rows), this
+// path at least two launches and a chunk of 64: 24 bf16 heads of 64 x 128, one sequence (n = 96), L = 96: 25.7 against
+// 30.7 us here, 192: 43.0 against 33.8; four (n = 384), 24: 22.5 against 28.7, 48: 33.0 against 28.7; eight,
+// 16: 25.9 against 28.6, 24: 36.1 against 28.6; 32 sequences of 80 heads, 2: 143 against 127. The backward pass gains
+// at every length (8 tokens of 24 heads: 80 against 54 us).
+bool delta_mma_supported(const DeltaProblem &p, bool backward) {
+    const int64_t per_sm = (p.B * p.H * ((p.P + 15) / 16) + 147) / 148;
+    if (!backward && p.L < 128 && p.L * per_sm < 128) return false;
     return p.dtype == SSD_BF16 && p.N <= 128 && p.N % 8 == 0 && p.P % 8 == 0 && p.L < (1ll << 31) &&
            p.B * p.H * ((p.L + kC - 1) / kC) < (1ll << 31);
 }
