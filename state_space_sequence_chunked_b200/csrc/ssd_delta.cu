@@ -533,22 +533,35 @@ __global__ void __launch_bounds__(kThr)
     }
 }
 
-// Sums over the heads of each group, in head order. One thread per output element.
-template <typename T>
-__global__ void k_delta_group_sum(const float *__restrict__ dB_part, const float *__restrict__ dC_part, int64_t tokens,
-                                  int H, int G, int N, T *__restrict__ dBm, T *__restrict__ dCm) {
-    const int64_t total = tokens * G * N;
-    const int per = H / G;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int n = (int)(i % N), g = (int)(i / N % G);
-        const int64_t t = i / N / G;
-        float sb = 0.f, sc = 0.f;
-        for (int h = g * per; h < (g + 1) * per; ++h) {
-            sb += dB_part[(t * H + h) * N + n];
-            sc += dC_part[(t * H + h) * N + n];
+// Sums over the `per` heads of each group, in head order; a thread takes V columns of a row (token, group), whose
+// heads' rows stand one after another.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThr)
+    k_delta_group_sum(const float *__restrict__ dB_part, const float *__restrict__ dC_part, int64_t rows, int per, int N,
+                      T *__restrict__ dBm, T *__restrict__ dCm) {
+    const int nv = N / V, at_once = kThr / nv, mine = threadIdx.x / nv, c = threadIdx.x % nv * V;
+    if (mine >= at_once) return;
+    for (int64_t row = (int64_t)blockIdx.x * at_once + mine; row < rows; row += (int64_t)gridDim.x * at_once) {
+        float sb[V], sc[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) sb[e] = sc[e] = 0.f;
+        for (int j = 0; j < per; ++j) {
+            const int64_t at = (row * per + j) * N + c;
+            float fb[V], fc[V];
+            if constexpr (V == 4) {
+                *reinterpret_cast<float4 *>(fb) = *reinterpret_cast<const float4 *>(dB_part + at);
+                *reinterpret_cast<float4 *>(fc) = *reinterpret_cast<const float4 *>(dC_part + at);
+            } else {
+                fb[0] = dB_part[at], fc[0] = dC_part[at];
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) sb[e] += fb[e], sc[e] += fc[e];
         }
-        store_as(dBm + i, sb);
-        store_as(dCm + i, sc);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            store_as(dBm + row * N + c + e, sb[e]);
+            store_as(dCm + row * N + c + e, sc[e]);
+        }
     }
 }
 
@@ -717,15 +730,18 @@ void step_launch(const DeltaProblem &p, const float *in, float *out, cudaStream_
 
 cudaError_t delta_group_sum_launch(const DeltaProblem &p, const float *dB_part, const float *dC_part, void *dBm, void *dCm,
                                    cudaStream_t s) {
-    const int64_t total = p.B * p.L * p.G * p.N, blocks = (total + 255) / 256;
-    const unsigned grid = (unsigned)(blocks < 148 * 16 ? blocks : 148 * 16);
+    const int64_t rows = p.B * p.L * p.G;
+    const int V = p.N % 4 ? 1 : 4, at_once = (int)(kThr / (p.N / V));
+    const int64_t blocks = (rows + at_once - 1) / at_once;
+    const unsigned grid = (unsigned)(blocks < 148 * 8 ? blocks : 148 * 8);
+    const auto go = [&](auto kernel, auto *b, auto *c) {
+        kernel<<<grid, kThr, 0, s>>>(dB_part, dC_part, rows, (int)(p.H / p.G), (int)p.N, b, c);
+    };
+    using bf = __nv_bfloat16;
     if (p.dtype == SSD_F32)
-        k_delta_group_sum<float><<<grid, 256, 0, s>>>(dB_part, dC_part, p.B * p.L, (int)p.H, (int)p.G, (int)p.N,
-                                                      static_cast<float *>(dBm), static_cast<float *>(dCm));
+        go(V == 4 ? k_delta_group_sum<float, 4> : k_delta_group_sum<float, 1>, static_cast<float *>(dBm), static_cast<float *>(dCm));
     else
-        k_delta_group_sum<__nv_bfloat16><<<grid, 256, 0, s>>>(dB_part, dC_part, p.B * p.L, (int)p.H, (int)p.G, (int)p.N,
-                                                              static_cast<__nv_bfloat16 *>(dBm),
-                                                              static_cast<__nv_bfloat16 *>(dCm));
+        go(V == 4 ? k_delta_group_sum<bf, 4> : k_delta_group_sum<bf, 1>, static_cast<bf *>(dBm), static_cast<bf *>(dCm));
     return cudaGetLastError();
 }
 
