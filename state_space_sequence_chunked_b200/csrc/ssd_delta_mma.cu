@@ -6,29 +6,23 @@
 // (K, Q: keys Bm and queries Cm; the inverse (I + M diag(beta))^-1 is I + W diag(beta), so no division by
 // beta is needed and its unit diagonal is exact).
 //
-//   k_delta_prep   everything that does not depend on the state: W and tril(Q K^T o E) per chunk and
-//                  head, all chunks at once, as the register fragments the chain multiplies by.
-//   k_delta_chain  the chain over the chunks. The rows p of the state are independent given K, Q
-//                  and W, so a warp keeps 16 rows of it in fp32 accumulators for the whole sequence
-//                  and nothing crosses warps: the accumulators of one product are, in place, the left
-//                  operand of the next (mma.sync m16n8k16: both layouts hold the same elements), and
-//                  tokens are the columns throughout (R^T, u^T, Y^T).
+//   k_delta_prep (here)             what does not depend on the state: W, tril(Q K^T o E) and the decays per
+//                                   chunk and head, all chunks at once, as right operands of the chain.
+//   k_delta_tc    (ssd_delta_tc.cu) the chain over the chunks, the state in tensor memory.
+//   k_delta_tc_bwd, k_delta_grads   the backward pass: the states again and the chain in reverse, then what sums
+//                                   over the rows of the state (ssd_delta_tc.cu, ssd_delta_grads.cu).
 //
 // Precision. The final state is fp32, so what enters it is kept to 2^-16: an fp32 left operand is
 // split in two bf16 parts (hi + lo) and W too (three products); K, Q are exact. Y is rounded to bf16,
 // so S and tril(Q K^T o E) enter it as one bf16 part, u as two.
-//
-// mma.sync because the chain is one of dependent small products: with the state in registers a chunk
-// costs no shared-memory or tensor-memory round trip between them. m16n8k16 measures 550 TFLOP/s
-// on this part (8.4 cycles per instruction and sub-partition).
-#include "ssd_delta.cuh"
+#include "delta_tc.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kC = kDeltaChunk;  // tokens per chunk
-constexpr int kThr = 128;        // 4 warps
-constexpr int kRowsCta = 64;     // state rows per CTA of the chain
+using namespace tc;
+
+constexpr int kThr = 128;  // 4 warps
 
 // Blocks (a, b) of 16 x 16 tokens with a >= b, in the order a (a + 1) / 2 + b.
 constexpr int kBlocks = 10;
@@ -53,8 +47,6 @@ struct Prep {
 // block (a, b) by column of blocks: four of column 0, three of column 1, ...
 __host__ __device__ constexpr int column_at(int a, int b) { return b * 4 - b * (b - 1) / 2 + a - b; }
 
-__device__ __forceinline__ uint32_t smem_addr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
@@ -69,21 +61,6 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
                  : "r"(a)
                  : "memory");
 }
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(a)
-                 : "memory");
-}
-__device__ __forceinline__ void stsm4(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
-                 : "memory");
-}
-__device__ __forceinline__ void stsm4t(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(r0), "r"(r1), "r"(r2),
-                 "r"(r3)
-                 : "memory");
-}
 __device__ __forceinline__ uint32_t trans8(uint32_t v) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -94,25 +71,12 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float low(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float high(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
-// hi + lo parts of a pair: what hi leaves of each value, rounded again (2^-17 of the value at worst).
-__device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo) {
-    hi = pack(x, y);
-    lo = pack(x - low(hi), y - high(hi));
-}
-
 // Left operand (16 x 16) from two neighbouring accumulator tiles: the same elements, converted.
 __device__ __forceinline__ void split_a(const float (&t0)[4], const float (&t1)[4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-    split(t0[0], t0[1], hi[0], lo[0]);
-    split(t0[2], t0[3], hi[1], lo[1]);
-    split(t1[0], t1[1], hi[2], lo[2]);
-    split(t1[2], t1[3], hi[3], lo[3]);
+    split2(t0[0], t0[1], hi[0], lo[0]);
+    split2(t0[2], t0[3], hi[1], lo[1]);
+    split2(t1[0], t1[1], hi[2], lo[2]);
+    split2(t1[2], t1[3], hi[3], lo[3]);
 }
 
 // Byte offset of 16-byte vector c of row r in a tile with rows of ROW bytes (a multiple of 128),
@@ -141,6 +105,7 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16 *__r
 // in fp32 (a lane per column), then the rows of blocks below, on tensor cores with every fp32 operand
 // in two bf16 parts:
 //     W_ab = -(I + W_aa diag(beta_a)) (M_ab (I + diag(beta_b) W_bb) + sum_{b<c<a} M_ac diag(beta_c) W_cb).
+constexpr double kLog2e = 1.4426950408889634;
 constexpr int kDl = 20;  // padded row of a diagonal block
 // The fp32 products are kept up to the diagonal block: row i of block row a has 16 (a + 1) columns and a
 // pad of 8 (a half warp's pairs then fall in different banks).
@@ -152,7 +117,7 @@ constexpr int kTriFloats = 16 * (24 + 40 + 56 + 72);
 
 struct PrepWarp {
     float diag[4][16 * kDl];
-    float2 cum[kC];  // cum as a sum of two floats
+    float ch[kC], cl[kC];  // log2(e) cum as a sum of two floats
     float beta[kC];
 };
 template <int NT>
@@ -166,14 +131,12 @@ union PrepSmem {
     };
 };
 
-__device__ __forceinline__ float decay_between(float2 i, float2 j) { return __expf((i.x - j.x) + (i.y - j.y)); }
-
 // Right-operand fragments (hi, lo) of a 16 x 16 fp32 block in accumulator layout, rows g and g + 8 scaled.
 __device__ __forceinline__ void split_b(const float (&b)[2][4], float s0, float s1, uint32_t (&h)[4], uint32_t (&l)[4]) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-        split(s0 * b[n][0], s0 * b[n][1], h[2 * n], l[2 * n]);
-        split(s1 * b[n][2], s1 * b[n][3], h[2 * n + 1], l[2 * n + 1]);
+        split2(s0 * b[n][0], s0 * b[n][1], h[2 * n], l[2 * n]);
+        split2(s1 * b[n][2], s1 * b[n][3], h[2 * n + 1], l[2 * n + 1]);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) h[e] = trans8(h[e]), l[e] = trans8(l[e]);
@@ -203,10 +166,10 @@ __device__ __forceinline__ void put_rows(char *out, int a, int b, int lane, cons
 template <bool BWD>
 __device__ __forceinline__ void put_w(char *out, int a, int b, int lane, const float (&w)[2][4]) {
     uint32_t hi[4], lo[4];  // rows 0-7: two halves of the columns, then rows 8-15
-    split(w[0][0], w[0][1], hi[0], lo[0]);
-    split(w[1][0], w[1][1], hi[1], lo[1]);
-    split(w[0][2], w[0][3], hi[2], lo[2]);
-    split(w[1][2], w[1][3], hi[3], lo[3]);
+    split2(w[0][0], w[0][1], hi[0], lo[0]);
+    split2(w[1][0], w[1][1], hi[1], lo[1]);
+    split2(w[0][2], w[0][3], hi[2], lo[2]);
+    split2(w[1][2], w[1][3], hi[3], lo[3]);
     uint32_t *t = reinterpret_cast<uint32_t *>(out + Prep<BWD>::W + column_at(a, b) * kBlockBytes) + lane;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -228,7 +191,7 @@ __global__ void __launch_bounds__(kThr, 4)
     const int64_t c = blockIdx.x, nc = gridDim.x, b = blockIdx.z, t0 = c * kC;
     const int grp = blockIdx.y / slices, slice = blockIdx.y % slices, per = H / G;
     const int h_begin = grp * per + per * slice / slices, h_end = grp * per + per * (slice + 1) / slices;
-    const uint32_t ka = smem_addr(sm.k), qa = smem_addr(sm.q);
+    const uint32_t ka = smem_u32(sm.k), qa = smem_u32(sm.q);
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
         for (int i = tid; i < nclear; i += kThr) clear[i] = 0;
     load_tile<NT / 8>(ka, Bm, b, L, t0, G, grp, N, 0);
@@ -293,9 +256,11 @@ __global__ void __launch_bounds__(kThr, 4)
             }
             const double total = __shfl_sync(0xffffffffu, sum, 31), first = sum - g1;
             const float f0 = (float)first, f1 = (float)sum, l0 = (float)(first - (double)f0), l1 = (float)(sum - (double)f1);
-            wm.cum[2 * lane] = make_float2(f0, l0);
-            wm.cum[2 * lane + 1] = make_float2(f1, l1);
-            wm.beta[2 * lane] = b0, wm.beta[2 * lane + 1] = b1;
+            const double e0 = kLog2e * first, e1 = kLog2e * sum;
+            const float2 eh = make_float2((float)e0, (float)e1);
+            reinterpret_cast<float2 *>(wm.ch)[lane] = eh;
+            reinterpret_cast<float2 *>(wm.cl)[lane] = make_float2((float)(e0 - (double)eh.x), (float)(e1 - (double)eh.y));
+            reinterpret_cast<float2 *>(wm.beta)[lane] = make_float2(b0, b1);
             float2 *scal = reinterpret_cast<float2 *>(out + Lay::scal) + lane;
             scal[0] = make_float2(expf(f0), expf(f1));
             scal[kC / 2] = make_float2(expf((float)(total - first)), expf((float)(total - sum)));
@@ -307,34 +272,40 @@ __global__ void __launch_bounds__(kThr, 4)
         // block (a, cc): M in accumulator layout; the masked Q K^T goes out
         const auto block = [&](int a, int cc, float (&m)[2][4]) {
             float p[2][4];
-            const float2 ri[2] = {wm.cum[16 * a + gr], wm.cum[16 * a + gr + 8]};
+            const float ih[2] = {wm.ch[16 * a + gr], wm.ch[16 * a + gr + 8]}, il[2] = {wm.cl[16 * a + gr], wm.cl[16 * a + gr + 8]};
+            const float2 minus = make_float2(-1.f, -1.f), one = make_float2(1.f, 1.f);
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int j = 16 * cc + 8 * n + 2 * tg;
-                const float4 cj = *reinterpret_cast<const float4 *>(&wm.cum[j]);
+                const float2 jh = *reinterpret_cast<const float2 *>(&wm.ch[j]), jl = *reinterpret_cast<const float2 *>(&wm.cl[j]);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int i = 16 * a + gr + 8 * r;
                     const int at = tri_at(i) + j;
-                    const float2 kk = *reinterpret_cast<const float2 *>(&sm.kk[at]);
-                    const float2 qk = *reinterpret_cast<const float2 *>(&sm.qk[at]);
-                    const float e0 = j <= i ? decay_between(ri[r], make_float2(cj.x, cj.y)) : 0.f;
-                    const float e1 = j + 1 <= i ? decay_between(ri[r], make_float2(cj.z, cj.w)) : 0.f;
-                    m[n][2 * r] = j < i ? kk.x * e0 : 0.f, m[n][2 * r + 1] = j + 1 < i ? kk.y * e1 : 0.f;
-                    p[n][2 * r] = j <= i ? qk.x * e0 : 0.f, p[n][2 * r + 1] = j + 1 <= i ? qk.y * e1 : 0.f;
+                    // (h_i - h_j) + (l_i - l_j): the difference of the large parts first
+                    const float2 d = fma2(one, fma2(jh, minus, make_float2(ih[r], ih[r])), fma2(jl, minus, make_float2(il[r], il[r])));
+                    const float2 e = make_float2(ex2(d.x), ex2(d.y));
+                    float2 kk = mul2(e, *reinterpret_cast<const float2 *>(&sm.kk[at]));
+                    float2 qk = mul2(e, *reinterpret_cast<const float2 *>(&sm.qk[at]));
+                    if (a == cc) {
+                        kk.x = j < i ? kk.x : 0.f, kk.y = j + 1 < i ? kk.y : 0.f;
+                        qk.x = j <= i ? qk.x : 0.f, qk.y = j + 1 <= i ? qk.y : 0.f;
+                    }
+                    m[n][2 * r] = kk.x, m[n][2 * r + 1] = kk.y;
+                    p[n][2 * r] = qk.x, p[n][2 * r + 1] = qk.y;
                 }
             }
             if constexpr (BWD) {
                 uint32_t ph[4], pl[4];
-                split(p[0][0], p[0][1], ph[0], pl[0]);
-                split(p[1][0], p[1][1], ph[1], pl[1]);
-                split(p[0][2], p[0][3], ph[2], pl[2]);
-                split(p[1][2], p[1][3], ph[3], pl[3]);
+                split2(p[0][0], p[0][1], ph[0], pl[0]);
+                split2(p[1][0], p[1][1], ph[1], pl[1]);
+                split2(p[0][2], p[0][3], ph[2], pl[2]);
+                split2(p[1][2], p[1][3], ph[3], pl[3]);
                 put_rows(out + Lay::Pr, a, cc, lane, ph, pl);
             } else {
                 uint32_t *o = reinterpret_cast<uint32_t *>(out + Lay::P + column_at(a, cc) * kBlockBytes) + lane;
-                o[0] = pack(p[0][0], p[0][1]), o[32] = pack(p[1][0], p[1][1]);
-                o[64] = pack(p[0][2], p[0][3]), o[96] = pack(p[1][2], p[1][3]);
+                o[0] = pack_bf16(p[0][0], p[0][1]), o[32] = pack_bf16(p[1][0], p[1][1]);
+                o[64] = pack_bf16(p[0][2], p[0][3]), o[96] = pack_bf16(p[1][2], p[1][3]);
             }
         };
 #pragma unroll
