@@ -16,16 +16,20 @@
 //                     dbeta), from the segment's entering state, leaving cotangent, err and z.
 //   k_delta_step      one token, HBM-bound: the state is read and written once.
 //
-// This is the exact path (fp32 throughout), bound by the latency of the token chain and not by a
-// unit; bf16 inputs of the usual sizes take the chunked tensor-core path in ssd_delta_mma.cu.
+// This is the exact path (fp32 throughout), bound by the latency of its chain and not by a unit: 2 x 777 fp32
+// tokens of 6 heads of 40 x 36 take 96 us, 0.12 us a token (token by token with a row in 32 lanes 335 us; two
+// rows per lane 141); 37 bf16 tokens of 24 heads of 64 x 128 take 13 us (24 on the tensor cores). bf16 inputs of the
+// usual sizes and lengths take the chunked tensor-core path in ssd_delta_mma.cu.
+//
+// k_delta_step is bound by HBM: 64 sequences of 32 heads of 128 x 128, 51 us, 82% of the measured 6.45 TB/s.
 #include "ssd_delta.cuh"
 
 namespace ssd {
 namespace {
 
 constexpr int kThr = 256, kWarps = kThr / 32;
-constexpr int kR = 1, kSeqRows = 16;  // state rows per lane and per CTA of the sequential kernels
-constexpr int kSeqWalk = kSeqRows / kR * 8, kSeqThr = kSeqWalk + 128;  // threads that walk, and with those that stage
+constexpr int kSeqRows = 16;  // state rows per CTA of the sequential kernels
+constexpr int kSeqWalk = kSeqRows * 8, kSeqThr = kSeqWalk + 128;  // threads that walk, and with those that stage
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -178,7 +182,7 @@ __device__ __forceinline__ float sums8(float (&v)[8], int lane) {
     return v[0];
 }
 
-// grid (ceil(P / 16), H, B), 2 warps that walk the tokens and 4 that stage the next ones.
+// grid (ceil(P / 16), H, B), 4 warps that walk the tokens (a row in 8 lanes) and 4 that stage the next ones.
 template <typename T, int NJ, bool kY>
 __global__ void __launch_bounds__(kSeqThr, NJ < 8 ? 2 : 1)
     k_delta_seq(const T *__restrict__ x, const T *__restrict__ g, const T *__restrict__ beta, const T *__restrict__ Bm,
@@ -188,9 +192,10 @@ __global__ void __launch_bounds__(kSeqThr, NJ < 8 ? 2 : 1)
     using S = SeqStage<NJ>;
     __shared__ S st[2];
     const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l8 = lane & 7;
-    const int pc = blockIdx.x * kSeqRows, r0 = (warp * 4 + (lane >> 3)) * kR, p0 = pc + r0;
+    const int pc = blockIdx.x * kSeqRows, r = warp * 4 + (lane >> 3), p = pc + r;
+    const bool live = p < P;
     
-    const int64_t row = ((int64_t)b * H + h) * P + p0, ns = (L + kSeg - 1) / kSeg;
+    const int64_t row = ((int64_t)b * H + h) * P + p, ns = (L + kSeg - 1) / kSeg;
     if (tid >= kSeqWalk) {
         SeqLoad<T, NJ> in;
         const auto fetch = [&](int64_t t0) { in.fetch(x, g, beta, Bm, Cm, L, t0, H, P, G, N, b, h, pc, tid - kSeqWalk); };
@@ -203,74 +208,57 @@ __global__ void __launch_bounds__(kSeqThr, NJ < 8 ? 2 : 1)
         }
         return;
     }
-    float2 s[kR][NJ][2];
-#pragma unroll
-    for (int e = 0; e < kR; ++e) row_load<NJ>(s[e], h0 + (row + e) * N, h0 && p0 + e < P, l8, N);
+    float2 s[NJ][2];
+    row_load<NJ>(s, h0 + row * N, h0 && live, l8, N);
     for (int64_t t0 = 0; t0 < L; t0 += S::tb) {
         const S &c = st[t0 / S::tb & 1];
         seq_sync();
         for (int blk = 0; blk < S::tb / 4 && t0 + 4 * blk < L; ++blk) {
             const int64_t t = t0 + 4 * blk;
-            if (seg_states && t % kSeg == 0)
-#pragma unroll
-                for (int e = 0; e < kR; ++e)
-                    if (p0 + e < P) row_store<NJ>(s[e], seg_states + ((((int64_t)b * H + h) * ns + t / kSeg) * P + p0 + e) * N, l8, N);
+            if (seg_states && t % kSeg == 0 && live)
+                row_store<NJ>(s, seg_states + ((((int64_t)b * H + h) * ns + t / kSeg) * P + p) * N, l8, N);
             const float4 *k = c.k + blk * S::cols, *q = c.q + blk * S::cols;
-            float own[kR];  // h.k of token l8, or h.q of token l8 - 4
-            {
-                float d[kR][8];
+            float d[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                    for (int e = 0; e < kR; ++e) {
-                        d[e][i] = row_dot<NJ>(s[e], k + i * (S::cols / 4), l8);
-                        d[e][4 + i] = kY ? row_dot<NJ>(s[e], q + i * (S::cols / 4), l8) : 0.f;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < kR; ++e) own[e] = sums8(d[e], lane);
+            for (int i = 0; i < 4; ++i) {
+                d[i] = row_dot<NJ>(s, k + i * (S::cols / 4), l8);
+                d[4 + i] = kY ? row_dot<NJ>(s, q + i * (S::cols / 4), l8) : 0.f;
             }
+            const float own = sums8(d, lane);  // h.k of token l8, or h.q of token l8 - 4
             const float4 a4 = *reinterpret_cast<const float4 *>(&c.a[4 * blk]), b4 = *reinterpret_cast<const float4 *>(&c.beta[4 * blk]);
             const float a[4] = {a4.x, a4.y, a4.z, a4.w}, bt[4] = {b4.x, b4.y, b4.z, b4.w};
             const float4 m0 = *reinterpret_cast<const float4 *>(&c.kk[blk][0]), m1 = *reinterpret_cast<const float4 *>(&c.kk[blk][4]);
             const float kk[6] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y};
             const float4 qr = *reinterpret_cast<const float4 *>(&c.qk[blk][l8 & 3][0]);
             const float qk[4] = {qr.x, qr.y, qr.z, qr.w};
-            float u[kR][4];
-            const int64_t tt = t + (l8 & 3), at = (((int64_t)b * L + tt) * H + h) * P + p0;
+            const float4 x4 = *reinterpret_cast<const float4 *>(&c.x[r][4 * blk]);
+            const float xv[4] = {x4.x, x4.y, x4.z, x4.w};
+            float u[4], err[4], yv = own;
 #pragma unroll
-            for (int e = 0; e < kR; ++e) {
-                const float4 x4 = *reinterpret_cast<const float4 *>(&c.x[r0 + e][4 * blk]);
-                const float xv[4] = {x4.x, x4.y, x4.z, x4.w};
-                float err[4], yv = own[e];
+            for (int i = 0; i < 4; ++i) {  // h' k_i: the block's earlier tokens by their keys' products
+                float v = __shfl_sync(0xffffffffu, own, (lane & 24) + i);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {  // h' k_i: the block's earlier tokens by their keys' products
-                    float v = __shfl_sync(0xffffffffu, own[e], (lane & 24) + i);
-#pragma unroll
-                    for (int j = 0; j < i; ++j) v = fmaf(u[e][j], kk[i * (i - 1) / 2 + j], a[j] * v);
-                    err[i] = xv[i] - a[i] * v;
-                    u[e][i] = bt[i] * err[i];
-                    const float n = fmaf(u[e][i], qk[i], a[i] * yv);
-                    yv = i <= (l8 & 3) ? n : yv;
-                }
-                if (p0 + e < P && tt < L) {
-                    if (l8 >= 4) {
-                        if (kY) store_as(y + at + e, yv);
-                    } else if (err_out) {
-                        err_out[at + e] = (l8 & 2) ? (l8 & 1 ? err[3] : err[2]) : (l8 & 1 ? err[1] : err[0]);
-                    }
+                for (int j = 0; j < i; ++j) v = fmaf(u[j], kk[i * (i - 1) / 2 + j], a[j] * v);
+                err[i] = xv[i] - a[i] * v;
+                u[i] = bt[i] * err[i];
+                const float n = fmaf(u[i], qk[i], a[i] * yv);
+                yv = i <= (l8 & 3) ? n : yv;
+            }
+            const int64_t tt = t + (l8 & 3), at = (((int64_t)b * L + tt) * H + h) * P + p;
+            if (live && tt < L) {
+                if (l8 >= 4) {
+                    if (kY) store_as(y + at, yv);
+                } else if (err_out) {
+                    err_out[at] = (l8 & 2) ? (l8 & 1 ? err[3] : err[2]) : (l8 & 1 ? err[1] : err[0]);
                 }
             }
             const float c2 = a[3], c1 = c2 * a[2], c0 = c1 * a[1], ci[4] = {c0, c1, c2, 1.f};
-            for (int e = 0; e < kR; ++e) row_scale<NJ>(s[e], c0 * a[0]);
+            row_scale<NJ>(s, c0 * a[0]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) for (int e = 0; e < kR; ++e) row_add<NJ>(s[e], ci[i] * u[e][i], k + i * (S::cols / 4), l8);
+            for (int i = 0; i < 4; ++i) row_add<NJ>(s, ci[i] * u[i], k + i * (S::cols / 4), l8);
         }
     }
-    if (h_final)
-#pragma unroll
-        for (int e = 0; e < kR; ++e)
-            if (p0 + e < P) row_store<NJ>(s[e], h_final + (row + e) * N, l8, N);
+    if (h_final && live) row_store<NJ>(s, h_final + row * N, l8, N);
 }
 
 // grid (ceil(P / 16), H, B), warps as above.
@@ -283,9 +271,10 @@ __global__ void __launch_bounds__(kSeqThr, NJ < 8 ? 2 : 1)
     using S = SeqStage<NJ>;
     __shared__ S st[2];
     const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l8 = lane & 7;
-    const int pc = blockIdx.x * kSeqRows, r0 = (warp * 4 + (lane >> 3)) * kR, p0 = pc + r0;
+    const int pc = blockIdx.x * kSeqRows, r = warp * 4 + (lane >> 3), p = pc + r;
+    const bool live = p < P;
     
-    const int64_t row = ((int64_t)b * H + h) * P + p0, ns = (L + kSeg - 1) / kSeg, first = (L - 1) / S::tb * S::tb;
+    const int64_t row = ((int64_t)b * H + h) * P + p, ns = (L + kSeg - 1) / kSeg, first = (L - 1) / S::tb * S::tb;
     if (tid >= kSeqWalk) {
         SeqLoad<T, NJ> in;
         const auto fetch = [&](int64_t t0) { in.fetch(dy, g, beta, Bm, Cm, L, t0, H, P, G, N, b, h, pc, tid - kSeqWalk); };
@@ -298,72 +287,54 @@ __global__ void __launch_bounds__(kSeqThr, NJ < 8 ? 2 : 1)
         }
         return;
     }
-    float2 s[kR][NJ][2];
-#pragma unroll
-    for (int e = 0; e < kR; ++e) row_load<NJ>(s[e], dh_final + (row + e) * N, dh_final && p0 + e < P, l8, N);
+    float2 s[NJ][2];
+    row_load<NJ>(s, dh_final + row * N, dh_final && live, l8, N);
     for (int64_t t0 = first; t0 >= 0; t0 -= S::tb) {
         const S &c = st[t0 / S::tb & 1];
         seq_sync();
         for (int blk = S::tb / 4 - 1; blk >= 0; --blk) {
             const int64_t t = t0 + 4 * blk;
             if (t >= L) continue;
-            if (t + 4 >= L || (t + 4) % kSeg == 0)
-#pragma unroll
-                for (int e = 0; e < kR; ++e)
-                    if (p0 + e < P) row_store<NJ>(s[e], seg_cot + ((((int64_t)b * H + h) * ns + t / kSeg) * P + p0 + e) * N, l8, N);
+            if ((t + 4 >= L || (t + 4) % kSeg == 0) && live)
+                row_store<NJ>(s, seg_cot + ((((int64_t)b * H + h) * ns + t / kSeg) * P + p) * N, l8, N);
             const float4 *k = c.k + blk * S::cols, *q = c.q + blk * S::cols;
-            float own;  // D k of token l8 & 3, rows l8 >> 2
-            {
-                float d[8];
+            // D k of the four tokens (as eight values; the last four are not used)
+            float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    d[i] = row_dot<NJ>(s[0], k + i * (S::cols / 4), l8);
-                    d[4 + i] = kR > 1 ? row_dot<NJ>(s[kR - 1], k + i * (S::cols / 4), l8) : 0.f;
-                }
-                own = sums8(d, lane);
-            }
+            for (int i = 0; i < 4; ++i) d[i] = row_dot<NJ>(s, k + i * (S::cols / 4), l8);
+            const float own = sums8(d, lane);
             const float4 a4 = *reinterpret_cast<const float4 *>(&c.a[4 * blk]), b4 = *reinterpret_cast<const float4 *>(&c.beta[4 * blk]);
             const float a[4] = {a4.x, a4.y, a4.z, a4.w}, bt[4] = {b4.x, b4.y, b4.z, b4.w};
             const float4 m0 = *reinterpret_cast<const float4 *>(&c.kk[blk][0]), m1 = *reinterpret_cast<const float4 *>(&c.kk[blk][4]);
             const float kk[6] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y};
-            float dv[kR][4], yv[kR][4], zi = 0.f;
+            const float4 y4 = *reinterpret_cast<const float4 *>(&c.x[r][4 * blk]);
+            const float yv[4] = {y4.x, y4.y, y4.z, y4.w};
+            float dv[4], zi = 0.f;
 #pragma unroll
-            for (int e = 0; e < kR; ++e) {
-                const float4 y4 = *reinterpret_cast<const float4 *>(&c.x[r0 + e][4 * blk]);
-                yv[e][0] = y4.x, yv[e][1] = y4.y, yv[e][2] = y4.z, yv[e][3] = y4.w;
+            for (int i = 3; i >= 0; --i) {  // D k_i: the later tokens of the block by their products with k_i
+                float v = __shfl_sync(0xffffffffu, own, (lane & 24) + i);
 #pragma unroll
-                for (int i = 3; i >= 0; --i) {  // D k_i: the later tokens of the block by their products with k_i
-                    float v = __shfl_sync(0xffffffffu, own, (lane & 24) + 4 * e + i);
-#pragma unroll
-                    for (int j = 3; j > i; --j)
-                        v = a[j] * fmaf(yv[e][j], c.qk[blk][j][i], fmaf(-dv[e][j], kk[j * (j - 1) / 2 + i], v));
-                    const float z = fmaf(yv[e][i], c.qk[blk][i][i], v);
-                    dv[e][i] = bt[i] * z;
-                    if (l8 == 4 * e + i) zi = z;
-                }
+                for (int j = 3; j > i; --j)
+                    v = a[j] * fmaf(yv[j], c.qk[blk][j][i], fmaf(-dv[j], kk[j * (j - 1) / 2 + i], v));
+                const float z = fmaf(yv[i], c.qk[blk][i][i], v);
+                dv[i] = bt[i] * z;
+                if (l8 == i) zi = z;
             }
             const float c1 = a[0] * a[1], c2 = c1 * a[2], c3 = c2 * a[3], ci[4] = {a[0], c1, c2, c3};
-            for (int e = 0; e < kR; ++e) row_scale<NJ>(s[e], c3);
+            row_scale<NJ>(s, c3);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                for (int e = 0; e < kR; ++e) {
-                    row_add<NJ>(s[e], ci[i] * yv[e][i], q + i * (S::cols / 4), l8);
-                    row_add<NJ>(s[e], -ci[i] * dv[e][i], k + i * (S::cols / 4), l8);
-                }
+                row_add<NJ>(s, ci[i] * yv[i], q + i * (S::cols / 4), l8);
+                row_add<NJ>(s, -ci[i] * dv[i], k + i * (S::cols / 4), l8);
             }
-            const int i = l8 & 3, e = l8 >> 2;
-            const int64_t at = (((int64_t)b * L + t + i) * H + h) * P + p0 + e;
-            if (e < kR && p0 + e < P && t + i < L) {
+            const int64_t at = (((int64_t)b * L + t + l8) * H + h) * P + p;
+            if (l8 < 4 && live && t + l8 < L) {
                 z_out[at] = zi;
-                store_as(dx + at, c.beta[4 * blk + i] * zi);
+                store_as(dx + at, c.beta[4 * blk + l8] * zi);
             }
         }
     }
-    if (dh0)
-#pragma unroll
-        for (int e = 0; e < kR; ++e)
-            if (p0 + e < P) row_store<NJ>(s[e], dh0 + (row + e) * N, l8, N);
+    if (dh0 && live) row_store<NJ>(s, dh0 + row * N, l8, N);
 }
 
 // One segment of one head: grid (segments, H, B). With S the entering state, D the leaving cotangent,

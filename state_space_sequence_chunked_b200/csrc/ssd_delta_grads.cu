@@ -20,9 +20,10 @@
 // Warps (640 threads): 0 loads (TMA, two stages), 1 issues the products, 2 ends a head (dg, dbeta), 4-19 the
 // elementwise work, four per 32 lanes with a quarter of the columns each.
 //
-// Bound by the elementwise warps: about 2500 issue slots per head and SM against 1400 cycles of products.
-// The same sums with mma.sync in registers (64 tokens by half or a quarter of the columns per warp) took 212 us
-// on the 130M-like backward, 23800 instructions a head.
+// Bound by the elementwise warps: 5200 cycles per head and 64 rows, of which they work 4400 (60% of the issue slots)
+// and the products take 2400. 24 heads of 64 x 128, 4 x 2048 tokens: 82 us, of 24 us for its bytes; the same sums
+// with mma.sync, dQ and dK in registers, took 212. Issuing a step's first products before the last step's pairs,
+// or waiting for fewer of them, gained nothing (87 and 93 us).
 //
 // Every wait is bounded (tc_ptx.cuh); one that runs out sets bit 0 of the workspace's status word.
 #include "delta_tc.cuh"
@@ -98,7 +99,7 @@ __device__ __forceinline__ float dot16(const uint32_t (&v)[16], uint4 a, uint4 b
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 1) k_delta_grads(const __grid_constant__ Maps m, const __grid_constant__ GradArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) k_delta_grads_tc(const __grid_constant__ Maps m, const __grid_constant__ GradArgs a) {
     using Z = Lay<NT>;
     extern __shared__ __align__(1024) unsigned char sm[];
     if ((smem_u32(sm) & 1023u) != 0) {
@@ -476,9 +477,9 @@ cudaError_t launch(const DeltaProblem &p, const DeltaGrads &g, const DeltaChain 
                      static_cast<const bf *>(ch.z), static_cast<const bf *>(ch.err), static_cast<bf *>(g.dBm), static_cast<bf *>(g.dCm),
                      static_cast<bf *>(g.dg), static_cast<bf *>(g.dbeta), dB_part, dC_part, ch.status, wait_limit_us()};
     constexpr int smem = Lay<NT>::bytes;
-    const cudaError_t e = cudaFuncSetAttribute(k_delta_grads<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(k_delta_grads_tc<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e) return e;
-    k_delta_grads<NT><<<dim3((unsigned)nc, (unsigned)(p.G * slices), (unsigned)p.B), kThreads, smem, s>>>(m, a);
+    k_delta_grads_tc<NT><<<dim3((unsigned)nc, (unsigned)(p.G * slices), (unsigned)p.B), kThreads, smem, s>>>(m, a);
     return cudaGetLastError();
 }
 

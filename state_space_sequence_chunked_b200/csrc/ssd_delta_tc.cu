@@ -17,14 +17,23 @@
 // zeros in the other's 64. W and P are lower triangular: a step of 16 tokens j multiplies only the
 // tokens i from its own block on (N = 64, 48, 32, 16).
 //
-// Warps (768 threads): 0 loads (TMA), 1 issues the products, 4-19 (T) form R, u and the state's operands (four warps per 32 lanes, a quarter of the
-// columns each), 20-23 (O) scale Yq and write Y out. TMEM, 512 columns: S 128, S hi 64, S lo 64 (later
-// ek u), R 64, Y 64, beta R then u 2 x 64.
+// Warps (768 threads): 0 loads (TMA), 1 issues the products, 4-19 (T) form R, u and the state's operands (four
+// warps per 32 lanes, a quarter of the columns each), 20-23 (O) scale Yq and write Y out; in the forward
+// chain 2-3 are idle (a T or O warp's TMEM lanes are those of its number modulo 4). TMEM, 512 columns: S 128,
+// S hi 64, S lo 64 (later ek u), R 64, Y 64, beta R then u 2 x 64.
 //
-// What bounds it: the chain of a chunk, S -> R -> u -> S, each link a product (0.1-0.25 us) and a pass of
-// the T warps over its result (0.25-0.35 us).
+// Streams (128 state rows over the sequence) are dealt to the CTAs in equal shares of chunks, so a stream may be cut
+// once and handed on through global memory: 160 streams of 128 chunks took 731 us with whole streams (two waves on
+// 148 SMs), 432 in shares.
 //
-// kStore is the backward pass's recomputation: no Y, but the state entering each chunk, err and u in bf16.
+// What bounds it: the chain of a chunk, S -> R -> u -> S, three products and three passes of the T warps over
+// their results, about 4700 cycles (2.5 us) per chunk and CTA, of which the 72 products take about 1950 to issue. 24 heads of
+// 64 x 128, 8 x 2048 tokens (96 CTAs, 32 chunks each): 104 us; 80 heads, 4 x 8192 (148 CTAs): 432 us. The
+// same chain on mma.sync, the state in registers, took 2200 us of the latter and the prep.
+//
+// kStore is the backward pass's recomputation: no Y, but the state entering each chunk, err and u, rounded to bf16:
+// they meet operands that are bf16 already (K, Q, dY) in gradients that are stored in bf16 (relative errors of
+// 3.2e-3 against 1.7e-3 for the storage alone); fp32 would double the pass's largest traffic.
 //
 // Every wait is bounded (tc_ptx.cuh); one that runs out sets bit 0 of the workspace's status word.
 #include "delta_tc.cuh"
@@ -614,7 +623,8 @@ __device__ __forceinline__ void chain_fwd(const CUtensorMap &tm_k, const CUtenso
 //   D -= (eg r)^T K          -eg r hi, lo (TMEM)       K                                   D
 // with F = Z + ek F0, z = F + E, r = beta z = dX. Rows, tokens and warps as above, plus warps 2-3, which
 // form eg dY. In a PAIR the left operands of Z come with a panel of zeros for the other head's rows.
-// z and dX go out in bf16, and D hi of every chunk (an operand of k_delta_grads_mma).
+// z and dX go out in bf16, and D hi of every chunk (an operand of k_delta_grads_tc). Both chains share a launch, since
+// neither needs the other: 24 heads of 64 x 128, 4 x 2048 tokens, 132 us for both.
 template <int NT, bool PAIR>
 struct RevLay {
     static constexpr int HB = PAIR ? 2 : 1;

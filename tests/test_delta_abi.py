@@ -201,3 +201,17 @@ def test_row_views():
         B._rows_view("z", torch.zeros(3, 4, 16)[..., ::2], like, cpu)
     with pytest.raises(ValueError):  # rows of the first axis are not evenly spaced with the second's
         B._rows_view("z", torch.zeros(3, 6, 8)[:, :4], like, cpu)
+
+
+def test_plan_rule(lib):
+    """The forward's rule of length and heads, the backward's of sizes alone; sizes past the range are refused."""
+    fwd_path = lambda *s: B.delta_fwd_plan(*s, B.SSD_BF16)["path"]  # noqa: E731
+    assert fwd_path(1, 127, 24, 64, 1, 128) == "simt" and fwd_path(1, 128, 24, 64, 1, 128) == "tcgen05"
+    assert fwd_path(8, 21, 24, 64, 1, 128) == "simt" and fwd_path(8, 22, 24, 64, 1, 128) == "tcgen05"
+    assert fwd_path(32, 2, 80, 64, 1, 128) == "tcgen05"
+    for L in (1, 37, 128):
+        plan = B.delta_bwd_plan(1, L, 4, 64, 1, 128, B.SSD_BF16)
+        assert plan["path"] == "tcgen05" and plan["workspace_bytes"] > 0
+    for size in ((4, 264, 1, 16), (4, 16, 1, 264)):
+        with pytest.raises(B.SSDError):
+            B.delta_fwd_plan(1, 131, *size, B.SSD_BF16)
