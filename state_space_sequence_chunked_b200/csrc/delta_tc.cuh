@@ -116,5 +116,12 @@ __device__ __forceinline__ void drain_loads(uint64_t *full, int it) {
     }
 }
 
+// tcgen05.wait::ld with 16 registers of an earlier load as operands: no use of them moves above it.
+#define SSD_W4(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3])
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : SSD_W4(0), SSD_W4(4), SSD_W4(8), SSD_W4(12)::"memory");
+}
+#undef SSD_W4
+
 }  // namespace tc
 }  // namespace ssd

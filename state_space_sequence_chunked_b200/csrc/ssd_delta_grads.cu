@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads_tc(const __grid_con
                 uint32_t v[16], w[16];
                 tmem_ld16(lo_ + kTmP + 16 * sub, v);
                 tmem_ld16(lo_ + kTmConst + 16 * sub, w);
-                tmem_wait_ld(v);
-                tmem_wait_ld(w);
+                tmem_wait_ld16(v);
+                tmem_wait_ld16(w);
                 const float ih = ch[i], il = cl[i], sign = upper ? -1.f : 1.f;
                 const int last = upper ? i - 1 : i;
                 const float2 minus = make_float2(-1.f, -1.f);
@@ -366,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads_tc(const __grid_con
                 uint32_t v[16], w[16];
                 tmem_ld16(lo_ + kTmS + 16 * sub, v);
                 tmem_ld16(lo_ + kTmD + 16 * sub, w);
-                tmem_wait_ld(v);
-                tmem_wait_ld(w);
+                tmem_wait_ld16(v);
+                tmem_wait_ld16(w);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(dfree);
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads_tc(const __grid_con
             for (int j = 0; j < W; j += 16) {
                 uint32_t v[16];
                 tmem_ld16(lo_ + kTmG + W * sub + j, v);
-                tmem_wait_ld(v);
+                tmem_wait_ld16(v);
 #pragma unroll
                 for (int n = 0; n < 16; n += 8) {
                     const int col = W * sub + j + n;
