@@ -286,9 +286,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads_tc(const __grid_con
             {
                 const uint32_t at = swz(lt, lc);
                 const float g = eg[lt], kf = ek[lt];
-                *reinterpret_cast<uint4 *>(sm + Z::x1 + at) = scale8(g, *reinterpret_cast<const uint4 *>(st + Z::dy + at));
-                *reinterpret_cast<uint4 *>(sm + Z::x1 + kPanel + at) = scale8(-g, *reinterpret_cast<const uint4 *>(st + Z::r + at));
-                *reinterpret_cast<uint4 *>(sm + Z::x2 + at) = scale8(kf, *reinterpret_cast<const uint4 *>(st + Z::u + at));
+                const uint4 yv = *reinterpret_cast<const uint4 *>(st + Z::dy + at), rv = *reinterpret_cast<const uint4 *>(st + Z::r + at);
+                const uint4 uv = *reinterpret_cast<const uint4 *>(st + Z::u + at);
+                *reinterpret_cast<uint4 *>(sm + Z::x1 + at) = scale8(g, yv);
+                *reinterpret_cast<uint4 *>(sm + Z::x1 + kPanel + at) = scale8(-g, rv);
+                *reinterpret_cast<uint4 *>(sm + Z::x2 + at) = scale8(kf, uv);
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(xb);

@@ -690,7 +690,7 @@ __device__ __forceinline__ void chain_rev(const CUtensorMap &tm_k, const CUtenso
         // ------------------------------------------------------------- loads
         if (lane == 0) {
             const uint64_t keep = policy_evict_last(), stream = policy_evict_first();
-            int it = 0, wp = 0;  // uses of the stages; of W and P
+            int it = 0, pp = 0, wp = 0;  // uses of the stages; of P; of W
             bool ok = true;
             for (int j = 0; ok && j < share.n; ++j) {
                 const Seg sg = share.at(j);
@@ -712,21 +712,22 @@ __device__ __forceinline__ void chain_rev(const CUtensorMap &tm_k, const CUtenso
                         tma_load_4d_hint(sm + Z::q + k * Z::kBytes + pn * kPanel, &tm_q, &full[k], 64 * pn, grp, c * kC, b, keep);
                     }
                     ++it;
+                    // P as soon as the last chunk's Z is done (its products come first in a chunk), then W
                     if (wp > 0 && !(ok = wait_phase(pfree, (uint32_t)(wp - 1) & 1u, abort_flag, status))) break;
-                    if (wp > 0 && !(ok = wait_phase(wfree, (uint32_t)(wp - 1) & 1u, abort_flag, status))) break;
                     mbar_arrive_tx(pfull, HB * 2 * kTri);
-                    mbar_arrive_tx(wfull, HB * 2 * kTri);
-                    for (int e = 0; e < HB; ++e) {
+                    for (int e = 0; e < HB; ++e)
                         bulk_load(sm + Z::p + e * 2 * kTri, prep(e) + a.rows_at + 2 * kTri, 2 * kTri, pfull);
-                        bulk_load(sm + Z::w + e * 2 * kTri, prep(e) + a.rows_at, 2 * kTri, wfull);
-                    }
+                    ++pp;
+                    if (wp > 0 && !(ok = wait_phase(wfree, (uint32_t)(wp - 1) & 1u, abort_flag, status))) break;
+                    mbar_arrive_tx(wfull, HB * 2 * kTri);
+                    for (int e = 0; e < HB; ++e) bulk_load(sm + Z::w + e * 2 * kTri, prep(e) + a.rows_at, 2 * kTri, wfull);
                     ++wp;
                 }
             }
             drain_loads(full, it);
-            if (wp > 0) {
+            if (pp > 0) {
                 const unsigned long long w0 = now_ns();
-                while (!(mbar_try(pfull, (uint32_t)(wp - 1) & 1u) && mbar_try(wfull, (uint32_t)(wp - 1) & 1u)) &&
+                while (!(mbar_try(pfull, (uint32_t)(pp - 1) & 1u) && (wp == 0 || mbar_try(wfull, (uint32_t)(wp - 1) & 1u))) &&
                        now_ns() - w0 < kWaitNs) {
                 }
             }
@@ -815,18 +816,32 @@ __device__ __forceinline__ void chain_rev(const CUtensorMap &tm_k, const CUtenso
             const int k = it & 1;
             if (!wait_warp(&full[k], (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
             if (it > 0 && !wait_warp(rdyS, ((uint32_t)it & 1u) ^ 1u, abort_flag, status)) break;
-#pragma unroll 4
-            for (int v = 0; v < 16; ++v) {
-                const int i = v * 64 + (warp & 1) * 32 + lane, pn = i >> 9, t = (i >> 3) & 63;
-                const uint32_t at = swz(t, i & 7);
-                const uint4 y = *reinterpret_cast<const uint4 *>(sm + (pn ? Z::dy1 : Z::dy0) + k * kPanel + at);
-                const float g = scal_of(k, PAIR ? pn : 0)[t];
-                const uint32_t in[4] = {y.x, y.y, y.z, y.w};
-                uint32_t hi[4], lo[4];
+            // four vectors are read before the first is written: through one array, the compiler keeps the order
 #pragma unroll
-                for (int e = 0; e < 4; ++e) split2(g * bf16_lo(in[e]), g * bf16_hi(in[e]), hi[e], lo[e]);
-                *reinterpret_cast<uint4 *>(sm + Z::e + pn * kPanel + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(sm + Z::e + (2 + pn) * kPanel + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            for (int v0 = 0; v0 < 16; v0 += 4) {
+                uint4 y[4];
+                float g[4];
+                uint32_t at[4];
+                const int pn = v0 >> 3;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int i = (v0 & 7) * 64 + v * 64 + (warp & 1) * 32 + lane;
+                    at[v] = swz(i >> 3, i & 7);
+                    y[v] = *reinterpret_cast<const uint4 *>(sm + (pn ? Z::dy1 : Z::dy0) + k * kPanel + at[v]);
+                    g[v] = scal_of(k, PAIR ? pn : 0)[i >> 3];
+                }
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const uint32_t in[4] = {y[v].x, y[v].y, y[v].z, y[v].w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 m = mul2(make_float2(g[v], g[v]), make_float2(bf16_lo(in[e]), bf16_hi(in[e])));
+                        split2(m.x, m.y, hi[e], lo[e]);
+                    }
+                    *reinterpret_cast<uint4 *>(sm + Z::e + pn * kPanel + at[v]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(sm + Z::e + (2 + pn) * kPanel + at[v]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
             }
             fence_proxy_async();
             __syncwarp();
