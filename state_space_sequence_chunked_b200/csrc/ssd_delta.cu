@@ -22,6 +22,8 @@
 // usual sizes and lengths take the chunked tensor-core path in ssd_delta_mma.cu.
 //
 // k_delta_step is bound by HBM: 64 sequences of 32 heads of 128 x 128, 51 us, 82% of the measured 6.45 TB/s.
+#include <type_traits>
+
 #include "ssd_delta.cuh"
 
 namespace ssd {
@@ -343,164 +345,279 @@ __global__ void __launch_bounds__(kSeqThr, NJ < 8 ? 2 : 1)
 //   dC_i = exp(cum_i) dy_i S + sum_j dP_ij k_j,
 //   dB_i = sum_j dP_ji q_j + (dM_ij + dM_ji) k_j + exp(cum_end - cum_i) u_i D - exp(cum_i) r_i S,
 //   dbeta_i = z_i.err_i, and dg the reverse cumulative sum of the derivative with respect to cum.
-// A thread owns one column n for all tokens; dy, u and r stand transposed in shared memory, so that
-// four tokens' values come with one 16-byte broadcast.
+// The three products with S and D are register tiles: a warp holds TK tokens by all columns (a lane every 32nd) and
+// takes them from dy, u and r, transposed in shared memory, four tokens per 16-byte broadcast. Where two warps
+// share a tile, each takes a half of the state rows and then a half of the pairs' tokens j; they meet once, at the end.
+// Bound by the latency of its loads and by shared memory: 50 heads of 64 x 128, 5 x 305 fp32 tokens, 410 us (452 with
+// TK = 8 there, which leaves room for one CTA per SM); 48 heads of 243 x 34, 3602 tokens, 1376 us (a thread per column and
+// all tokens 1236 and 6919).
 constexpr int kTp = kSeg + 4;  // padded token stride of the transposed arrays (16-byte rows)
+// row stride of keys and queries: 4 modulo 32 floats, so that 8 rows' 16-byte vectors fall in different banks
+__host__ __device__ constexpr int grads_stride(int N) { return N <= 4 ? 4 : (N - 4 + 31) / 32 * 32 + 4; }
 
-template <typename T>
+template <int NJ>
+struct GradsTile {
+    static constexpr int TK = NJ >= 4 ? 4 : 8, groups = kSeg / TK, split = kWarps / groups;  // tokens; warps by tokens, by rows
+    static constexpr int U = NJ <= 2 ? 8 : 2;  // rows of S and D in flight
+};
+
+template <typename T, int NJ>
 __global__ void __launch_bounds__(kThr)
     k_delta_grads(const T *__restrict__ dy, const T *__restrict__ g, const T *__restrict__ beta, const T *__restrict__ Bm,
                   const T *__restrict__ Cm, const float *__restrict__ seg_states, const float *__restrict__ seg_cot,
                   const float *__restrict__ err, const float *__restrict__ zz, int64_t L, int H, int P, int G, int N,
                   float *__restrict__ dB_part, float *__restrict__ dC_part, T *__restrict__ dg, T *__restrict__ dbeta) {
+    using Z = GradsTile<NJ>;
+    constexpr int TK = Z::TK, PS = Z::split;
     extern __shared__ __align__(16) float sm[];
-    const int N1 = N | 1;
+    const int NP = grads_stride(N);
     float *dyT = sm;                      // [P][kTp]
     float *uT = dyT + P * kTp;            // [P][kTp]
     float *rT = uT + P * kTp;             // [P][kTp]
-    float *ks = rT + P * kTp;             // [kSeg][N1]
-    float *qs = ks + kSeg * N1;           // [kSeg][N1]
-    float *wP = qs + kSeg * N1;           // [kSeg][33]
-    float *wM = wP + kSeg * 33;           // [kSeg][33], dM + dM^T
-    float *pair = wM + kSeg * 33;         // [kSeg][33]
-    float *dots = pair + kSeg * 33;       // [kWarps][kSeg]
-    float *tail = dots + kWarps * kSeg;   // [kWarps]
-    float *eg = tail + kWarps;            // [kSeg]
-    float *ek = eg + kSeg;                // [kSeg]
-    float *bt = ek + kSeg;                // [kSeg]
-    float *zd = bt + kSeg;                // [kSeg]
+    float *ks = rT + P * kTp;             // [kSeg][NP]
+    float *qs = ks + kSeg * NP;           // [kSeg][NP]
+    float *wPt = qs + kSeg * NP;          // [j][kTp]: dP_tj
+    float *wP = wPt + kSeg * kTp;         // [j][kTp]: dP_jt
+    float *wM = wP + kSeg * kTp;          // [j][kTp]: dM_tj + dM_jt
+    float *pair = wM + kSeg * kTp;        // [kSeg][33]
+    __shared__ float dots[PS][kSeg], ends[kWarps], eg[kSeg], ek[kSeg], bt[kSeg], zd[kSeg];
     __shared__ double cum[kSeg];
     const int64_t c = blockIdx.x, ns = gridDim.x, t0 = c * kSeg;
     const int h = blockIdx.y, b = blockIdx.z, grp = h / (H / G);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nt = L - t0 < kSeg ? (int)(L - t0) : kSeg;
-    if (tid == 0) {
-        double acc = 0.0;
-        for (int t = 0; t < kSeg; ++t) {
-            if (t < nt) acc += clamp_log_decay(to_f32(g[((int64_t)b * L + t0 + t) * H + h]));
-            cum[t] = acc;
+    if (warp == 0) {  // cumulated log decay, a token per lane
+        double sum = lane < nt ? clamp_log_decay(to_f32(g[((int64_t)b * L + t0 + lane) * H + h])) : 0.0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double up = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += up;
         }
+        const double end = __shfl_sync(0xffffffffu, sum, 31);
+        cum[lane] = sum;
+        eg[lane] = expf((float)sum);
+        ek[lane] = expf((float)(end - sum));
+        bt[lane] = lane < nt ? to_f32(beta[((int64_t)b * L + t0 + lane) * H + h]) : 0.f;
     }
-    if (tid < kSeg) bt[tid] = tid < nt ? to_f32(beta[((int64_t)b * L + t0 + tid) * H + h]) : 0.f;
-    for (int i = tid; i < kSeg * N; i += kThr) {
-        const int t = i / N, n = i % N;
-        const int64_t at = (((int64_t)b * L + t0 + t) * G + grp) * N + n;
-        ks[t * N1 + n] = t < nt ? to_f32(Bm[at]) : 0.f;
-        qs[t * N1 + n] = t < nt ? to_f32(Cm[at]) : 0.f;
+    constexpr int kMine = kSeg / kWarps;  // tokens warp, warp + 8, ...: a batch of loads covers all of them
+    for (int n = lane; n < NP; n += 32) {
+        float kv[kMine], qv[kMine];
+#pragma unroll
+        for (int e = 0; e < kMine; ++e) {
+            const int t = warp + kWarps * e;
+            const int64_t at = (((int64_t)b * L + t0 + t) * G + grp) * N + n;
+            kv[e] = t < nt && n < N ? to_f32(Bm[at]) : 0.f;
+            qv[e] = t < nt && n < N ? to_f32(Cm[at]) : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < kMine; ++e) ks[(warp + kWarps * e) * NP + n] = kv[e], qs[(warp + kWarps * e) * NP + n] = qv[e];
     }
     __syncthreads();
-    if (tid < kSeg) {
-        eg[tid] = expf((float)cum[tid]);
-        ek[tid] = expf((float)(cum[kSeg - 1] - cum[tid]));
-    }
-    for (int t = warp; t < kSeg; t += kWarps) {  // a warp per token: also z.err
-        float d = 0.f;
+    {  // also z.err
+        float d[kMine] = {};
+#pragma unroll 2
         for (int p = lane; p < P; p += 32) {
-            const int64_t at = (((int64_t)b * L + t0 + t) * H + h) * P + p;
-            const float ev = t < nt ? err[at] : 0.f, zv = t < nt ? zz[at] : 0.f;
-            dyT[p * kTp + t] = t < nt ? to_f32(dy[at]) : 0.f;
-            uT[p * kTp + t] = bt[t] * ev;
-            rT[p * kTp + t] = bt[t] * zv;
-            d = fmaf(zv, ev, d);
+            float ev[kMine], zv[kMine], yv[kMine];
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) {
+                const int t = warp + kWarps * e;
+                const int64_t at = (((int64_t)b * L + t0 + t) * H + h) * P + p;
+                ev[e] = t < nt ? err[at] : 0.f, zv[e] = t < nt ? zz[at] : 0.f, yv[e] = t < nt ? to_f32(dy[at]) : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) {
+                const int t = warp + kWarps * e;
+                dyT[p * kTp + t] = yv[e];
+                uT[p * kTp + t] = bt[t] * ev[e];
+                rT[p * kTp + t] = bt[t] * zv[e];
+                d[e] = fmaf(zv[e], ev[e], d[e]);
+            }
         }
-        d = warp_sum(d);
-        if (lane == 0) zd[t] = d;
+#pragma unroll
+        for (int e = 0; e < kMine; ++e) {
+            d[e] = warp_sum(d[e]);
+            if (lane == 0) zd[warp + kWarps * e] = d[e];
+        }
     }
     __syncthreads();
     if (tid < nt) store_as(dbeta + ((int64_t)b * L + t0 + tid) * H + h, zd[tid]);
-    for (int i = warp; i < kSeg; i += kWarps) {
-        const int j = lane;
-        float dp = 0.f, dm = 0.f, qk = 0.f, kk = 0.f;
-        if (j <= i) {
-            for (int p = 0; p < P; ++p) {
-                dp = fmaf(dyT[p * kTp + i], uT[p * kTp + j], dp);
-                dm = fmaf(rT[p * kTp + i], uT[p * kTp + j], dm);
-            }
-            for (int n = 0; n < N; ++n) {
-                qk = fmaf(qs[i * N1 + n], ks[j * N1 + n], qk);
-                kk = fmaf(ks[i * N1 + n], ks[j * N1 + n], kk);
-            }
-            const float e = expf((float)(cum[i] - cum[j]));
-            dp *= e;
-            dm = j < i ? -dm * e : 0.f;
+    {  // pairs: tokens i = 4 warp .. + 3 by j = lane
+        float dp[4] = {0.f, 0.f, 0.f, 0.f}, dm[4] = {0.f, 0.f, 0.f, 0.f}, qk[4] = {0.f, 0.f, 0.f, 0.f}, kk[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int p = 0; p < P; ++p) {
+            const float4 y = *reinterpret_cast<const float4 *>(dyT + p * kTp + 4 * warp);
+            const float4 r = *reinterpret_cast<const float4 *>(rT + p * kTp + 4 * warp);
+            const float u = uT[p * kTp + lane];
+            dp[0] = fmaf(y.x, u, dp[0]), dp[1] = fmaf(y.y, u, dp[1]), dp[2] = fmaf(y.z, u, dp[2]), dp[3] = fmaf(y.w, u, dp[3]);
+            dm[0] = fmaf(r.x, u, dm[0]), dm[1] = fmaf(r.y, u, dm[1]), dm[2] = fmaf(r.z, u, dm[2]), dm[3] = fmaf(r.w, u, dm[3]);
         }
-        wP[i * 33 + j] = j <= i ? dp : 0.f;
-        pair[i * 33 + j] = j <= i ? dp * qk + dm * kk : 0.f;
-        if (j < i) wM[i * 33 + j] = wM[j * 33 + i] = dm;
-        if (j == i) wM[i * 33 + i] = 0.f;
+        for (int n = 0; n < N; n += 4) {  // (zeros past N)
+            const float4 kj = *reinterpret_cast<const float4 *>(ks + lane * NP + n);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 qi = *reinterpret_cast<const float4 *>(qs + (4 * warp + e) * NP + n);
+                const float4 ki = *reinterpret_cast<const float4 *>(ks + (4 * warp + e) * NP + n);
+                qk[e] = fmaf(qi.x, kj.x, fmaf(qi.y, kj.y, fmaf(qi.z, kj.z, fmaf(qi.w, kj.w, qk[e]))));
+                kk[e] = fmaf(ki.x, kj.x, fmaf(ki.y, kj.y, fmaf(ki.z, kj.z, fmaf(ki.w, kj.w, kk[e]))));
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = 4 * warp + e, j = lane;
+            const float ex = j <= i ? expf((float)(cum[i] - cum[j])) : 0.f;
+            const float pv = j <= i ? dp[e] * ex : 0.f, mv = j < i ? -dm[e] * ex : 0.f;
+            wPt[j * kTp + i] = wP[i * kTp + j] = pv;
+            pair[i * 33 + j] = pv * qk[e] + mv * kk[e];
+            if (j < i) wM[i * kTp + j] = wM[j * kTp + i] = mv;
+            if (j == i) wM[i * kTp + i] = 0.f;
+        }
     }
     const float *S = seg_states + (((int64_t)b * H + h) * ns + c) * P * N;
     const float *D = seg_cot + (((int64_t)b * H + h) * ns + c) * P * N;
-    const int n = tid;
-    float fq[kSeg], fk[kSeg], fu[kSeg], ds = 0.f;
+    const int tg = warp % Z::groups, ps = warp / Z::groups, tk0 = TK * tg;  // this warp's tokens; its share of the rows
+    float2 fq[TK / 2][NJ], fk[TK / 2][NJ], fu[TK / 2][NJ];
 #pragma unroll
-    for (int t = 0; t < kSeg; ++t) fq[t] = fk[t] = fu[t] = 0.f;
-    if (n < N) {
-        for (int p = 0; p < P; ++p) {
-            const float sv = S[(int64_t)p * N + n], dv = D[(int64_t)p * N + n];
-            ds = fmaf(sv, dv, ds);
+    for (int t = 0; t < TK / 2; ++t)
 #pragma unroll
-            for (int t = 0; t < kSeg; t += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(dyT + p * kTp + t);
-                const float4 r = *reinterpret_cast<const float4 *>(rT + p * kTp + t);
-                const float4 u = *reinterpret_cast<const float4 *>(uT + p * kTp + t);
-                fq[t] = fmaf(a.x, sv, fq[t]), fq[t + 1] = fmaf(a.y, sv, fq[t + 1]);
-                fq[t + 2] = fmaf(a.z, sv, fq[t + 2]), fq[t + 3] = fmaf(a.w, sv, fq[t + 3]);
-                fk[t] = fmaf(r.x, sv, fk[t]), fk[t + 1] = fmaf(r.y, sv, fk[t + 1]);
-                fk[t + 2] = fmaf(r.z, sv, fk[t + 2]), fk[t + 3] = fmaf(r.w, sv, fk[t + 3]);
-                fu[t] = fmaf(u.x, dv, fu[t]), fu[t + 1] = fmaf(u.y, dv, fu[t + 1]);
-                fu[t + 2] = fmaf(u.z, dv, fu[t + 2]), fu[t + 3] = fmaf(u.w, dv, fu[t + 3]);
+        for (int j = 0; j < NJ; ++j) fq[t][j] = fk[t][j] = fu[t][j] = make_float2(0.f, 0.f);
+    float ds = 0.f;
+    const int p_end = P * (ps + 1) / PS;
+    struct Rows {
+        float s[Z::U][NJ], d[Z::U][NJ];
+    };
+    const auto load = [&](Rows &to, int p0) {
+#pragma unroll
+        for (int i = 0; i < Z::U; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const int n = lane + 32 * j;
+                const bool in = n < N && p0 + i < p_end;
+                const int64_t at = in ? (int64_t)(p0 + i) * N + n : 0;
+                to.s[i][j] = in ? S[at] : 0.f;
+                to.d[i][j] = in ? D[at] : 0.f;
             }
+    };
+    Rows next;
+    load(next, P * ps / PS);
+    for (int p0 = P * ps / PS; p0 < p_end; p0 += Z::U) {  // the next rows are on their way
+        const Rows now = next;
+        load(next, p0 + Z::U);
+#pragma unroll
+        for (int i = 0; i < Z::U; ++i) {
+            const int p = p0 + i;
+            if (p >= p_end) break;
+#pragma unroll
+            for (int t = 0; t < TK; t += 4) {
+                const float4 y = *reinterpret_cast<const float4 *>(dyT + p * kTp + tk0 + t);
+                const float4 r = *reinterpret_cast<const float4 *>(rT + p * kTp + tk0 + t);
+                const float4 u = *reinterpret_cast<const float4 *>(uT + p * kTp + tk0 + t);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    const float2 sv = both(now.s[i][j]), dv = both(now.d[i][j]);
+                    fq[t / 2][j] = fma2(low2(y), sv, fq[t / 2][j]), fq[t / 2 + 1][j] = fma2(high2(y), sv, fq[t / 2 + 1][j]);
+                    fk[t / 2][j] = fma2(low2(r), sv, fk[t / 2][j]), fk[t / 2 + 1][j] = fma2(high2(r), sv, fk[t / 2 + 1][j]);
+                    fu[t / 2][j] = fma2(low2(u), dv, fu[t / 2][j]), fu[t / 2 + 1][j] = fma2(high2(u), dv, fu[t / 2 + 1][j]);
+                }
+            }
+            if (tg == 0)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) ds = fmaf(now.s[i][j], now.d[i][j], ds);
         }
     }
-    // the derivative with respect to cum: per token in `dots`, the end's share in `tail`
-    float end = expf((float)cum[kSeg - 1]) * ds;
+    // the derivative with respect to cum, as far as these rows go: per token, and the end's share
+    float tok[TK], end = eg[kSeg - 1] * ds;
 #pragma unroll
-    for (int t = 0; t < kSeg; ++t) {
-        const float kn = n < N ? ks[t * N1 + n] : 0.f, qn = n < N ? qs[t * N1 + n] : 0.f;
-        fq[t] *= eg[t];
-        fu[t] *= ek[t];
-        const float U = fu[t] * kn;
-        end += U;
-        const float d = warp_sum(fq[t] * qn - eg[t] * fk[t] * kn - U);
-        if (lane == 0) dots[warp * kSeg + t] = d;
-        fk[t] = fu[t] - eg[t] * fk[t];
+    for (int t = 0; t < TK; t += 2) {
+        float d[2] = {0.f, 0.f};
+        const float e0 = eg[tk0 + t], e1 = eg[tk0 + t + 1], k0 = ek[tk0 + t], k1 = ek[tk0 + t + 1];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int n = lane + 32 * j;
+            const bool in = n < N;
+            const float2 q2 = make_float2(in ? qs[(tk0 + t) * NP + n] : 0.f, in ? qs[(tk0 + t + 1) * NP + n] : 0.f);
+            const float2 n2 = make_float2(in ? ks[(tk0 + t) * NP + n] : 0.f, in ? ks[(tk0 + t + 1) * NP + n] : 0.f);
+            float2 &q = fq[t / 2][j], &k = fk[t / 2][j], &u = fu[t / 2][j];
+            q.x *= e0, q.y *= e1, k.x *= e0, k.y *= e1, u.x *= k0, u.y *= k1;
+            const float U0 = u.x * n2.x, U1 = u.y * n2.y;
+            end += U0 + U1;
+            d[0] += q.x * q2.x - k.x * n2.x - U0;
+            d[1] += q.y * q2.y - k.y * n2.y - U1;
+            k.x = u.x - k.x, k.y = u.y - k.y;
+        }
+        tok[t] = d[0], tok[t + 1] = d[1];
+    }
+#pragma unroll
+    for (int t = 0; t < TK; ++t) {
+        tok[t] = warp_sum(tok[t]);
+        if (lane == 0) dots[ps][tk0 + t] = tok[t];
     }
     end = warp_sum(end);
-    if (lane == 0) tail[warp] = end;
-    __syncthreads();
-    if (n < N) {
-        for (int j = 0; j < kSeg; ++j) {
-            const float kn = ks[j * N1 + n], qn = qs[j * N1 + n];
+    if (lane == 0) ends[warp] = end;
+    __syncthreads();  // the pairs' weights are there
+    // dQ += dP K, dK += dP^T Q + (dM + dM^T) K: this warp's share of the tokens j
+    for (int i = kSeg * ps / PS; i < kSeg * (ps + 1) / PS; ++i) {
+        float kn[NJ], qn[NJ];
 #pragma unroll
-            for (int t = 0; t < kSeg; ++t) {
-                fq[t] = fmaf(wP[t * 33 + j], kn, fq[t]);
-                fk[t] = fmaf(wP[j * 33 + t], qn, fk[t]);
-                fk[t] = fmaf(wM[j * 33 + t], kn, fk[t]);
-            }
+        for (int j = 0; j < NJ; ++j) {
+            const int n = lane + 32 * j;
+            kn[j] = n < N ? ks[i * NP + n] : 0.f;
+            qn[j] = n < N ? qs[i * NP + n] : 0.f;
         }
 #pragma unroll
-        for (int t = 0; t < kSeg; ++t) {
-            if (t < nt) {
-                const int64_t at = (((int64_t)b * L + t0 + t) * H + h) * N + n;
-                dC_part[at] = fq[t];
-                dB_part[at] = fk[t];
+        for (int t = 0; t < TK; t += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(wPt + i * kTp + tk0 + t);
+            const float4 w = *reinterpret_cast<const float4 *>(wP + i * kTp + tk0 + t);
+            const float4 m = *reinterpret_cast<const float4 *>(wM + i * kTp + tk0 + t);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                fq[t / 2][j] = fma2(low2(a), both(kn[j]), fq[t / 2][j]), fq[t / 2 + 1][j] = fma2(high2(a), both(kn[j]), fq[t / 2 + 1][j]);
+                fk[t / 2][j] = fma2(low2(w), both(qn[j]), fk[t / 2][j]), fk[t / 2 + 1][j] = fma2(high2(w), both(qn[j]), fk[t / 2 + 1][j]);
+                fk[t / 2][j] = fma2(low2(m), both(kn[j]), fk[t / 2][j]), fk[t / 2 + 1][j] = fma2(high2(m), both(kn[j]), fk[t / 2 + 1][j]);
             }
         }
     }
     if (warp == 0) {
-        const int i = lane;
         float d = 0.f;
-        for (int w = 0; w < kWarps; ++w) d += dots[w * kSeg + i];
-        for (int j = 0; j < kSeg; ++j) d += pair[i * 33 + j] - pair[j * 33 + i];
-        if (i == kSeg - 1)
-            for (int w = 0; w < kWarps; ++w) d += tail[w];
+        for (int w = 0; w < PS; ++w) d += dots[w][lane];
+        for (int j = 0; j < kSeg; ++j) d += pair[lane * 33 + j] - pair[j * 33 + lane];
+        if (lane == kSeg - 1)
+            for (int w = 0; w < kWarps; ++w) d += ends[w];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {  // sum over the tokens from i to the end
+        for (int o = 1; o < 32; o <<= 1) {  // sum over the tokens from this one to the end
             const float up = __shfl_down_sync(0xffffffffu, d, o);
-            if (i + o < 32) d += up;
+            if (lane + o < 32) d += up;
         }
-        if (i < nt) store_as(dg + ((int64_t)b * L + t0 + i) * H + h, d);
+        if (lane < nt) store_as(dg + ((int64_t)b * L + t0 + lane) * H + h, d);
+    }
+    if constexpr (PS > 1) {  // the other half's sums, through shared memory (all of which is free now)
+        __syncthreads();
+        float4 *buf = reinterpret_cast<float4 *>(sm) + tg * (TK / 2 * NJ * 32) + lane;
+        if (ps == 1)
+#pragma unroll
+            for (int t = 0; t < TK / 2; ++t)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) buf[(t * NJ + j) * 32] = make_float4(fq[t][j].x, fq[t][j].y, fk[t][j].x, fk[t][j].y);
+        __syncthreads();
+        if (ps == 1) return;
+#pragma unroll
+        for (int t = 0; t < TK / 2; ++t)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const float4 o = buf[(t * NJ + j) * 32];
+                fq[t][j].x += o.x, fq[t][j].y += o.y, fk[t][j].x += o.z, fk[t][j].y += o.w;
+            }
+    }
+#pragma unroll
+    for (int t = 0; t < TK; ++t) {
+        if (tk0 + t >= nt) continue;
+        const int64_t at = (((int64_t)b * L + t0 + tk0 + t) * H + h) * N;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int n = lane + 32 * j;
+            if (n >= N) continue;
+            dC_part[at + n] = t & 1 ? fq[t / 2][j].y : fq[t / 2][j].x;
+            dB_part[at + n] = t & 1 ? fk[t / 2][j].y : fk[t / 2][j].x;
+        }
     }
 }
 
@@ -631,8 +748,26 @@ cudaError_t seq_bwd_launch(const DeltaProblem &p, const DeltaGrads &gr, float *z
     return cudaGetLastError();
 }
 
+template <int NJ>
 size_t grads_smem(const DeltaProblem &p) {
-    return sizeof(float) * (size_t)(3 * p.P * kTp + 2 * kSeg * (p.N | 1) + 3 * kSeg * 33 + kWarps * kSeg + kWarps + 4 * kSeg);
+    const size_t tiles = 3 * p.P * kTp + 2 * kSeg * grads_stride((int)p.N) + 3 * kSeg * kTp + kSeg * 33;
+    const size_t joined = GradsTile<NJ>::split > 1 ? (size_t)kSeg * NJ * 32 * 2 : 0;  // dQ and dK of half of the warps
+    return sizeof(float) * (tiles > joined ? tiles : joined);
+}
+
+template <typename T, int NJ>
+cudaError_t grads_launch(const DeltaProblem &p, const DeltaGrads &gr, const float *states, const float *cot, const float *err,
+                         const float *z, float *dB, float *dC, cudaStream_t s) {
+    const size_t smem = grads_smem<NJ>(p);
+    const cudaError_t e = cudaFuncSetAttribute(k_delta_grads<T, NJ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e) return e;
+    dim3 grid((unsigned)((p.L + kSeg - 1) / kSeg), (unsigned)p.H, (unsigned)p.B);
+    k_delta_grads<T, NJ><<<grid, kThr, smem, s>>>(static_cast<const T *>(gr.dy), static_cast<const T *>(p.g),
+                                                  static_cast<const T *>(p.beta), static_cast<const T *>(p.Bm),
+                                                  static_cast<const T *>(p.Cm), states, cot, err, z, p.L, (int)p.H, (int)p.P,
+                                                  (int)p.G, (int)p.N, dB, dC, static_cast<T *>(gr.dg),
+                                                  static_cast<T *>(gr.dbeta));
+    return cudaGetLastError();
 }
 
 // Workspace of the general backward, as byte offsets.
@@ -671,20 +806,16 @@ cudaError_t bwd_typed(const DeltaProblem &p, const DeltaGrads &gr, void *ws, cud
     f.h_final = nullptr;
     cudaError_t e = seq_typed<T>(f, states, err, s);
     if (e) return e;
-    if (p.N <= 32) e = seq_bwd_launch<T, 1>(p, gr, z, cot, s);
-    else if (p.N <= 64) e = seq_bwd_launch<T, 2>(p, gr, z, cot, s);
-    else if (p.N <= 128) e = seq_bwd_launch<T, 4>(p, gr, z, cot, s);
-    else e = seq_bwd_launch<T, 8>(p, gr, z, cot, s);
+    const auto both_of = [&](auto nj) {
+        constexpr int NJ = decltype(nj)::value;
+        const cudaError_t f = seq_bwd_launch<T, NJ>(p, gr, z, cot, s);
+        return f ? f : grads_launch<T, NJ>(p, gr, states, cot, err, z, dB, dC, s);
+    };
+    if (p.N <= 32) e = both_of(std::integral_constant<int, 1>());
+    else if (p.N <= 64) e = both_of(std::integral_constant<int, 2>());
+    else if (p.N <= 128) e = both_of(std::integral_constant<int, 4>());
+    else e = both_of(std::integral_constant<int, 8>());
     if (e) return e;
-    const size_t smem = grads_smem(p);
-    if ((e = cudaFuncSetAttribute(k_delta_grads<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))) return e;
-    dim3 grid((unsigned)((p.L + kSeg - 1) / kSeg), (unsigned)p.H, (unsigned)p.B);
-    k_delta_grads<T><<<grid, kThr, smem, s>>>(static_cast<const T *>(gr.dy), static_cast<const T *>(p.g),
-                                              static_cast<const T *>(p.beta), static_cast<const T *>(p.Bm),
-                                              static_cast<const T *>(p.Cm), states, cot, err, z, p.L, (int)p.H, (int)p.P,
-                                              (int)p.G, (int)p.N, dB, dC, static_cast<T *>(gr.dg),
-                                              static_cast<T *>(gr.dbeta));
-    if ((e = cudaGetLastError())) return e;
     return delta_group_sum_launch(p, dB, dC, gr.dBm, gr.dCm, s);
 }
 
