@@ -399,9 +399,10 @@ ssd_status_t ssd_gated_rmsnorm(int64_t rows, int64_t dim, int64_t ngroups, ssd_d
  *   y        [B, L, H, P]   dtype          output
  *   h_final  [B, H, P, N]   fp32 or NULL   state after the last token
  * Outputs may not overlap inputs. seqlen == 0 writes only h_final; batch == 0 does nothing.
- * ssd_delta_fwd_plan: SSD_PATH_TCGEN05 (bf16 with dstate <= 128, dstate and headdim multiples of 8, and
- * 128 tokens, or fewer with many heads: chunks of 64 tokens on tensor cores, what enters the state kept
- * to 2^-16) or SSD_PATH_SIMT (everything else: four tokens at a time in fp32). On SSD_PATH_TCGEN05
+ * ssd_delta_fwd_plan: SSD_PATH_TCGEN05 (bf16 with headdim >= 8, 8 <= dstate <= 128 and 128 tokens, or
+ * fewer with many heads: chunks of 64 tokens on tensor cores, what enters the state kept to 2^-16; dstate or headdim
+ * that is no multiple of 8 from 256 tokens on, on padded copies in the workspace) or SSD_PATH_SIMT
+ * (everything else: four tokens at a time in fp32). On SSD_PATH_TCGEN05
  * the warps of a CTA wait on one another through bounded waits, as in ssd_fwd; ssd_delta_status, called
  * with the shape and workspace of an ssd_delta_fwd or ssd_delta_bwd (NULL if its plan has none),
  * synchronizes `stream` and returns SSD_ERR_TIMEOUT if one ran out (outputs are then incomplete),

@@ -402,7 +402,7 @@ ssd_plan_t delta_plan_of(const ssd::DeltaProblem &p, bool backward) {
         out.path = SSD_PATH_NONE;
     } else if (delta_mma_supported(p, backward)) {
         out.path = SSD_PATH_TCGEN05;
-        out.kernels = backward ? delta_mma_bwd_kernels(p) : 2;
+        out.kernels = backward ? delta_mma_bwd_kernels(p) : delta_mma_fwd_kernels(p);
         out.workspace_bytes = backward ? delta_mma_bwd_workspace_bytes(p) : delta_mma_fwd_workspace_bytes(p);
     } else {
         out.path = SSD_PATH_SIMT;

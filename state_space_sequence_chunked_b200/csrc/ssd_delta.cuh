@@ -36,10 +36,11 @@ cudaError_t delta_seq_bwd(const DeltaProblem &p, const DeltaGrads &g, void *ws, 
 // dBm, dCm [B, L, G, N] from per-head fp32 parts [B, L, H, N], added in head order
 cudaError_t delta_group_sum_launch(const DeltaProblem &p, const float *dB_part, const float *dC_part, void *dBm, void *dCm,
                                    cudaStream_t s);
-// ---- chunked tensor-core path (bf16, dstate <= 128, dstate and headdim multiples of 8) ----
+// ---- chunked tensor-core path (bf16, dstate <= 128) ----
 constexpr int kDeltaChunk = 64;
 bool delta_mma_supported(const DeltaProblem &p, bool backward);
 size_t delta_mma_fwd_workspace_bytes(const DeltaProblem &p);
+int delta_mma_fwd_kernels(const DeltaProblem &p);
 cudaError_t delta_mma_fwd(const DeltaProblem &p, void *ws, cudaStream_t s);
 size_t delta_mma_bwd_workspace_bytes(const DeltaProblem &p);
 int delta_mma_bwd_kernels(const DeltaProblem &p);

@@ -1,5 +1,5 @@
-// The gated delta rule on tensor cores, chunked: bf16 inputs, dstate <= 128 and headdim in multiples
-// of 8. With cum the cumulated log decay in a chunk of 64 tokens, E_ij = exp(cum_i - cum_j),
+// The gated delta rule on tensor cores, chunked: bf16 inputs, dstate <= 128 (sizes that are no multiples of 8 on
+// padded copies, at the end). With cum the cumulated log decay in a chunk of 64 tokens, E_ij = exp(cum_i - cum_j),
 // M = tril(K K^T o E, -1), and W the strictly lower solution of W = -M (I + diag(beta) W):
 //     R = X - exp(cum) K S^T,   err = R + W (beta R),   u = beta err,
 //     Y = exp(cum) Q S^T + tril(Q K^T o E) u,   S <- exp(cum_end) S + u^T (exp(cum_end - cum) K)
@@ -492,34 +492,168 @@ cudaError_t bwd_launch(const DeltaProblem &p, const DeltaGrads &gr, char *ws, cu
     return delta_group_sum_launch(q, dB, dC, gr.dBm, gr.dCm, s);
 }
 
+// ---------------------------------------------------------------------------------------------
+// TMA takes rows of 16-byte multiples. Other headdims and dstates run on copies with zero rows and columns added
+// up to the next multiple of 8, which leave the rest as it is; the outputs are copied back. Backward pass of 48 heads of
+// 243 x 34, 3602 tokens: 72 + 52 us of copies (an element per lane: 128 + 118) in 630, where the general path takes 4470.
+struct Repack {
+    const void *src;
+    void *dst;                   // [outer][rows_out][out] from [outer][rows_in][in]
+    int64_t outer;
+    int rows_in, rows_out, in, out;
+    int bytes;  // of an element
+};
+struct Repacks {
+    Repack r[6];
+    int n = 0;
+    void add(const void *src, void *dst, int64_t outer, int64_t rows_in, int64_t rows_out, int64_t in, int64_t out, int bytes) {
+        if (src && dst) r[n++] = Repack{src, dst, outer, (int)rows_in, (int)rows_out, (int)in, (int)out, bytes};
+    }
+};
+// grid.y: which copy; a warp per row of the destination
+template <typename E>
+__device__ __forceinline__ void repack_rows(const Repack &c) {
+    const E *src = static_cast<const E *>(c.src);
+    E *dst = static_cast<E *>(c.dst);
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = c.outer * c.rows_out;
+    for (int64_t r = (int64_t)blockIdx.x * (kThr / 32) + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * (kThr / 32)) {
+        const int64_t o = c.rows_out == 1 ? r : r / c.rows_out;
+        const int i = (int)(r - o * c.rows_out), in = i < c.rows_in ? c.in : 0;
+        const E *from = src + (o * c.rows_in + i) * c.in;
+        E *to = dst + r * c.out;
+        for (int j0 = lane; j0 < c.out; j0 += 128) {  // four loads, then four stores
+            E v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = j0 + 32 * e < in ? from[j0 + 32 * e] : E(0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (j0 + 32 * e < c.out) to[j0 + 32 * e] = v[e];
+        }
+    }
+}
+__global__ void __launch_bounds__(kThr) k_delta_repack(const __grid_constant__ Repacks c) {
+    const Repack &r = c.r[blockIdx.y];
+    if (r.bytes == 2) repack_rows<uint16_t>(r);
+    else repack_rows<float>(r);
+}
+cudaError_t repack(const Repacks &c, cudaStream_t s) {
+    k_delta_repack<<<dim3(148 * 8, (unsigned)c.n), kThr, 0, s>>>(c);
+    return cudaGetLastError();
+}
+
+bool whole(const DeltaProblem &p) { return p.P % 8 == 0 && p.N % 8 == 0; }
+DeltaProblem padded(const DeltaProblem &p) {
+    DeltaProblem q = p;
+    q.P = (p.P + 7) / 8 * 8, q.N = (p.N + 7) / 8 * 8;
+    return q;
+}
+// Byte offsets of the copies behind the workspace of the padded problem: headdim rows (x, then y, or dy and dx),
+// dstate rows (B, C, and their gradients), states.
+struct Copies {
+    size_t rows, cols, states, row, col, state, total;
+};
+Copies copies_of(const DeltaProblem &q, size_t at, bool backward) {
+    Copies c{};
+    c.row = align_up((size_t)(q.B * q.L * q.H * q.P) * 2, kWsAlign);
+    c.col = align_up((size_t)(q.B * q.L * q.G * q.N) * 2, kWsAlign);
+    c.state = align_up((size_t)(q.B * q.H * q.P * q.N) * 4, kWsAlign);
+    c.rows = align_up(at, kWsAlign);
+    c.cols = c.rows + (backward ? 3 : 2) * c.row;
+    c.states = c.cols + (backward ? 4 : 2) * c.col;
+    c.total = c.states + (backward ? 3 : 2) * c.state;
+    return c;
+}
+
+size_t fwd_bytes(const DeltaProblem &p) {
+    return head_bytes(p, false) + align_up(delta_tc_hand_bytes(p, false), kWsAlign) +
+           (size_t)(p.B * p.H) * (size_t)((p.L + kC - 1) / kC) * Prep<false>::bytes;
+}
+cudaError_t fwd_of(const DeltaProblem &p, char *ws, cudaStream_t s) {
+    return p.N <= 64 ? fwd_launch<64>(p, ws, s) : fwd_launch<128>(p, ws, s);
+}
+cudaError_t bwd_of(const DeltaProblem &p, const DeltaGrads &g, char *ws, cudaStream_t s) {
+    return p.N <= 64 ? bwd_launch<64>(p, g, ws, s) : bwd_launch<128>(p, g, ws, s);
+}
+
 }  // namespace
 
 // The sequential kernel takes as long as its token chain (0.2 us a token and CTA; n CTAs of 16 rows), this
 // path at least two launches and a chunk of 64: 24 bf16 heads of 64 x 128, one sequence (n = 96), L = 96: 25.7 against
 // 30.7 us here, 192: 43.0 against 33.8; four (n = 384), 24: 22.5 against 28.7, 48: 33.0 against 28.7; eight,
-// 16: 25.9 against 28.6, 24: 36.1 against 28.6; 32 sequences of 80 heads, 2: 143 against 127. The backward pass gains
-// at every length (8 tokens of 24 heads: 80 against 54 us).
+// 16: 25.9 against 28.6, 24: 36.1 against 28.6; 32 sequences of 80 heads, 2: 143 against 127. Copies of odd sizes cost two
+// launches more. The backward pass gains at every length (8 tokens of 24 heads: 80 against 54 us).
 bool delta_mma_supported(const DeltaProblem &p, bool backward) {
-    const int64_t per_sm = (p.B * p.H * ((p.P + 15) / 16) + 147) / 148;
-    if (!backward && p.L < 128 && p.L * per_sm < 128) return false;
-    return p.dtype == SSD_BF16 && p.N <= 128 && p.N % 8 == 0 && p.P % 8 == 0 && p.L < (1ll << 31) &&
-           p.B * p.H * ((p.L + kC - 1) / kC) < (1ll << 31);
+    const int64_t per_sm = (p.B * p.H * ((p.P + 15) / 16) + 147) / 148, least = whole(p) ? 128 : 256;
+    if (!backward && p.L < least && p.L * per_sm < least) return false;
+    // Below 8 rows or columns a padded tile is mostly zeros, and an output of few numbers can be small against the terms
+    // that cancel in it, which are kept to 2^-17: fp32 there.
+    if (p.P < 8 || p.N < 8) return false;
+    return p.dtype == SSD_BF16 && p.N <= 128 && p.L < (1ll << 31) && p.B * p.H * ((p.L + kC - 1) / kC) < (1ll << 31);
 }
 
 size_t delta_mma_fwd_workspace_bytes(const DeltaProblem &p) {
-    return head_bytes(p, false) + align_up(delta_tc_hand_bytes(p, false), kWsAlign) +
-           (size_t)(p.B * p.H) * (size_t)((p.L + kC - 1) / kC) * Prep<false>::bytes;
+    if (whole(p)) return fwd_bytes(p);
+    const DeltaProblem q = padded(p);
+    return copies_of(q, fwd_bytes(q), false).total;
 }
+int delta_mma_fwd_kernels(const DeltaProblem &p) { return whole(p) ? 2 : 4; }
 
 cudaError_t delta_mma_fwd(const DeltaProblem &p, void *ws, cudaStream_t s) {
-    return p.N <= 64 ? fwd_launch<64>(p, static_cast<char *>(ws), s) : fwd_launch<128>(p, static_cast<char *>(ws), s);
+    char *w = static_cast<char *>(ws);
+    if (whole(p)) return fwd_of(p, w, s);
+    DeltaProblem q = padded(p);
+    const Copies c = copies_of(q, fwd_bytes(q), false);
+    const int64_t rows = p.B * p.L * p.H, cols = p.B * p.L * p.G, heads = p.B * p.H;
+    Repacks in, out;
+    in.add(p.x, w + c.rows, rows, 1, 1, p.P, q.P, 2);
+    in.add(p.Bm, w + c.cols, cols, 1, 1, p.N, q.N, 2);
+    in.add(p.Cm, w + c.cols + c.col, cols, 1, 1, p.N, q.N, 2);
+    in.add(p.h0, w + c.states, heads, p.P, q.P, p.N, q.N, 4);
+    q.x = w + c.rows, q.Bm = w + c.cols, q.Cm = w + c.cols + c.col, q.y = w + c.rows + c.row;
+    if (p.h0) q.h0 = reinterpret_cast<float *>(w + c.states);
+    if (p.h_final) q.h_final = reinterpret_cast<float *>(w + c.states + c.state);
+    out.add(q.y, p.y, rows, 1, 1, q.P, p.P, 2);
+    out.add(q.h_final, p.h_final, heads, q.P, p.P, q.N, p.N, 4);
+    cudaError_t e = repack(in, s);
+    if (!e) e = fwd_of(q, w, s);
+    return e ? e : repack(out, s);
 }
 
-size_t delta_mma_bwd_workspace_bytes(const DeltaProblem &p) { return bwd_layout(p).total; }
-int delta_mma_bwd_kernels(const DeltaProblem &p) { return delta_grads_slices(p) > 1 ? 4 : 3; }
+size_t delta_mma_bwd_workspace_bytes(const DeltaProblem &p) {
+    if (whole(p)) return bwd_layout(p).total;
+    const DeltaProblem q = padded(p);
+    return copies_of(q, bwd_layout(q).total, true).total;
+}
+int delta_mma_bwd_kernels(const DeltaProblem &p) { return (delta_grads_slices(p) > 1 ? 4 : 3) + (whole(p) ? 0 : 2); }
 
 cudaError_t delta_mma_bwd(const DeltaProblem &p, const DeltaGrads &g, void *ws, cudaStream_t s) {
-    return p.N <= 64 ? bwd_launch<64>(p, g, static_cast<char *>(ws), s) : bwd_launch<128>(p, g, static_cast<char *>(ws), s);
+    char *w = static_cast<char *>(ws);
+    if (whole(p)) return bwd_of(p, g, w, s);
+    DeltaProblem q = padded(p);
+    DeltaGrads r = g;
+    const Copies c = copies_of(q, bwd_layout(q).total, true);
+    const int64_t rows = p.B * p.L * p.H, cols = p.B * p.L * p.G, heads = p.B * p.H;
+    const auto state = [&](int i) { return reinterpret_cast<float *>(w + c.states + i * c.state); };
+    Repacks in, out;
+    in.add(p.x, w + c.rows, rows, 1, 1, p.P, q.P, 2);
+    in.add(g.dy, w + c.rows + c.row, rows, 1, 1, p.P, q.P, 2);
+    in.add(p.Bm, w + c.cols, cols, 1, 1, p.N, q.N, 2);
+    in.add(p.Cm, w + c.cols + c.col, cols, 1, 1, p.N, q.N, 2);
+    in.add(p.h0, state(0), heads, p.P, q.P, p.N, q.N, 4);
+    in.add(g.dh_final, state(1), heads, p.P, q.P, p.N, q.N, 4);
+    q.x = w + c.rows, r.dy = w + c.rows + c.row, r.dx = w + c.rows + 2 * c.row;
+    q.Bm = w + c.cols, q.Cm = w + c.cols + c.col, r.dBm = w + c.cols + 2 * c.col, r.dCm = w + c.cols + 3 * c.col;
+    if (p.h0) q.h0 = state(0);
+    if (g.dh_final) r.dh_final = state(1);
+    if (g.dh0) r.dh0 = state(2);
+    out.add(r.dx, g.dx, rows, 1, 1, q.P, p.P, 2);
+    out.add(r.dBm, g.dBm, cols, 1, 1, q.N, p.N, 2);
+    out.add(r.dCm, g.dCm, cols, 1, 1, q.N, p.N, 2);
+    out.add(r.dh0, g.dh0, heads, q.P, p.P, q.N, p.N, 4);
+    cudaError_t e = repack(in, s);
+    if (!e) e = bwd_of(q, r, w, s);
+    return e ? e : repack(out, s);
 }
 
 }  // namespace ssd

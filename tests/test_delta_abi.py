@@ -85,7 +85,7 @@ def test_plans(lib):
         assert plan(2, 0, 4, 64, 2, 128, B.SSD_BF16) == {"path": "none", "kernels": 0, "workspace_bytes": 0}
         assert plan(0, 9, 4, 64, 2, 128, B.SSD_BF16)["path"] == "none"
         assert plan(1, 9, 4, 64, 2, 128, B.SSD_F32)["path"] == "simt"
-        assert plan(1, 999, 4, 40, 2, 36, B.SSD_BF16)["path"] == "simt"
+        assert plan(1, 999, 4, 40, 2, 136, B.SSD_BF16)["path"] == "simt"
     for f in (lib.ssd_delta_fwd_plan, lib.ssd_delta_bwd_plan):
         assert f(ctypes.byref(B.ShapeT(1, 1, 1, 1, 1, 1)), 0, None) == INVALID
 
@@ -209,6 +209,8 @@ def test_plan_rule(lib):
     assert fwd_path(1, 127, 24, 64, 1, 128) == "simt" and fwd_path(1, 128, 24, 64, 1, 128) == "tcgen05"
     assert fwd_path(8, 21, 24, 64, 1, 128) == "simt" and fwd_path(8, 22, 24, 64, 1, 128) == "tcgen05"
     assert fwd_path(32, 2, 80, 64, 1, 128) == "tcgen05"
+    assert fwd_path(1, 255, 4, 40, 2, 36) == "simt" and fwd_path(1, 256, 4, 40, 2, 36) == "tcgen05"  # padded copies
+    assert B.delta_fwd_plan(1, 256, 4, 40, 2, 36, B.SSD_BF16)["kernels"] == 4
     for L in (1, 37, 128):
         plan = B.delta_bwd_plan(1, L, 4, 64, 1, 128, B.SSD_BF16)
         assert plan["path"] == "tcgen05" and plan["workspace_bytes"] > 0

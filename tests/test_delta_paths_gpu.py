@@ -27,8 +27,32 @@ def test_part_filled_tiles(cuda_device, shape):
     check_bwd(d, cuda_device, "bf16")
 
 
+ODD = [(1, 300, 3, 17, 1, 5), (2, 260, 4, 243, 2, 34), (1, 256, 2, 1, 1, 1), (1, 270, 6, 64, 3, 127), (3, 333, 2, 63, 1, 64)]
+
+
+@pytest.mark.parametrize("h0", [True, False])
+@pytest.mark.parametrize("shape", ODD, ids=str)
+def test_sizes_of_no_whole_vectors(cuda_device, shape, h0):
+    """On padded copies (from 8 on; smaller sizes in fp32); outputs stay within their own bounds and the call can
+    be captured."""
+    assert ssd.delta_fwd_plan(*shape, ssd.SSD_BF16)["path"] == ("tcgen05" if min(shape[3], shape[5]) >= 8 else "simt")
+    d = draw(*shape, "bf16", seed=102, h0=h0)
+    check_fwd(d, cuda_device, "bf16")
+    check_bwd(d, cuda_device, "bf16")
+    a = on(d, cuda_device)
+    y, h = ssd.ssd_delta_fwd(*a)
+    pad = torch.full((y.numel() + 64,), 3.0, dtype=y.dtype, device=cuda_device)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ssd.ssd_delta_fwd(*a, y=pad[32:32 + y.numel()].view(y.shape), return_final_state=False)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert same([pad[32:32 + y.numel()].view(y.shape)], [y])
+    assert bool((pad[:32] == 3).all()) and bool((pad[32 + y.numel():] == 3).all())
+
+
 @pytest.mark.parametrize("L", [1, 2, 3, 9, 31, 63])
-@pytest.mark.parametrize("size", [(2, 5, 64, 1, 64), (1, 4, 16, 2, 128)], ids=str)
+@pytest.mark.parametrize("size", [(2, 5, 64, 1, 64), (1, 4, 16, 2, 128), (1, 3, 19, 1, 35)], ids=str)
 def test_short_backward_on_tensor_cores(cuda_device, L, size):
     B, H, P, G, N = size
     assert ssd.delta_bwd_plan(B, L, H, P, G, N, ssd.SSD_BF16)["path"] == "tcgen05"
