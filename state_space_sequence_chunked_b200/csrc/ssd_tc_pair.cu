@@ -648,8 +648,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int mode = cd.w & 3, h0i = 2 * cd.y, t0 = cd.z * kQ;
                 // each half as soon as its previous y is out (the exact form writes the other half too)
                 if (mode == kModePair) {
-                    mbar_arrive_tx(&full_x[k], 2 * kTxXHead);
+                    // The barrier is armed after the first half's wait: that half's y is out only once the
+                    // slot's last x has landed. Armed before, it could be armed twice in one phase (the third
+                    // task is described long before the first one's x need have arrived), which took its
+                    // arrival count below zero and ended back-to-back launches with a launch failure.
                     if (tx >= 2 && !wait_phase(&empty_x0[k], pe, abort_flag, status)) break;
+                    mbar_arrive_tx(&full_x[k], 2 * kTxXHead);
                     tma_load_4d_hint(xslot(k), &tm_x, &full_x[k], 0, h0i, t0, cd.x, pol_stream);
                     last_x[k] = tx;  // (an abort here still drains this load, with the bounded wait)
                     if (tx >= 2 && !wait_phase(&empty_x1[k], pe, abort_flag, status)) break;
