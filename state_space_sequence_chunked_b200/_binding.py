@@ -592,7 +592,8 @@ def ssd_add_rmsnorm(x, residual, weight, *, scale=None, eps=1e-5, res_out=None, 
     residual (None = 0) is in x's type or fp32, weight and scale (None = 1) are fp32. res_out may be
     residual itself. want_res=False (and no res_out given) returns None for r."""
     dev, dim = x.get_device(), x.shape[-1] if x.dim() else 0
-    rdt = next((t.dtype for t in (residual, res_out) if t is not None), x.dtype)
+    like = next((t for t in (residual, res_out) if t is not None), x)
+    rdt, code, rcode = like.dtype, _dtype_code(x), _dtype_code(like)  # (a type that the library lacks ends here)
     _need("x", x, x.shape, x.dtype, dev)
     _need("residual", residual, x.shape, rdt, dev)
     _need("weight", weight, (dim,), torch.float32, dev)
@@ -604,9 +605,8 @@ def ssd_add_rmsnorm(x, residual, weight, *, scale=None, eps=1e-5, res_out=None, 
             res_out = torch.empty(x.shape, dtype=rdt, device=dev)
         if out is None:
             out = torch.empty_like(x)
-        _check(lib().ssd_add_rmsnorm(x.numel() // dim if dim else 0, dim, _dtype_code(x), SSD_F32 if rdt == torch.float32 else
-                                     SSD_BF16, _at(x), _at(residual), _at(scale), _at(weight), float(eps), _at(res_out),
-                                     _at(out), st), "ssd_add_rmsnorm")
+        _check(lib().ssd_add_rmsnorm(x.numel() // dim if dim else 0, dim, code, rcode, _at(x), _at(residual), _at(scale),
+                                     _at(weight), float(eps), _at(res_out), _at(out), st), "ssd_add_rmsnorm")
     return res_out, out
 
 
@@ -618,13 +618,13 @@ def ssd_add_rmsnorm_bwd(res, weight, dout, dres_in=None, *, x=None, scale=None, 
     the forward's x are given); `out` may supply any of those tensors to write into (dres may be
     dres_in, dx may be dout)."""
     dev, dim = dout.get_device(), dout.shape[-1] if dout.dim() else 0
+    code, rcode = _dtype_code(dout), _dtype_code(res)
     _need("dout", dout, dout.shape, dout.dtype, dev)
     _need("res", res, dout.shape, res.dtype, dev)
     _need("dres_in", dres_in, dout.shape, res.dtype, dev)
     _need("x", x, dout.shape, dout.dtype, dev)
     _need("weight", weight, (dim,), torch.float32, dev)
     _need("scale", scale, (dim,), torch.float32, dev)
-    code, rcode = _dtype_code(dout), _dtype_code(res)
     rows = dout.numel() // dim if dim else 0
     o = dict(out or {})
     with _On(dev, stream) as st:

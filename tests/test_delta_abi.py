@@ -187,6 +187,22 @@ def test_binding_refuses_wrong_tensors():
         B.ssd_norm_gate(x, x, torch.ones(8), ngroups=1)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float64, torch.int16, torch.int8, torch.uint8, torch.bool, torch.float8_e4m3fn])
+def test_binding_refuses_types_of_the_residual_stream(dtype):
+    """Types other than fp32 and bf16 are refused, also where the residual or res_out alone has them: read as bf16,
+    a type of one byte would end before the kernel does."""
+    other = torch.zeros(3, 8).to(dtype)
+    for x in (torch.zeros(3, 8), torch.zeros(3, 8, dtype=torch.bfloat16)):
+        w = torch.ones(8)
+        for args in (dict(residual=other), dict(residual=None, res_out=other), dict(residual=other, res_out=other)):
+            with pytest.raises(TypeError):
+                B.ssd_add_rmsnorm(x, weight=w, **args)
+        with pytest.raises(TypeError):
+            B.ssd_add_rmsnorm_bwd(other, w, x)
+    with pytest.raises(TypeError):
+        B.ssd_add_rmsnorm(other, None, torch.ones(8))
+
+
 def test_row_views():
     like = torch.zeros(3, 4, 8)
     wide = torch.zeros(3, 4, 20)
