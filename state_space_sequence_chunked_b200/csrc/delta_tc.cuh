@@ -49,6 +49,26 @@ __device__ __forceinline__ void mma_ss_el(uint32_t leader, uint32_t d, uint64_t 
         "l"(left), "l"(right), "r"(id), "r"(leader), "r"(acc)
         : "memory");
 }
+// The same for one head of a pair: its 64 accumulator lanes (head 0: lanes 0-63) are written, the others stay as they
+// are, so that nothing of one head's operands, not even 0 x inf, enters the other's rows.
+template <bool kAcc>
+__device__ __forceinline__ void mma_half_el(uint32_t leader, int head, uint32_t d, uint32_t left, uint64_t right, uint32_t id) {
+    const uint32_t off0 = head ? 0xffffffffu : 0u;  // lanes 0-63 not written
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.ne.b32 p, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %6, %6}, p;\n\t}" ::"r"(d),
+        "r"(left), "l"(right), "r"(id), "r"(leader), "r"(off0), "r"(~off0), "n"(kAcc ? 1 : 0)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ss_half_el(uint32_t leader, int head, uint32_t d, uint64_t left, uint64_t right, uint32_t id,
+                                               uint32_t acc) {
+    const uint32_t off0 = head ? 0xffffffffu : 0u;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%6, %6, %7, %7}, p;\n\t}" ::"r"(d),
+        "l"(left), "l"(right), "r"(id), "r"(leader), "r"(acc), "r"(off0), "r"(~off0)
+        : "memory");
+}
 __device__ __forceinline__ void commit_el(uint32_t leader, uint64_t *bar) {
     if (leader) mma_commit(bar);
     __syncwarp();

@@ -13,14 +13,15 @@
 //   S += (ek u)^T K          ek u hi, lo             K, columns contiguous          S   N, fp32
 //   Y  = eg Yq + u P^T       u hi, lo                P  [64 x 64]                   Y
 // with R = X - eg R0, err = R + E, u = beta err, eg = exp(cum), ek = exp(cum_end - cum). W and P differ by
-// head, so in a PAIR the left operand of their products is 128 tokens wide, each head's rows holding
-// zeros in the other's 64. W and P are lower triangular: a step of 16 tokens j multiplies only the
-// tokens i from its own block on (N = 64, 48, 32, 16).
+// head, so in a PAIR each of their products is issued once per head and writes that head's 64 lanes alone: a head's
+// values that are not finite stay its own. W and P are lower triangular: a step of 16 tokens j
+// multiplies only the tokens i from its own block on (N = 64, 48, 32, 16). (Within such a step the zeros above the
+// diagonal are multiplied: a value that is not finite reaches the tokens before it in its block of 16.)
 //
 // Warps (768 threads): 0 loads (TMA), 1 issues the products, 4-19 (T) form R, u and the state's operands (four
 // warps per 32 lanes, a quarter of the columns each), 20-23 (O) scale Yq and write Y out; in the forward
 // chain 2-3 are idle (a T or O warp's TMEM lanes are those of its number modulo 4). TMEM, 512 columns: S 128,
-// S hi 64, S lo 64 (later ek u), R 64, Y 64, beta R then u 2 x 64.
+// S hi 64, S lo 64 (later ek u), R 64, Y 64, beta R then u 32 + 32 (hi, lo).
 //
 // Streams (128 state rows over the sequence) are dealt to the CTAs in equal shares of chunks, so a stream may be cut
 // once and handed on through global memory: 160 streams of 128 chunks took 731 us with whole streams (two waves on
@@ -46,7 +47,7 @@ using namespace tc;
 constexpr int kTWarps = 16, kOWarp = 4 + kTWarps, kThreads = 32 * (kOWarp + 4);
 constexpr int kTriLbo = 128, kTriSbo = 256;  // see tri_rows
 constexpr int kTri = 10 * 512;     // bytes of a 64 x 64 lower triangle of 16 x 16 blocks, bf16
-constexpr int kTmS = 0, kTmHi = 128, kTmLo = 192, kTmR = 256, kTmY = 320, kTmA = 384, kTmAl = 448;
+constexpr int kTmS = 0, kTmHi = 128, kTmLo = 192, kTmR = 256, kTmY = 320, kTmA = 384, kTmAl = 416;
 constexpr int kEk = kTmLo, kEkl = kTmLo + 32;  // ek u over S lo
 
 template <int NT, bool PAIR, bool kStore>
@@ -255,16 +256,24 @@ __device__ __forceinline__ void chain_fwd(const CUtensorMap &tm_k, const CUtenso
         // A lower triangle as right operand, a column of blocks (16 tokens) at a time, rows from its own block
         // on. No swizzle: core matrices of 128 bytes, the two of a block's row 128 apart, rows of them 256.
         const uint32_t el = elect_one();
-        const auto tri = [&](uint32_t d, uint32_t left, uint32_t tile, auto acc) {
+        const auto tri = [&](int head, uint32_t d, uint32_t left, uint32_t tile, auto acc) {
             const uint64_t td = (uint64_t)((tile >> 4) & 0x3FFFu) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(256 >> 4) << 32 |
                                 (uint64_t)1 << 46;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint64_t ti = td + (uint64_t)((i * 4 - i * (i - 1) / 2) * 512 >> 4);
-                if (i == 0)
-                    mma_el<decltype(acc)::value>(el, d, left, ti, idesc(128, 64, false, false));
-                else
-                    mma_el<true>(el, d + 16 * i, left + 8 * i, ti, idesc(128, 64 - 16 * i, false, false));
+                constexpr auto id = [](int i) { return idesc(128, 64 - 16 * i, false, false); };
+                if constexpr (PAIR) {
+                    if (i == 0)
+                        mma_half_el<decltype(acc)::value>(el, head, d, left, ti, id(0));
+                    else
+                        mma_half_el<true>(el, head, d + 16 * i, left + 8 * i, ti, id(i));
+                } else {
+                    if (i == 0)
+                        mma_el<decltype(acc)::value>(el, d, left, ti, id(0));
+                    else
+                        mma_el<true>(el, d + 16 * i, left + 8 * i, ti, id(i));
+                }
             }
         };
         constexpr std::true_type add{};
@@ -306,12 +315,9 @@ __device__ __forceinline__ void chain_fwd(const CUtensorMap &tm_k, const CUtenso
 #pragma unroll
             for (int e = 0; e < HB; ++e) {
                 const uint32_t wh = st + Z::w + e * Z::head;
-                if (e == 0)
-                    tri(tm + kTmR, tm + kTmAl, wh, set);
-                else
-                    tri(tm + kTmR, tm + kTmAl + 32 * e, wh, add);
-                tri(tm + kTmR, tm + kTmA + 32 * e, wh + kTri, add);
-                tri(tm + kTmR, tm + kTmA + 32 * e, wh, add);
+                tri(e, tm + kTmR, tm + kTmAl, wh, set);
+                tri(e, tm + kTmR, tm + kTmA, wh + kTri, add);
+                tri(e, tm + kTmR, tm + kTmA, wh, add);
             }
             commit_el(el, rdyE);
             if (!wait_warp(ub, par, abort_flag, status)) break;
@@ -329,8 +335,8 @@ __device__ __forceinline__ void chain_fwd(const CUtensorMap &tm_k, const CUtenso
                 tc_fence_after();
 #pragma unroll
                 for (int e = 0; e < HB; ++e) {
-                    tri(tm + kTmY, tm + kTmAl + 32 * e, st + Z::w + e * Z::head + Z::p, add);
-                    tri(tm + kTmY, tm + kTmA + 32 * e, st + Z::w + e * Z::head + Z::p, add);
+                    tri(e, tm + kTmY, tm + kTmAl, st + Z::w + e * Z::head + Z::p, add);
+                    tri(e, tm + kTmY, tm + kTmA, st + Z::w + e * Z::head + Z::p, add);
                 }
                 commit_el(el, rdyY);
             }
@@ -346,11 +352,6 @@ __device__ __forceinline__ void chain_fwd(const CUtensorMap &tm_k, const CUtenso
         const int pp = (qtr & 1) * 32 + lane;                      // row within the x panel qtr >> 1
         constexpr int SC = NT / 4;  // state columns of this warp, from n0 on
         const int n0 = sub * SC, tk0 = 16 * sub;  // and tokens
-        if constexpr (PAIR) {  // zeros in the other head's tokens
-            const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            tmem_st8(lo_ + kTmA + 32 * (1 - e) + 8 * sub, zero);
-            tmem_st8(lo_ + kTmAl + 32 * (1 - e) + 8 * sub, zero);
-        }
         int it = 0;
         bool ok = true;
         for (int j = 0; ok && j < share.n; ++j) {
@@ -435,8 +436,8 @@ __device__ __forceinline__ void chain_fwd(const CUtensorMap &tm_k, const CUtenso
                                                make_float2(bx[2 * i], bx[2 * i + 1]));
                         split2(br.x, br.y, hi[i], lw[i]);
                     }
-                    tmem_st8(lo_ + kTmA + 32 * e + 8 * sub, hi);
-                    tmem_st8(lo_ + kTmAl + 32 * e + 8 * sub, lw);
+                    tmem_st8(lo_ + kTmA + 8 * sub, hi);
+                    tmem_st8(lo_ + kTmAl + 8 * sub, lw);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -490,8 +491,8 @@ __device__ __forceinline__ void chain_fwd(const CUtensorMap &tm_k, const CUtenso
                         tmem_st8(lo_ + kTmY + 8 * sub, hi);
                         tmem_st8(lo_ + kTmY + 32 + 8 * sub, lw);
                     } else {
-                        tmem_st8(lo_ + kTmA + 32 * e + 8 * sub, hi);
-                        tmem_st8(lo_ + kTmAl + 32 * e + 8 * sub, lw);
+                        tmem_st8(lo_ + kTmA + 8 * sub, hi);
+                        tmem_st8(lo_ + kTmAl + 8 * sub, lw);
                     }
                     tmem_wait_st();
                     tc_fence_before();
@@ -622,7 +623,7 @@ __device__ __forceinline__ void chain_fwd(const CUtensorMap &tm_k, const CUtenso
 //   D += (eg dY)^T Q         eg dY hi, lo (sh. mem.)   Q, columns contiguous               D   N, fp32
 //   D -= (eg r)^T K          -eg r hi, lo (TMEM)       K                                   D
 // with F = Z + ek F0, z = F + E, r = beta z = dX. Rows, tokens and warps as above, plus warps 2-3, which
-// form eg dY. In a PAIR the left operands of Z come with a panel of zeros for the other head's rows.
+// form eg dY. In a PAIR the products with P and W write one head's lanes at a time, as above.
 // z and dX go out in bf16, and D hi of every chunk (an operand of k_delta_grads_tc). Both chains share a launch, since
 // neither needs the other: 24 heads of 64 x 128, 4 x 2048 tokens, 132 us for both.
 template <int NT, bool PAIR>
@@ -630,7 +631,7 @@ struct RevLay {
     static constexpr int HB = PAIR ? 2 : 1;
     static constexpr int kBytes = NT / 64 * kPanel;
     static constexpr int k = 0, q = k + 2 * kBytes;                // two stages each
-    static constexpr int dy0 = q + 2 * kBytes, zero = dy0 + 2 * kPanel, dy1 = zero + (PAIR ? kPanel : 0);
+    static constexpr int dy0 = q + 2 * kBytes, dy1 = dy0 + 2 * kPanel;
     static constexpr int e = dy1 + 2 * kPanel;                     // eg dY: hi, lo, two panels each
     static constexpr int out = e + 4 * kPanel;                     // O warps: two buffers of 4 KB each
     static constexpr int w = out + 4 * 8192, p = w + HB * 2 * kTri;  // W hi, lo per head; P hi, lo per head
@@ -675,11 +676,6 @@ __device__ __forceinline__ void chain_rev(const CUtensorMap &tm_k, const CUtenso
         const int tile = stream % a.tiles, hy = stream / a.tiles % (a.H / HB);
         b = stream / a.tiles / (a.H / HB), h = hy * HB, pc = 128 * tile;
     };
-    if constexpr (PAIR) {
-        for (int i = threadIdx.x; i < kPanel / 16; i += kThreads)
-            reinterpret_cast<uint4 *>(sm + Z::zero)[i] = make_uint4(0, 0, 0, 0);
-        fence_proxy_async();
-    }
     constexpr int counts[20] = {1, 1, 1 + kTWarps, 1 + kTWarps, 1, 1, 1, 1, 1, 1, 1, 1, kTWarps, kTWarps, kTWarps, kTWarps, 2, 4, 4, 1};
     const Setup su = set_up(bar, counts, a.wait_us, warp);
     const uint32_t tmem = su.tmem;
@@ -748,14 +744,18 @@ __device__ __forceinline__ void chain_rev(const CUtensorMap &tm_k, const CUtenso
             tc_fence_after();
 #pragma unroll
             for (int e = 0; e < HB; ++e) {
-                const uint32_t y0 = base + Z::dy0 + k * kPanel, y1 = base + Z::dy1 + k * kPanel, zr = base + Z::zero;
-                const uint64_t ya = !PAIR ? sdesc(y0, y1 - y0, 1024) : e == 0 ? sdesc(y0, zr - y0, 1024) : sdesc(zr, y1 - zr, 1024);
+                const uint64_t ya = sdesc(base + Z::dy0 + k * kPanel, Z::dy1 - Z::dy0, 1024);
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int i = 3; i >= 0; --i)
-                        mma_ss_el(el, tm + kTmY, ya + 128 * i, tri_rows(base + Z::p + (2 * e + 1 - part) * kTri, i),
-                                  idesc(128, 16 * (i + 1), true, true), e > 0 || part > 0 || i < 3);
+                    for (int i = 3; i >= 0; --i) {
+                        const uint64_t right = tri_rows(base + Z::p + (2 * e + 1 - part) * kTri, i);
+                        const uint32_t id = idesc(128, 16 * (i + 1), true, true);
+                        if constexpr (PAIR)
+                            mma_ss_half_el(el, e, tm + kTmY, ya + 128 * i, right, id, part > 0 || i < 3);
+                        else
+                            mma_ss_el(el, tm + kTmY, ya + 128 * i, right, id, part > 0 || i < 3);
+                    }
             }
             commit_el(el, rdyZ);
             commit_el(el, pfree);
@@ -781,13 +781,20 @@ __device__ __forceinline__ void chain_rev(const CUtensorMap &tm_k, const CUtenso
                 for (int part = 0; part < 3; ++part)  // lo W hi, hi W lo, hi W hi
 #pragma unroll
                     for (int i = 3; i >= 0; --i) {
-                        const uint32_t left = tm + (part == 0 ? kTmAl : kTmA) + 32 * e + 8 * i;
+                        const uint32_t left = tm + (part == 0 ? kTmAl : kTmA) + 8 * i;
                         const uint64_t right = tri_rows(base + Z::w + (2 * e + (part == 1 ? 1 : 0)) * kTri, i);
                         const uint32_t id = idesc(128, 16 * (i + 1), false, true);
-                        if (e == 0 && part == 0 && i == 3)
-                            mma_el<false>(el, tm + kTmR, left, right, id);
-                        else
-                            mma_el<true>(el, tm + kTmR, left, right, id);
+                        if constexpr (PAIR) {
+                            if (part == 0 && i == 3)
+                                mma_half_el<false>(el, e, tm + kTmR, left, right, id);
+                            else
+                                mma_half_el<true>(el, e, tm + kTmR, left, right, id);
+                        } else {
+                            if (part == 0 && i == 3)
+                                mma_el<false>(el, tm + kTmR, left, right, id);
+                            else
+                                mma_el<true>(el, tm + kTmR, left, right, id);
+                        }
                     }
             commit_el(el, rdyE);
             commit_el(el, wfree);
@@ -853,11 +860,6 @@ __device__ __forceinline__ void chain_rev(const CUtensorMap &tm_k, const CUtenso
         const uint32_t lo_ = tmem + ((uint32_t)(32 * qtr) << 16);
         constexpr int SC = NT / 4;
         const int n0 = sub * SC, tk0 = 16 * sub;
-        if constexpr (PAIR) {  // zeros in the other head's tokens
-            const uint32_t none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            tmem_st8(lo_ + kTmA + 32 * (1 - e) + 8 * sub, none);
-            tmem_st8(lo_ + kTmAl + 32 * (1 - e) + 8 * sub, none);
-        }
         int it = 0;
         bool ok = true;
         for (int j = 0; ok && j < share.n; ++j) {
@@ -942,8 +944,8 @@ __device__ __forceinline__ void chain_rev(const CUtensorMap &tm_k, const CUtenso
                                                make_float2(F[2 * i], F[2 * i + 1]));
                         split2(bf.x, bf.y, hi[i], lw[i]);
                     }
-                    tmem_st8(lo_ + kTmA + 32 * e + 8 * sub, hi);
-                    tmem_st8(lo_ + kTmAl + 32 * e + 8 * sub, lw);
+                    tmem_st8(lo_ + kTmA + 8 * sub, hi);
+                    tmem_st8(lo_ + kTmAl + 8 * sub, lw);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();

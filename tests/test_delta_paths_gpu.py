@@ -200,3 +200,42 @@ def test_orders_of_magnitude(cuda_device):
     yr, hr = oracle.delta_recurrent(*[to_np(v) for v in a])
     assert err(h, hr) <= F32_TOL and err(y, yr) <= tol(y, "bf16")
     assert np.isfinite(yr).all()
+
+
+BAD = {  # input, value at head 1 of four, token 20
+    "NaN decay": ("g", float("nan")), "infinite decay": ("g", float("inf")), "NaN strength": ("beta", float("nan")),
+    "infinite strength": ("beta", float("inf")), "an inverse that overflows": ("beta", 3e38), "infinite x": ("x", float("inf")),
+    "NaN cotangent": ("dy", float("nan")),
+}
+
+
+@pytest.mark.parametrize("bad", list(BAD))
+@pytest.mark.parametrize("dtype,shape", [("f32", (1, 41, 4, 24, 2, 36)), ("bf16", (1, 200, 4, 64, 2, 128)), ("bf16", (2, 150, 4, 40, 1, 64)),
+                                         ("bf16", (1, 130, 4, 128, 2, 128))], ids=str)
+def test_values_that_are_not_numbers_stay_in_their_head(cuda_device, dtype, shape, bad):
+    """The definition keeps heads apart but for the gradients of shared keys and queries: one head's values that are not
+    finite leave the others' outputs, states and own gradients as they were, bit by bit."""
+    d = draw(*shape, dtype, seed=151)
+    names = ("x", "g", "beta", "Bm", "Cm", "h0", "dy", "dh")
+    a = dict(zip(names, on(d, cuda_device, names)))
+    if bad == "an inverse that overflows":
+        a["Bm"][:, 20:30] = a["Bm"][:, 20:21].clone()  # keys alike: products of strengths in the inverse
+
+    def run():
+        y, h = ssd.ssd_delta_fwd(*[a[n] for n in names[:6]])
+        o = ssd.ssd_delta_bwd(*[a[n] for n in names])
+        torch.cuda.synchronize()
+        return {"y": y, "h": h, "dx": o["dx"], "dg": o["dg"], "dbeta": o["dbeta"], "dh0": o["dh0"]}
+
+    want = run()
+    name, value = BAD[bad]
+    if bad == "an inverse that overflows":
+        a[name][:, 20:30, 1] = value
+    else:
+        a[name][:, 20, 1] = value
+    got = run()
+    axis = {"y": 2, "h": 1, "dx": 2, "dg": 2, "dbeta": 2, "dh0": 1}
+    for n in want:
+        for head in (0, 2, 3):
+            assert torch.equal(got[n].select(axis[n], head), want[n].select(axis[n], head)), (n, head)
+    assert not all(bool(torch.isfinite(got[n].select(axis[n], 1)).all()) for n in got)
