@@ -344,7 +344,11 @@ __global__ void __launch_bounds__(kSeqThr, NJ < 8 ? 2 : 1)
 //   dP_ij = (dy_i.u_j) E_ij (i >= j),  dM_ij = -(r_i.u_j) E_ij (i > j),  u = beta err, r = beta z,
 //   dC_i = exp(cum_i) dy_i S + sum_j dP_ij k_j,
 //   dB_i = sum_j dP_ji q_j + (dM_ij + dM_ji) k_j + exp(cum_end - cum_i) u_i D - exp(cum_i) r_i S,
-//   dbeta_i = z_i.err_i, and dg the reverse cumulative sum of the derivative with respect to cum.
+//   dbeta_i = z_i.err_i, and dg_i the sum of what passes the decay of token i:
+//   sum over t >= i > j of dP_tj q_t.k_j + dM_tj k_t.k_j,  sum over t >= i of exp(cum_t) (dy_t.S q_t - r_t.S k_t),
+//   sum over t < i of U_t = exp(cum_end - cum_t) u_t.D k_t,  and exp(cum_end) <D, S>.
+// No term of these is taken off again (as it is in a cumulative sum of the derivative with respect to cum, where
+// the pairs on one side of i come in and go out): dg shrinks with exp(g), and its errors with it.
 // The three products with S and D are register tiles: a warp holds TK tokens by all columns (a lane every 32nd) and
 // takes them from dy, u and r, transposed in shared memory, four tokens per 16-byte broadcast. Where two warps
 // share a tile, each takes a half of the state rows and then a half of the pairs' tokens j; they meet once, at the end.
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(kThr)
     float *wP = wPt + kSeg * kTp;         // [j][kTp]: dP_jt
     float *wM = wP + kSeg * kTp;          // [j][kTp]: dM_tj + dM_jt
     float *pair = wM + kSeg * kTp;        // [kSeg][33]
-    __shared__ float dots[PS][kSeg], ends[kWarps], eg[kSeg], ek[kSeg], bt[kSeg], zd[kSeg];
+    __shared__ float dots[2][PS][kSeg], ends[kWarps], eg[kSeg], ek[kSeg], bt[kSeg], zd[kSeg];
     __shared__ double cum[kSeg];
     const int64_t c = blockIdx.x, ns = gridDim.x, t0 = c * kSeg;
     const int h = blockIdx.y, b = blockIdx.z, grp = h / (H / G);
@@ -524,11 +528,11 @@ __global__ void __launch_bounds__(kThr)
                 for (int j = 0; j < NJ; ++j) ds = fmaf(now.s[i][j], now.d[i][j], ds);
         }
     }
-    // the derivative with respect to cum, as far as these rows go: per token, and the end's share
-    float tok[TK], end = eg[kSeg - 1] * ds;
+    // dg's terms with S and D, as far as these rows go: per token, and the end's
+    float tok[2][TK], end = eg[kSeg - 1] * ds;
 #pragma unroll
     for (int t = 0; t < TK; t += 2) {
-        float d[2] = {0.f, 0.f};
+        float d[2] = {0.f, 0.f}, U[2] = {0.f, 0.f};
         const float e0 = eg[tk0 + t], e1 = eg[tk0 + t + 1], k0 = ek[tk0 + t], k1 = ek[tk0 + t + 1];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
@@ -538,19 +542,20 @@ __global__ void __launch_bounds__(kThr)
             const float2 n2 = make_float2(in ? ks[(tk0 + t) * NP + n] : 0.f, in ? ks[(tk0 + t + 1) * NP + n] : 0.f);
             float2 &q = fq[t / 2][j], &k = fk[t / 2][j], &u = fu[t / 2][j];
             q.x *= e0, q.y *= e1, k.x *= e0, k.y *= e1, u.x *= k0, u.y *= k1;
-            const float U0 = u.x * n2.x, U1 = u.y * n2.y;
-            end += U0 + U1;
-            d[0] += q.x * q2.x - k.x * n2.x - U0;
-            d[1] += q.y * q2.y - k.y * n2.y - U1;
+            U[0] = fmaf(u.x, n2.x, U[0]), U[1] = fmaf(u.y, n2.y, U[1]);
+            d[0] += q.x * q2.x - k.x * n2.x;
+            d[1] += q.y * q2.y - k.y * n2.y;
             k.x = u.x - k.x, k.y = u.y - k.y;
         }
-        tok[t] = d[0], tok[t + 1] = d[1];
+        tok[0][t] = d[0], tok[0][t + 1] = d[1], tok[1][t] = U[0], tok[1][t + 1] = U[1];
     }
 #pragma unroll
-    for (int t = 0; t < TK; ++t) {
-        tok[t] = warp_sum(tok[t]);
-        if (lane == 0) dots[ps][tk0 + t] = tok[t];
-    }
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int t = 0; t < TK; ++t) {
+            tok[m][t] = warp_sum(tok[m][t]);
+            if (lane == 0) dots[m][ps][tk0 + t] = tok[m][t];
+        }
     end = warp_sum(end);
     if (lane == 0) ends[warp] = end;
     __syncthreads();  // the pairs' weights are there
@@ -577,17 +582,26 @@ __global__ void __launch_bounds__(kThr)
         }
     }
     if (warp == 0) {
-        float d = 0.f;
-        for (int w = 0; w < PS; ++w) d += dots[w][lane];
-        for (int j = 0; j < kSeg; ++j) d += pair[lane * 33 + j] - pair[j * 33 + lane];
-        if (lane == kSeg - 1)
-            for (int w = 0; w < kWarps; ++w) d += ends[w];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {  // sum over the tokens from this one to the end
-            const float up = __shfl_down_sync(0xffffffffu, d, o);
-            if (lane + o < 32) d += up;
+        // a row of pairs per lane becomes its sums of columns before i, i up to the row's own token
+        float run = 0.f;
+        for (int i = 0; i < kSeg; ++i) {
+            const float v = pair[lane * 33 + i];
+            pair[lane * 33 + i] = i <= lane ? run : 0.f;
+            run += v;
         }
-        if (lane < nt) store_as(dg + ((int64_t)b * L + t0 + lane) * H + h, d);
+        float after = 0.f, before = 0.f, d = 0.f;
+        for (int w = 0; w < PS; ++w) after += dots[0][w][lane], before += dots[1][w][lane];
+        for (int w = 0; w < kWarps; ++w) d += ends[w];
+        __syncwarp();
+        for (int t = 0; t < kSeg; ++t) d += pair[t * 33 + lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {  // the tokens from this one to the end; those up to this one
+            const float a = __shfl_down_sync(0xffffffffu, after, o), u = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane + o < 32) after += a;
+            if (lane >= o) before += u;
+        }
+        before = __shfl_up_sync(0xffffffffu, before, 1);  // (without this one)
+        if (lane < nt) store_as(dg + ((int64_t)b * L + t0 + lane) * H + h, d + after + (lane ? before : 0.f));
     }
     if constexpr (PS > 1) {  // the other half's sums, through shared memory (all of which is free now)
         __syncthreads();

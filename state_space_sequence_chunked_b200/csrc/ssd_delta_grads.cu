@@ -4,10 +4,14 @@
 //     dP = tril((dY u^T) o E),   dM = -tril((r u^T) o E, -1),
 //     dQ = eg dY S + dP K,
 //     dK = -eg r S + ek u D + dM K + dP^T Q + dM^T K,
-//     dbeta_i = z_i.err_i,   dg = the sum from i to the chunk's end of
-//         rows - columns of (dP o Q K^T + dM o K K^T) + eg dY_i.S q_i - eg r_i.S k_i - U_i,
-//         U_i = ek_i u_i.D k_i, and at the last token + sum U + exp(cum_end) <D, S>.
-// No sum runs across chunks, and each pair of tokens enters once, in fp32.
+//     dbeta_i = z_i.err_i,   dg_i = what passes the decay of token i:
+//         sum over t >= i > j of F_tj,  F = dP o Q K^T + dM o K K^T,
+//         sum over t >= i of eg_t (dY_t.S q_t - r_t.S k_t),
+//         sum over t < i of U_t = ek_t u_t.D k_t,  and exp(cum_end) <D, S>.
+// No sum runs across chunks, each pair of tokens enters once, in fp32, and nothing that came in goes out again (as
+// in a sum from i to the end of the derivative with respect to cum): under strong decays dg shrinks with
+// exp(g), and its errors with it. The pairs t >= i > j are summed in two parts, by quarters of 16 tokens: j in the quarter
+// of i, from sums of a row's columns within the quarter (cols), and j in the quarters before, whole (pairs).
 //
 // A CTA takes a chunk of a group and walks its heads (of its slice), 64 state rows at a time. dQ and dK of
 // the chunk stand in TMEM for all of them, tokens by lane (dQ in lanes 0-63, dK in 64-127), and every term is
@@ -38,8 +42,9 @@ constexpr float kLog2e = 1.44269504f;
 constexpr int kTmG = 0, kTmP = 128, kTmS = 192, kTmD = 256, kTmConst = 320;
 
 struct HeadSums {
-    float rows[4][128];  // by column quarter: dQ-side and dK-side tokens
-    float cols[4][kC];   // by lane quarter
+    float rows[4][128];   // eg dY.S q and -eg r.S k by quarter of the state rows: dQ-side and dK-side tokens
+    float pairs[3][128];  // F's rows over the columns of a quarter
+    float cols[4][kC];    // its pairs t >= i > j with j in the quarter of i, by lane quarter
     float U[4][kC];
     float dot[kCWarps / 2], db[kC];
 };
@@ -225,37 +230,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads_tc(const __grid_con
         for (int turn = 0; turn < h_end - h_begin; ++turn) {
             if (!wait_warp(&hd[turn & 1], (uint32_t)(turn >> 1) & 1u, abort_flag, status)) break;
             const HeadSums &s = *sums_of(turn);
-            float d[2], us = 0.f, end = lane < kCWarps / 2 ? s.dot[lane] : 0.f;
+            float end = lane < kCWarps / 2 ? s.dot[lane] : 0.f;
+            // from a token on: rows, pairs with columns in quarter 0, 1, 2; up to a token: U; and its own
+            float after[2][4], u[2], d[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 2 * lane + e;
-                us += (s.U[0][i] + s.U[1][i]) + (s.U[2][i] + s.U[3][i]);
-                d[e] = 0.f;
+                after[e][0] = d[e] = 0.f;
 #pragma unroll
-                for (int o = 0; o < 4; ++o) d[e] += (s.rows[o][i] + s.rows[o][64 + i]) - s.cols[o][i];
+                for (int o = 0; o < 4; ++o) after[e][0] += s.rows[o][i] + s.rows[o][64 + i], d[e] += s.cols[o][i];
+#pragma unroll
+                for (int o = 0; o < 3; ++o) after[e][1 + o] = s.pairs[o][i] + s.pairs[o][64 + i];
+                u[e] = (s.U[0][i] + s.U[1][i]) + (s.U[2][i] + s.U[3][i]);
             }
             const float b0 = s.db[2 * lane], b1 = s.db[2 * lane + 1];
             __syncwarp();
             if (lane == 0) mbar_arrive(&hfree[turn & 1]);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                us += __shfl_xor_sync(0xffffffffu, us, o);
-                end += __shfl_xor_sync(0xffffffffu, end, o);
-            }
-            float s2 = d[0] + d[1];
-            if (lane == 31) s2 += us + end;  // (dot comes with exp(cum_end))
-            const float odd = lane == 31 ? d[1] + us + end : d[1];
+            for (int o = 16; o > 0; o >>= 1) end += __shfl_xor_sync(0xffffffffu, end, o);
+            float from[4], upto = u[0] + u[1];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) from[m] = after[0][m] + after[1][m];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const float up = __shfl_down_sync(0xffffffffu, s2, o);
-                if (lane + o < 32) s2 += up;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const float v = __shfl_down_sync(0xffffffffu, from[m], o);
+                    if (lane + o < 32) from[m] += v;
+                }
+                const float v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
             }
-            // s2: from token 2 lane on; the next lane's from 2 lane + 2 on
-            const float nxt = __shfl_down_sync(0xffffffffu, s2, 1);
+            upto = __shfl_up_sync(0xffffffffu, upto, 1);  // the tokens before 2 lane
+            if (lane == 0) upto = 0.f;
+            const int quarter = lane >> 3;
+            d[0] += end + upto, d[1] += end + (upto + u[0]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                float nxt = __shfl_down_sync(0xffffffffu, from[m], 1);  // from token 2 lane + 2 on
+                nxt = lane < 31 ? nxt : 0.f;
+                if (m <= quarter) d[0] += from[m], d[1] += after[1][m] + nxt;
+            }
             const int64_t at = ((int64_t)b * a.L + t0 + 2 * lane) * a.H + h_begin + turn;
-            if (2 * lane < nt) a.dg[at] = __float2bfloat16_rn(s2), a.dbeta[at] = __float2bfloat16_rn(b0);
+            if (2 * lane < nt) a.dg[at] = __float2bfloat16_rn(d[0]), a.dbeta[at] = __float2bfloat16_rn(b0);
             if (2 * lane + 1 < nt)
-                a.dg[at + a.H] = __float2bfloat16_rn(odd + (lane < 31 ? nxt : 0.f)), a.dbeta[at + a.H] = __float2bfloat16_rn(b1);
+                a.dg[at + a.H] = __float2bfloat16_rn(d[1]), a.dbeta[at + a.H] = __float2bfloat16_rn(b1);
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------- elementwise
@@ -315,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads_tc(const __grid_con
                 const float ih = ch[i], il = cl[i], sign = upper ? -1.f : 1.f;
                 const int last = upper ? i - 1 : i;
                 const float2 minus = make_float2(-1.f, -1.f);
-                float pr[16];
+                float pr[16], run = 0.f;  // F's columns of the quarter before each one, in rows from its token on
                 uint32_t o[8];
                 if (16 * sub > (i | 31)) {  // (warp-uniform) above the diagonal
 #pragma unroll
@@ -339,8 +358,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads_tc(const __grid_con
                             const float2 m = mul2(ex, pair_of(v[j + n], v[j + n + 1]));
                             x[n] = jj + n <= last ? m.x : 0.f, x[n + 1] = jj + n + 1 <= last ? m.y : 0.f;
                             const float2 pq = mul2(make_float2(x[n], x[n + 1]), pair_of(w[j + n], w[j + n + 1]));
-                            pr[j + n] = pq.x, pr[j + n + 1] = pq.y;
-                            rowsum += pq.x + pq.y;
+                            pr[j + n] = jj + n <= i ? run : 0.f;
+                            run += pq.x;
+                            pr[j + n + 1] = jj + n + 1 <= i ? run : 0.f;
+                            run += pq.y;
                         }
                         o[j / 2] = pack_bf16(x[0], x[1]), o[j / 2 + 1] = pack_bf16(x[2], x[3]);
                     }
@@ -361,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads_tc(const __grid_con
                     }
                 pr[0] += __shfl_xor_sync(0xffffffffu, pr[0], 1);
                 if ((lane & 1) == 0) s.cols[qtr][16 * sub + (lane >> 1)] = pr[0];
+                if (sub < 3) s.pairs[sub][row] = run;
             } else if (lane == 0) {
                 mbar_arrive(pb);
             }
@@ -381,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_delta_grads_tc(const __grid_con
                                            *reinterpret_cast<const uint4 *>(st + Z::u + swz(i, 2 * sub + 1)));
                     const float U = ek[i] * d2;
                     usum += U;
-                    rowsum -= eg[i] * d1 + U;
+                    rowsum -= eg[i] * d1;
                 } else {
                     rowsum += eg[i] * d1;
                 }
