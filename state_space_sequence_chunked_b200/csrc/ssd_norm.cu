@@ -37,11 +37,23 @@ struct Geom {
     float inv;  // 1 / gs
 };
 
-// 1 / (1 + 2^(-v log2 e)) by the approximate instructions (2^-22 relative each); 0 where the power
-// overflows.
+// 1 / (1 + 2^(-v log2 e)) by the approximate instructions (2^-22 and 2^-23 of the value). The product v log2 e is
+// rounded, which moves the power by up to |v| 2^-24 of itself: below -20 that is more than the rest. For outputs stored in
+// bf16 it stays (5e-6 at the most, of 2^-8); for fp32 what the rounding took is multiplied back in. 0 below -87.3, where the
+// quotient is no normal number. v is held within +-200, so that infinities have no remainder; a NaN v
+// comes back with the factor v beside.
+template <typename T>
 __device__ __forceinline__ float sigmoid(float v) {
+    constexpr float kLog2e = 1.44269502f, kRest = 1.92596299e-8f;  // log2 e in two parts
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504f * v));
+    if constexpr (sizeof(T) == 4) {
+        v = fminf(fmaxf(v, -200.f), 200.f);
+        const float p = -kLog2e * v, rest = fmaf(-kRest, v, fmaf(-kLog2e, v, -p));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(p));
+        e *= fmaf(rest, 0.693147181f, 1.f);
+    } else {
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-kLog2e * v));
+    }
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     return r;
 }
@@ -422,7 +434,7 @@ __global__ void __launch_bounds__(V == 8 && S == 1 ? 1024 : kMaxThr)
                 unpack(now.y[s], f);
                 unpack(now.z[s], zv);
 #pragma unroll
-                for (int v = 0; v < V; ++v) f[v] *= (rstd * wv[s][v]) * (zv[v] * sigmoid(zv[v]));
+                for (int v = 0; v < V; ++v) f[v] *= (rstd * wv[s][v]) * (zv[v] * sigmoid<T>(zv[v]));
                 store_v<T, V>(out + (int64_t)row * dim + (col + e), f);
             }
         }
@@ -482,7 +494,7 @@ __global__ void __launch_bounds__(V == 8 && S == 1 ? 640 : kMaxThr)
                 unpack(now.d[s], dv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    sg[s][v] = sigmoid(zv[v]);
+                    sg[s][v] = sigmoid<T>(zv[v]);
                     const float gate = zv[v] * sg[s][v];
                     const float a = kGateFirst ? yv[v] * gate : yv[v];             // what is normalised
                     const float b = wv[s][v] * dv[v] * (kGateFirst ? 1.f : gate);  // its cotangent

@@ -251,3 +251,37 @@ def test_block_core_gradients(cuda_device):
     pairs += [(ga[m], r_ga[m], m) for m in ("dres", "dx", "dw", "dscale")]
     for got, ref, name in pairs:
         assert np.linalg.norm(to_np(got) - ref) <= 5 * TOL[torch.float32] * np.linalg.norm(ref), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gate_of_negative_values(cuda_device, dtype):
+    """Where the gate is small, against each value's own size. Half steps u = 2^-24: the exponential 4 u, the quotient 2 u,
+    the square root 4 u, sums of 64 squares in eights and three exchanges 11 / 2 u, and a dozen products and sums: below
+    32 u = 2^-19; the output's rounding to bf16 2^-8 more. dz of the norm-first order has the same factors."""
+    r = np.random.default_rng(5)
+    rows, dim, groups = 300, 512, 8
+    y, do, w = normal(r, (rows, dim), dtype), normal(r, (rows, dim), dtype), normal(r, dim, "f32", 1.0, 0.1)
+    z = Tensor(r.uniform(-80.0, -10.0, (rows, dim)), dtype)
+    yt, zt, wt, dot = (v.torch(cuda_device) for v in (y, z, w, do))
+    out = ssd.ssd_norm_gate(yt, zt, wt, ngroups=groups, eps=EPS)
+    dz = ssd.ssd_norm_gate_bwd(yt, zt, wt, dot, ngroups=groups, eps=EPS)["dz"]
+    torch.cuda.synchronize()
+    off = 2.0 ** -19 + (2.0 ** -8 if dtype == "bf16" else 0.0)
+    ref = oracle.gate_norm_backward(y.value, z.value, w.value, do.value, ngroups=groups, eps=EPS, gate_first=False)["dz"]
+    for got, want in ((out, oracle.norm_gate(y.value, z.value, w.value, ngroups=groups, eps=EPS)), (dz, ref)):
+        assert np.all(np.abs(to_np(got) - want) <= off * np.abs(want))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gate_at_its_ends(cuda_device, dtype):
+    """Large and infinite z: the gate is z or 0, and a NaN stays in its channel."""
+    z = torch.tensor([[100.0, 1e4, float("inf"), -100.0, -1e4, float("nan"), 0.0, 1.0]], device=cuda_device)
+    y = torch.ones(1, 8, device=cuda_device)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    out = ssd.ssd_norm_gate(y.to(dt), z.to(dt), torch.ones(8, device=cuda_device), ngroups=1, eps=0.0).float()
+    torch.cuda.synchronize()
+    want = torch.tensor([100.0, 1e4, float("inf"), 0.0, 0.0, float("nan"), 0.0, 1 / (1 + np.exp(-1.0))], dtype=torch.float32,
+                        device=cuda_device)
+    assert torch.equal(torch.isnan(out[0]), torch.isnan(want))
+    fine = ~torch.isnan(want)
+    assert torch.allclose(out[0][fine], want[fine], rtol=2.0 ** -8 if dtype == "bf16" else 2.0 ** -19, atol=1e-30)
