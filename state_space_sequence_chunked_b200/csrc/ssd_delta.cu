@@ -849,7 +849,8 @@ cudaError_t delta_group_sum_launch(const DeltaProblem &p, const float *dB_part, 
     const int64_t rows = p.B * p.L * p.G;
     const int V = p.N % 4 ? 1 : 4, at_once = (int)(kThr / (p.N / V));
     const int64_t blocks = (rows + at_once - 1) / at_once;
-    const unsigned grid = (unsigned)(blocks < 148 * 8 ? blocks : 148 * 8);
+    const int64_t most = (int64_t)sm_count() * 8;
+    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
     const auto go = [&](auto kernel, auto *b, auto *c) {
         kernel<<<grid, kThr, 0, s>>>(dB_part, dC_part, rows, (int)(p.H / p.G), (int)p.N, b, c);
     };

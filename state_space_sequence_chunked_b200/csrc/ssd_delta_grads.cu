@@ -509,15 +509,15 @@ cudaError_t launch(const DeltaProblem &p, const DeltaGrads &g, const DeltaChain 
 
 }  // namespace
 
-// Slices of a group's heads: the number that makes (waves of CTAs on 148 SMs) x (heads a CTA walks)
+// Slices of a group's heads: the number that makes (waves of CTAs on the SMs) x (heads a CTA walks)
 // smallest, the fewest of them unless more save an eighth (more than one costs fp32 parts and a second
 // pass).
 int delta_grads_slices(const DeltaProblem &p) {
-    const int64_t units = (p.L + kC - 1) / kC * p.G * p.B, per = p.H / p.G;
+    const int64_t units = (p.L + kC - 1) / kC * p.G * p.B, per = p.H / p.G, sms = sm_count();
     int best = 1;
-    int64_t cost = (units + 147) / 148 * per;
+    int64_t cost = (units + sms - 1) / sms * per;
     for (int s = 2; s <= per && s <= 16; ++s) {
-        const int64_t here = (units * s + 147) / 148 * ((per + s - 1) / s);
+        const int64_t here = (units * s + sms - 1) / sms * ((per + s - 1) / s);
         if (here * 8 < cost * 7) cost = here, best = s;
     }
     return best;

@@ -410,7 +410,8 @@ cudaError_t prep_launch(const DeltaProblem &p, char *ws, int *clear, int nclear,
     const int per = (int)(p.H / p.G);
     // a CTA walks all heads of a group while that leaves 4 CTAs (what fits) for every SM, and
     // four heads at least, one per warp
-    int slices = units >= 148 * 4 ? 1 : (int)((148 * 4 + units - 1) / units);
+    const int64_t fit = (int64_t)sm_count() * 4;
+    int slices = units >= fit ? 1 : (int)((fit + units - 1) / units);
     if (slices > (per + 3) / 4) slices = (per + 3) / 4;
     cudaError_t e;
     constexpr int smem = sizeof(PrepSmem<NT>);
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(kThr) k_delta_repack(const __grid_constant__ R
     else repack_rows<float>(r);
 }
 cudaError_t repack(const Repacks &c, cudaStream_t s) {
-    k_delta_repack<<<dim3(148 * 8, (unsigned)c.n), kThr, 0, s>>>(c);
+    k_delta_repack<<<dim3((unsigned)(sm_count() * 8), (unsigned)c.n), kThr, 0, s>>>(c);
     return cudaGetLastError();
 }
 
@@ -584,7 +585,7 @@ cudaError_t bwd_of(const DeltaProblem &p, const DeltaGrads &g, char *ws, cudaStr
 // 16: 25.9 against 28.6, 24: 36.1 against 28.6; 32 sequences of 80 heads, 2: 143 against 127. Copies of odd sizes cost two
 // launches more. The backward pass gains at every length (8 tokens of 24 heads: 80 against 54 us).
 bool delta_mma_supported(const DeltaProblem &p, bool backward) {
-    const int64_t per_sm = (p.B * p.H * ((p.P + 15) / 16) + 147) / 148, least = whole(p) ? 128 : 256;
+    const int64_t sms = sm_count(), per_sm = (p.B * p.H * ((p.P + 15) / 16) + sms - 1) / sms, least = whole(p) ? 128 : 256;
     if (!backward && p.L < least && p.L * per_sm < least) return false;
     // Below 8 rows or columns a padded tile is mostly zeros, and an output of few numbers can be small against the terms
     // that cancel in it, which are kept to 2^-17: fp32 there.

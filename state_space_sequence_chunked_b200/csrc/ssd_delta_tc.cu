@@ -1185,7 +1185,7 @@ cudaError_t bwd(const DeltaProblem &p, const DeltaGrads &g, const DeltaChain &ch
 // One CTA per SM (it takes all of TMEM), or per stream where there are fewer; half of them for each of
 // the backward pass's two chains.
 int delta_tc_grid(const DeltaProblem &p, bool backward) {
-    const int sms = num_sms() > 0 ? num_sms() : 148, most = backward ? sms / 2 : sms;
+    const int sms = sm_count(), most = backward ? sms / 2 : sms;
     const int64_t streams = streams_of(p);
     return (int)(streams < most ? streams : most) * (backward ? 2 : 1);
 }

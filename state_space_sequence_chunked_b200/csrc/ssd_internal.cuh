@@ -46,6 +46,13 @@ struct CpProblem {
 constexpr size_t kWsAlign = 256;
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
+// SMs of the current device; 148, a B200's, where there is none (plans made without a GPU).
+inline int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) n = 0;
+    return n > 0 ? n : 148;
+}
+
 // ---- argument rules shared by every forward entry point ----------------------------
 constexpr int64_t kMaxDim = 256;       // headdim, dstate
 constexpr int64_t kMaxChunk = 256;

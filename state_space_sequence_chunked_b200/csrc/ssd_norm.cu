@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kMaxThr = 512;
 constexpr int kPer = 16;      // channels a thread may hold
-constexpr int kMaxParts = 592;  // partial rows of a column sum: 4 CTAs per SM
+constexpr int kMaxParts = 592;  // partial rows of a column sum at most: 4 CTAs on each of 148 SMs
 
 struct Geom {
     uint32_t rows;  // below 2^31, so that a step past the end does not wrap
@@ -600,7 +600,7 @@ Launch geom(K kernel, int64_t rows, int gs, int ngroups, int V, int S, int U, si
     int fit = 1;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, thr, l.smem) != cudaSuccess || fit < 1) fit = 1;
     int64_t gy = (rows + rpc * U - 1) / (rpc * U);
-    const int64_t most = 148 * fit / gx > 1 ? 148 * fit / gx : 1;
+    const int64_t wave = (int64_t)sm_count() * fit, most = wave / gx > 1 ? wave / gx : 1;
     if (gy > most) gy = most;
     if (gy > kMaxParts) gy = kMaxParts;
     l.q = Geom{(uint32_t)rows, gs, ngroups, tpg, gpc, rpc, (float)(1.0 / gs)};

@@ -1,6 +1,8 @@
 """The gated delta rule's and the norms' entry points without a GPU: plans and refusals, all before
 anything is launched."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -233,3 +235,13 @@ def test_plan_rule(lib):
     for size in ((4, 264, 1, 16), (4, 16, 1, 264)):
         with pytest.raises(B.SSDError):
             B.delta_fwd_plan(1, 131, *size, B.SSD_BF16)
+
+
+def test_grids_ask_the_device():
+    """The launch rules of these kernels take the number of SMs from the device, not from a constant."""
+    csrc = os.path.join(os.path.dirname(B.LIB_PATH), "csrc")
+    for name in sorted(os.listdir(csrc)):
+        if name.startswith(("ssd_delta", "ssd_norm", "delta_tc")):
+            with open(os.path.join(csrc, name)) as f:
+                code = re.sub(r"//[^\n]*", "", f.read())
+            assert not re.search(r"\b14[78]\b", code), name
