@@ -404,7 +404,7 @@ ssd_status_t ssd_gated_rmsnorm(int64_t rows, int64_t dim, int64_t ngroups, ssd_d
  * that is no multiple of 8 from 256 tokens on, on padded copies in the workspace) or SSD_PATH_SIMT
  * (everything else: four tokens at a time in fp32). On SSD_PATH_TCGEN05
  * a value that is not finite stays in its head (but for the keys and queries that heads share), and may
- * also reach the tokens before it in its block of 16: what pads a sequence has to be finite. There
+ * also reach the other tokens of its block of 16: what pads a sequence has to be finite. There
  * the warps of a CTA wait on one another through bounded waits, as in ssd_fwd; ssd_delta_status, called
  * with the shape and workspace of an ssd_delta_fwd or ssd_delta_bwd (NULL if its plan has none),
  * synchronizes `stream` and returns SSD_ERR_TIMEOUT if one ran out (outputs are then incomplete),
