@@ -359,18 +359,30 @@ constexpr int kTp = kSeg + 4;  // padded token stride of the transposed arrays (
 // row stride of keys and queries: 4 modulo 32 floats, so that 8 rows' 16-byte vectors fall in different banks
 __host__ __device__ constexpr int grads_stride(int N) { return N <= 4 ? 4 : (N - 4 + 31) / 32 * 32 + 4; }
 
+// err or z as the sequential kernels leave them, or in two parts
+template <typename T, bool kParts>
+struct Row {
+    const float *v;
+    __device__ __forceinline__ float operator[](int64_t i) const { return __ldg(v + i); }
+};
+template <typename T>
+struct Row<T, true> {
+    const T *hi, *lo;
+    __device__ __forceinline__ float operator[](int64_t i) const { return to_f32(hi[i]) + to_f32(lo[i]); }
+};
 template <int NJ>
 struct GradsTile {
     static constexpr int TK = NJ >= 4 ? 4 : 8, groups = kSeg / TK, split = kWarps / groups;  // tokens; warps by tokens, by rows
     static constexpr int U = NJ <= 2 ? 8 : 2;  // rows of S and D in flight
 };
 
-template <typename T, int NJ>
+template <typename T, int NJ, bool kParts>
 __global__ void __launch_bounds__(kThr)
     k_delta_grads(const T *__restrict__ dy, const T *__restrict__ g, const T *__restrict__ beta, const T *__restrict__ Bm,
                   const T *__restrict__ Cm, const float *__restrict__ seg_states, const float *__restrict__ seg_cot,
-                  const float *__restrict__ err, const float *__restrict__ zz, int64_t L, int H, int P, int G, int N,
-                  float *__restrict__ dB_part, float *__restrict__ dC_part, T *__restrict__ dg, T *__restrict__ dbeta) {
+                  const Row<T, kParts> err, const Row<T, kParts> zz, int64_t L, int H, int P, int G, int N,
+                  float *__restrict__ dB_part, float *__restrict__ dC_part, T *__restrict__ dg, T *__restrict__ dbeta,
+                  T *__restrict__ dx) {
     using Z = GradsTile<NJ>;
     constexpr int TK = Z::TK, PS = Z::split;
     extern __shared__ __align__(16) float sm[];
@@ -434,6 +446,7 @@ __global__ void __launch_bounds__(kThr)
                 dyT[p * kTp + t] = yv[e];
                 uT[p * kTp + t] = bt[t] * ev[e];
                 rT[p * kTp + t] = bt[t] * zv[e];
+                if (kParts && t < nt) store_as(dx + (((int64_t)b * L + t0 + t) * H + h) * P + p, bt[t] * zv[e]);
                 d[e] = fmaf(zv[e], ev[e], d[e]);
             }
         }
@@ -476,8 +489,8 @@ __global__ void __launch_bounds__(kThr)
             if (j == i) wM[i * kTp + i] = 0.f;
         }
     }
-    const float *S = seg_states + (((int64_t)b * H + h) * ns + c) * P * N;
-    const float *D = seg_cot + (((int64_t)b * H + h) * ns + c) * P * N;
+    const int64_t seg_at = (((int64_t)b * H + h) * ns + c) * P * N;
+    const float *S = seg_states ? seg_states + seg_at : nullptr, *D = seg_cot ? seg_cot + seg_at : nullptr;  // (NULL: zeros)
     const int tg = warp % Z::groups, ps = warp / Z::groups, tk0 = TK * tg;  // this warp's tokens; its share of the rows
     float2 fq[TK / 2][NJ], fk[TK / 2][NJ], fu[TK / 2][NJ];
 #pragma unroll
@@ -497,8 +510,8 @@ __global__ void __launch_bounds__(kThr)
                 const int n = lane + 32 * j;
                 const bool in = n < N && p0 + i < p_end;
                 const int64_t at = in ? (int64_t)(p0 + i) * N + n : 0;
-                to.s[i][j] = in ? S[at] : 0.f;
-                to.d[i][j] = in ? D[at] : 0.f;
+                to.s[i][j] = in && S ? S[at] : 0.f;
+                to.d[i][j] = in && D ? D[at] : 0.f;
             }
     };
     Rows next;
@@ -769,18 +782,17 @@ size_t grads_smem(const DeltaProblem &p) {
     return sizeof(float) * (tiles > joined ? tiles : joined);
 }
 
-template <typename T, int NJ>
-cudaError_t grads_launch(const DeltaProblem &p, const DeltaGrads &gr, const float *states, const float *cot, const float *err,
-                         const float *z, float *dB, float *dC, cudaStream_t s) {
+template <typename T, int NJ, bool kParts>
+cudaError_t grads_launch(const DeltaProblem &p, const DeltaGrads &gr, const float *states, const float *cot, Row<T, kParts> err,
+                         Row<T, kParts> z, float *dB, float *dC, cudaStream_t s) {
     const size_t smem = grads_smem<NJ>(p);
-    const cudaError_t e = cudaFuncSetAttribute(k_delta_grads<T, NJ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(k_delta_grads<T, NJ, kParts>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e) return e;
     dim3 grid((unsigned)((p.L + kSeg - 1) / kSeg), (unsigned)p.H, (unsigned)p.B);
-    k_delta_grads<T, NJ><<<grid, kThr, smem, s>>>(static_cast<const T *>(gr.dy), static_cast<const T *>(p.g),
-                                                  static_cast<const T *>(p.beta), static_cast<const T *>(p.Bm),
-                                                  static_cast<const T *>(p.Cm), states, cot, err, z, p.L, (int)p.H, (int)p.P,
-                                                  (int)p.G, (int)p.N, dB, dC, static_cast<T *>(gr.dg),
-                                                  static_cast<T *>(gr.dbeta));
+    k_delta_grads<T, NJ, kParts><<<grid, kThr, smem, s>>>(
+        static_cast<const T *>(gr.dy), static_cast<const T *>(p.g), static_cast<const T *>(p.beta), static_cast<const T *>(p.Bm),
+        static_cast<const T *>(p.Cm), states, cot, err, z, p.L, (int)p.H, (int)p.P, (int)p.G, (int)p.N, dB, dC,
+        static_cast<T *>(gr.dg), static_cast<T *>(gr.dbeta), static_cast<T *>(gr.dx));
     return cudaGetLastError();
 }
 
@@ -823,7 +835,7 @@ cudaError_t bwd_typed(const DeltaProblem &p, const DeltaGrads &gr, void *ws, cud
     const auto both_of = [&](auto nj) {
         constexpr int NJ = decltype(nj)::value;
         const cudaError_t f = seq_bwd_launch<T, NJ>(p, gr, z, cot, s);
-        return f ? f : grads_launch<T, NJ>(p, gr, states, cot, err, z, dB, dC, s);
+        return f ? f : grads_launch<T, NJ, false>(p, gr, states, cot, Row<T, false>{err}, Row<T, false>{z}, dB, dC, s);
     };
     if (p.N <= 32) e = both_of(std::integral_constant<int, 1>());
     else if (p.N <= 64) e = both_of(std::integral_constant<int, 2>());
@@ -864,6 +876,16 @@ cudaError_t delta_group_sum_launch(const DeltaProblem &p, const float *dB_part, 
 
 cudaError_t delta_seq_fwd(const DeltaProblem &p, cudaStream_t s) {
     return p.dtype == SSD_F32 ? seq_typed<float>(p, nullptr, nullptr, s) : seq_typed<__nv_bfloat16>(p, nullptr, nullptr, s);
+}
+
+cudaError_t delta_short_grads(const DeltaProblem &p, const DeltaGrads &g, const DeltaParts &parts, float *dB, float *dC,
+                              cudaStream_t s) {
+    using bf = __nv_bfloat16;
+    const Row<bf, true> err{static_cast<const bf *>(parts.err), static_cast<const bf *>(parts.err_lo)};
+    const Row<bf, true> z{static_cast<const bf *>(parts.z), static_cast<const bf *>(parts.z_lo)};
+    if (p.N <= 32) return grads_launch<bf, 1, true>(p, g, p.h0, g.dh_final, err, z, dB, dC, s);
+    if (p.N <= 64) return grads_launch<bf, 2, true>(p, g, p.h0, g.dh_final, err, z, dB, dC, s);
+    return grads_launch<bf, 4, true>(p, g, p.h0, g.dh_final, err, z, dB, dC, s);
 }
 
 size_t delta_seq_bwd_workspace_bytes(const DeltaProblem &p) { return bwd_layout(p).total; }

@@ -24,6 +24,11 @@ struct DeltaGrads {
 };
 
 constexpr int kSeg = 32;  // tokens per segment of the general backward
+// What the gradients that sum over state rows need of sequences of at most kSeg tokens, err and z each in two bf16
+// parts [B, L, H, P] (their states are the initial one and the final one's cotangent).
+struct DeltaParts {
+    const void *err, *err_lo, *z, *z_lo;
+};
 
 // A log decay as it enters a cumulated sum: exp of anything below is 0 in fp32 all the same, and a
 // decay of minus infinity (a reset of the state) must not turn differences of sums into NaN.
@@ -33,6 +38,8 @@ __device__ __forceinline__ double clamp_log_decay(float g) { return g < -1e4f ? 
 cudaError_t delta_seq_fwd(const DeltaProblem &p, cudaStream_t s);
 size_t delta_seq_bwd_workspace_bytes(const DeltaProblem &p);
 cudaError_t delta_seq_bwd(const DeltaProblem &p, const DeltaGrads &g, void *ws, cudaStream_t s);
+// dx, dg, dbeta and the per-head fp32 parts of dB, dC [B, L, H, N] of bf16 sequences of at most kSeg tokens
+cudaError_t delta_short_grads(const DeltaProblem &p, const DeltaGrads &g, const DeltaParts &parts, float *dB, float *dC, cudaStream_t s);
 // dBm, dCm [B, L, G, N] from per-head fp32 parts [B, L, H, N], added in head order
 cudaError_t delta_group_sum_launch(const DeltaProblem &p, const float *dB_part, const float *dC_part, void *dBm, void *dCm,
                                    cudaStream_t s);
@@ -48,14 +55,15 @@ cudaError_t delta_mma_bwd(const DeltaProblem &p, const DeltaGrads &g, void *ws, 
 
 // The chains over the chunks on tcgen05 (ssd_delta_tc.cu), after k_delta_prep: the forward's, or the
 // backward pass's recomputation and reverse chain together. states and cots [B, H, chunks, P, N], err, u
-// and z [B, L, H, P], bf16, are the latter's.
+// and z [B, L, H, P], bf16, are the latter's; with z_lo there, no states and cotangents leave the chains, nor dx, but
+// err and z in two parts each, err's second in the place of u.
 struct DeltaChain {
     const char *prep;
     int64_t prep_bytes;    // per chunk and head
     int scal_at, rows_at;  // the backward pass: the scalars; W and P by rows of blocks
     int *status, *flags;   // cleared before: the status word, a counter per CTA
     float *hand;           // delta_tc_hand_bytes
-    void *states, *err, *u, *cots, *z;
+    void *states, *err, *u, *cots, *z, *z_lo;
 };
 int delta_tc_grid(const DeltaProblem &p, bool backward);
 size_t delta_tc_hand_bytes(const DeltaProblem &p, bool backward);

@@ -438,19 +438,28 @@ cudaError_t fwd_launch(const DeltaProblem &p, char *ws, cudaStream_t s) {
     const cudaError_t e = prep_launch<NT, false>(p, prep, status, (int)(at / sizeof(int)), s);
     return e ? e
              : delta_tc_fwd(p, DeltaChain{prep, L::bytes, L::scal, 0, status, status + kWsAlign / sizeof(int),
-                                          reinterpret_cast<float *>(ws + at), nullptr, nullptr, nullptr, nullptr, nullptr},
+                                          reinterpret_cast<float *>(ws + at), nullptr, nullptr, nullptr, nullptr, nullptr, nullptr},
                             s);
 }
 
 // Workspace of the backward pass, as byte offsets.
 struct BwdLayout {
-    size_t hand, prep, states, cots, err, u, z, dB, dC, total;
+    size_t hand, prep, states, cots, err, u, z, z_lo, dB, dC, total;
 };
+// Short sequences keep err and z to 2^-16 and sum over the state rows in fp32 (k_delta_grads in ssd_delta.cu, whose
+// segment they fit): where dB, dC, dg and dbeta are made of few numbers, these can be small against the terms that
+// cancel in them, and bf16 operands (2^-9) then show. Drawn cases with an output off by more than 3 * 2^-8 on bf16 operands, of 150
+// each: 1 token of 1, 4, 16 heads 32, 13, 8; 2 tokens 14, 2, 2; 8 tokens 3, 0, 0; 32 tokens none (beyond 2^-8.6: 9, 6, 1); in fp32
+// none, and no error above 3.5e-3. It costs 72 us against 47 (24 heads of 64 x 128, 1 token), and 427 against 183 (16 x 80 heads,
+// 8 tokens, where it is not taken).
+bool in_parts(const DeltaProblem &p) { return p.L < 4 || (p.L <= kSeg && p.B * p.H < 16); }
 BwdLayout bwd_layout(const DeltaProblem &p) {
     const size_t chunks = (size_t)(p.B * p.H) * (size_t)((p.L + kC - 1) / kC);
     const size_t rows = (size_t)(p.B * p.L * p.H * p.P) * 2;
     const int slices = delta_grads_slices(p);
-    const size_t part = slices > 1 ? (size_t)(p.B * p.L * p.G * slices * p.N) * 4 : 0;
+    const size_t part = in_parts(p) ? (size_t)(p.B * p.L * p.H * p.N) * 4
+                        : slices > 1 ? (size_t)(p.B * p.L * p.G * slices * p.N) * 4 : 0;
+    const size_t state = in_parts(p) ? 0 : chunks * (size_t)(p.P * p.N) * 2;
     BwdLayout l{};
     size_t at = head_bytes(p, true);
     const auto take = [&](size_t bytes) {
@@ -460,11 +469,12 @@ BwdLayout bwd_layout(const DeltaProblem &p) {
     };
     l.hand = take(delta_tc_hand_bytes(p, true));
     l.prep = take(chunks * Prep<true>::bytes);
-    l.states = take(chunks * (size_t)(p.P * p.N) * 2);
-    l.cots = take(chunks * (size_t)(p.P * p.N) * 2);
+    l.states = take(state);
+    l.cots = take(state);
     l.err = take(rows);
     l.u = take(rows);
     l.z = take(rows);
+    l.z_lo = take(in_parts(p) ? rows : 0);
     l.dB = take(part);
     l.dC = take(part);
     l.total = at;
@@ -483,8 +493,12 @@ cudaError_t bwd_launch(const DeltaProblem &p, const DeltaGrads &gr, char *ws, cu
     int *status = reinterpret_cast<int *>(ws);
     cudaError_t e = prep_launch<NT, true>(p, ws + l.prep, status, (int)(head_bytes(p, true) / sizeof(int)), s);
     const DeltaChain ch{prep, Lay::bytes, Lay::scal, Lay::Wr, status, status + kWsAlign / sizeof(int),
-                        reinterpret_cast<float *>(ws + l.hand), states, err, u, cots, z};
+                        reinterpret_cast<float *>(ws + l.hand), states, err, u, cots, z, in_parts(p) ? ws + l.z_lo : nullptr};
     if (!e) e = delta_tc_bwd(p, gr, ch, s);
+    if (in_parts(p)) {
+        if (!e) e = delta_short_grads(p, gr, DeltaParts{err, u, z, ch.z_lo}, dB, dC, s);
+        return e ? e : delta_group_sum_launch(p, dB, dC, gr.dBm, gr.dCm, s);
+    }
     if (!e) e = delta_grads(p, gr, ch, dB, dC, s);
     const int slices = delta_grads_slices(p);
     if (e || slices == 1) return e;
@@ -626,7 +640,9 @@ size_t delta_mma_bwd_workspace_bytes(const DeltaProblem &p) {
     const DeltaProblem q = padded(p);
     return copies_of(q, bwd_layout(q).total, true).total;
 }
-int delta_mma_bwd_kernels(const DeltaProblem &p) { return (delta_grads_slices(p) > 1 ? 4 : 3) + (whole(p) ? 0 : 2); }
+int delta_mma_bwd_kernels(const DeltaProblem &p) {
+    return (in_parts(p) || delta_grads_slices(p) > 1 ? 4 : 3) + (whole(p) ? 0 : 2);
+}
 
 cudaError_t delta_mma_bwd(const DeltaProblem &p, const DeltaGrads &g, void *ws, cudaStream_t s) {
     char *w = static_cast<char *>(ws);

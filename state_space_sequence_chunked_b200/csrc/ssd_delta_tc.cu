@@ -34,7 +34,8 @@
 //
 // kStore is the backward pass's recomputation: no Y, but the state entering each chunk, err and u, rounded to bf16:
 // they meet operands that are bf16 already (K, Q, dY) in gradients that are stored in bf16 (relative errors of
-// 3.2e-3 against 1.7e-3 for the storage alone); fp32 would double the pass's largest traffic.
+// 3.2e-3 against 1.7e-3 for the storage alone); fp32 would double the pass's largest traffic. kParts, for short
+// sequences (see kSeg in ssd_delta_mma.cu), leaves err in two bf16 parts alone.
 //
 // Every wait is bounded (tc_ptx.cuh); one that runs out sets bit 0 of the workspace's status word.
 #include "delta_tc.cuh"
@@ -174,7 +175,7 @@ __device__ __forceinline__ void put_pairs(const uint32_t (&o)[32], unsigned char
     }
 }
 
-template <int NT, bool PAIR, bool kStore>
+template <int NT, bool PAIR, bool kStore, bool kParts>
 __device__ __forceinline__ void chain_fwd(const CUtensorMap &tm_k, const CUtensorMap &tm_q, const CUtensorMap &tm_x,
                                           const CUtensorMap &tm_o0, const CUtensorMap &tm_o1, const CUtensorMap &tm_s,
                                           const ChainArgs &a, int cta, int ctas) {
@@ -369,7 +370,7 @@ __device__ __forceinline__ void chain_fwd(const CUtensorMap &tm_k, const CUtenso
                 const float *eg = scal_of(k, e), *ek = eg + kC, *bt = eg + 2 * kC;
                 if (it > 0) {
                     if (!wait_warp(rdyS, par ^ 1u, abort_flag, status)) break;
-                    if (kStore && !wait_warp(ost, par ^ 1u, abort_flag, status)) break;
+                    if (kStore && !kParts && !wait_warp(ost, par ^ 1u, abort_flag, status)) break;
                     tc_fence_after();
                 }
                 // The state's operands; then, while S K^T runs, the state times exp(cum_end) for the next product to
@@ -479,7 +480,10 @@ __device__ __forceinline__ void chain_fwd(const CUtensorMap &tm_k, const CUtenso
                     for (int i = 0; i < 16; i += 4) {
                         const float4 b4 = *reinterpret_cast<const float4 *>(bt + tk0 + i);
                         const float u[4] = {b4.x * R[i], b4.y * R[i + 1], b4.z * R[i + 2], b4.w * R[i + 3]};
-                        if constexpr (kStore) {  // u and err go out rounded; no product here takes u itself
+                        if constexpr (kParts) {
+                            split2(R[i], R[i + 1], hi[i / 2], lw[i / 2]);
+                            split2(R[i + 2], R[i + 3], hi[i / 2 + 1], lw[i / 2 + 1]);
+                        } else if constexpr (kStore) {  // u and err go out rounded; no product here takes u itself
                             hi[i / 2] = pack_bf16(u[0], u[1]), hi[i / 2 + 1] = pack_bf16(u[2], u[3]);
                             lw[i / 2] = pack_bf16(R[i], R[i + 1]), lw[i / 2 + 1] = pack_bf16(R[i + 2], R[i + 3]);
                         } else {
@@ -558,21 +562,23 @@ __device__ __forceinline__ void chain_fwd(const CUtensorMap &tm_k, const CUtenso
                         mbar_arrive(&sfree[k]);
                     }
                     if (!wait_warp(rdyY, par, abort_flag, status)) break;
-                } else {  // the entering state, as S hi holds it
-                    if (!wait_warp(sb, par, abort_flag, status)) break;
-                    tc_fence_after();
-                    if (lane == 0) bulk_wait_read();  // the staging's last store has read it
-                    __syncwarp();
-                    put_state<NT>(lo_ + kTmHi, stage2, lane);
-                    tc_fence_before();
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(ost);
-                    if (lane == 0 && p0 < a.P) {
-                        const int unit = (b * a.H + h + e) * nc + c;
-                        for (int pn = 0; pn < NT / 64; ++pn)
-                            if (64 * pn < a.N) tma_store_4d(&tm_s, stage2 + pn * 4096, 64 * pn, p0, unit, 0, pol);
-                        bulk_commit();
+                } else {
+                    if constexpr (!kParts) {  // the entering state, as S hi holds it
+                        if (!wait_warp(sb, par, abort_flag, status)) break;
+                        tc_fence_after();
+                        if (lane == 0) bulk_wait_read();  // the staging's last store has read it
+                        __syncwarp();
+                        put_state<NT>(lo_ + kTmHi, stage2, lane);
+                        tc_fence_before();
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(ost);
+                        if (lane == 0 && p0 < a.P) {
+                            const int unit = (b * a.H + h + e) * nc + c;
+                            for (int pn = 0; pn < NT / 64; ++pn)
+                                if (64 * pn < a.N) tma_store_4d(&tm_s, stage2 + pn * 4096, 64 * pn, p0, unit, 0, pol);
+                            bulk_commit();
+                        }
                     }
                     if (!wait_warp(yu, par, abort_flag, status)) break;
                 }
@@ -589,7 +595,7 @@ __device__ __forceinline__ void chain_fwd(const CUtensorMap &tm_k, const CUtenso
                         __syncwarp();
                         if (lane == 0) mbar_arrive(ofree);
                     }
-                    if constexpr (kStore) {  // pairs of tokens: u, then err
+                    if constexpr (kStore) {  // pairs of tokens: u, then err; or err's parts
                         put_pairs(o, half ? stage1 : stage0, lane);
                     } else {
 #pragma unroll
@@ -647,7 +653,7 @@ __device__ __forceinline__ uint64_t tri_rows(uint32_t tile, int a) {
     return (uint64_t)(((tile + 512 * (a * (a + 1) / 2)) >> 4) & 0x3FFFu) | (uint64_t)(kTriLbo >> 4) << 16 |
            (uint64_t)(kTriSbo >> 4) << 32 | (uint64_t)1 << 46;
 }
-template <int NT, bool PAIR>
+template <int NT, bool PAIR, bool kParts>
 __device__ __forceinline__ void chain_rev(const CUtensorMap &tm_k, const CUtensorMap &tm_q, const CUtensorMap &tm_dy,
                                           const CUtensorMap &tm_z, const CUtensorMap &tm_dx, const CUtensorMap &tm_d,
                                           const ChainArgs &a, int cta, int ctas) {
@@ -877,7 +883,7 @@ __device__ __forceinline__ void chain_rev(const CUtensorMap &tm_k, const CUtenso
                 const float *eg = scal_of(k, e), *ek = eg + kC, *bt = eg + 2 * kC;
                 if (it > 0) {
                     if (!wait_warp(rdyS, par ^ 1u, abort_flag, status)) break;
-                    if (!wait_warp(ost, par ^ 1u, abort_flag, status)) break;
+                    if (!kParts && !wait_warp(ost, par ^ 1u, abort_flag, status)) break;
                     tc_fence_after();
                 }
                 {  // D's operands; then D times exp(cum_end)
@@ -981,9 +987,14 @@ __device__ __forceinline__ void chain_rev(const CUtensorMap &tm_k, const CUtenso
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(ub);
-                    // z and dX, rounded, over Z (which every T warp has read by now)
+                    // z and dX, rounded, or z's parts, over Z (which every T warp has read by now)
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
+                        if constexpr (kParts) {
+                            split2(F[i], F[i + 1], hi[i / 2], lw[i / 2]);
+                            split2(F[i + 2], F[i + 3], hi[i / 2 + 1], lw[i / 2 + 1]);
+                            continue;
+                        }
                         const float4 b4 = *reinterpret_cast<const float4 *>(bt + tk0 + i);
                         hi[i / 2] = pack_bf16(F[i], F[i + 1]), hi[i / 2 + 1] = pack_bf16(F[i + 2], F[i + 3]);
                         lw[i / 2] = pack_bf16(b4.x * F[i], b4.y * F[i + 1]), lw[i / 2 + 1] = pack_bf16(b4.z * F[i + 2], b4.w * F[i + 3]);
@@ -1025,20 +1036,22 @@ __device__ __forceinline__ void chain_rev(const CUtensorMap &tm_k, const CUtenso
             for (; t < sg.c1; ++t, ++it) {
                 const int c = nc - 1 - t;
                 const uint32_t par = (uint32_t)it & 1u;
-                if (!wait_warp(sb, par, abort_flag, status)) break;
-                tc_fence_after();
-                if (lane == 0) bulk_wait_read();
-                __syncwarp();
-                put_state<NT>(lo_ + kTmHi, stage, lane);
-                tc_fence_before();
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(ost);
-                if (lane == 0 && p0 < a.P) {
-                    const int unit = (b * a.H + h + e) * nc + c;
-                    for (int pn = 0; pn < NT / 64; ++pn)
-                        if (64 * pn < a.N) tma_store_4d(&tm_d, stage + pn * 4096, 64 * pn, p0, unit, 0, pol);
-                    bulk_commit();
+                if constexpr (!kParts) {
+                    if (!wait_warp(sb, par, abort_flag, status)) break;
+                    tc_fence_after();
+                    if (lane == 0) bulk_wait_read();
+                    __syncwarp();
+                    put_state<NT>(lo_ + kTmHi, stage, lane);
+                    tc_fence_before();
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ost);
+                    if (lane == 0 && p0 < a.P) {
+                        const int unit = (b * a.H + h + e) * nc + c;
+                        for (int pn = 0; pn < NT / 64; ++pn)
+                            if (64 * pn < a.N) tma_store_4d(&tm_d, stage + pn * 4096, 64 * pn, p0, unit, 0, pol);
+                        bulk_commit();
+                    }
                 }
                 if (!wait_warp(yu, par, abort_flag, status)) break;
                 tc_fence_after();
@@ -1078,20 +1091,20 @@ struct Maps {
 
 template <int NT, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) k_delta_tc(const __grid_constant__ Maps m, const __grid_constant__ ChainArgs a) {
-    chain_fwd<NT, PAIR, false>(m.k, m.q, m.x, m.o0, m.o1, m.s, a, blockIdx.x, gridDim.x);
+    chain_fwd<NT, PAIR, false, false>(m.k, m.q, m.x, m.o0, m.o1, m.s, a, blockIdx.x, gridDim.x);
 }
 
 // Both chains of the backward pass, which do not depend on one another: the first half of the CTAs
 // recomputes the states, the other half walks back.
-template <int NT, bool PAIR>
+template <int NT, bool PAIR, bool kParts>
 __global__ void __launch_bounds__(kThreads, 1)
     k_delta_tc_bwd(const __grid_constant__ Maps mf, const __grid_constant__ Maps mr, const __grid_constant__ ChainArgs f,
                    const __grid_constant__ ChainArgs r) {
     const int half = gridDim.x / 2;
     if ((int)blockIdx.x < half)
-        chain_fwd<NT, PAIR, true>(mf.k, mf.q, mf.x, mf.o0, mf.o1, mf.s, f, blockIdx.x, half);
+        chain_fwd<NT, PAIR, true, kParts>(mf.k, mf.q, mf.x, mf.o0, mf.o1, mf.s, f, blockIdx.x, half);
     else
-        chain_rev<NT, PAIR>(mr.k, mr.q, mr.x, mr.o0, mr.o1, mr.s, r, blockIdx.x - half, half);
+        chain_rev<NT, PAIR, kParts>(mr.k, mr.q, mr.x, mr.o0, mr.o1, mr.s, r, blockIdx.x - half, half);
 }
 
 // [B, L, X, inner] bf16, boxes of 32 columns by 64 tokens, not swizzled (the O warps' staging).
@@ -1132,7 +1145,7 @@ bool encode_maps(Maps *m, const DeltaProblem &p, const void *x, const void *o0, 
         return false;
     m->o1 = m->o0;
     m->s = m->o0;
-    return !states || (encode_out(&m->o1, o1, p.P, p.H, p.L, p.B) && encode_states(&m->s, states, p.N, p.P, units));
+    return (!o1 || encode_out(&m->o1, o1, p.P, p.H, p.L, p.B)) && (!states || encode_states(&m->s, states, p.N, p.P, units));
 }
 
 template <typename K, typename... A>
@@ -1172,12 +1185,14 @@ cudaError_t fwd(const DeltaProblem &p, const DeltaChain &ch, cudaStream_t s) {
 template <int NT, bool PAIR>
 cudaError_t bwd(const DeltaProblem &p, const DeltaGrads &g, const DeltaChain &ch, cudaStream_t s) {
     Maps mf, mr;
-    if (!encode_maps(&mf, p, p.x, ch.u, ch.err, ch.states) || !encode_maps(&mr, p, g.dy, ch.z, g.dx, ch.cots))
+    const bool parts = ch.z_lo;
+    if (!(parts ? encode_maps(&mf, p, p.x, ch.err, ch.u, nullptr) && encode_maps(&mr, p, g.dy, ch.z, ch.z_lo, nullptr)
+                : encode_maps(&mf, p, p.x, ch.u, ch.err, ch.states) && encode_maps(&mr, p, g.dy, ch.z, g.dx, ch.cots)))
         return cudaErrorInvalidValue;
     const int grid = delta_tc_grid(p, true);
     constexpr int f = Lay<NT, PAIR, true>::bytes, r = RevLay<NT, PAIR>::bytes;
-    return launch(k_delta_tc_bwd<NT, PAIR>, grid, f > r ? f : r, streams_of(p) > grid / 2, s, mf, mr,
-                  args_of(p, ch, p.h0, nullptr, 0), args_of(p, ch, g.dh_final, g.dh0, grid / 2));
+    return launch(parts ? k_delta_tc_bwd<NT, PAIR, true> : k_delta_tc_bwd<NT, PAIR, false>, grid, f > r ? f : r, streams_of(p) > grid / 2,
+                  s, mf, mr, args_of(p, ch, p.h0, nullptr, 0), args_of(p, ch, g.dh_final, g.dh0, grid / 2));
 }
 
 }  // namespace

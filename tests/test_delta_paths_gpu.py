@@ -239,3 +239,21 @@ def test_values_that_are_not_numbers_stay_in_their_head(cuda_device, dtype, shap
         for head in (0, 2, 3):
             assert torch.equal(got[n].select(axis[n], head), want[n].select(axis[n], head)), (n, head)
     assert not all(bool(torch.isfinite(got[n].select(axis[n], 1)).all()) for n in got)
+
+
+@pytest.mark.parametrize("L", [1, 2, 3, 5, 17, 32, 33])
+@pytest.mark.parametrize("size", [(2, 37, 128, 1, 64), (1, 48, 64, 2, 128), (1, 30, 40, 1, 24), (1, 21, 19, 1, 35)], ids=str)
+def test_few_tokens_of_many_heads(cuda_device, L, size):
+    """Gradients made of few numbers, that can be small against the heads' terms that cancel in them: without a state,
+    one token's dB and dC are one number per batch row and group."""
+    for seed in range(12 if L < 4 else 2):
+        d = draw(size[0], L, *size[1:], "bf16", seed=1000 * L + seed, h0=seed % 3 == 0)
+        check_bwd(d, cuda_device, "bf16")
+
+
+@pytest.mark.parametrize("L", [1, 2, 4, 9, 20, 32])
+@pytest.mark.parametrize("size", [(1, 1, 64, 1, 128), (1, 2, 128, 1, 64), (3, 1, 24, 1, 40), (1, 3, 35, 1, 19)], ids=str)
+def test_few_tokens_of_few_heads(cuda_device, L, size):
+    """dg and dbeta are few numbers as well."""
+    for seed in range(10):
+        check_bwd(draw(size[0], L, *size[1:], "bf16", seed=2000 * L + seed, h0=seed % 2 == 0), cuda_device, "bf16")
