@@ -490,7 +490,8 @@ __global__ void __launch_bounds__(kThr)
         }
     }
     const int64_t seg_at = (((int64_t)b * H + h) * ns + c) * P * N;
-    const float *S = seg_states ? seg_states + seg_at : nullptr, *D = seg_cot ? seg_cot + seg_at : nullptr;  // (NULL: zeros)
+    const float *S = seg_states + seg_at, *D = seg_cot + seg_at;
+    const bool has_s = !kParts || seg_states, has_d = !kParts || seg_cot;  // (else zeros)
     const int tg = warp % Z::groups, ps = warp / Z::groups, tk0 = TK * tg;  // this warp's tokens; its share of the rows
     float2 fq[TK / 2][NJ], fk[TK / 2][NJ], fu[TK / 2][NJ];
 #pragma unroll
@@ -510,8 +511,8 @@ __global__ void __launch_bounds__(kThr)
                 const int n = lane + 32 * j;
                 const bool in = n < N && p0 + i < p_end;
                 const int64_t at = in ? (int64_t)(p0 + i) * N + n : 0;
-                to.s[i][j] = in && S ? S[at] : 0.f;
-                to.d[i][j] = in && D ? D[at] : 0.f;
+                to.s[i][j] = in && has_s ? S[at] : 0.f;
+                to.d[i][j] = in && has_d ? D[at] : 0.f;
             }
     };
     Rows next;
