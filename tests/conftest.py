@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -19,3 +20,10 @@ def cuda_device():
     if not torch.cuda.is_available():
         pytest.fail("GPU test run without a CUDA device")
     return torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def nothing_left_of_earlier_modules():
+    """Tensors that earlier tests left in reference cycles are freed here, not in the middle of a test that counts
+    the device memory in use."""
+    gc.collect()
