@@ -444,7 +444,10 @@ ssd_status_t ssd_delta_decode_step(const ssd_shape_t *shape, ssd_dtype_t dtype, 
  *   dBm, dCm  [B, L, G, N]   dtype          out, summed over the heads of each group in a fixed order
  *   dh0       [B, H, P, N]   fp32 or NULL   out (also when h0 is NULL: the gradient at h0 = 0)
  *   workspace, workspace_bytes              >= ssd_delta_bwd_plan's workspace_bytes
- * Outputs may not overlap inputs. seqlen == 0 writes dh0 = dh_final (or zeros).
+ * Outputs may not overlap inputs. seqlen == 0 writes dh0 = dh_final (or zeros). On SSD_PATH_TCGEN05
+ * the sums over state rows are fp32 sums of products of bf16 operands: dBm, dCm, dg and dbeta are right to
+ * 2^-8 of the terms that are summed in them, of fewer than 4 tokens, or up to 32 of fewer than 16 heads
+ * and rows, to 2^-8 of themselves.
  */
 ssd_status_t ssd_delta_bwd_plan(const ssd_shape_t *shape, ssd_dtype_t dtype, ssd_plan_t *plan);
 ssd_status_t ssd_delta_bwd(const ssd_shape_t *shape, ssd_dtype_t dtype, const void *x, const void *g, const void *beta,

@@ -24,8 +24,8 @@
 // Warps (640 threads): 0 loads (TMA, two stages), 1 issues the products, 2 ends a head (dg, dbeta), 4-19 the
 // elementwise work, four per 32 lanes with a quarter of the columns each.
 //
-// Bound by the elementwise warps: 5200 cycles per head and 64 rows, of which they work 4400 (60% of the issue slots)
-// and the products take 2400. 24 heads of 64 x 128, 4 x 2048 tokens: 82 us, of 24 us for its bytes; the same sums
+// Bound by the elementwise warps: 6100 cycles per head and 64 rows with the ends of a CTA, of which they work 4400 and
+// the products take 2400. 24 heads of 64 x 128, 4 x 2048 tokens: 84 us, of 24 us for its bytes; the same sums
 // with mma.sync, dQ and dK in registers, took 212. Issuing a step's first products before the last step's pairs,
 // or waiting for fewer of them, gained nothing (87 and 93 us).
 //

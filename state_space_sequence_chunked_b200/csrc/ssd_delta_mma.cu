@@ -14,7 +14,9 @@
 //
 // Precision. The final state is fp32, so what enters it is kept to 2^-16: an fp32 left operand is
 // split in two bf16 parts (hi + lo) and W too (three products); K, Q are exact. Y is rounded to bf16,
-// so S and tril(Q K^T o E) enter it as one bf16 part, u as two.
+// so S and tril(Q K^T o E) enter it as one bf16 part, u as two: off by 2.4e-3 of its norm, where rounding it takes
+// 1.7e-3. Two parts of each leave only that; they were timed at 145 us against 141 (24 heads, 8 x 2048 tokens)
+// and, with 168 MB more of workspace written and read, at 682 against 615 (80 heads, 4 x 8192).
 #include "delta_tc.cuh"
 
 namespace ssd {

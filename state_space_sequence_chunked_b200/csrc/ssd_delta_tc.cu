@@ -25,11 +25,11 @@
 //
 // Streams (128 state rows over the sequence) are dealt to the CTAs in equal shares of chunks, so a stream may be cut
 // once and handed on through global memory: 160 streams of 128 chunks took 731 us with whole streams (two waves on
-// 148 SMs), 432 in shares.
+// 148 SMs), 440 in shares.
 //
 // What bounds it: the chain of a chunk, S -> R -> u -> S, three products and three passes of the T warps over
-// their results, about 4700 cycles (2.5 us) per chunk and CTA, of which the 72 products take about 1950 to issue. 24 heads of
-// 64 x 128, 8 x 2048 tokens (96 CTAs, 32 chunks each): 104 us; 80 heads, 4 x 8192 (148 CTAs): 432 us. The
+// their results, about 5400 cycles (3.2 us) per chunk and CTA, of which the 72 products take about 1950 to issue. 24 heads of
+// 64 x 128, 8 x 2048 tokens (96 CTAs, 32 chunks each): 104 us; 80 heads, 4 x 8192 (148 CTAs): 440 us. The
 // same chain on mma.sync, the state in registers, took 2200 us of the latter and the prep.
 //
 // kStore is the backward pass's recomputation: no Y, but the state entering each chunk, err and u, rounded to bf16:
@@ -631,7 +631,8 @@ __device__ __forceinline__ void chain_fwd(const CUtensorMap &tm_k, const CUtenso
 // with F = Z + ek F0, z = F + E, r = beta z = dX. Rows, tokens and warps as above, plus warps 2-3, which
 // form eg dY. In a PAIR the products with P and W write one head's lanes at a time, as above.
 // z and dX go out in bf16, and D hi of every chunk (an operand of k_delta_grads_tc). Both chains share a launch, since
-// neither needs the other: 24 heads of 64 x 128, 4 x 2048 tokens, 132 us for both.
+// neither needs the other: 24 heads of 64 x 128, 4 x 2048 tokens, 117 us for both. 768 threads leave
+// 80 registers each, and the T warps of both spill (N = 128: 196 bytes in a PAIR, 252 without; 12 to 32 in the forward chain).
 template <int NT, bool PAIR>
 struct RevLay {
     static constexpr int HB = PAIR ? 2 : 1;

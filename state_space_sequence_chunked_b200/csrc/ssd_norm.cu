@@ -17,9 +17,9 @@
 // needed. Statistics and sums are fp32; an output that is stored in bf16 is rounded once, and the scaled
 // gradient dx is rounded from dr before dr is.
 //
-// Measured, bf16 rows: k_add_rmsnorm 32768 x 2560, fp32 residual, 161 us, 97%. k_add_rmsnorm_bwd 8191 x 2560 with all
+// Measured, bf16 rows: k_add_rmsnorm 32768 x 2560, fp32 residual, 165 us a call, 94%. k_add_rmsnorm_bwd 8191 x 2560 with all
 // outputs 53 us and its column sums 5.5, 66% together: two CTAs per SM hold dw and dscale in registers, and a
-// third does not fit. k_norm_gate 32768 x 5120 in groups of 64, 182 us, 86%. k_gate_bwd 16384 x 1536 in groups of 64,
+// third does not fit. k_norm_gate 32768 x 5120 in groups of 64, 191 us a call, 82%. k_gate_bwd 16384 x 1536 in groups of 64,
 // 53 us and 5.5, 66%. The next row is loaded before the present one is reduced (gradients 71 -> 59 us
 // and 62 -> 59); two rows ahead 73 and 59 (spills), loads through a ring in shared memory 10% slower (issue).
 #include "ssd_norm.cuh"
