@@ -452,7 +452,7 @@ struct BwdLayout {
 // segment they fit): where dB, dC, dg and dbeta are made of few numbers, these can be small against the terms that
 // cancel in them, and bf16 operands (2^-9) then show. Drawn cases with an output off by more than 3 * 2^-8 on bf16 operands, of 150
 // each: 1 token of 1, 4, 16 heads 32, 13, 8; 2 tokens 14, 2, 2; 8 tokens 3, 0, 0; 32 tokens none (beyond 2^-8.6: 9, 6, 1); in fp32
-// none, and no error above 3.5e-3. It costs 72 us against 47 (24 heads of 64 x 128, 1 token), and 427 against 183 (16 x 80 heads,
+// none (5.8e-3 at most). It costs 72 us against 47 (24 heads of 64 x 128, 1 token), and 427 against 183 (16 x 80 heads,
 // 8 tokens, where it is not taken).
 bool in_parts(const DeltaProblem &p) { return p.L < 4 || (p.L <= kSeg && p.B * p.H < 16); }
 BwdLayout bwd_layout(const DeltaProblem &p) {

@@ -35,7 +35,7 @@
 // kStore is the backward pass's recomputation: no Y, but the state entering each chunk, err and u, rounded to bf16:
 // they meet operands that are bf16 already (K, Q, dY) in gradients that are stored in bf16 (relative errors of
 // 3.2e-3 against 1.7e-3 for the storage alone); fp32 would double the pass's largest traffic. kParts, for short
-// sequences (see kSeg in ssd_delta_mma.cu), leaves err in two bf16 parts alone.
+// sequences (see in_parts in ssd_delta_mma.cu), leaves err in two bf16 parts alone.
 //
 // Every wait is bounded (tc_ptx.cuh); one that runs out sets bit 0 of the workspace's status word.
 #include "delta_tc.cuh"
